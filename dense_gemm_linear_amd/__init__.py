@@ -12,6 +12,10 @@ Functions mirror the C entry points:
   shuffle_b(B, dtype=None, out=None) -> Bs (uint8 device tensor)
   gemm_bf16(A, Bs, N, out=None, tile=None) -> C
   gemm_fp8_scaled(A, Bs, N, scale_a, scale_b, out=None, tile=None) -> C
+  linear_cross_entropy(X, W, labels, ...) -> (loss, lse)
+  linear_cross_entropy_grad(X, W, labels, loss, lse, dloss, ...) -> (dX, dW)
+  linear_distillation(X, W, index, teacher, ...) -> (loss, lse, logp)
+  linear_distillation_grad(X, W, index, teacher, lse, logp, dloss, ...) -> (dX, dW)
   gemm_status_string(code) -> str
 """
 from __future__ import annotations
@@ -43,7 +47,9 @@ GEMM_KERNEL_TILED_PP = 3
 EXPORTS = ("select_tile", "shuffle_b_bytes", "shuffle_b", "gemm_bf16", "gemm_fp8_scaled",
            "gemm_tile_check", "gemm_status_string", "select_tile_ws", "gemm_workspace_bytes",
            "gemm_bf16_ws", "gemm_fp8_scaled_ws", "gemm_bf16_ex", "gemm_fp8_scaled_ex", "shuffle_b_t",
-           "transpose_2d", "gemm_plan", "gemm_bf16_noalloc", "gemm_read_probe")
+           "transpose_2d", "gemm_plan", "gemm_bf16_noalloc", "gemm_read_probe",
+           "linear_loss_workspace_bytes", "linear_cross_entropy", "linear_cross_entropy_grad",
+           "linear_distillation", "linear_distillation_grad")
 
 # gemm_activation
 GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_SILU, GEMM_ACT_GELU_ERF, GEMM_ACT_GELU_TANH = 0, 1, 2, 3, 4
@@ -257,6 +263,21 @@ def _load_lib():
     lib.gemm_tile_check.restype = ctypes.c_int
     lib.gemm_read_probe.argtypes = [P, ctypes.c_uint64, P, P]
     lib.gemm_read_probe.restype = ctypes.c_int
+    F = ctypes.c_float
+    head = [P, I64, P, I64]                                       # X, W and their pitches
+    space = [P, ctypes.c_size_t, P]                               # workspace, stream
+    grads = [P, I64, P, I64, P, I64]                              # dloss, dX, dW
+    lib.linear_loss_workspace_bytes.argtypes = [I64, I64, I64, I64, ctypes.c_int32]
+    lib.linear_loss_workspace_bytes.restype = ctypes.c_size_t
+    lib.linear_cross_entropy.argtypes = head + [P, I64, I64, I64, F, F, I64, P, P] + space
+    lib.linear_cross_entropy.restype = ctypes.c_int
+    lib.linear_cross_entropy_grad.argtypes = head + [P, I64, I64, I64, F, F, I64, P, P] + grads + space
+    lib.linear_cross_entropy_grad.restype = ctypes.c_int
+    lib.linear_distillation.argtypes = head + [P, I64, P, I64, I64, I64, I64, I64, F, P, P, P] + space
+    lib.linear_distillation.restype = ctypes.c_int
+    lib.linear_distillation_grad.argtypes = head + [P, I64, P, I64, I64, I64, I64, I64, F, P, P] + \
+        grads + space
+    lib.linear_distillation_grad.restype = ctypes.c_int
     lib.gemm_status_string.argtypes = [ctypes.c_int]
     lib.gemm_status_string.restype = ctypes.c_char_p
     return lib
@@ -612,3 +633,201 @@ def gemm_bf16_noalloc(A, Bs, N: int, out, tile: Tile | None = None):
     if st != GEMM_OK:
         raise GemmError("gemm_bf16_noalloc", st)
     return C
+
+
+# ------------------------------------------------- losses of a linear head
+def linear_loss_workspace_bytes(T: int, V: int, D: int, slots: int = 0, backward: bool = False) -> int:
+    """Workspace of the linear_* losses for X [T, D], W [V, D] and `slots`
+    target slots a row (0: cross entropy).  backward: of the gradient call; it
+    serves the forward call too.  0 for T == 0 and for sizes the calls refuse."""
+    return int(lib.linear_loss_workspace_bytes(T, V, D, slots, int(bool(backward))))
+
+
+def _loss_operands(fn: str, X, W, per_row=(), per_slot=()):
+    """Element types, shapes and devices the C ABI cannot see.  per_row: (name,
+    tensor, dtype) vectors of T; per_slot: [T, k] tensors.  Types first, so
+    that the checks also run on a machine without a GPU."""
+    torch = _torch()
+    for name, t in (("X", X), ("W", W)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+            raise ValueError(f"{fn}: {name} must be a bfloat16 tensor")
+    for name, t, dt in tuple(per_row) + tuple(per_slot):
+        if not isinstance(t, torch.Tensor) or t.dtype != dt:
+            raise ValueError(f"{fn}: {name} must be a {dt} tensor")
+    for name, t in (("X", X), ("W", W)):
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{fn}: {name} must be a 2-D tensor with contiguous rows")
+    if X.shape[1] != W.shape[1]:
+        raise ValueError(f"{fn}: X has {X.shape[1]} columns, W {W.shape[1]}")
+    T = X.shape[0]
+    for name, t, _ in per_row:
+        if tuple(t.shape) != (T,) or (T > 1 and t.stride(0) != 1):
+            raise ValueError(f"{fn}: {name} must be a contiguous vector of {T} values")
+    for name, t, _ in per_slot:
+        if t.dim() != 2 or tuple(t.shape) != (T, per_slot[0][1].shape[-1]) or \
+                (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{fn}: {name} must be a [{T}, slots] tensor with contiguous rows")
+    for name, t in [("X", X), ("W", W)] + [(a, b) for a, b, _ in tuple(per_row) + tuple(per_slot)]:
+        if not t.is_cuda or t.device != X.device:
+            raise ValueError(f"{fn}: {name} must be a device tensor on X's device")
+
+
+def _pitch(t):
+    """Row pitch in elements (a single row's stride means nothing to a call)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _row_pitch8(t):
+    """_pitch for operands whose pitch the C ABI wants in multiples of 8."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _loss_workspace(fn: str, X, V: int, slots: int, backward: bool, workspace):
+    torch = _torch()
+    need = linear_loss_workspace_bytes(X.shape[0], V, X.shape[1], slots, backward)
+    if workspace is None:
+        # freed on return: the caching allocator reuses it on this stream only
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+    elif not workspace.is_cuda or workspace.device != X.device or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous device tensor on X's device")
+    elif workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"{fn}: workspace holds {workspace.numel() * workspace.element_size()} "
+                         f"bytes, {need} are needed")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _loss_grads(fn: str, X, W, dloss, need_dX, need_dW, dX, dW):
+    """(dloss, count, dX or None, dW or None) with the outputs made or checked."""
+    torch = _torch()
+    if not isinstance(dloss, torch.Tensor) or dloss.dtype != torch.float32:
+        raise ValueError(f"{fn}: dloss must be a float32 tensor")
+    T = X.shape[0]
+    if dloss.numel() != 1:
+        if tuple(dloss.shape) != (T,):
+            raise ValueError(f"{fn}: dloss must hold {T} values or one")
+        if dloss.stride(0) == 0:
+            dloss = dloss[:1]                    # one value expanded to every row
+        elif dloss.stride(0) != 1:
+            raise ValueError(f"{fn}: dloss must be contiguous")
+    if not dloss.is_cuda or dloss.device != X.device:
+        raise ValueError(f"{fn}: dloss must be a device tensor on X's device")
+    outs = []
+    for name, need, given, like in (("dX", need_dX, dX, X), ("dW", need_dW, dW, W)):
+        if not need:
+            if given is not None:
+                raise ValueError(f"{fn}: {name} given, but need_{name} is false")
+            outs.append(None)
+            continue
+        if given is None:
+            given = torch.empty(like.shape, dtype=torch.bfloat16, device=X.device)
+        elif given.dtype != torch.bfloat16 or tuple(given.shape) != tuple(like.shape) or \
+                not given.is_cuda or given.device != X.device or \
+                (given.shape[1] > 1 and given.stride(1) != 1) or \
+                (given.shape[0] > 1 and given.stride(0) < given.shape[1]):
+            raise ValueError(f"{fn}: {name} must be a bfloat16 {tuple(like.shape)} view with "
+                             "contiguous rows on X's device")
+        outs.append(given)
+    if outs[0] is None and outs[1] is None:
+        raise ValueError(f"{fn}: neither dX nor dW is asked for")
+    return dloss, (T if dloss.numel() == T else 1), outs[0], outs[1]
+
+
+def _grad_pointers(dX, dW):
+    out = []
+    for t in (dX, dW):
+        out += [None, 0] if t is None else [t.data_ptr(), _pitch(t)]
+    return out
+
+
+def _loss_call(fn: str, X, args, ws, nbytes):
+    # launches go to X's device, whichever device is current
+    with _torch().cuda.device(X.device):
+        st = getattr(lib, fn)(*args, ws.data_ptr(), nbytes, _stream_ptr(X))
+    if st != GEMM_OK:
+        raise GemmError(fn, st)
+
+
+def linear_cross_entropy(X, W, labels, *, scale: float = 1.0, z_loss: float = 0.0,
+                         ignore_index: int = -100, workspace=None):
+    """Softmax cross entropy of a linear head, one loss a row, without the
+    logits in memory: z = scale * X W^T (X [T, D], W [V, D] bf16), labels int64
+    [T]; loss[t] = lse[t] - z[t, labels[t]] + z_loss * lse[t]^2.  Returns (loss,
+    lse), float32 [T].  Rows with label ignore_index get 0 in both; a label
+    outside the vocabulary gives a NaN loss.  workspace: a uint8 device tensor
+    of linear_loss_workspace_bytes bytes (made for the call if not given)."""
+    torch = _torch()
+    fn = "linear_cross_entropy"
+    _loss_operands(fn, X, W, (("labels", labels, torch.int64),))
+    (T, D), V = X.shape, W.shape[0]
+    loss = torch.empty(T, dtype=torch.float32, device=X.device)
+    lse = torch.empty(T, dtype=torch.float32, device=X.device)
+    ws, nbytes = _loss_workspace(fn, X, V, 0, False, workspace)
+    _loss_call(fn, X, (X.data_ptr(), _row_pitch8(X), W.data_ptr(), _row_pitch8(W), labels.data_ptr(), T, V,
+                       D, scale, z_loss, ignore_index, loss.data_ptr(), lse.data_ptr()), ws, nbytes)
+    return loss, lse
+
+
+def linear_cross_entropy_grad(X, W, labels, loss, lse, dloss, *, scale: float = 1.0,
+                              z_loss: float = 0.0, ignore_index: int = -100, need_dX: bool = True,
+                              need_dW: bool = True, dX=None, dW=None, workspace=None):
+    """The gradients of linear_cross_entropy, with the loss and lse it returned
+    for the same arguments and dloss (float32, [T] or one value) the gradient
+    with respect to each row's loss.  Returns (dX, dW), bf16, None for one that
+    is not needed (need_dX, need_dW); dX / dW: views to write instead of new
+    tensors."""
+    torch = _torch()
+    fn = "linear_cross_entropy_grad"
+    _loss_operands(fn, X, W, (("labels", labels, torch.int64), ("loss", loss, torch.float32),
+                              ("lse", lse, torch.float32)))
+    (T, D), V = X.shape, W.shape[0]
+    dloss, count, dX, dW = _loss_grads(fn, X, W, dloss, need_dX, need_dW, dX, dW)
+    ws, nbytes = _loss_workspace(fn, X, V, 0, True, workspace)
+    _loss_call(fn, X, (X.data_ptr(), _row_pitch8(X), W.data_ptr(), _row_pitch8(W), labels.data_ptr(), T, V,
+                       D, scale, z_loss, ignore_index, loss.data_ptr(), lse.data_ptr(),
+                       dloss.data_ptr(), count, *_grad_pointers(dX, dW)), ws, nbytes)
+    return dX, dW
+
+
+def linear_distillation(X, W, index, teacher, *, scale: float = 1.0, workspace=None):
+    """Distillation loss of a linear head against a teacher's top logits,
+    without the student's logits in memory.  index int64 [T, slots] names the
+    teacher's columns, teacher float32 [T, slots] its logits there; a negative
+    index or a logit of -inf leaves a slot empty.  With z = scale * X W^T and q =
+    softmax(scale * teacher) over a row's filled slots, loss[t] = sum_j q_j (log
+    q_j - logp[t, j]), logp[t, j] = z[t, index[t, j]] - lse[t].  Returns (loss,
+    lse, logp), float32; a row with no filled slot gets 0 in all three."""
+    torch = _torch()
+    fn = "linear_distillation"
+    _loss_operands(fn, X, W, (), (("index", index, torch.int64), ("teacher", teacher, torch.float32)))
+    (T, D), V, k = X.shape, W.shape[0], index.shape[1]
+    loss = torch.empty(T, dtype=torch.float32, device=X.device)
+    lse = torch.empty(T, dtype=torch.float32, device=X.device)
+    logp = torch.empty((T, k), dtype=torch.float32, device=X.device)
+    ws, nbytes = _loss_workspace(fn, X, V, k, False, workspace)
+    _loss_call(fn, X, (X.data_ptr(), _row_pitch8(X), W.data_ptr(), _row_pitch8(W), index.data_ptr(),
+                       _pitch(index), teacher.data_ptr(), _pitch(teacher), T, V, D, k, scale,
+                       loss.data_ptr(), lse.data_ptr(), logp.data_ptr()), ws, nbytes)
+    return loss, lse, logp
+
+
+def linear_distillation_grad(X, W, index, teacher, lse, logp, dloss, *, scale: float = 1.0,
+                             need_dX: bool = True, need_dW: bool = True, dX=None, dW=None,
+                             workspace=None):
+    """The gradients of linear_distillation, with the lse and logp it returned
+    for the same arguments; dloss, need_*, dX, dW and the result as for
+    linear_cross_entropy_grad.  The teacher's logits get no gradient."""
+    torch = _torch()
+    fn = "linear_distillation_grad"
+    _loss_operands(fn, X, W, (("lse", lse, torch.float32),),
+                   (("index", index, torch.int64), ("teacher", teacher, torch.float32),
+                    ("logp", logp, torch.float32)))
+    (T, D), V, k = X.shape, W.shape[0], index.shape[1]
+    if not logp.is_contiguous():
+        raise ValueError(f"{fn}: logp must be contiguous")
+    dloss, count, dX, dW = _loss_grads(fn, X, W, dloss, need_dX, need_dW, dX, dW)
+    ws, nbytes = _loss_workspace(fn, X, V, k, True, workspace)
+    _loss_call(fn, X, (X.data_ptr(), _row_pitch8(X), W.data_ptr(), _row_pitch8(W), index.data_ptr(),
+                       _pitch(index), teacher.data_ptr(), _pitch(teacher), T, V, D, k, scale,
+                       lse.data_ptr(), logp.data_ptr(), dloss.data_ptr(), count,
+                       *_grad_pointers(dX, dW)), ws, nbytes)
+    return dX, dW

@@ -66,7 +66,8 @@ struct DeviceInfo {
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 
-// Current device: is it gfx950, and how many CUs.  Cached per device.
+}  // namespace
+
 gemm_status device_info(int* cus)
 {
     int dev = 0;
@@ -87,6 +88,8 @@ gemm_status device_info(int* cus)
     *cus = d.cus;
     return GEMM_OK;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 

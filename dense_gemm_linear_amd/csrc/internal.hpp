@@ -87,6 +87,9 @@ constexpr SkinnyRung kSkinnyLadder[] = {
 #undef DG_SR
 };
 
+// Current device: is it gfx950, and how many CUs.  Cached per device.
+gemm_status device_info(int* cus);
+
 // Index of the ladder rung a request names, or -1 (st, ktb: 0 = any).
 int tiled_rung(int tm, int tn, int waves, int atom, int st, int ktb);
 int ab_rung(int tm, int tn, int waves, int atom, int st, int ktb);

@@ -1,0 +1,762 @@
+// The linear head's losses: row selection, targets, the joins of the partial
+// log-sum-exps, the sparse columns of the gradient, and the launches around
+// the products of loss_kernels.hpp.
+//
+// Rows that are out (ignored labels, rows without a target) leave the
+// products: the kept rows of X are copied together first (memory-bound, T D
+// values against T V D multiply-adds), which skips the ignored rows' work and
+// keeps whatever their X holds, NaN included, out of every sum over rows.
+// How many are kept is known on the device only: grids are sized for every
+// row and surplus workgroups return.
+#include "loss.hpp"
+
+#include <math.h>
+#include <string.h>
+
+#include "internal.hpp"
+#include "loss_kernels.hpp"
+
+namespace dg {
+namespace {
+
+constexpr int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+constexpr int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+// Rows counted per entry of the chunk table, and up to how many rows one
+// workgroup counts the rows in front of it by itself (128 KiB of labels, L2).
+constexpr int kChunk = 1024;
+constexpr int64_t kOwnCount = 16384;
+constexpr int kSelRows = 16;     // rows one workgroup of the selection moves
+
+// Row state: out, kept, or kept with a target outside the vocabulary (loss
+// and gradient NaN).
+enum { ROW_OUT = 0, ROW_KEPT = 1, ROW_BAD = 2 };
+
+struct RowSource {
+    const int64_t* labels;       // cross entropy
+    int64_t ignore_index, V;
+    const int* flag;             // distillation: [T][2] row state, lead column
+};
+
+__device__ __forceinline__ int row_state(const RowSource& s, int64_t t, int& label)
+{
+    if (s.flag) {
+        const int f = s.flag[2 * t];
+        label = s.flag[2 * t + 1];
+        return f;
+    }
+    const int64_t y = s.labels[t];
+    if (y == s.ignore_index)
+        return ROW_OUT;
+    const bool in = y >= 0 && y < s.V;
+    label = in ? (int)y : -1;
+    return in ? ROW_KEPT : ROW_BAD;
+}
+
+__device__ __forceinline__ int wave_sum(int x)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        x += __shfl_xor(x, d);
+    return x;
+}
+__device__ __forceinline__ float wave_sum(float x)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        x += __shfl_xor(x, d);
+    return x;
+}
+__device__ __forceinline__ float wave_max(float x)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        x = fmaxf(x, __shfl_xor(x, d));
+    return x;
+}
+
+// Kept rows in [t0, t1), counted by a workgroup of 256 threads.
+__device__ __forceinline__ int count_kept(const RowSource& src, int64_t t0, int64_t t1, int* red)
+{
+    int c = 0, label;
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += 256)
+        c += row_state(src, t, label) != ROW_OUT;
+    c = wave_sum(c);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = c;
+    __syncthreads();
+    return red[0] + red[1] + red[2] + red[3];
+}
+
+__global__ __launch_bounds__(256) void loss_count_kernel(RowSource src, int64_t T, int* chunks)
+{
+    __shared__ int red[4];
+    const int64_t t0 = (int64_t)blockIdx.x * kChunk;
+    const int c = count_kept(src, t0, min(T, t0 + kChunk), red);
+    if (threadIdx.x == 0)
+        chunks[blockIdx.x] = c;
+}
+
+struct SelectArgs {
+    RowSource src;
+    int64_t T;
+    const int* chunks;           // kept rows per kChunk rows, or null: count them here
+    const uint8_t* X;
+    int64_t ldx_b;
+    uint8_t* Xc;                 // [n][D] compact
+    int64_t row_b;               // D * 2
+    int* n_kept;
+    int* map;                    // compact row -> row
+    int* pos;                    // row -> compact row, -1: out
+    RowInfo* rows;
+    // forward
+    float* zlabel;
+    float* loss;
+    float* lse_out;
+    // gradient
+    const float* loss_in;
+    const float* lse_in;
+    const float* dloss;
+    int64_t dloss_stride;
+    float scale, z_loss;
+};
+
+// 16 rows a workgroup: how many kept rows lie in front of them, each row's
+// place, what the row's gradient needs, and the copy of the kept rows.
+__global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
+{
+    __shared__ int red[4];
+    __shared__ int place[kSelRows];
+    const int64_t t0 = (int64_t)blockIdx.x * kSelRows;
+    int before;
+    if (p.chunks) {
+        const int64_t c0 = t0 / kChunk;
+        int c = 0;
+        for (int64_t i = threadIdx.x; i < c0; i += 256)
+            c += p.chunks[i];
+        c = wave_sum(c);
+        if ((threadIdx.x & 63) == 0)
+            red[threadIdx.x >> 6] = c;
+        __syncthreads();
+        before = red[0] + red[1] + red[2] + red[3];
+        before += count_kept(p.src, c0 * kChunk, t0, red);
+    } else {
+        before = count_kept(p.src, 0, t0, red);
+    }
+    if (threadIdx.x < 64) {
+        const int64_t t = t0 + threadIdx.x;
+        const bool mine = threadIdx.x < kSelRows && t < p.T;
+        int label = -1;
+        const int st = mine ? row_state(p.src, t, label) : ROW_OUT;
+        const uint64_t kept = __ballot(st != ROW_OUT);
+        const int at = before + __popcll(kept & ((1ull << threadIdx.x) - 1));
+        if (mine) {
+            place[threadIdx.x] = st != ROW_OUT ? at : -1;
+            p.pos[t] = st != ROW_OUT ? at : -1;
+            if (st != ROW_OUT) {
+                RowInfo ri = {0.f, 0.f, 0.f, label};
+                if (p.lse_in) {
+                    const float lse = p.lse_in[t];
+                    const float g = p.dloss[t * p.dloss_stride] * p.scale;
+                    const float extra = 2.f * p.z_loss * lse;
+                    ri.lse = lse;
+                    ri.a = g * (1.f + extra);
+                    if (p.loss_in) {
+                        // p - 1 = expm1(-nll), exact for p near 1 too
+                        const float nll = p.loss_in[t] - p.z_loss * lse * lse;
+                        ri.b = g * (expm1f(-nll) + extra * expf(-nll));
+                    } else {
+                        ri.label = -1;         // distillation: sparse columns come after
+                        ri.b = g;
+                    }
+                    if (st == ROW_BAD)
+                        ri.a = ri.b = NAN;
+                }
+                if (p.zlabel)
+                    p.zlabel[at] = NAN;        // stays for a target outside the vocabulary
+                p.rows[at] = ri;
+                p.map[at] = (int)t;
+            } else if (p.loss) {
+                p.loss[t] = 0.f;
+                p.lse_out[t] = 0.f;
+            }
+        }
+        if (threadIdx.x == 0 && t0 + kSelRows >= p.T)
+            *p.n_kept = before + __popcll(kept);
+    }
+    __syncthreads();
+    const int64_t pieces = p.row_b / 16;
+    const int nrows = (int)min((int64_t)kSelRows, p.T - t0);
+    for (int64_t i = threadIdx.x; i < nrows * pieces; i += 256) {
+        const int r = (int)(i / pieces);
+        const int64_t c = i - r * pieces;
+        if (place[r] >= 0)
+            *reinterpret_cast<i32x4*>(p.Xc + place[r] * p.row_b + c * 16) =
+                *reinterpret_cast<const i32x4*>(p.X + (t0 + r) * p.ldx_b + c * 16);
+    }
+}
+
+// Joins the tile columns' (maximum, sum) pairs of each kept row and, with the
+// label's z, gives lse and the negative log-probability of the label.  16
+// rows a workgroup, 16 threads a row.
+__global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, int64_t ldpart, int tiles_n,
+                                                        const int* n_kept, const int* map,
+                                                        const float* zlabel, float z_loss, float* loss,
+                                                        float* lse)
+{
+    __shared__ float2 red[16][17];
+    const int n = *n_kept;
+    const int r = threadIdx.x & 15, q = threadIdx.x >> 4;
+    const int row = blockIdx.x * 16 + r;
+    if (blockIdx.x * 16 >= n)
+        return;
+    float m = -INFINITY, s = 0.f;
+    if (row < n)
+        for (int t = q; t < tiles_n; t += 16) {
+            const float2 v = part[t * ldpart + row];
+            const float nm = fmaxf(m, v.x);
+            const float ref = nm == -INFINITY ? 0.f : nm;
+            s = s * exp_diff(m, ref) + (v.x == -INFINITY ? v.y : v.y * exp_diff(v.x, ref));
+            m = nm;
+        }
+    red[q][r] = make_float2(m, s);
+    __syncthreads();
+    if (q != 0 || row >= n)
+        return;
+    float top = -INFINITY;
+    for (int i = 0; i < 16; ++i)
+        top = fmaxf(top, red[i][r].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    for (int i = 0; i < 16; ++i) {
+        const float2 v = red[i][r];
+        sum += v.x == -INFINITY ? v.y : v.y * exp_diff(v.x, ref);
+    }
+    const float others = sum == 0.f ? -INFINITY : ref + logf(sum);   // one column: no others
+    const float zl = zlabel[row];
+    const float d = others - zl;
+    const float nll = fmaxf(d, 0.f) + log1pf(expf(-fabsf(d))) + (d != d ? d : 0.f);
+    // no label column (NaN), or one of z = -inf: lse of all that was summed
+    const float l = d != d || zl == -INFINITY ? others : zl + nll;
+    const int t = map[row];
+    loss[t] = nll + z_loss * l * l;
+    lse[t] = l;
+}
+
+// ---------------------------------------------------------------------------
+// Distillation targets.  One wave a row: q = softmax(scale * teacher) over the
+// row's filled slots; slots that name one column together count once, in the
+// first of them (the leader); the row's lead is the column of the largest q.
+// For a leader, rest = 1 - (its q) is the sum of the other slots' q, so that
+// p - q of a column that both sides are sure of keeps its digits.
+struct TargetArgs {
+    const int64_t* index;
+    const float* teacher;
+    int64_t ld_index, ld_teacher, T, V;
+    int k;
+    float scale;
+    float* q;                    // [T][k]: q of the slot, 0 where it is empty
+    float* qsum;                 // [T][k]: q of the slot's column, all its slots
+    float* rest;                 // [T][k]: 1 - qsum
+    int* leader;                 // [T][k]: column, or -1: empty or not the first
+    int* flag;                   // [T][2]: row state, lead column
+};
+
+__global__ __launch_bounds__(64) void loss_target_kernel(TargetArgs p)
+{
+    __shared__ int idx[kMaxLossSlots];
+    __shared__ float qs[kMaxLossSlots];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x;
+    float m = -INFINITY;
+    bool bad = false, any = false;
+    for (int j = lane; j < p.k; j += 64) {
+        const int64_t i = p.index[t * p.ld_index + j];
+        const float z = p.teacher[t * p.ld_teacher + j] * p.scale;
+        const bool filled = i >= 0 && p.teacher[t * p.ld_teacher + j] != -INFINITY;
+        const bool in = filled && i < p.V;
+        any |= filled;
+        bad |= filled && (!in || !(fabsf(z) < INFINITY));
+        idx[j] = in ? (int)i : -1;
+        qs[j] = filled ? z : -INFINITY;
+        if (in)
+            m = fmaxf(m, z);
+    }
+    m = wave_max(m);
+    any = __any(any);
+    bad = __any(bad);
+    __syncthreads();
+    float s = 0.f;
+    for (int j = lane; j < p.k; j += 64)
+        s += idx[j] >= 0 ? expf(qs[j] - m) : 0.f;
+    s = wave_sum(s);
+    __syncthreads();
+    for (int j = lane; j < p.k; j += 64)
+        qs[j] = idx[j] >= 0 ? expf(qs[j] - m) / s : 0.f;
+    __syncthreads();
+    // the lead: the largest q, the lowest slot among equals
+    float best = -1.f;
+    int slot = p.k;
+    for (int j = lane; j < p.k; j += 64)
+        if (idx[j] >= 0 && qs[j] > best) {
+            best = qs[j];
+            slot = j;
+        }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const float ob = __shfl_xor(best, d);
+        const int os = __shfl_xor(slot, d);
+        if (ob > best || (ob == best && os < slot)) {
+            best = ob;
+            slot = os;
+        }
+    }
+    if (lane == 0) {
+        p.flag[2 * t] = !any ? ROW_OUT : bad ? ROW_BAD : ROW_KEPT;
+        p.flag[2 * t + 1] = slot < p.k ? idx[slot] : -1;
+    }
+    for (int j = lane; j < p.k; j += 64) {
+        const int me = idx[j];
+        bool first = me >= 0;
+        float rest = 0.f, sum = 0.f;
+        for (int i = 0; i < p.k; ++i) {
+            const bool same = idx[i] == me;
+            first = first && !(same && i < j);
+            rest += same ? 0.f : qs[i];
+            sum += same ? qs[i] : 0.f;
+        }
+        p.q[t * p.k + j] = qs[j];
+        p.qsum[t * p.k + j] = sum;
+        p.rest[t * p.k + j] = rest;
+        p.leader[t * p.k + j] = first ? me : -1;
+    }
+}
+
+struct PickArgs {
+    const uint8_t* W;
+    int64_t ldw_b;
+    const uint8_t* Xc;
+    int64_t row_b;
+    const int* pos;
+    const int64_t* index;
+    int64_t ld_index, V;
+    const float* teacher;
+    int64_t ld_teacher;
+    const float* q;
+    const int* flag;
+    int k;
+    float scale;
+    const float* zlabel;
+    float* loss;                 // in: the lead's negative log-probability; out: the loss
+    const float* lse;
+    float* logp;                 // [T][k]
+};
+
+__device__ __forceinline__ float dot8(i32x4 a, i32x4 b, float s)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = (uint32_t)a[i], y = (uint32_t)b[i];
+        s = fmaf(__uint_as_float(x << 16), __uint_as_float(y << 16), s);
+        s = fmaf(__uint_as_float(x & 0xFFFF0000u), __uint_as_float(y & 0xFFFF0000u), s);
+    }
+    return s;
+}
+
+// The student's log-probabilities at a row's slots, and the row's loss: a
+// workgroup of 4 waves a row, four slots at a time a wave, each a dot product of the
+// row of X with the slot's row of W.
+__global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p)
+{
+    __shared__ float z[kMaxLossSlots];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int at = p.pos[t];
+    float* out = p.logp + t * p.k;
+    if (at < 0) {
+        for (int j = threadIdx.x; j < p.k; j += 256)
+            out[j] = 0.f;
+        return;
+    }
+    const uint8_t* x = p.Xc + at * p.row_b;
+    const int lead = p.flag[2 * t + 1];
+    for (int j0 = 4 * wave; j0 < p.k; j0 += 16) {
+        const uint8_t* w[4];
+        int use[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = j0 + u < p.k ? p.index[t * p.ld_index + j0 + u] : -1;
+            use[u] = i >= 0 && i < p.V;
+            w[u] = p.W + (use[u] ? i : 0) * p.ldw_b;
+        }
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t b = lane * 16; b < p.row_b; b += 1024) {
+            const i32x4 xv = *reinterpret_cast<const i32x4*>(x + b);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                s[u] = dot8(xv, *reinterpret_cast<const i32x4*>(w[u] + b), s[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            s[u] = wave_sum(s[u]);
+            if (lane == 0 && j0 + u < p.k)
+                z[j0 + u] = s[u] * p.scale;
+        }
+    }
+    __syncthreads();
+    if (wave != 0)
+        return;
+    // the lead's own log-probability is the well-conditioned one of the join;
+    // the others' follow from their distance to it
+    const float lead_nll = p.loss[t], zl = p.zlabel[at];
+    float mx = -INFINITY;
+    for (int j = lane; j < p.k; j += 64) {
+        const int64_t i = p.index[t * p.ld_index + j];
+        const float te = p.teacher[t * p.ld_teacher + j];
+        if (i >= 0 && i < p.V && te != -INFINITY)
+            mx = fmaxf(mx, te * p.scale);
+    }
+    mx = wave_max(mx);
+    float es = 0.f;
+    for (int j = lane; j < p.k; j += 64) {
+        const int64_t i = p.index[t * p.ld_index + j];
+        const float te = p.teacher[t * p.ld_teacher + j];
+        if (i >= 0 && i < p.V && te != -INFINITY)
+            es += expf(te * p.scale - mx);
+    }
+    const float log_es = logf(wave_sum(es));
+    float part = 0.f;
+    for (int j = lane; j < p.k; j += 64) {
+        const int64_t i = p.index[t * p.ld_index + j];
+        const float te = p.teacher[t * p.ld_teacher + j];
+        if (i < 0 || te == -INFINITY) {
+            out[j] = 0.f;
+            continue;
+        }
+        const float lp = i >= p.V ? NAN : i == lead ? -lead_nll : (z[j] - zl) - lead_nll;
+        out[j] = lp;
+        const float qj = p.q[t * p.k + j];
+        if (qj > 0.f)
+            part += qj * ((te * p.scale - mx) - log_es - lp);
+    }
+    part = wave_sum(part);
+    if (lane == 0)
+        p.loss[t] = p.flag[2 * t] == ROW_BAD ? NAN : part;
+}
+
+// Distillation: the sparse columns of the gradient piece, p - q in place of
+// p.  One wave a kept row.
+__global__ __launch_bounds__(256) void loss_sparse_kernel(const int* n_kept, const int* map,
+                                                          const RowInfo* rows, const int* leader,
+                                                          const float* qsum, const float* rest,
+                                                          const float* logp, int k, int64_t v0,
+                                                          int64_t vp, uint16_t* G, int64_t ldg)
+{
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= *n_kept)
+        return;
+    const int64_t t = map[row];
+    const float g = rows[row].b;
+    for (int j = threadIdx.x & 63; j < k; j += 64) {
+        const int64_t col = leader[t * k + j];
+        if (col < v0 || col >= v0 + vp)
+            continue;
+        const float lp = logp[t * k + j], r = rest[t * k + j];
+        // q of the column: the sum of its slots' q is 1 - rest
+        // p - q with q = 1 - rest: near p = q = 1 both sides are taken from 1
+        const float d = r < 0.5f ? expm1f(lp) + r : expf(lp) - qsum[t * k + j];
+        G[row * ldg + (col - v0)] = bf16_rne(g * d);
+    }
+}
+
+// dX: the sum of the K slices' planes in slice order, rounded once; zero for
+// rows that are out.
+__global__ __launch_bounds__(256) void loss_dx_kernel(const float* planes, int splits, int64_t plane,
+                                                      int64_t ldplane, const int* pos, uint16_t* dX,
+                                                      int64_t lddx, int64_t D)
+{
+    const int64_t t = blockIdx.x;
+    const int at = pos[t];
+    for (int64_t d = threadIdx.x; d < D; d += 256) {
+        float s = 0.f;
+        if (at >= 0)
+            for (int i = 0; i < splits; ++i)
+                s += planes[i * plane + at * ldplane + d];
+        dX[t * lddx + d] = bf16_rne(s);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launches.
+using Big = LossShape<256, 256, 2, 4, 4, 64, 1>;
+using Mid = LossShape<128, 128, 2, 2, 4, 64, 2>;
+using Low = LossShape<32, 128, 1, 4, 4, 128, 2>;
+
+template <class S, int ROLE>
+hipError_t go(const LossArgs& a, int64_t tiles_m, hipStream_t s)
+{
+    LossArgs copy = a;
+    copy.tiles_n = (int)cdiv(a.N, S::TN);
+    if constexpr (ROLE == ROLE_DX) {
+        const int nkt = (int)cdiv(a.K, S::KT);
+        copy.kt_per = (int)cdiv(nkt, a.splits);
+    }
+    const int64_t grid = tiles_m * copy.tiles_n * (ROLE == ROLE_DX ? a.splits : 1);
+    if (grid > INT32_MAX)
+        return hipErrorInvalidValue;
+    void* args[] = {&copy};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&loss_gemm_kernel<S, ROLE>), dim3((unsigned)grid),
+                           dim3(S::THREADS), args, 0, s);
+}
+
+template <int ROLE>
+hipError_t launch_role(const LossArgs& a, int64_t rows, int cus, hipStream_t s)
+{
+    if constexpr (ROLE != ROLE_DW) {
+        if (rows <= 32)
+            return go<Low, ROLE>(a, cdiv(rows, Low::TM), s);
+    }
+    if (cdiv(rows, 256) * cdiv(a.N, 256) * (ROLE == ROLE_DX ? a.splits : 1) >= cus / 2)
+        return go<Big, ROLE>(a, cdiv(rows, Big::TM), s);
+    return go<Mid, ROLE>(a, cdiv(rows, Mid::TM), s);
+}
+
+hipError_t last() { return hipGetLastError(); }
+
+#define DG_TRY(x)                    \
+    do {                             \
+        const hipError_t e_ = (x);   \
+        if (e_ != hipSuccess)        \
+            return e_;               \
+    } while (0)
+
+hipError_t select_rows(const LossCall& c, const LossPlan& pl, bool backward)
+{
+    uint8_t* ws = c.ws;
+    RowSource src = {c.labels, c.ignore_index, c.V, nullptr};
+    if (c.slots) {
+        TargetArgs t;
+        t.index = c.index;
+        t.teacher = c.teacher;
+        t.ld_index = c.ld_index;
+        t.ld_teacher = c.ld_teacher;
+        t.T = c.T;
+        t.V = c.V;
+        t.k = (int)c.slots;
+        t.scale = c.scale;
+        t.q = reinterpret_cast<float*>(ws + pl.off_q);
+        t.qsum = reinterpret_cast<float*>(ws + pl.off_qsum);
+        t.rest = reinterpret_cast<float*>(ws + pl.off_rest);
+        t.leader = reinterpret_cast<int*>(ws + pl.off_lead);
+        t.flag = reinterpret_cast<int*>(ws + pl.off_flag);
+        src.flag = t.flag;
+        loss_target_kernel<<<dim3((unsigned)c.T), dim3(64), 0, c.stream>>>(t);
+        DG_TRY(last());
+    }
+    int* chunks = nullptr;
+    if (c.T > kOwnCount) {
+        chunks = reinterpret_cast<int*>(ws + pl.off_chunks);
+        loss_count_kernel<<<dim3((unsigned)cdiv(c.T, kChunk)), dim3(256), 0, c.stream>>>(src, c.T, chunks);
+        DG_TRY(last());
+    }
+    SelectArgs a;
+    a.src = src;
+    a.T = c.T;
+    a.chunks = chunks;
+    a.X = reinterpret_cast<const uint8_t*>(c.X);
+    a.ldx_b = c.ldx * 2;
+    a.Xc = ws + pl.off_x;
+    a.row_b = c.D * 2;
+    a.n_kept = reinterpret_cast<int*>(ws + pl.off_count);
+    a.map = reinterpret_cast<int*>(ws + pl.off_map);
+    a.pos = reinterpret_cast<int*>(ws + pl.off_pos);
+    a.rows = reinterpret_cast<RowInfo*>(ws + pl.off_rows);
+    a.zlabel = backward ? nullptr : reinterpret_cast<float*>(ws + pl.off_zlabel);
+    a.loss = c.loss;
+    a.lse_out = c.lse;
+    a.loss_in = c.loss_in;
+    a.lse_in = c.lse_in;
+    a.dloss = c.dloss;
+    a.dloss_stride = c.dloss_stride;
+    a.scale = c.scale;
+    a.z_loss = c.z_loss;
+    loss_select_kernel<<<dim3((unsigned)cdiv(c.T, kSelRows)), dim3(256), 0, c.stream>>>(a);
+    return last();
+}
+
+LossArgs product_args(const LossCall& c, const LossPlan& pl)
+{
+    LossArgs a;
+    memset(&a, 0, sizeof a);
+    a.n_kept = reinterpret_cast<const int*>(c.ws + pl.off_count);
+    a.rows = reinterpret_cast<const RowInfo*>(c.ws + pl.off_rows);
+    a.scale = c.scale;
+    a.splits = 1;
+    return a;
+}
+
+}  // namespace
+
+LossPlan loss_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool backward)
+{
+    LossPlan p;
+    memset(&p, 0, sizeof p);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t o = at;
+        at = round_up(at + bytes, 256);
+        return o;
+    };
+    p.rows_pad = round_up(T, 256);
+    p.off_count = take(256);
+    p.off_chunks = take(cdiv(T, kChunk) * 4);
+    p.off_map = take(p.rows_pad * 4);
+    p.off_pos = take(p.rows_pad * 4);
+    p.off_rows = take(p.rows_pad * 16);
+    p.off_x = take(T * D * 2);
+    if (slots) {
+        p.off_q = take(T * slots * 4);
+        p.off_qsum = take(T * slots * 4);
+        p.off_rest = take(T * slots * 4);
+        p.off_lead = take(T * slots * 4);
+        p.off_flag = take(T * 8);
+    }
+    const int64_t shared = at;
+    p.tiles_n_max = cdiv(V, 128);
+    p.off_part = take(p.tiles_n_max * p.rows_pad * 8);
+    p.off_zlabel = take(p.rows_pad * 4);
+    p.bytes = at;
+    if (backward) {
+        at = shared;
+        // G of one piece: about 64 MiB, a multiple of 256 columns
+        int64_t piece = (INT64_C(64) << 20) / 2 / p.rows_pad / 256 * 256;
+        piece = std::max<int64_t>(piece, 256);
+        piece = std::min(piece, round_up(V, 256));
+        p.piece = piece;
+        const int64_t tiles = cdiv(T, 128) * cdiv(D, 128);
+        p.splits = (int)std::min<int64_t>(16, std::max<int64_t>(1, 512 / tiles));
+        p.splits = (int)std::min<int64_t>(p.splits, std::max<int64_t>(1, piece / 512));
+        p.off_g = take(p.rows_pad * piece * 2);
+        p.off_planes = take((int64_t)p.splits * T * D * 4);
+        p.bytes = std::max(p.bytes, at);
+    }
+    return p;
+}
+
+hipError_t loss_forward(const LossCall& c)
+{
+    const LossPlan pl = loss_plan(c.T, c.V, c.D, c.slots, false);
+    uint8_t* ws = c.ws;
+    DG_TRY(select_rows(c, pl, false));
+    LossArgs a = product_args(c, pl);
+    a.A = ws + pl.off_x;
+    a.lda_b = c.D * 2;
+    a.B = reinterpret_cast<const uint8_t*>(c.W);
+    a.ldb_b = c.ldw * 2;
+    a.N = (int)c.V;
+    a.K = (int)c.D;
+    a.part = reinterpret_cast<float2*>(ws + pl.off_part);
+    a.ldpart = pl.rows_pad;
+    a.zlabel = reinterpret_cast<float*>(ws + pl.off_zlabel);
+    DG_TRY(launch_role<ROLE_LSE>(a, c.T, c.cus, c.stream));
+    const bool big = c.T > 32 && cdiv(c.T, 256) * cdiv(c.V, 256) >= c.cus / 2;
+    loss_join_kernel<<<dim3((unsigned)cdiv(c.T, 16)), dim3(256), 0, c.stream>>>(
+        a.part, a.ldpart, (int)cdiv(c.V, big ? 256 : 128), a.n_kept,
+        reinterpret_cast<const int*>(ws + pl.off_map), a.zlabel, c.slots ? 0.f : c.z_loss, c.loss, c.lse);
+    DG_TRY(last());
+    if (!c.slots)
+        return hipSuccess;
+    PickArgs k;
+    k.W = a.B;
+    k.ldw_b = a.ldb_b;
+    k.Xc = a.A;
+    k.row_b = a.lda_b;
+    k.pos = reinterpret_cast<const int*>(ws + pl.off_pos);
+    k.index = c.index;
+    k.ld_index = c.ld_index;
+    k.V = c.V;
+    k.teacher = c.teacher;
+    k.ld_teacher = c.ld_teacher;
+    k.q = reinterpret_cast<const float*>(ws + pl.off_q);
+    k.flag = reinterpret_cast<const int*>(ws + pl.off_flag);
+    k.k = (int)c.slots;
+    k.scale = c.scale;
+    k.zlabel = a.zlabel;
+    k.loss = c.loss;
+    k.lse = c.lse;
+    k.logp = c.logp;
+    loss_pick_kernel<<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(k);
+    return last();
+}
+
+hipError_t loss_backward(const LossCall& c)
+{
+    const LossPlan pl = loss_plan(c.T, c.V, c.D, c.slots, true);
+    uint8_t* ws = c.ws;
+    DG_TRY(select_rows(c, pl, true));
+    const int* pos = reinterpret_cast<const int*>(ws + pl.off_pos);
+    const int* map = reinterpret_cast<const int*>(ws + pl.off_map);
+    uint16_t* G = reinterpret_cast<uint16_t*>(ws + pl.off_g);
+    const uint8_t* Xc = ws + pl.off_x;
+    float* planes = reinterpret_cast<float*>(ws + pl.off_planes);
+    for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
+        const int64_t vp = std::min(pl.piece, c.V - v0);
+        const uint8_t* W = reinterpret_cast<const uint8_t*>(c.W) + v0 * c.ldw * 2;
+        LossArgs a = product_args(c, pl);
+        a.A = Xc;
+        a.lda_b = c.D * 2;
+        a.B = W;
+        a.ldb_b = c.ldw * 2;
+        a.N = (int)vp;
+        a.K = (int)c.D;
+        a.v0 = (int)v0;
+        a.C = G;
+        a.ldc = pl.piece;
+        DG_TRY(launch_role<ROLE_GRAD>(a, c.T, c.cus, c.stream));
+        if (c.slots) {
+            loss_sparse_kernel<<<dim3((unsigned)cdiv(c.T, 4)), dim3(256), 0, c.stream>>>(
+                a.n_kept, map, a.rows, reinterpret_cast<const int*>(ws + pl.off_lead),
+                reinterpret_cast<const float*>(ws + pl.off_qsum),
+                reinterpret_cast<const float*>(ws + pl.off_rest), c.logp_in, (int)c.slots, v0, vp, G,
+                pl.piece);
+            DG_TRY(last());
+        }
+        if (c.dX) {
+            LossArgs d = product_args(c, pl);
+            d.A = reinterpret_cast<const uint8_t*>(G);
+            d.lda_b = pl.piece * 2;
+            d.B = W;
+            d.ldb_b = c.ldw * 2;
+            d.N = (int)c.D;
+            d.K = (int)vp;
+            d.splits = pl.splits;
+            d.planes = planes;
+            d.plane = c.T * c.D;
+            d.ldplane = c.D;
+            d.first = v0 == 0;
+            DG_TRY(launch_role<ROLE_DX>(d, c.T, c.cus, c.stream));
+        }
+        if (c.dW) {
+            LossArgs d = product_args(c, pl);
+            d.A = reinterpret_cast<const uint8_t*>(G);
+            d.lda_b = pl.piece * 2;
+            d.B = Xc;
+            d.ldb_b = c.D * 2;
+            d.M = (int)vp;
+            d.N = (int)c.D;
+            d.C = c.dW + v0 * c.lddw;
+            d.ldc = c.lddw;
+            d.c_vec = ((uintptr_t)c.dW & 15u) == 0 && c.lddw % 8 == 0;
+            DG_TRY(launch_role<ROLE_DW>(d, vp, c.cus, c.stream));
+        }
+    }
+    if (c.dX) {
+        loss_dx_kernel<<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(
+            planes, pl.splits, c.T * c.D, c.D, pos, c.dX, c.lddx, c.D);
+        DG_TRY(last());
+    }
+    return hipSuccess;
+}
+
+}  // namespace dg

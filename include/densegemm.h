@@ -481,6 +481,102 @@ gemm_status gemm_tile_check(const gemm_tile* tile, int64_t M, gemm_dtype dtype);
 #define GEMM_READ_PROBE_SLOTS 32768
 gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void* stream);
 
+/*
+ * Losses of a linear head.  A head's logits over a vocabulary of V columns are
+ *     z[t][v] = scale * sum_d X[t][d] * W[v][d]
+ * with X the hidden rows [T, D] and W the nn.Linear weight [V, D], bf16, sums
+ * in fp32.  The entry points below take losses from z, and the gradients of X
+ * and W, without storing z: the forward pass keeps one pair of floats per row
+ * and 128 or 256 columns, the gradient one piece of the vocabulary at a time
+ * (about 64 MiB of bf16), recomputed from X and W.
+ *
+ * Rows that are out -- an ignored label, no filled target slot -- have loss
+ * 0, lse 0 and gradient 0, take no part in the products, and whatever their X
+ * holds (NaN, infinities) reaches nothing.  A target outside the vocabulary
+ * is an error the device finds: the row's loss is NaN, and so are its
+ * gradients (all of dW, if that is asked for); no memory is touched for it.
+ *
+ * Common arguments:
+ *   X   device bf16 [T, ldx], W device bf16 [V, ldw]: rows of D contiguous
+ *       values, 16-byte aligned, pitches multiples of 8 elements and at
+ *       least D.  D a multiple of 8.
+ *   scale  multiplies the logits (1 / temperature); finite.
+ *   lse    fp32 [T]: log sum_v exp z[t][v].
+ *   dloss  device fp32: the gradient of the whole with respect to each row's
+ *       loss, dloss_count = T values, or 1 value for every row.
+ *   dX  device bf16 [T, lddx], dW device bf16 [V, lddw], 2-byte aligned,
+ *       pitches at least D; NULL leaves that gradient out (not both).  Every
+ *       element of the T x D / V x D region is overwritten, nothing else is.
+ *       Rounded once, to nearest even, from fp32 sums; the logits' gradient
+ *       they are products of is rounded to bf16 first.
+ *   workspace  device, 256-byte aligned, at least
+ *       linear_loss_workspace_bytes(T, V, D, slots, backward) bytes (slots 0
+ *       for cross entropy; backward 1 also serves the forward call).  Its
+ *       contents on entry are ignored and on return unspecified; calls that
+ *       share one must not overlap in time.
+ *
+ * Every sum has a fixed order: a call's results are bitwise repeatable.  All
+ * work is enqueued on `stream`, without allocation, synchronisation or memset
+ * nodes, and may be captured in a graph.
+ *
+ * Errors: INVALID_VALUE for a null, misaligned or too small argument, V or D
+ * below 1, T below 0, a scale or z_loss that is not finite, dloss_count other
+ * than 1 or T; UNSUPPORTED for D % 8 != 0, D > 65536, T > 2^20, V > 2^24,
+ * slots > 256 or a pitch above 2^21 elements; HIP.  T == 0: no row, no launch
+ * but the zeros of dW; only W is looked at then.
+ *
+ * linear_cross_entropy -- with one label a row,
+ *     loss[t] = lse[t] - z[t][labels[t]] + z_loss * lse[t]^2
+ * labels device int64 [T]; a row whose label equals ignore_index is out.  The
+ * log-sum-exp leaves the label's column apart, so that the loss of a label of
+ * probability near 1 keeps its relative accuracy.
+ *
+ * linear_cross_entropy_grad -- with loss and lse as the forward call wrote
+ * them for the same arguments, and n(t) = dloss[t]:
+ *     dz[t][v] = n(t) ((1 + 2 z_loss lse) softmax(z[t])[v] - [v = labels[t]])
+ *     dX = scale dz W,  dW = scale dz^T X
+ *
+ * linear_distillation -- against a teacher's top logits: `slots` columns a
+ * row, index device int64 [T, ld_index] and the teacher's logits there,
+ * device fp32 [T, ld_teacher].  A slot is empty when its index is negative
+ * or its logit is -inf; over the row's filled slots q = softmax(scale *
+ * teacher), and
+ *     logp[t][j] = z[t][index[t][j]] - lse[t]      (0 in empty slots)
+ *     loss[t] = sum_j q_j (log q_j - logp[t][j])
+ * logp device fp32 [T, slots], dense.  Slots may name one column several
+ * times.  A filled slot of an index >= V, or of a logit that is not finite,
+ * makes the row's loss and gradients NaN.
+ *
+ * linear_distillation_grad -- with lse and logp as the forward call wrote
+ * them:
+ *     dz[t][v] = n(t) (softmax(z[t])[v] - sum over slots j of v of q_j)
+ *     dX = scale dz W,  dW = scale dz^T X
+ */
+size_t linear_loss_workspace_bytes(int64_t T, int64_t V, int64_t D, int64_t slots, int32_t backward);
+gemm_status linear_cross_entropy(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                 const int64_t* labels, int64_t T, int64_t V, int64_t D, float scale,
+                                 float z_loss, int64_t ignore_index, float* loss, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+gemm_status linear_cross_entropy_grad(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                      const int64_t* labels, int64_t T, int64_t V, int64_t D,
+                                      float scale, float z_loss, int64_t ignore_index,
+                                      const float* loss, const float* lse, const float* dloss,
+                                      int64_t dloss_count, uint16_t* dX, int64_t lddx, uint16_t* dW,
+                                      int64_t lddw, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+gemm_status linear_distillation(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                const int64_t* index, int64_t ld_index, const float* teacher,
+                                int64_t ld_teacher, int64_t T, int64_t V, int64_t D, int64_t slots,
+                                float scale, float* loss, float* lse, float* logp, void* workspace,
+                                size_t workspace_bytes, void* stream);
+gemm_status linear_distillation_grad(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                                     const int64_t* index, int64_t ld_index, const float* teacher,
+                                     int64_t ld_teacher, int64_t T, int64_t V, int64_t D,
+                                     int64_t slots, float scale, const float* lse, const float* logp,
+                                     const float* dloss, int64_t dloss_count, uint16_t* dX,
+                                     int64_t lddx, uint16_t* dW, int64_t lddw, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code ("GEMM_OK", ...). */
 const char* gemm_status_string(gemm_status status);
 
