@@ -23,10 +23,10 @@ constexpr int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 constexpr int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
 // Rows counted per entry of the chunk table, and up to how many rows one
-// workgroup counts the rows in front of it by itself (128 KiB of labels, L2).
+// workgroup counts the rows in front of it by itself (32 KiB of labels, L2).
 constexpr int kChunk = 1024;
-constexpr int64_t kOwnCount = 16384;
-constexpr int kSelRows = 16;     // rows one workgroup of the selection moves
+constexpr int64_t kOwnCount = 4096;
+constexpr int kSelRows = 4;      // rows one workgroup of the selection moves, one a wave
 
 // Row state: out, kept, or kept with a target outside the vocabulary (loss
 // and gradient NaN).
@@ -122,7 +122,7 @@ struct SelectArgs {
     float scale, z_loss;
 };
 
-// 16 rows a workgroup: how many kept rows lie in front of them, each row's
+// 4 rows a workgroup: how many kept rows lie in front of them, each row's
 // place, what the row's gradient needs, and the copy of the kept rows.
 __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
 {
@@ -186,53 +186,73 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
             *p.n_kept = before + __popcll(kept);
     }
     __syncthreads();
-    const int64_t pieces = p.row_b / 16;
-    const int nrows = (int)min((int64_t)kSelRows, p.T - t0);
-    for (int64_t i = threadIdx.x; i < nrows * pieces; i += 256) {
-        const int r = (int)(i / pieces);
-        const int64_t c = i - r * pieces;
-        if (place[r] >= 0)
-            *reinterpret_cast<i32x4*>(p.Xc + place[r] * p.row_b + c * 16) =
-                *reinterpret_cast<const i32x4*>(p.X + (t0 + r) * p.ldx_b + c * 16);
+    const int r = threadIdx.x >> 6;
+    if (t0 + r >= p.T || place[r] < 0)
+        return;
+    const uint8_t* from = p.X + (t0 + r) * p.ldx_b;
+    uint8_t* to = p.Xc + place[r] * p.row_b;
+    for (int64_t b = (threadIdx.x & 63) * 16; b < p.row_b; b += 4096) {
+        i32x4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (b + u * 1024 < p.row_b)
+                v[u] = *reinterpret_cast<const i32x4*>(from + b + u * 1024);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (b + u * 1024 < p.row_b)
+                *reinterpret_cast<i32x4*>(to + b + u * 1024) = v[u];
     }
 }
 
+// (maximum, sum) pairs of two sets of columns -> of both.  A set of no column
+// is (-inf, 0); a maximum of -inf with a NaN sum carries the NaN on.
+__device__ __forceinline__ float2 lse_merge(float2 a, float2 b)
+{
+    const float m = fmaxf(a.x, b.x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    return make_float2(m, a.y * exp_diff(fmaxf(a.x, -3.4e38f), ref) + b.y * exp_diff(fmaxf(b.x, -3.4e38f), ref));
+}
+
 // Joins the tile columns' (maximum, sum) pairs of each kept row and, with the
-// label's z, gives lse and the negative log-probability of the label.  16
-// rows a workgroup, 16 threads a row.
+// label's z, gives lse and the negative log-probability of the label.  R rows
+// a workgroup, 256 / R threads a row: 16 rows read whole 128-byte lines of
+// the table where there are many; few rows get all threads (one row of 393
+// pairs: 16 threads took 11 us, 256 take 3).
+template <int R>
 __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, int64_t ldpart, int tiles_n,
                                                         const int* n_kept, const int* map,
                                                         const float* zlabel, float z_loss, float* loss,
                                                         float* lse)
 {
-    __shared__ float2 red[16][17];
+    constexpr int Q = 256 / R;
+    __shared__ float2 red[256];
     const int n = *n_kept;
-    const int r = threadIdx.x & 15, q = threadIdx.x >> 4;
-    const int row = blockIdx.x * 16 + r;
-    if (blockIdx.x * 16 >= n)
+    const int r = threadIdx.x % R, q = threadIdx.x / R;
+    const int row = blockIdx.x * R + r;
+    if (blockIdx.x * R >= n)
         return;
-    float m = -INFINITY, s = 0.f;
+    float2 acc = make_float2(-INFINITY, 0.f);
     if (row < n)
-        for (int t = q; t < tiles_n; t += 16) {
-            const float2 v = part[t * ldpart + row];
-            const float nm = fmaxf(m, v.x);
-            const float ref = nm == -INFINITY ? 0.f : nm;
-            s = s * exp_diff(m, ref) + (v.x == -INFINITY ? v.y : v.y * exp_diff(v.x, ref));
-            m = nm;
+        for (int t = q; t < tiles_n; t += 4 * Q) {
+            float2 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                v[u] = t + u * Q < tiles_n ? part[(int64_t)(t + u * Q) * ldpart + row]
+                                           : make_float2(-INFINITY, 0.f);
+            acc = lse_merge(acc, lse_merge(lse_merge(v[0], v[1]), lse_merge(v[2], v[3])));
         }
-    red[q][r] = make_float2(m, s);
+    red[threadIdx.x] = acc;
     __syncthreads();
+#pragma unroll
+    for (int half = Q / 2; half; half /= 2) {
+        if (q < half)
+            red[threadIdx.x] = lse_merge(red[threadIdx.x], red[threadIdx.x + half * R]);
+        __syncthreads();
+    }
     if (q != 0 || row >= n)
         return;
-    float top = -INFINITY;
-    for (int i = 0; i < 16; ++i)
-        top = fmaxf(top, red[i][r].x);
+    const float top = red[r].x, sum = red[r].y;
     const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    for (int i = 0; i < 16; ++i) {
-        const float2 v = red[i][r];
-        sum += v.x == -INFINITY ? v.y : v.y * exp_diff(v.x, ref);
-    }
     const float others = sum == 0.f ? -INFINITY : ref + logf(sum);   // one column: no others
     const float zl = zlabel[row];
     const float d = others - zl;
@@ -471,19 +491,33 @@ __global__ __launch_bounds__(256) void loss_sparse_kernel(const int* n_kept, con
 }
 
 // dX: the sum of the K slices' planes in slice order, rounded once; zero for
-// rows that are out.
+// rows that are out.  Four columns a thread, four planes' loads in flight.
 __global__ __launch_bounds__(256) void loss_dx_kernel(const float* planes, int splits, int64_t plane,
                                                       int64_t ldplane, const int* pos, uint16_t* dX,
                                                       int64_t lddx, int64_t D)
 {
     const int64_t t = blockIdx.x;
     const int at = pos[t];
-    for (int64_t d = threadIdx.x; d < D; d += 256) {
-        float s = 0.f;
-        if (at >= 0)
-            for (int i = 0; i < splits; ++i)
-                s += planes[i * plane + at * ldplane + d];
-        dX[t * lddx + d] = bf16_rne(s);
+    for (int64_t d = threadIdx.x * 4; d < D; d += 1024) {
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        if (at >= 0) {
+            const float* from = planes + at * ldplane + d;
+            for (int i = 0; i < splits; i += 4) {
+                f32x4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    v[u] = i + u < splits ? *reinterpret_cast<const f32x4*>(from + (i + u) * plane)
+                                          : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    s += v[u];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float x = s[u];
+            dX[t * lddx + d + u] = bf16_rne(x);
+        }
     }
 }
 
@@ -661,10 +695,17 @@ hipError_t loss_forward(const LossCall& c)
     a.zlabel = reinterpret_cast<float*>(ws + pl.off_zlabel);
     DG_TRY(launch_role<ROLE_LSE>(a, c.T, c.cus, c.stream));
     const bool big = c.T > 32 && cdiv(c.T, 256) * cdiv(c.V, 256) >= c.cus / 2;
-    loss_join_kernel<<<dim3((unsigned)cdiv(c.T, 16)), dim3(256), 0, c.stream>>>(
-        a.part, a.ldpart, (int)cdiv(c.V, big ? 256 : 128), a.n_kept,
-        reinterpret_cast<const int*>(ws + pl.off_map), a.zlabel, c.slots ? 0.f : c.z_loss, c.loss, c.lse);
-    DG_TRY(last());
+    auto join = [&](auto r) {
+        constexpr int R = decltype(r)::value;
+        loss_join_kernel<R><<<dim3((unsigned)cdiv(c.T, R)), dim3(256), 0, c.stream>>>(
+            a.part, a.ldpart, (int)cdiv(c.V, big ? 256 : 128), a.n_kept,
+            reinterpret_cast<const int*>(ws + pl.off_map), a.zlabel, c.slots ? 0.f : c.z_loss, c.loss,
+            c.lse);
+        return last();
+    };
+    DG_TRY(c.T >= 2048 ? join(std::integral_constant<int, 16>{})
+           : c.T >= 256 ? join(std::integral_constant<int, 4>{})
+                        : join(std::integral_constant<int, 1>{}));
     if (!c.slots)
         return hipSuccess;
     PickArgs k;

@@ -91,9 +91,16 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // gfx950's transposing LDS read of 16-bit values: in each group of 16 lanes,
 // lane i supplies the address of four values, (row i / 4, columns 4 (i % 4)
 // ..), of a 4 x 16 block and receives column i, rows 0 .. 3.
-__device__ __forceinline__ s16x4 lds_read_tr16(const uint8_t* p)
+//
+// The pointer is restrict so that the read carries alias information, as an
+// ordinary load does by its type: without any, the compiler waits before it
+// for every LDS DMA in flight (vmcnt(0) in front of each group of reads),
+// which empties the pipeline k_loop fills.  What those loads write and when it
+// may be read is k_loop's own barrier.
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ s16x4 lds_read_tr16(lds_s16x4* __restrict p)
 {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
 }
 
 // Rows of a transposed operand's stage: TW columns of 2 bytes, 32-byte unit u
@@ -296,8 +303,10 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                        __attribute__((always_inline)) {
         i32x4 v;
         const uint32_t c1 = c + 4u * (uint32_t)pitch;
-        const s16x4 lo = lds_read_tr16(lds + (at.b[c >> 16] ^ ((uint32_t)i << 5)) + (c & 0xFFFFu));
-        const s16x4 hi = lds_read_tr16(lds + (at.b[c1 >> 16] ^ ((uint32_t)i << 5)) + (c1 & 0xFFFFu));
+        const s16x4 lo = lds_read_tr16(
+            (lds_s16x4*)(lds + (at.b[c >> 16] ^ ((uint32_t)i << 5)) + (c & 0xFFFFu)));
+        const s16x4 hi = lds_read_tr16(
+            (lds_s16x4*)(lds + (at.b[c1 >> 16] ^ ((uint32_t)i << 5)) + (c1 & 0xFFFFu)));
         typedef int i32x2 __attribute__((ext_vector_type(2)));
         const i32x2 l2 = __builtin_bit_cast(i32x2, lo), h2 = __builtin_bit_cast(i32x2, hi);
         v[0] = l2[0];
