@@ -959,7 +959,10 @@ __device__ __forceinline__ void run_tail(F& f, int kt, int nkt, std::integer_seq
 //                                          n % nparts == part (zeros past K)
 //   read(stage, step, set, g, G)           LDS -> fragment registers, group g
 //   mma(stage, step, set, g, G)            the MFMAs of group g of one K step
-template <int ST, int STEPS, int LOADS, int G, class Load, class Read, class Mma>
+// PRELOADED: the caller has issued the loads of the first ST - 1 k-tiles (a
+// persistent workgroup does so before it stores its previous tile); whatever
+// else it has in flight is waited for with them.
+template <int ST, int STEPS, int LOADS, int G, bool PRELOADED = false, class Load, class Read, class Mma>
 __device__ __forceinline__ void k_loop(int nkt, int nomask_end, Load& load, Read& read, Mma& mma)
 {
     constexpr int NS = frag_sets(ST, STEPS);
@@ -968,10 +971,14 @@ __device__ __forceinline__ void k_loop(int nkt, int nomask_end, Load& load, Read
     constexpr int LPARTS = NP * G;                   // load parts per k-tile
     constexpr int VM = AFTER ? (ST - 3) * LOADS : (ST - 2) * LOADS;
     static_assert(ST >= 2 && (ST - 2) * LOADS <= 63, "pipeline depth vs vmcnt");
+    if constexpr (PRELOADED) {
+        DG_STAGE_BARRIER(0);
+    } else {
 #pragma unroll
-    for (int t = 0; t < ST - 1; ++t)
-        load(t, t, 0, 1, std::false_type{});
-    DG_STAGE_BARRIER((ST - 2) * LOADS);
+        for (int t = 0; t < ST - 1; ++t)
+            load(t, t, 0, 1, std::false_type{});
+        DG_STAGE_BARRIER((ST - 2) * LOADS);
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g)
         read(0, 0, 0, g, G);

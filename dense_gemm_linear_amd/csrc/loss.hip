@@ -160,7 +160,7 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
                     const float lse = p.lse_in[t];
                     const float g = p.dloss[t * p.dloss_stride] * p.scale;
                     const float extra = 2.f * p.z_loss * lse;
-                    ri.lse = lse;
+                    ri.lse2 = lse * kLog2e;
                     ri.a = g * (1.f + extra);
                     if (p.loss_in) {
                         // p - 1 = expm1(-nll), exact for p near 1 too
@@ -204,16 +204,7 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
     }
 }
 
-// (maximum, sum) pairs of two sets of columns -> of both.  A set of no column
-// is (-inf, 0); a maximum of -inf with a NaN sum carries the NaN on.
-__device__ __forceinline__ float2 lse_merge(float2 a, float2 b)
-{
-    const float m = fmaxf(a.x, b.x);
-    const float ref = m == -INFINITY ? 0.f : m;
-    return make_float2(m, a.y * exp_diff(fmaxf(a.x, -3.4e38f), ref) + b.y * exp_diff(fmaxf(b.x, -3.4e38f), ref));
-}
-
-// Joins the tile columns' (maximum, sum) pairs of each kept row and, with the
+// Joins the tile columns' (reference, sum) pairs of each kept row and, with the
 // label's z, gives lse and the negative log-probability of the label.  R rows
 // a workgroup, 256 / R threads a row: 16 rows read whole 128-byte lines of
 // the table where there are many; few rows get all threads (one row of 393
@@ -221,8 +212,8 @@ __device__ __forceinline__ float2 lse_merge(float2 a, float2 b)
 template <int R>
 __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, int64_t ldpart, int tiles_n,
                                                         const int* n_kept, const int* map,
-                                                        const float* zlabel, float z_loss, float* loss,
-                                                        float* lse)
+                                                        const float* zlabel, float scale, float z_loss,
+                                                        float* loss, float* lse)
 {
     constexpr int Q = 256 / R;
     __shared__ float2 red[256];
@@ -251,11 +242,15 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, int6
     }
     if (q != 0 || row >= n)
         return;
-    const float top = red[r].x, sum = red[r].y;
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float others = sum == 0.f ? -INFINITY : ref + logf(sum);   // one column: no others
-    const float zl = zlabel[row];
-    const float d = others - zl;
+    // others = (reference + log2 sum) ln 2; its distance to the label's z from
+    // the label's own sum over d, so that what they share cancels before it is
+    // rounded
+    constexpr float kLn2 = 0.69314718055994530942f;
+    const float ref = red[r].x, sum = red[r].y, logs = logf(sum);
+    const bool none = ref == -INFINITY && sum == 0.f;     // one column: no others
+    const float xl = zlabel[row], zl = xl * scale;
+    const float others = none ? -INFINITY : fmaf(ref, kLn2, logs);
+    const float d = none ? -INFINITY : fmaf(fmaf(-xl, scale * kLog2e, ref), kLn2, logs);
     const float nll = fmaxf(d, 0.f) + log1pf(expf(-fabsf(d))) + (d != d ? d : 0.f);
     // no label column (NaN), or one of z = -inf: lse of all that was summed
     const float l = d != d || zl == -INFINITY ? others : zl + nll;
@@ -429,7 +424,7 @@ __global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p)
         return;
     // the lead's own log-probability is the well-conditioned one of the join;
     // the others' follow from their distance to it
-    const float lead_nll = p.loss[t], zl = p.zlabel[at];
+    const float lead_nll = p.loss[t], zl = p.zlabel[at] * fabsf(p.scale);
     float mx = -INFINITY;
     for (int j = lane; j < p.k; j += 64) {
         const int64_t i = p.index[t * p.ld_index + j];
@@ -525,10 +520,10 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(const float* planes, int s
 // Launches.
 using Big = LossShape<256, 256, 2, 4, 4, 64, 1>;
 using Mid = LossShape<128, 128, 2, 2, 4, 64, 2>;
-using Low = LossShape<32, 128, 1, 4, 4, 128, 2>;
+using Low = LossShape<32, 128, 1, 4, 3, 128, 2>;
 
 template <class S, int ROLE>
-hipError_t go(const LossArgs& a, int64_t tiles_m, hipStream_t s)
+hipError_t go(const LossArgs& a, int64_t tiles_m, int cus, hipStream_t s)
 {
     LossArgs copy = a;
     copy.tiles_n = (int)cdiv(a.N, S::TN);
@@ -536,9 +531,10 @@ hipError_t go(const LossArgs& a, int64_t tiles_m, hipStream_t s)
         const int nkt = (int)cdiv(a.K, S::KT);
         copy.kt_per = (int)cdiv(nkt, a.splits);
     }
-    const int64_t grid = tiles_m * copy.tiles_n * (ROLE == ROLE_DX ? a.splits : 1);
-    if (grid > INT32_MAX)
+    const int64_t items = tiles_m * copy.tiles_n * (ROLE == ROLE_DX ? a.splits : 1);
+    if (items > INT32_MAX)
         return hipErrorInvalidValue;
+    const int64_t grid = std::min<int64_t>(items, (int64_t)cus * S::PER_CU);
     void* args[] = {&copy};
     return hipLaunchKernel(reinterpret_cast<const void*>(&loss_gemm_kernel<S, ROLE>), dim3((unsigned)grid),
                            dim3(S::THREADS), args, 0, s);
@@ -549,11 +545,11 @@ hipError_t launch_role(const LossArgs& a, int64_t rows, int cus, hipStream_t s)
 {
     if constexpr (ROLE != ROLE_DW) {
         if (rows <= 32)
-            return go<Low, ROLE>(a, cdiv(rows, Low::TM), s);
+            return go<Low, ROLE>(a, cdiv(rows, Low::TM), cus, s);
     }
     if (cdiv(rows, 256) * cdiv(a.N, 256) * (ROLE == ROLE_DX ? a.splits : 1) >= cus / 2)
-        return go<Big, ROLE>(a, cdiv(rows, Big::TM), s);
-    return go<Mid, ROLE>(a, cdiv(rows, Mid::TM), s);
+        return go<Big, ROLE>(a, cdiv(rows, Big::TM), cus, s);
+    return go<Mid, ROLE>(a, cdiv(rows, Mid::TM), cus, s);
 }
 
 hipError_t last() { return hipGetLastError(); }
@@ -699,7 +695,7 @@ hipError_t loss_forward(const LossCall& c)
         constexpr int R = decltype(r)::value;
         loss_join_kernel<R><<<dim3((unsigned)cdiv(c.T, R)), dim3(256), 0, c.stream>>>(
             a.part, a.ldpart, (int)cdiv(c.V, big ? 256 : 128), a.n_kept,
-            reinterpret_cast<const int*>(ws + pl.off_map), a.zlabel, c.slots ? 0.f : c.z_loss, c.loss,
+            reinterpret_cast<const int*>(ws + pl.off_map), a.zlabel, fabsf(c.scale), c.slots ? 0.f : c.z_loss, c.loss,
             c.lse);
         return last();
     };

@@ -2,9 +2,12 @@
 // them).  With z = scale * X W^T over the vocabulary (X [T, D], W [V, D] bf16)
 // four products are needed, none of which may leave z in memory:
 //
-//   ROLE_LSE   z tile of X W^T -> per row and tile column: maximum and
-//              sum of exp(z - maximum) over the columns other than the row's
-//              label, the pieces of a log-sum-exp, and the label's z apart.
+//   ROLE_LSE   z tile of X W^T -> per row and tile column: a reference m and
+//              the sum of 2^(z / ln 2 - m) over the columns other than the
+//              row's label, the pieces of a log-sum-exp, and the label's z
+//              apart.  m is the maximum of z / ln 2 rounded up to an integer:
+//              the sums of two sets of columns then join by a power of two,
+//              which rounds nothing.
 //              (With both in one sum, the loss lse - z[label] of a label of
 //              probability near 1 would be the difference of two equal
 //              numbers; apart, it is log(1 + exp(lse_others - z[label])),
@@ -33,7 +36,7 @@ enum { ROLE_LSE = 0, ROLE_GRAD = 1, ROLE_DX = 2, ROLE_DW = 3 };
 
 // One kept row: what its gradient needs, in compact row order.
 struct RowInfo {
-    float lse;
+    float lse2;   // lse / ln 2
     float a;      // factor of exp(z - lse): dloss * scale * (1 + 2 z_loss lse)
     float b;      // the gradient at the label's column
     int label;    // column of W, -1: none
@@ -49,9 +52,9 @@ struct LossArgs {
     int splits, kt_per;    // DX: K slices, k-tiles per slice
     float scale;
     const RowInfo* rows;
-    float2* part;          // LSE: [tiles_n][ldpart] (maximum, sum)
+    float2* part;          // LSE: [tiles_n][ldpart] (reference, sum)
     int64_t ldpart;
-    float* zlabel;         // LSE: z at the label, compact rows
+    float* zlabel;         // LSE: the label's sum over d, with scale's sign; compact rows
     int v0;                // GRAD: first column of the piece
     float* planes;         // DX: [splits][plane_rows][ldplane]
     int64_t plane;         // elements of one plane
@@ -76,14 +79,21 @@ struct LossShape {
     static constexpr int KT = KTB / 2;                 // k-tile in elements
     static constexpr int WCOLS = TN / WN;
     static constexpr int SROW = WCOLS * 2 + 16;
-    static constexpr int ROWS_LDS = TM * 16;           // RowInfo of the tile's rows
-    static constexpr int CH = fit_stage_rows(MR, WAVES, R, SROW, ST * STAGE - ROWS_LDS);
-    static constexpr int LDS = ST * STAGE;
+    // After the k-tile stages: RowInfo of the tile's rows, twice (this tile's
+    // and the next one's); then, one tile at a time, each wave's block of 16
+    // rows of output or the row sums of the wave columns.
+    static constexpr int ROWS_AT = ST * STAGE, ROWS_LDS = TM * 16 > 1024 ? TM * 16 : 1024;
+    static constexpr int OUT_AT = ROWS_AT + 2 * ROWS_LDS;
+    static constexpr int OUT_LDS = WAVES * R * SROW > WN * TM * 8 ? WAVES * R * SROW : WN * TM * 8;
+    static constexpr int LDS = OUT_AT + OUT_LDS;
+    // workgroups a CU holds
+    static constexpr int PER_CU = (160 * 1024 / LDS < 4 * OCC / WAVES || OCC == 1) ? 160 * 1024 / LDS
+                                                                                  : 4 * OCC / WAVES;
     static_assert(MR >= 1 && NR >= 1 && MR * WM * R == TM && NR * WN * R == TN, "tile shape");
     static_assert(A_DMA >= 1 && B_DMA >= 1 && A_DMA * 1024 * WAVES == A_BUF &&
                       B_DMA * 1024 * WAVES == B_BUF, "DMA split");
-    static_assert(WAVES * CH * R * SROW + ROWS_LDS <= LDS && LDS <= 160 * 1024, "LDS budget");
-    static_assert(TM * 4 + WN * TM * 8 <= LDS, "LSE reduction space");
+    static_assert(LDS <= 160 * 1024, "LDS budget");
+    static_assert(ROWS_LDS <= 1024 * WAVES, "one RowInfo load a wave");
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -110,34 +120,81 @@ __device__ __forceinline__ s16x4 lds_read_tr16(lds_s16x4* __restrict p)
 // spans of the 256 bytes the banks cover.
 __host__ __device__ constexpr uint32_t tr_key(uint32_t row) { return (row & 3u) | ((row >> 1) & 4u); }
 
-// Maximum / sum over the 16 lanes of a row group, in every lane of it.
-template <int CTRL>
-__device__ __forceinline__ float dpp_f32(float x)
+// Maximum / sum over the four lanes that share lane % 16, in each of them.
+__device__ __forceinline__ float quad_max(float x)
 {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
 }
-__device__ __forceinline__ float row16_max(float x)
+__device__ __forceinline__ float quad_sum(float x)
 {
-    x = fmaxf(x, dpp_f32<0x128>(x));   // row_ror:8, 4, 2, 1
-    x = fmaxf(x, dpp_f32<0x124>(x));
-    x = fmaxf(x, dpp_f32<0x122>(x));
-    return fmaxf(x, dpp_f32<0x121>(x));
-}
-__device__ __forceinline__ float row16_sum(float x)
-{
-    x += dpp_f32<0x128>(x);
-    x += dpp_f32<0x124>(x);
-    x += dpp_f32<0x122>(x);
-    return x + dpp_f32<0x121>(x);
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// exp(z - m): the difference first, so that a large common part of z and m
-// leaves no error in the exponent (one hardware exponential, 1 ulp).
-__device__ __forceinline__ float exp_diff(float z, float m)
+// (reference, sum) pairs of two sets of columns -> of both.  References are
+// integers (-inf: a set of no column, or of -inf only, with sum 0 or NaN).
+__device__ __forceinline__ float2 lse_merge(float2 a, float2 b)
 {
-    return __builtin_amdgcn_exp2f((z - m) * kLog2e);
+    const float m = fmaxf(a.x, b.x);
+    if (m == -INFINITY)
+        return make_float2(m, a.y + b.y);
+    // 2^(reference - m): differences of integers; -inf converts to the least int
+    return make_float2(m, __builtin_amdgcn_ldexpf(a.y, (int)(a.x - m)) +
+                              __builtin_amdgcn_ldexpf(b.y, (int)(b.x - m)));
+}
+
+// A wave's (MR 16) x WCOLS block of accumulators as bf16 into rows of C from
+// (row0, col_w) on, through its own LDS region, CH atom rows at a time: a lane
+// holds four consecutive columns (one 8-byte LDS write) and stores 16-byte
+// pieces of rows, or single elements where C's rows do not allow that.  Rows
+// past `rows` and columns past N are not stored.
+template <int MR, int NR, int CH, int SROW>
+__device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N, int c_vec,
+                                                 const f32x4 (&acc)[MR][NR], uint8_t* stage, int m0,
+                                                 int rows, int row0, int col_w, int lane)
+{
+    constexpr int WCOLS = NR * 16, PPR = WCOLS / 8;
+    const int lc = lane & 15, lg = lane >> 4;
+    const rsrc_t rc = make_rsrc(C + (int64_t)m0 * ldc + col_w,
+                                (uint32_t)(((int64_t)(rows - 1) * ldc + max(N - col_w, 0)) * 2));
+    const uint32_t pitch = (uint32_t)ldc * 2u;
+    static_for<MR / CH>([&](auto cc_c) __attribute__((always_inline)) {
+        constexpr int cc = decltype(cc_c)::value;
+#pragma unroll
+        for (int ml = 0; ml < CH; ++ml)
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                uint2 v;
+                const f32x4 a = acc[cc * CH + ml][j];
+                const float a0 = a[0], a1 = a[1], a2 = a[2], a3 = a[3];
+                v.x = (uint32_t)bf16_rne(a0) | (uint32_t)bf16_rne(a1) << 16;
+                v.y = (uint32_t)bf16_rne(a2) | (uint32_t)bf16_rne(a3) << 16;
+                *reinterpret_cast<uint2*>(stage + (ml * 16 + lc) * SROW + (j * 16 + 4 * lg) * 2) = v;
+            }
+        wave_lds_order();
+        const int r0 = row0 + cc * CH * 16;
+        if (c_vec) {
+#pragma unroll
+            for (int q0 = 0; q0 < CH * 16 * PPR; q0 += 64) {
+                const int q = q0 + lane, r = q / PPR, c = q % PPR * 8;
+                const i32x4 v = *reinterpret_cast<const i32x4*>(stage + r * SROW + c * 2);
+                const uint32_t off = (uint32_t)(r0 + r) * pitch + (uint32_t)c * 2u;
+                // N is a multiple of 8 wherever c_vec is given
+                store16(rc, col_w + c < N ? off : kOOB, v);
+            }
+        } else {
+            for (int q = lane; q < CH * 16 * WCOLS; q += 64) {
+                const int r = q / WCOLS, c = q % WCOLS;
+                if (col_w + c < N)
+                    store2(rc, (uint32_t)(r0 + r) * pitch + (uint32_t)c * 2u,
+                           *reinterpret_cast<const uint16_t*>(stage + r * SROW + c * 2));
+            }
+        }
+        wave_lds_order();
+    });
 }
 
 template <class S, int ROLE>
@@ -158,39 +215,19 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     const int n = *p.n_kept;
     const int M = ROLE == ROLE_DW ? p.M : n;
     const int tiles_m = (M + TM - 1) / TM;
-    // the grid is sized for every row of X; n may be less
-    const int grid = tiles_m * p.tiles_n;
-    int slice = 0, wg = (int)blockIdx.x;
-    if constexpr (ROLE == ROLE_DX) {
-        if (grid == 0)
-            return;
-        slice = wg / grid;
-        wg -= slice * grid;
-        if (slice >= p.splits)
-            return;
-    } else if (wg >= grid) {
+    // A persistent grid: workgroup b takes items b, b + gridDim, ...  The grid
+    // is sized for every row of X; n may be less.
+    const int tiles = tiles_m * p.tiles_n;
+    const int items = ROLE == ROLE_DX ? tiles * p.splits : tiles;
+    int item = (int)blockIdx.x;
+    if (item >= items)
         return;
-    }
-    int tm, tn;
-    tile_raster<DG_GROUP_M>(xcd_remap(wg, grid), tiles_m, p.tiles_n, tm, tn);
-    const int m0 = tm * TM, n0 = tn * TN;
-    const int rows = min(TM, M - m0);
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int lc = lane & 15, lg = lane >> 4;
-
-    // K range in elements and k-tiles
-    const int K = ROLE == ROLE_DW ? n : p.K;
-    int kt0 = 0, nkt = (K + KT - 1) / KT, k_end = K;
-    if constexpr (ROLE == ROLE_DX) {
-        kt0 = slice * p.kt_per;
-        const int kt_end = min(nkt, kt0 + p.kt_per);
-        nkt = max(0, kt_end - kt0);
-        k_end = min(K, kt_end * KT);
-    }
 
     // ---- loads.  Plain operand: rows of K, KTB bytes a k-tile, chunk c of
     // row r at c ^ key(r); rows past the bound read zero, chunks past K go out
@@ -225,19 +262,46 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
             b_col[i] = d.col;
         }
     }
-    const int brows = min(TN, p.N - n0);
-    const uint8_t* a_base = TRA ? p.A + (int64_t)m0 * 2 : p.A + (int64_t)m0 * p.lda_b;
-    const uint8_t* b_base = TRB ? p.B + (int64_t)n0 * 2 : p.B + (int64_t)n0 * p.ldb_b;
-    // a transposed operand's bytes from its base to the end of row K - 1
-    // (G's rows are padded: its last, partial 16 bytes are read whole)
-    const int64_t a_span = TRA ? (int64_t)(k_end - 1) * p.lda_b + (int64_t)(p.M - m0 + 7) / 8 * 16 : 0;
-    const int64_t b_span = TRB ? (int64_t)(k_end - 1) * p.ldb_b + (int64_t)(p.N - n0) * 2 : 0;
-    const rsrc_t ra = make_rsrc(
-        a_base, TRA ? 0u : (uint32_t)((int64_t)(rows - 1) * p.lda_b + (int64_t)(K + 7) / 8 * 16));
-    const rsrc_t rb = make_rsrc(b_base, TRB ? 0u : (uint32_t)((int64_t)(brows - 1) * p.ldb_b + (int64_t)K * 2));
-    const int kb_end = k_end * 2;                    // bytes of K a plain operand may read
-    const int last_full = kb_end / KTB;
-
+    // ---- the item: output tile, K range (elements and k-tiles), operands
+    const int K = ROLE == ROLE_DW ? n : p.K;
+    const int all_kt = (K + KT - 1) / KT;
+    int slice = 0, m0 = 0, n0 = 0, rows = 0;
+    int kt0 = 0, nkt = all_kt, kb_end = K * 2, last_full = 0;
+    const uint8_t *a_base = nullptr, *b_base = nullptr;
+    int64_t a_span = 0, b_span = 0;
+    uint32_t a_bytes = 0, b_bytes = 0;
+    auto set_item = [&](int it) __attribute__((always_inline)) {
+        int t = it, tm, tn;
+        if constexpr (ROLE == ROLE_DX) {
+            slice = it / tiles;
+            t -= slice * tiles;
+        }
+        tile_raster<DG_GROUP_M>(xcd_remap(t, tiles), tiles_m, p.tiles_n, tm, tn);
+        m0 = tm * TM;
+        n0 = tn * TN;
+        rows = min(TM, M - m0);
+        int k_end = K;
+        if constexpr (ROLE == ROLE_DX) {
+            kt0 = slice * p.kt_per;
+            const int kt_end = min(all_kt, kt0 + p.kt_per);
+            nkt = max(0, kt_end - kt0);
+            k_end = min(K, kt_end * KT);
+        }
+        kb_end = k_end * 2;                        // bytes of K a plain operand may read
+        last_full = kb_end / KTB;
+        a_base = TRA ? p.A + (int64_t)m0 * 2 : p.A + (int64_t)m0 * p.lda_b;
+        b_base = TRB ? p.B + (int64_t)n0 * 2 : p.B + (int64_t)n0 * p.ldb_b;
+        // a transposed operand's bytes from its base to the end of row K - 1
+        // (G's rows are padded: its last, partial 16 bytes are read whole)
+        if constexpr (TRA)
+            a_span = (int64_t)(k_end - 1) * p.lda_b + (int64_t)(p.M - m0 + 7) / 8 * 16;
+        else
+            a_bytes = (uint32_t)((int64_t)(rows - 1) * p.lda_b + (int64_t)(K + 7) / 8 * 16);
+        if constexpr (TRB)
+            b_span = (int64_t)(k_end - 1) * p.ldb_b + (int64_t)(p.N - n0) * 2;
+        else
+            b_bytes = (uint32_t)((int64_t)(min(TN, p.N - n0) - 1) * p.ldb_b + (int64_t)K * 2);
+    };
     auto rebase = [&](const uint8_t* base, int64_t span, int64_t off) __attribute__((always_inline)) {
         const int64_t left = span - off;
         return make_rsrc(base + off, left <= 0 ? 0u : (uint32_t)min(left, (int64_t)0x7FFFFFFF));
@@ -248,8 +312,10 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
         const int kt = kt0 + kt_local;
         const bool mask = kt >= last_full;
         uint8_t* base = lds + stage * STAGE;
-        const rsrc_t rat = TRA ? rebase(a_base, a_span, (int64_t)kt * KT * p.lda_b) : ra;
-        const rsrc_t rbt = TRB ? rebase(b_base, b_span, (int64_t)kt * KT * p.ldb_b) : rb;
+        const rsrc_t rat = TRA ? rebase(a_base, a_span, (int64_t)kt * KT * p.lda_b)
+                               : make_rsrc(a_base, a_bytes);
+        const rsrc_t rbt = TRB ? rebase(b_base, b_span, (int64_t)kt * KT * p.ldb_b)
+                               : make_rsrc(b_base, b_bytes);
         auto one = [&](rsrc_t r, uint8_t* dst, uint32_t goff, uint32_t col, auto tr)
                        __attribute__((always_inline)) {
             if constexpr (decltype(tr)::value) {
@@ -318,12 +384,6 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
 
     i32x4 af[frag_sets(ST, STEPS)][MR], bf[frag_sets(ST, STEPS)][NR];
     acc_t acc[MR][NR];
-#pragma unroll
-    for (int mi = 0; mi < MR; ++mi)
-#pragma unroll
-        for (int j = 0; j < NR; ++j)
-            acc[mi][j] = zero_acc<AT>();
-
     auto read = [&](int stage, int s, int set, int g, int G) __attribute__((always_inline)) {
         constexpr int NF = MR + NR;
 #pragma unroll
@@ -353,143 +413,202 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
             if (a * G / (MR * NR) != g)
                 continue;
             const int mi = a / NR, j = a % NR;
-            acc[mi][j] = mfma_bf16(af[set][mi], bf[set][j], acc[mi][j]);
+            acc[mi][j] = mfma_bf16(bf[set][j], af[set][mi], acc[mi][j]);
         }
     };
-    k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR)>(nkt, min(nkt, last_full - kt0), load, read, mma);
-
-    // ---- outputs.  Lane l holds, in element e of atom (mi, j), row
-    // 16 mi + 4 lg + e of the wave's block and column 16 j + lc.
+    // ---- outputs.  The products are formed with the operands exchanged, so
+    // that lane l holds, in element e of atom (mi, j), row 16 mi + lc of the
+    // wave's block and column 16 j + 4 lg + e: four consecutive columns of one
+    // row.  A row's reductions then run inside the lane and over four lanes
+    // (with the rows in the elements they took 8 cross-lane steps for every row
+    // of 4 values, and the log-sum-exp of a 256 x 256 tile 6 us), and the
+    // stores take 8 or 16 bytes a lane.
+    auto output = [&](int m0, int n0, int rows, int slice, int parity) __attribute__((always_inline)) {
+    // the lane again, as a value of its own: what the outputs derive from it
+    // would otherwise be kept in registers through the K loop
+    int ol = lane;
+    asm volatile("" : "+v"(ol));
+    const int lc = ol & 15, lg = ol >> 4;
+    const int col_w = n0 + (int)col0;
+    [[maybe_unused]] const uint8_t* info = lds + S::ROWS_AT + parity * S::ROWS_LDS;
+    uint8_t* out_lds = lds + S::OUT_AT;
     if constexpr (ROLE == ROLE_LSE) {
-        int* lab = reinterpret_cast<int*>(lds);
-        float2* red = reinterpret_cast<float2*>(lds + TM * 4);
-        for (int r = tid; r < TM; r += S::THREADS)
-            lab[r] = r < rows ? p.rows[m0 + r].label : -1;
-        __syncthreads();
-        const int col_w = n0 + (int)col0;
+        const int* lab = reinterpret_cast<const int*>(info + 12);
+        float2* red = reinterpret_cast<float2*>(out_lds);
+        // z / ln 2 = acc * c with c >= 0: a negative scale turns acc's sign
+        const float c = fabsf(p.scale) * kLog2e;
+        if (p.scale < 0.f) {
 #pragma unroll
-        for (int mi = 0; mi < MR; ++mi) {
-            const int r4 = (int)row0 + mi * R + 4 * lg;
-            const i32x4 l4 = *reinterpret_cast<const i32x4*>(lab + r4);
+            for (int mi = 0; mi < MR; ++mi)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float z[NR];
+                for (int j = 0; j < NR; ++j)
+                    acc[mi][j] = -acc[mi][j];
+        }
+        auto rows_of = [&](auto full_c) __attribute__((always_inline)) {
+            constexpr bool FULL = decltype(full_c)::value;   // every column of the block is in W
 #pragma unroll
-                for (int j = 0; j < NR; ++j) {
-                    z[j] = acc[mi][j][e] * p.scale;
-                    z[j] = col_w + j * R + lc < p.N ? z[j] : -INFINITY;
-                }
+            for (int mi = 0; mi < MR; ++mi) {
+                const int r = (int)row0 + mi * R + lc;
+                float x[NR][4];
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[j][e] = acc[mi][j][e];
+                        if (!FULL && col_w + j * R + 4 * lg + e >= p.N)
+                            x[j][e] = -INFINITY;
+                    }
                 // the label's column, in the one lane that holds it
-                const uint32_t d = (uint32_t)(l4[e] - (col_w + lc));
-                if (d < (uint32_t)(NR * R) && (d & 15u) == 0) {
-                    float zl = z[0];
-#pragma unroll
-                    for (int j = 1; j < NR; ++j)
-                        zl = (int)(d >> 4) == j ? z[j] : zl;
+                const uint32_t d = (uint32_t)(lab[4 * r] - col_w);
+                if (d < (uint32_t)(NR * R) && (int)(d >> 2 & 3u) == lg) {
+                    float xl = 0.f;
 #pragma unroll
                     for (int j = 0; j < NR; ++j)
-                        z[j] = (int)(d >> 4) == j ? -INFINITY : z[j];
-                    p.zlabel[m0 + r4 + e] = zl;
-                }
-                float m = z[0];
 #pragma unroll
-                for (int j = 1; j < NR; ++j)
-                    m = fmaxf(m, z[j]);
-                m = row16_max(m);
-                const float ms = m == -INFINITY ? 0.f : m;   // a block of no column, or all -inf
+                        for (int e = 0; e < 4; ++e) {
+                            const bool at = d == (uint32_t)(j * R + 4 * lg + e);
+                            xl = at ? x[j][e] : xl;
+                            x[j][e] = at ? -INFINITY : x[j][e];
+                        }
+                    p.zlabel[m0 + r] = xl;
+                }
+                float m = x[0][0];
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        m = fmaxf(m, x[j][e]);
+                m = quad_max(m);
+                // no column of it: reference -inf, 0 in its place below.  With
+                // scale 0 every column counts the same.
+                const bool none = m == -INFINITY;
+                m = none ? 0.f : ceilf(m * c);
                 float s = 0.f;
 #pragma unroll
                 for (int j = 0; j < NR; ++j)
-                    s += exp_diff(z[j], ms);
-                s = row16_sum(s);
-                if (lc == 0)
-                    red[wn * TM + r4 + e] = make_float2(m, s);
-            }
-        }
-        __syncthreads();
-        for (int r = tid; r < rows; r += S::THREADS) {
-            float m = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < WN; ++w)
-                m = fmaxf(m, red[w * TM + r].x);
-            const float ms = m == -INFINITY ? 0.f : m;
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < WN; ++w) {
-                const float2 v = red[w * TM + r];
-                // an empty block's sum is 0 (exp(-inf)); its maximum stays out
-                s += v.x == -INFINITY ? v.y : v.y * exp_diff(v.x, ms);
+                    for (int e = 0; e < 4; ++e) {
+                        const float t = __builtin_amdgcn_exp2f(fmaf(x[j][e], c, -m));
+                        s += p.scale == 0.f && x[j][e] == -INFINITY ? 0.f : t;
+                    }
+                s = quad_sum(s);
+                if (lg == 0)
+                    red[wn * TM + r] = make_float2(none ? -INFINITY : m, s);
             }
-            p.part[(int64_t)tn * p.ldpart + m0 + r] = make_float2(m, s);
+        };
+        if (col_w + S::WCOLS <= p.N)
+            rows_of(std::true_type{});
+        else
+            rows_of(std::false_type{});
+        // LDS only: the next item's loads stay in flight
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        for (int r = wave * 64 + ol; r < rows; r += S::THREADS) {
+            float2 v = red[r];
+#pragma unroll
+            for (int w = 1; w < WN; ++w)
+                v = lse_merge(v, red[w * TM + r]);
+            p.part[(int64_t)(n0 / TN) * p.ldpart + m0 + r] = v;
         }
     } else if constexpr (ROLE == ROLE_GRAD) {
-        float4* info = reinterpret_cast<float4*>(lds + S::LDS - S::ROWS_LDS);
-        for (int r = tid; r < TM; r += S::THREADS)
-            info[r] = *reinterpret_cast<const float4*>(p.rows + m0 + min(r, rows - 1));
-        __syncthreads();
-        const int col_w = n0 + (int)col0;
+        const float c = p.scale * kLog2e;
+        const bool full = col_w + S::WCOLS <= p.N;
 #pragma unroll
-        for (int mi = 0; mi < MR; ++mi)
+        for (int mi = 0; mi < MR; ++mi) {
+            const float4 ri = reinterpret_cast<const float4*>(info)[(int)row0 + mi * R + lc];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 ri = info[(int)row0 + mi * R + 4 * lg + e];
-                const int label = __float_as_int(ri.w) - p.v0;
+            for (int j = 0; j < NR; ++j)
 #pragma unroll
-                for (int j = 0; j < NR; ++j) {
-                    const int col = col_w + j * R + lc;
-                    const float zz = acc[mi][j][e] * p.scale;
-                    const float g = col == label ? ri.z : ri.y * exp_diff(zz, ri.x);
-                    acc[mi][j][e] = col < p.N ? g : 0.f;   // columns of no weight row: zero
-                }
+                for (int e = 0; e < 4; ++e)
+                    acc[mi][j][e] = ri.y * __builtin_amdgcn_exp2f(fmaf(acc[mi][j][e], c, -ri.x));
+            const uint32_t d = (uint32_t)(__float_as_int(ri.w) - p.v0 - col_w);
+            if (d < (uint32_t)(NR * R) && (int)(d >> 2 & 3u) == lg) {
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[mi][j][e] = d == (uint32_t)(j * R + 4 * lg + e) ? ri.z : acc[mi][j][e];
             }
-        GemmArgs c;
-        c.C = p.C;
-        c.ldc = p.ldc;
-        c.N = (int)p.ldc;              // whole tiles: G's pitch is a multiple of the tile
-        c.c_vec = 1;
-        store_c_tile<DT_BF16, AT, MR, NR, S::CH, S::SROW, S::WCOLS, false>(
-            c, acc, lds + wave * (S::CH * R * S::SROW), m0, rows, col_w, (int)row0, lane, 1.f, 1.f);
+            if (!full) {                       // columns of no weight row: zero
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[mi][j][e] = col_w + j * R + 4 * lg + e < p.N ? acc[mi][j][e] : 0.f;
+            }
+        }
+        // whole tiles: G's pitch is a multiple of the tile
+        store_bf16_block<MR, NR, 1, S::SROW>(p.C, p.ldc, (int)p.ldc, 1, acc,
+                                                 out_lds + wave * (R * S::SROW), m0, rows,
+                                                 (int)row0, col_w, ol);
     } else if constexpr (ROLE == ROLE_DX) {
         float* plane = p.planes + (int64_t)slice * p.plane + (int64_t)m0 * p.ldplane + n0;
         const rsrc_t rp = make_rsrc(plane, (uint32_t)(((int64_t)(rows - 1) * p.ldplane + (p.N - n0)) * 4));
         const uint32_t pitch = (uint32_t)p.ldplane * 4u;
 #pragma unroll
         for (int mi = 0; mi < MR; ++mi) {
-            uint32_t base[NR];
+            uint32_t off[NR];
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
-                const int col = (int)col0 + j * R + lc;
-                base[j] = n0 + col < p.N
-                              ? (row0 + (uint32_t)(mi * R + 4 * lg)) * pitch + (uint32_t)col * 4u
-                              : kOOB;
+                const int col = (int)col0 + j * R + 4 * lg;
+                off[j] = n0 + col < p.N ? (row0 + (uint32_t)(mi * R + lc)) * pitch + (uint32_t)col * 4u
+                                        : kOOB;
             }
             if (!p.first) {
+                i32x4 old[NR];
 #pragma unroll
                 for (int j = 0; j < NR; ++j)
+                    old[j] = load16(rp, off[j]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float old = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-                            rp, (int)(base[j] + (uint32_t)e * pitch), 0, 0));
-                        acc[mi][j][e] += old;
-                    }
+                for (int j = 0; j < NR; ++j)
+                    acc[mi][j] += __builtin_bit_cast(f32x4, old[j]);
             }
 #pragma unroll
             for (int j = 0; j < NR; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = acc[mi][j][e];
-                    store4(rp, base[j] + (uint32_t)e * pitch, __float_as_uint(v));
-                }
+                store16(rp, off[j], __builtin_bit_cast(i32x4, acc[mi][j]));
         }
     } else {
-        GemmArgs c;
-        c.C = p.C;
-        c.ldc = p.ldc;
-        c.N = p.N;
-        c.c_vec = p.c_vec;
-        store_c_tile<DT_BF16, AT, MR, NR, S::CH, S::SROW, S::WCOLS, false>(
-            c, acc, lds + wave * (S::CH * R * S::SROW), m0, rows, n0 + (int)col0, (int)row0, lane, 1.f,
-            1.f);
+        store_bf16_block<MR, NR, 1, S::SROW>(p.C, p.ldc, p.N, p.c_vec, acc,
+                                                 out_lds + wave * (R * S::SROW), m0, rows,
+                                                 (int)row0, col_w, ol);
+    }
+    };
+
+    // The first k-tiles of an item, and its rows' RowInfo (by LDS DMA too, so
+    // that nothing waits for it before the first barrier; rows past n: zeros,
+    // which reach no row that is kept).
+    auto preload = [&](int parity) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < ST - 1; ++t)
+            load(t, t, 0, 1, std::false_type{});
+        if constexpr (ROLE == ROLE_LSE || ROLE == ROLE_GRAD)
+            if (wave * 64 < TM)
+                dma16(make_rsrc(p.rows + m0, (uint32_t)rows * 16u),
+                      lds + S::ROWS_AT + parity * S::ROWS_LDS + wave * 1024, (uint32_t)lane * 16u + (uint32_t)wave * 1024u, 0);
+    };
+    set_item(item);
+    preload(0);
+    for (int parity = 0;; parity ^= 1) {
+#pragma unroll
+        for (int mi = 0; mi < MR; ++mi)
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+                acc[mi][j] = zero_acc<AT>();
+        k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, min(nkt, last_full - kt0), load,
+                                                                read, mma);
+        // the next item's loads go out before this one's outputs
+        const int o_m0 = m0, o_n0 = n0, o_rows = rows, o_slice = slice;
+        item += (int)gridDim.x;
+        const bool more = item < items;
+        if (more) {
+            set_item(item);
+            preload(parity ^ 1);
+        }
+        output(o_m0, o_n0, o_rows, o_slice, parity);
+        if (!more)
+            break;
     }
 }
 
