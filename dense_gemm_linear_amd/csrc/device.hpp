@@ -76,6 +76,13 @@ __device__ __forceinline__ i32x4 load16_nt(rsrc_t r, uint32_t off)
     return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 2);
 }
 
+// The LDS DMA with the same hint.
+__device__ __forceinline__ void dma16_nt(rsrc_t r, void* lds_base, uint32_t voff, uint32_t soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (__attribute__((address_space(3))) void*)lds_base, 16, (int)voff, (int)soff, 0, 2);
+}
+
 __device__ __forceinline__ void store16(rsrc_t r, uint32_t off, i32x4 v)
 {
     __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, 0);

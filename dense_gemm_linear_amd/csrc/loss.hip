@@ -212,12 +212,12 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
 template <int R>
 __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, int64_t ldpart, int tiles_n,
                                                         const int* n_kept, const int* map,
-                                                        const float* zlabel, float scale, float z_loss,
+                                                        RowSource src, int few, const float* zlabel, float scale, float z_loss,
                                                         float* loss, float* lse)
 {
     constexpr int Q = 256 / R;
     __shared__ float2 red[256];
-    const int n = *n_kept;
+    const int n = few ? few : *n_kept;       // few rows: all of them, none moved
     const int r = threadIdx.x % R, q = threadIdx.x / R;
     const int row = blockIdx.x * R + r;
     if (blockIdx.x * R >= n)
@@ -248,13 +248,24 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, int6
     constexpr float kLn2 = 0.69314718055994530942f;
     const float ref = red[r].x, sum = red[r].y, logs = logf(sum);
     const bool none = ref == -INFINITY && sum == 0.f;     // one column: no others
-    const float xl = zlabel[row], zl = xl * scale;
+    float xl = zlabel[row];
+    if (few) {
+        int label;
+        const int st = row_state(src, row, label);
+        if (st == ROW_OUT) {
+            loss[row] = lse[row] = 0.f;
+            return;
+        }
+        if (st == ROW_BAD)
+            xl = NAN;
+    }
+    const float zl = xl * scale;
     const float others = none ? -INFINITY : fmaf(ref, kLn2, logs);
     const float d = none ? -INFINITY : fmaf(fmaf(-xl, scale * kLog2e, ref), kLn2, logs);
     const float nll = fmaxf(d, 0.f) + log1pf(expf(-fabsf(d))) + (d != d ? d : 0.f);
     // no label column (NaN), or one of z = -inf: lse of all that was summed
     const float l = d != d || zl == -INFINITY ? others : zl + nll;
-    const int t = map[row];
+    const int t = few ? row : map[row];
     loss[t] = nll + z_loss * l * l;
     lse[t] = l;
 }
@@ -353,7 +364,8 @@ struct PickArgs {
     int64_t ldw_b;
     const uint8_t* Xc;
     int64_t row_b;
-    const int* pos;
+    int64_t ldx_b;
+    const int* pos;              // null: Xc is X itself
     const int64_t* index;
     int64_t ld_index, V;
     const float* teacher;
@@ -387,14 +399,15 @@ __global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p)
     __shared__ float z[kMaxLossSlots];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int at = p.pos[t];
+    // few rows: none moved
+    const int at = p.pos ? p.pos[t] : p.flag[2 * t] == ROW_OUT ? -1 : (int)t;
     float* out = p.logp + t * p.k;
     if (at < 0) {
         for (int j = threadIdx.x; j < p.k; j += 256)
             out[j] = 0.f;
         return;
     }
-    const uint8_t* x = p.Xc + at * p.row_b;
+    const uint8_t* x = p.Xc + at * p.ldx_b;
     const int lead = p.flag[2 * t + 1];
     for (int j0 = 4 * wave; j0 < p.k; j0 += 16) {
         const uint8_t* w[4];
@@ -518,11 +531,105 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(const float* planes, int s
 
 // ---------------------------------------------------------------------------
 // Launches.
+//
+// Tile shapes.  kt and epi are what one round (every CU holding its fill of
+// workgroups) measured on MI355X, in microseconds: kt for each 32 values of K,
+// epi for the rest of a tile; kt1 where there is at most one workgroup a CU.
+// The large tile does twice the work of the middle ones in 1.0 to 1.5 times
+// their time, so it is taken where its tiles fill the CUs (1024 x 50257 x 512
+// logits: 75 us against 92 and 92), the others where they do not (264 x 11007
+// x 1024: 22 us against 29).  Up to 64 rows the product is a read of W; there
+// the tile that covers the rows keeps the most of it in flight (48 x 50257 x
+// 4096: 140 us against 153 to 159 of the others with W cold).
 using Big = LossShape<256, 256, 2, 4, 4, 64, 1>;
+using Tall = LossShape<256, 128, 4, 2, 4, 64, 2>;
 using Mid = LossShape<128, 128, 2, 2, 4, 64, 2>;
+using Few = LossShape<64, 128, 1, 4, 3, 128, 2>;
 using Low = LossShape<32, 128, 1, 4, 3, 128, 2>;
+enum { SHAPE_BIG = 0, SHAPE_TALL, SHAPE_MID, SHAPE_FEW, SHAPE_LOW };
+struct ShapeCost {
+    int tm, tn, per_cu;
+    double kt, kt1, epi;
+};
+constexpr ShapeCost kShapes[] = {{Big::TM, Big::TN, Big::PER_CU, 0.72, 0.72, 9.0},
+                                 {Tall::TM, Tall::TN, Tall::PER_CU, 0.46, 0.46, 3.5},
+                                 {Mid::TM, Mid::TN, Mid::PER_CU, 0.64, 0.50, 0.5},
+                                 {Few::TM, Few::TN, Few::PER_CU, 0.5, 0.4, 2.0},
+                                 {Low::TM, Low::TN, Low::PER_CU, 0.5, 0.4, 2.0}};
+constexpr int kPlanCus = 256;            // the workspace must not depend on the device
+constexpr double kLaunchUs = 5.0;        // a further launch, start to start
+constexpr double kPlaneBytesPerUs = 2.0e6;
 
-template <class S, int ROLE>
+// Estimated time of a product of rows x cols outputs over k values.
+double product_us(int shape, int64_t rows, int64_t cols, int64_t k, int splits, int cus)
+{
+    const ShapeCost& s = kShapes[shape];
+    const int64_t items = cdiv(rows, s.tm) * cdiv(cols, s.tn) * splits;
+    const int64_t kts = cdiv(cdiv(k, 32), splits);
+    const int64_t full = items / (cus * s.per_cu), left = items % (cus * s.per_cu);
+    return full * (kts * s.kt + s.epi) + (left ? kts * (left > cus ? s.kt : s.kt1) + s.epi : 0.0);
+}
+
+// Shape of a product whose outputs are rows x cols: by the row count where it
+// is small (not for dW: its rows are W's), else by the estimate.
+int pick_shape(int64_t rows, int64_t cols, int64_t k, int splits, int cus, bool few_rows)
+{
+    if (few_rows && rows <= 32)
+        return SHAPE_LOW;
+    if (few_rows && rows <= 64)
+        return SHAPE_FEW;
+    int best = SHAPE_BIG;
+    for (int i = SHAPE_TALL; i <= SHAPE_MID; ++i)
+        if (product_us(i, rows, cols, k, splits, cus) < product_us(best, rows, cols, k, splits, cus))
+            best = i;
+    return best;
+}
+
+// A product over a range of the vocabulary, v values of it: the first `main`
+// of them with one shape, in whole rounds of tiles, and the rest with the shape that
+// suits so few, when two launches are estimated to take less than one (597
+// rows x 50257: 591 large tiles are 2.3 rounds; 510 of them and the rest in
+// smaller tiles).  main == v: one launch.
+struct RangePlan {
+    int shape, rest_shape;
+    int64_t main;
+};
+RangePlan plan_range(int64_t t, int64_t v, int64_t k, int64_t other, bool by_rows, int cus)
+{
+    // by_rows (dW): outputs are v x other; else (logits) t x v
+    auto us = [&](int sh, int64_t n) {
+        return by_rows ? product_us(sh, n, other, k, 1, cus) : product_us(sh, t, n, k, 1, cus);
+    };
+    auto pick = [&](int64_t n) {
+        return by_rows ? pick_shape(n, other, k, 1, cus, false) : pick_shape(t, n, k, 1, cus, true);
+    };
+    RangePlan p;
+    p.shape = p.rest_shape = pick(v);
+    p.main = v;
+    if (p.shape >= SHAPE_FEW)
+        return p;
+    double best = us(p.shape, v);
+    const ShapeCost& b = kShapes[SHAPE_BIG];
+    const int64_t across = by_rows ? cdiv(other, b.tn) : cdiv(t, b.tm);
+    const int64_t step = by_rows ? b.tm : b.tn;
+    for (int64_t rounds = v / step * across / cus; rounds >= 1; --rounds) {
+        const int64_t main = rounds * cus / across * step;
+        if (main <= 0 || main >= v)
+            continue;
+        const int rest = pick(v - main);
+        const double two = us(SHAPE_BIG, main) + us(rest, v - main) + kLaunchUs;
+        if (two < best) {
+            best = two;
+            p.shape = SHAPE_BIG;
+            p.rest_shape = rest;
+            p.main = main;
+        }
+        break;                   // fewer rounds only leave more to the smaller tiles
+    }
+    return p;
+}
+
+template <class S, int ROLE, bool FEW = false>
 hipError_t go(const LossArgs& a, int64_t tiles_m, int cus, hipStream_t s)
 {
     LossArgs copy = a;
@@ -536,19 +643,24 @@ hipError_t go(const LossArgs& a, int64_t tiles_m, int cus, hipStream_t s)
         return hipErrorInvalidValue;
     const int64_t grid = std::min<int64_t>(items, (int64_t)cus * S::PER_CU);
     void* args[] = {&copy};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&loss_gemm_kernel<S, ROLE>), dim3((unsigned)grid),
+    return hipLaunchKernel(reinterpret_cast<const void*>(&loss_gemm_kernel<S, ROLE, FEW>), dim3((unsigned)grid),
                            dim3(S::THREADS), args, 0, s);
 }
 
 template <int ROLE>
-hipError_t launch_role(const LossArgs& a, int64_t rows, int cus, hipStream_t s)
+hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipStream_t s)
 {
-    if constexpr (ROLE != ROLE_DW) {
-        if (rows <= 32)
+    // (few rows' LSE has a launch of its own)
+    if constexpr (ROLE == ROLE_GRAD || ROLE == ROLE_DX) {
+        if (shape == SHAPE_LOW)
             return go<Low, ROLE>(a, cdiv(rows, Low::TM), cus, s);
+        if (shape == SHAPE_FEW)
+            return go<Few, ROLE>(a, cdiv(rows, Few::TM), cus, s);
     }
-    if (cdiv(rows, 256) * cdiv(a.N, 256) * (ROLE == ROLE_DX ? a.splits : 1) >= cus / 2)
+    if (shape == SHAPE_BIG)
         return go<Big, ROLE>(a, cdiv(rows, Big::TM), cus, s);
+    if (shape == SHAPE_TALL)
+        return go<Tall, ROLE>(a, cdiv(rows, Tall::TM), cus, s);
     return go<Mid, ROLE>(a, cdiv(rows, Mid::TM), cus, s);
 }
 
@@ -561,10 +673,12 @@ hipError_t last() { return hipGetLastError(); }
             return e_;               \
     } while (0)
 
-hipError_t select_rows(const LossCall& c, const LossPlan& pl, bool backward)
+// Distillation: the targets' kernel.  Returns where the rows' states are.
+hipError_t row_targets(const LossCall& c, const LossPlan& pl, RowSource* out)
 {
     uint8_t* ws = c.ws;
-    RowSource src = {c.labels, c.ignore_index, c.V, nullptr};
+    RowSource& src = *out;
+    src = {c.labels, c.ignore_index, c.V, nullptr};
     if (c.slots) {
         TargetArgs t;
         t.index = c.index;
@@ -584,6 +698,12 @@ hipError_t select_rows(const LossCall& c, const LossPlan& pl, bool backward)
         loss_target_kernel<<<dim3((unsigned)c.T), dim3(64), 0, c.stream>>>(t);
         DG_TRY(last());
     }
+    return hipSuccess;
+}
+
+hipError_t select_rows(const LossCall& c, const LossPlan& pl, const RowSource& src, bool backward)
+{
+    uint8_t* ws = c.ws;
     int* chunks = nullptr;
     if (c.T > kOwnCount) {
         chunks = reinterpret_cast<int*>(ws + pl.off_chunks);
@@ -628,7 +748,7 @@ LossArgs product_args(const LossCall& c, const LossPlan& pl)
 
 }  // namespace
 
-LossPlan loss_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool backward)
+static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool backward)
 {
     LossPlan p;
     memset(&p, 0, sizeof p);
@@ -659,14 +779,30 @@ LossPlan loss_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool backward
     p.bytes = at;
     if (backward) {
         at = shared;
-        // G of one piece: about 64 MiB, a multiple of 256 columns
-        int64_t piece = (INT64_C(64) << 20) / 2 / p.rows_pad / 256 * 256;
+        // G of one piece: at most 256 MiB (the Infinity Cache's size), at
+        // least 256 columns.  Fewer pieces make fuller rounds of tiles and
+        // fewer passes over dX's planes: 2048 x 131072 x 4096 measured 5351,
+        // 5316, 5222 and 5172 us with 64, 128, 256 and 512 MiB.
+        int64_t piece = (INT64_C(256) << 20) / 2 / p.rows_pad / 256 * 256;
         piece = std::max<int64_t>(piece, 256);
         piece = std::min(piece, round_up(V, 256));
         p.piece = piece;
-        const int64_t tiles = cdiv(T, 128) * cdiv(D, 128);
-        p.splits = (int)std::min<int64_t>(16, std::max<int64_t>(1, 512 / tiles));
-        p.splits = (int)std::min<int64_t>(p.splits, std::max<int64_t>(1, piece / 512));
+        // dX: shape and K slices by the estimate, the planes' traffic included
+        // (each slice writes one, the last kernel reads them, and every
+        // further piece reads and writes them again)
+        const int64_t passes = 2 * cdiv(V, piece);
+        double best = 0.0;
+        for (int sh = T <= 32 ? SHAPE_LOW : T <= 64 ? SHAPE_FEW : SHAPE_BIG;
+             sh <= (T <= 32 ? SHAPE_LOW : T <= 64 ? SHAPE_FEW : SHAPE_MID); ++sh)
+            for (int sp = 1; sp <= 64 && (sp == 1 || piece / sp >= 256); ++sp) {
+                const double us = cdiv(V, piece) * product_us(sh, T, D, piece, sp, kPlanCus) +
+                                  (double)(passes * sp * T * D * 4) / kPlaneBytesPerUs;
+                if (best == 0.0 || us < best) {
+                    best = us;
+                    p.dx_shape = sh;
+                    p.splits = sp;
+                }
+            }
         p.off_g = take(p.rows_pad * piece * 2);
         p.off_planes = take((int64_t)p.splits * T * D * 4);
         p.bytes = std::max(p.bytes, at);
@@ -674,14 +810,42 @@ LossPlan loss_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool backward
     return p;
 }
 
+// A call asks for its plan two or three times, and a program calls with the
+// same sizes again and again: each thread keeps the last few.
+LossPlan loss_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool backward)
+{
+    struct Entry {
+        int64_t T, V, D, slots, backward;
+        LossPlan plan;
+    };
+    thread_local Entry kept[4];
+    thread_local int next = 0;
+    for (const Entry& e : kept)
+        if (e.T == T && e.V == V && e.D == D && e.slots == slots && e.backward == backward)
+            return e.plan;
+    Entry& e = kept[next];
+    next = (next + 1) % 4;
+    e = {T, V, D, slots, backward, make_plan(T, V, D, slots, backward)};
+    return e.plan;
+}
+
 hipError_t loss_forward(const LossCall& c)
 {
     const LossPlan pl = loss_plan(c.T, c.V, c.D, c.slots, false);
     uint8_t* ws = c.ws;
-    DG_TRY(select_rows(c, pl, false));
+    RowSource src;
+    DG_TRY(row_targets(c, pl, &src));
+    // Few rows are not selected: the launch takes longer than the work it could
+    // save (one row of 50257 x 512: 20 us with it, 16 without).
+    const bool few = c.T <= Few::TM;
+    if (!few)
+        DG_TRY(select_rows(c, pl, src, false));
     LossArgs a = product_args(c, pl);
-    a.A = ws + pl.off_x;
-    a.lda_b = c.D * 2;
+    a.A = few ? reinterpret_cast<const uint8_t*>(c.X) : ws + pl.off_x;
+    a.lda_b = few ? c.ldx * 2 : c.D * 2;
+    a.n = (int)c.T;
+    a.labels = c.labels;
+    a.lead = src.flag;
     a.B = reinterpret_cast<const uint8_t*>(c.W);
     a.ldb_b = c.ldw * 2;
     a.N = (int)c.V;
@@ -689,13 +853,30 @@ hipError_t loss_forward(const LossCall& c)
     a.part = reinterpret_cast<float2*>(ws + pl.off_part);
     a.ldpart = pl.rows_pad;
     a.zlabel = reinterpret_cast<float*>(ws + pl.off_zlabel);
-    DG_TRY(launch_role<ROLE_LSE>(a, c.T, c.cus, c.stream));
-    const bool big = c.T > 32 && cdiv(c.T, 256) * cdiv(c.V, 256) >= c.cus / 2;
+    const RangePlan rp = plan_range(c.T, c.V, c.D, 0, false, c.cus);
+    int64_t tiles = 0;                       // tile columns so far
+    for (int64_t v0 = 0; v0 < c.V; v0 += rp.main) {
+        const int shape = v0 == 0 ? rp.shape : rp.rest_shape;
+        LossArgs m = a;
+        m.v0 = (int)v0;
+        m.N = (int)(v0 == 0 ? rp.main : c.V - v0);
+        m.B = a.B + v0 * a.ldb_b;
+        m.part = a.part + tiles * a.ldpart;
+        if (c.T <= Low::TM)
+            DG_TRY((go<Low, ROLE_LSE, true>(m, 1, c.cus, c.stream)));
+        else if (few)
+            DG_TRY((go<Few, ROLE_LSE, true>(m, 1, c.cus, c.stream)));
+        else
+            DG_TRY(launch_role<ROLE_LSE>(shape, m, c.T, c.cus, c.stream));
+        tiles += cdiv(m.N, kShapes[shape].tn);
+        if (v0 != 0)
+            break;
+    }
     auto join = [&](auto r) {
         constexpr int R = decltype(r)::value;
         loss_join_kernel<R><<<dim3((unsigned)cdiv(c.T, R)), dim3(256), 0, c.stream>>>(
-            a.part, a.ldpart, (int)cdiv(c.V, big ? 256 : 128), a.n_kept,
-            reinterpret_cast<const int*>(ws + pl.off_map), a.zlabel, fabsf(c.scale), c.slots ? 0.f : c.z_loss, c.loss,
+            a.part, a.ldpart, (int)tiles, a.n_kept,
+            reinterpret_cast<const int*>(ws + pl.off_map), src, few ? (int)c.T : 0, a.zlabel, fabsf(c.scale), c.slots ? 0.f : c.z_loss, c.loss,
             c.lse);
         return last();
     };
@@ -708,8 +889,9 @@ hipError_t loss_forward(const LossCall& c)
     k.W = a.B;
     k.ldw_b = a.ldb_b;
     k.Xc = a.A;
-    k.row_b = a.lda_b;
-    k.pos = reinterpret_cast<const int*>(ws + pl.off_pos);
+    k.row_b = c.D * 2;
+    k.ldx_b = a.lda_b;
+    k.pos = few ? nullptr : reinterpret_cast<const int*>(ws + pl.off_pos);
     k.index = c.index;
     k.ld_index = c.ld_index;
     k.V = c.V;
@@ -731,7 +913,9 @@ hipError_t loss_backward(const LossCall& c)
 {
     const LossPlan pl = loss_plan(c.T, c.V, c.D, c.slots, true);
     uint8_t* ws = c.ws;
-    DG_TRY(select_rows(c, pl, true));
+    RowSource src;
+    DG_TRY(row_targets(c, pl, &src));
+    DG_TRY(select_rows(c, pl, src, true));
     const int* pos = reinterpret_cast<const int*>(ws + pl.off_pos);
     const int* map = reinterpret_cast<const int*>(ws + pl.off_map);
     uint16_t* G = reinterpret_cast<uint16_t*>(ws + pl.off_g);
@@ -740,20 +924,28 @@ hipError_t loss_backward(const LossCall& c)
     for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
         const int64_t vp = std::min(pl.piece, c.V - v0);
         const uint8_t* W = reinterpret_cast<const uint8_t*>(c.W) + v0 * c.ldw * 2;
-        LossArgs a = product_args(c, pl);
-        a.A = Xc;
-        a.lda_b = c.D * 2;
-        a.B = W;
-        a.ldb_b = c.ldw * 2;
-        a.N = (int)vp;
-        a.K = (int)c.D;
-        a.v0 = (int)v0;
-        a.C = G;
-        a.ldc = pl.piece;
-        DG_TRY(launch_role<ROLE_GRAD>(a, c.T, c.cus, c.stream));
+        const RangePlan gp = plan_range(c.T, vp, c.D, 0, false, c.cus);
+        for (int64_t u = 0; u < vp; u += gp.main) {
+            LossArgs a = product_args(c, pl);
+            a.A = Xc;
+            a.lda_b = c.D * 2;
+            a.B = W + u * c.ldw * 2;
+            a.ldb_b = c.ldw * 2;
+            a.N = (int)(u == 0 ? gp.main : vp - u);
+            a.K = (int)c.D;
+            a.v0 = (int)(v0 + u);
+            a.C = G + u;
+            a.ldc = pl.piece;
+            a.c_cols = (int)(pl.piece - u);
+            DG_TRY(launch_role<ROLE_GRAD>(u == 0 ? gp.shape : gp.rest_shape, a, c.T, c.cus, c.stream));
+            if (u != 0)
+                break;
+        }
         if (c.slots) {
             loss_sparse_kernel<<<dim3((unsigned)cdiv(c.T, 4)), dim3(256), 0, c.stream>>>(
-                a.n_kept, map, a.rows, reinterpret_cast<const int*>(ws + pl.off_lead),
+                reinterpret_cast<const int*>(ws + pl.off_count), map,
+                reinterpret_cast<const RowInfo*>(ws + pl.off_rows),
+                reinterpret_cast<const int*>(ws + pl.off_lead),
                 reinterpret_cast<const float*>(ws + pl.off_qsum),
                 reinterpret_cast<const float*>(ws + pl.off_rest), c.logp_in, (int)c.slots, v0, vp, G,
                 pl.piece);
@@ -772,20 +964,25 @@ hipError_t loss_backward(const LossCall& c)
             d.plane = c.T * c.D;
             d.ldplane = c.D;
             d.first = v0 == 0;
-            DG_TRY(launch_role<ROLE_DX>(d, c.T, c.cus, c.stream));
+            DG_TRY(launch_role<ROLE_DX>(pl.dx_shape, d, c.T, c.cus, c.stream));
         }
         if (c.dW) {
-            LossArgs d = product_args(c, pl);
-            d.A = reinterpret_cast<const uint8_t*>(G);
-            d.lda_b = pl.piece * 2;
-            d.B = Xc;
-            d.ldb_b = c.D * 2;
-            d.M = (int)vp;
-            d.N = (int)c.D;
-            d.C = c.dW + v0 * c.lddw;
-            d.ldc = c.lddw;
-            d.c_vec = ((uintptr_t)c.dW & 15u) == 0 && c.lddw % 8 == 0;
-            DG_TRY(launch_role<ROLE_DW>(d, vp, c.cus, c.stream));
+            const RangePlan wp = plan_range(c.T, vp, c.T, c.D, true, c.cus);
+            for (int64_t u = 0; u < vp; u += wp.main) {
+                LossArgs d = product_args(c, pl);
+                d.A = reinterpret_cast<const uint8_t*>(G + u);
+                d.lda_b = pl.piece * 2;
+                d.B = Xc;
+                d.ldb_b = c.D * 2;
+                d.M = (int)(u == 0 ? wp.main : vp - u);
+                d.N = (int)c.D;
+                d.C = c.dW + (v0 + u) * c.lddw;
+                d.ldc = c.lddw;
+                d.c_vec = ((uintptr_t)c.dW & 15u) == 0 && c.lddw % 8 == 0;
+                DG_TRY(launch_role<ROLE_DW>(u == 0 ? wp.shape : wp.rest_shape, d, d.M, c.cus, c.stream));
+                if (u != 0)
+                    break;
+            }
         }
     }
     if (c.dX) {

@@ -46,7 +46,10 @@ struct LossArgs {
     const uint8_t* A;      // X compact [n, lda] (LSE, GRAD), G [n, lda] (DX, DW)
     const uint8_t* B;      // W [., ldb] from the piece's first row (LSE, GRAD, DX), X compact (DW)
     int64_t lda_b, ldb_b;  // row pitches in bytes
-    const int* n_kept;     // rows of X that take part (device)
+    const int* n_kept;     // rows of X that take part (device); null (few rows, LSE): n of them
+    int n;
+    const int64_t* labels; // few rows, LSE: the rows' labels, or with lead non-null the
+    const int* lead;       // columns of their largest targets, [n][2]; A is X itself then
     int M, N, K;           // M: DW only (the piece's rows of W); K: not for DW (n)
     int tiles_n;
     int splits, kt_per;    // DX: K slices, k-tiles per slice
@@ -55,12 +58,13 @@ struct LossArgs {
     float2* part;          // LSE: [tiles_n][ldpart] (reference, sum)
     int64_t ldpart;
     float* zlabel;         // LSE: the label's sum over d, with scale's sign; compact rows
-    int v0;                // GRAD: first column of the piece
+    int v0;                // LSE, GRAD: the vocabulary's column of B's first row
     float* planes;         // DX: [splits][plane_rows][ldplane]
     int64_t plane;         // elements of one plane
     int64_t ldplane;
     int first;             // DX: the first piece writes, later ones add
     uint16_t* C;           // GRAD: G; DW: dW
+    int c_cols;            // GRAD: columns of G from C on that may be written (whole tiles)
     int64_t ldc;
     int c_vec;
 };
@@ -197,9 +201,14 @@ __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N
     });
 }
 
-template <class S, int ROLE>
+// FEW: few rows, whose selection would take longer than what it saves.  A is X
+// itself and every row is computed (a row's X reaches its own logits only),
+// labels are read where they are needed, and W, read once, is loaded with the
+// non-temporal hint.
+template <class S, int ROLE, bool FEW = false>
 __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs p)
 {
+    static_assert(!FEW || ROLE == ROLE_LSE, "the gradient needs its rows selected");
     using AT = Atom<DT_BF16, 16>;
     using KTL = KTile<S::KTB>;
     using acc_t = AT::acc_t;
@@ -212,7 +221,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     static_assert(!TRB || TN >= 128, "a transposed operand's unit key needs 8 units a row");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
 
-    const int n = *p.n_kept;
+    const int n = FEW ? p.n : *p.n_kept;
     const int M = ROLE == ROLE_DW ? p.M : n;
     const int tiles_m = (M + TM - 1) / TM;
     // A persistent grid: workgroup b takes items b, b + gridDim, ...  The grid
@@ -316,29 +325,32 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                                : make_rsrc(a_base, a_bytes);
         const rsrc_t rbt = TRB ? rebase(b_base, b_span, (int64_t)kt * KT * p.ldb_b)
                                : make_rsrc(b_base, b_bytes);
-        auto one = [&](rsrc_t r, uint8_t* dst, uint32_t goff, uint32_t col, auto tr)
+        auto one = [&](rsrc_t r, uint8_t* dst, uint32_t goff, uint32_t col, auto tr, auto nt)
                        __attribute__((always_inline)) {
+            uint32_t off = goff, soff = 0;
             if constexpr (decltype(tr)::value) {
-                dma16(r, dst, goff, 0);
             } else if constexpr (NOMASK) {
-                dma16(r, dst, goff, (uint32_t)kt * KTB);
+                soff = (uint32_t)kt * KTB;
             } else {
-                uint32_t off = goff + (uint32_t)kt * KTB;
+                off = goff + (uint32_t)kt * KTB;
                 if (mask && (int)((uint32_t)kt * KTB + col) >= kb_end)
                     off = kOOB;
-                dma16(r, dst, off, 0);
             }
+            if constexpr (decltype(nt)::value)
+                dma16_nt(r, dst, off, soff);
+            else
+                dma16(r, dst, off, soff);
         };
 #pragma unroll
         for (int i = 0; i < A_DMA; ++i)
             if (i % nparts == part)
                 one(rat, base + (wave + WAVES * i) * 1024, a_goff[i], a_col[i],
-                    std::integral_constant<bool, TRA>{});
+                    std::integral_constant<bool, TRA>{}, std::false_type{});
 #pragma unroll
         for (int i = 0; i < B_DMA; ++i)
             if ((A_DMA + i) % nparts == part)
                 one(rbt, base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i], b_col[i],
-                    std::integral_constant<bool, TRB>{});
+                    std::integral_constant<bool, TRB>{}, std::integral_constant<bool, FEW>{});
     };
 
     // ---- fragments.  Plain: one 16-byte read, K values 8 lg .. 8 lg + 7 of
@@ -433,7 +445,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     [[maybe_unused]] const uint8_t* info = lds + S::ROWS_AT + parity * S::ROWS_LDS;
     uint8_t* out_lds = lds + S::OUT_AT;
     if constexpr (ROLE == ROLE_LSE) {
-        const int* lab = reinterpret_cast<const int*>(info + 12);
+        [[maybe_unused]] const int* lab = reinterpret_cast<const int*>(info + 12);
         float2* red = reinterpret_cast<float2*>(out_lds);
         // z / ln 2 = acc * c with c >= 0: a negative scale turns acc's sign
         const float c = fabsf(p.scale) * kLog2e;
@@ -459,7 +471,15 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                             x[j][e] = -INFINITY;
                     }
                 // the label's column, in the one lane that holds it
-                const uint32_t d = (uint32_t)(lab[4 * r] - col_w);
+                int label;
+                if constexpr (FEW) {
+                    const int64_t at = min(m0 + r, n - 1);
+                    const int64_t y = p.lead ? p.lead[2 * at + 1] : p.labels[at];
+                    label = y >= 0 && y < (1 << 30) ? (int)y : -1;
+                } else {
+                    label = lab[4 * r];
+                }
+                const uint32_t d = (uint32_t)(label - p.v0 - col_w);
                 if (d < (uint32_t)(NR * R) && (int)(d >> 2 & 3u) == lg) {
                     float xl = 0.f;
 #pragma unroll
@@ -540,7 +560,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
             }
         }
         // whole tiles: G's pitch is a multiple of the tile
-        store_bf16_block<MR, NR, 1, S::SROW>(p.C, p.ldc, (int)p.ldc, 1, acc,
+        store_bf16_block<MR, NR, 1, S::SROW>(p.C, p.ldc, p.c_cols, 1, acc,
                                                  out_lds + wave * (R * S::SROW), m0, rows,
                                                  (int)row0, col_w, ol);
     } else if constexpr (ROLE == ROLE_DX) {
@@ -583,7 +603,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
 #pragma unroll
         for (int t = 0; t < ST - 1; ++t)
             load(t, t, 0, 1, std::false_type{});
-        if constexpr (ROLE == ROLE_LSE || ROLE == ROLE_GRAD)
+        if constexpr ((ROLE == ROLE_LSE && !FEW) || ROLE == ROLE_GRAD)
             if (wave * 64 < TM)
                 dma16(make_rsrc(p.rows + m0, (uint32_t)rows * 16u),
                       lds + S::ROWS_AT + parity * S::ROWS_LDS + wave * 1024, (uint32_t)lane * 16u + (uint32_t)wave * 1024u, 0);

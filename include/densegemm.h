@@ -488,7 +488,7 @@ gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void
  * in fp32.  The entry points below take losses from z, and the gradients of X
  * and W, without storing z: the forward pass keeps one pair of floats per row
  * and 128 or 256 columns, the gradient one piece of the vocabulary at a time
- * (about 64 MiB of bf16), recomputed from X and W.
+ * (at most 256 MiB of bf16, or 256 columns), recomputed from X and W.
  *
  * Rows that are out -- an ignored label, no filled target slot -- have loss
  * 0, lse 0 and gradient 0, take no part in the products, and whatever their X

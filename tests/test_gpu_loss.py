@@ -14,10 +14,11 @@ pytestmark = pytest.mark.gpu
 # 128, 256 columns; 32, 64 values of K), one and several pieces of the vocabulary
 SHAPES = [(1, 1, 8), (1, 50257, 64), (3, 7, 24), (17, 130, 64), (32, 1000, 136), (33, 257, 72),
           (130, 1003, 520), (257, 129, 40), (600, 5003, 136)]
-LARGE = [(600, 11008, 72),        # the 256 x 256 tiles
+LARGE = [(48, 3001, 136), (64, 700, 64),       # the tile of 64 rows
+         (600, 11008, 72),        # the 256 x 256 tiles
+         (600, 23001, 520),       # whole rounds of them, and the rest apart
          (1100, 11001, 520),      # and for dX
-         (8192, 5003, 64),        # two pieces of the vocabulary
-         (20000, 300, 16)]        # rows counted in chunks
+         (8192, 5003, 64), (20000, 7001, 16)]     # rows counted in chunks, two pieces of the vocabulary
 
 
 def _say(*a):
@@ -71,7 +72,7 @@ def test_cross_entropy(T, V, D):
 @pytest.mark.parametrize("T,V,D,k", [(1, 1, 8, 1), (1, 5000, 64, 1), (3, 7, 24, 3), (33, 257, 72, 5),
                                      (130, 1003, 520, 64), (257, 129, 40, 65), (600, 5003, 136, 17),
                                      (40, 3000, 64, 256), (1100, 11001, 520, 9), (8192, 5003, 64, 4),
-                                     (20000, 300, 16, 2)])
+                                     (20000, 7001, 16, 2)])
 def test_distillation(T, V, D, k):
     _say("distill", T, V, D, k)
     X, W, lead = problem(T, V, D, T + V + D + k)
@@ -90,7 +91,7 @@ def test_scale_and_z_loss(scale, z_loss):
           reference(X, W, labels=lab, dloss=dl, scale=scale, z_loss=z_loss), f"scale {scale} z {z_loss}")
 
 
-@pytest.mark.parametrize("T,V,D", [(130, 1003, 136), (600, 11008, 72)])
+@pytest.mark.parametrize("T,V,D", [(30, 500, 72), (64, 500, 72), (130, 1003, 136), (600, 11008, 72)])
 @pytest.mark.parametrize("keep", [0.0, 0.03, 0.5])
 @pytest.mark.parametrize("kind", ["ce", "distill"])
 def test_rows_out(T, V, D, keep, kind):
