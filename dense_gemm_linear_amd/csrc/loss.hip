@@ -535,25 +535,32 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(const float* planes, int s
 // Tile shapes.  kt and epi are what one round (every CU holding its fill of
 // workgroups) measured on MI355X, in microseconds: kt for each 32 values of K,
 // epi for the rest of a tile; kt1 where there is at most one workgroup a CU.
-// The large tile does twice the work of the middle ones in 1.0 to 1.5 times
-// their time, so it is taken where its tiles fill the CUs (1024 x 50257 x 512
-// logits: 75 us against 92 and 92), the others where they do not (264 x 11007
-// x 1024: 22 us against 29).  Up to 64 rows the product is a read of W; there
-// the tile that covers the rows keeps the most of it in flight (48 x 50257 x
-// 4096: 140 us against 153 to 159 of the others with W cold).
+//   Big   taken where its tiles fill the CUs: twice the work of Tall, four
+//         times that of the others, in 1.0 to 1.6 times their time (4095 x
+//         50257 x 4096 logits: 1291 us; the next best shape 1414).
+//   Line  for the logits: two stages of whole 128-byte lines of X and W.
+//         Against four of 64 bytes (Mid): 597 x 50257 x 4096 298 us : 357,
+//         100 x 50257 x 2048 41 : 46, 528 x 11007 x 1024 26 : 29.  Deeper
+//         rings of 64-byte k-tiles gained nothing (31 to 33 us there).
+//   Mid   for dX and dW, whose transposed operands are whole lines anyway.
+//   Few, Low  up to 64 and 32 rows, where the product is a read of W: the
+//         tile that just covers the rows keeps the most of it in flight (48 x
+//         50257 x 4096, W cold: 141 us against 153 to 159 of the others).
 using Big = LossShape<256, 256, 2, 4, 4, 64, 1>;
 using Tall = LossShape<256, 128, 4, 2, 4, 64, 2>;
 using Mid = LossShape<128, 128, 2, 2, 4, 64, 2>;
+using Line = LossShape<128, 128, 2, 2, 2, 128, 2>;
 using Few = LossShape<64, 128, 1, 4, 3, 128, 2>;
 using Low = LossShape<32, 128, 1, 4, 3, 128, 2>;
-enum { SHAPE_BIG = 0, SHAPE_TALL, SHAPE_MID, SHAPE_FEW, SHAPE_LOW };
+enum { SHAPE_BIG = 0, SHAPE_TALL, SHAPE_MID, SHAPE_LINE, SHAPE_FEW, SHAPE_LOW };
 struct ShapeCost {
     int tm, tn, per_cu;
     double kt, kt1, epi;
 };
 constexpr ShapeCost kShapes[] = {{Big::TM, Big::TN, Big::PER_CU, 0.72, 0.72, 9.0},
-                                 {Tall::TM, Tall::TN, Tall::PER_CU, 0.46, 0.46, 3.5},
+                                 {Tall::TM, Tall::TN, Tall::PER_CU, 0.48, 0.48, 4.5},
                                  {Mid::TM, Mid::TN, Mid::PER_CU, 0.64, 0.50, 0.5},
+                                 {Line::TM, Line::TN, Line::PER_CU, 0.56, 0.47, 1.0},
                                  {Few::TM, Few::TN, Few::PER_CU, 0.5, 0.4, 2.0},
                                  {Low::TM, Low::TN, Low::PER_CU, 0.5, 0.4, 2.0}};
 constexpr int kPlanCus = 256;            // the workspace must not depend on the device
@@ -572,15 +579,13 @@ double product_us(int shape, int64_t rows, int64_t cols, int64_t k, int splits, 
 
 // Shape of a product whose outputs are rows x cols: by the row count where it
 // is small (not for dW: its rows are W's), else by the estimate.
-int pick_shape(int64_t rows, int64_t cols, int64_t k, int splits, int cus, bool few_rows)
+int pick_shape(bool logits, int64_t rows, int64_t cols, int64_t k, int cus)
 {
-    if (few_rows && rows <= 32)
-        return SHAPE_LOW;
-    if (few_rows && rows <= 64)
-        return SHAPE_FEW;
+    if (logits && rows <= Few::TM)
+        return rows <= Low::TM ? SHAPE_LOW : SHAPE_FEW;
     int best = SHAPE_BIG;
-    for (int i = SHAPE_TALL; i <= SHAPE_MID; ++i)
-        if (product_us(i, rows, cols, k, splits, cus) < product_us(best, rows, cols, k, splits, cus))
+    for (int i : {(int)SHAPE_TALL, logits ? (int)SHAPE_LINE : (int)SHAPE_MID})
+        if (product_us(i, rows, cols, k, 1, cus) < product_us(best, rows, cols, k, 1, cus))
             best = i;
     return best;
 }
@@ -601,7 +606,7 @@ RangePlan plan_range(int64_t t, int64_t v, int64_t k, int64_t other, bool by_row
         return by_rows ? product_us(sh, n, other, k, 1, cus) : product_us(sh, t, n, k, 1, cus);
     };
     auto pick = [&](int64_t n) {
-        return by_rows ? pick_shape(n, other, k, 1, cus, false) : pick_shape(t, n, k, 1, cus, true);
+        return by_rows ? pick_shape(false, n, other, k, cus) : pick_shape(true, t, n, k, cus);
     };
     RangePlan p;
     p.shape = p.rest_shape = pick(v);
@@ -661,7 +666,8 @@ hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipS
         return go<Big, ROLE>(a, cdiv(rows, Big::TM), cus, s);
     if (shape == SHAPE_TALL)
         return go<Tall, ROLE>(a, cdiv(rows, Tall::TM), cus, s);
-    return go<Mid, ROLE>(a, cdiv(rows, Mid::TM), cus, s);
+    using Other = std::conditional_t<ROLE == ROLE_LSE || ROLE == ROLE_GRAD, Line, Mid>;
+    return go<Other, ROLE>(a, cdiv(rows, Other::TM), cus, s);
 }
 
 hipError_t last() { return hipGetLastError(); }
@@ -835,9 +841,10 @@ hipError_t loss_forward(const LossCall& c)
     uint8_t* ws = c.ws;
     RowSource src;
     DG_TRY(row_targets(c, pl, &src));
-    // Few rows are not selected: the launch takes longer than the work it could
-    // save (one row of 50257 x 512: 20 us with it, 16 without).
-    const bool few = c.T <= Few::TM;
+    // Rows that one tile holds are not selected: W is read for one of them as
+    // for all, and the launch takes longer than the rest could save (one row of
+    // 50257 x 512: 20 us with it, 16 without).
+    const bool few = c.T <= Line::TM;
     if (!few)
         DG_TRY(select_rows(c, pl, src, false));
     LossArgs a = product_args(c, pl);
@@ -853,7 +860,9 @@ hipError_t loss_forward(const LossCall& c)
     a.part = reinterpret_cast<float2*>(ws + pl.off_part);
     a.ldpart = pl.rows_pad;
     a.zlabel = reinterpret_cast<float*>(ws + pl.off_zlabel);
-    const RangePlan rp = plan_range(c.T, c.V, c.D, 0, false, c.cus);
+    RangePlan rp = plan_range(c.T, c.V, c.D, 0, false, c.cus);
+    if (few)
+        rp = {c.T <= Low::TM ? SHAPE_LOW : c.T <= Few::TM ? SHAPE_FEW : SHAPE_LINE, 0, c.V};
     int64_t tiles = 0;                       // tile columns so far
     for (int64_t v0 = 0; v0 < c.V; v0 += rp.main) {
         const int shape = v0 == 0 ? rp.shape : rp.rest_shape;
@@ -864,8 +873,10 @@ hipError_t loss_forward(const LossCall& c)
         m.part = a.part + tiles * a.ldpart;
         if (c.T <= Low::TM)
             DG_TRY((go<Low, ROLE_LSE, true>(m, 1, c.cus, c.stream)));
-        else if (few)
+        else if (c.T <= Few::TM)
             DG_TRY((go<Few, ROLE_LSE, true>(m, 1, c.cus, c.stream)));
+        else if (few)
+            DG_TRY((go<Line, ROLE_LSE, true>(m, 1, c.cus, c.stream)));
         else
             DG_TRY(launch_role<ROLE_LSE>(shape, m, c.T, c.cus, c.stream));
         tiles += cdiv(m.N, kShapes[shape].tn);

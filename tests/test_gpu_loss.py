@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 # 128, 256 columns; 32, 64 values of K), one and several pieces of the vocabulary
 SHAPES = [(1, 1, 8), (1, 50257, 64), (3, 7, 24), (17, 130, 64), (32, 1000, 136), (33, 257, 72),
           (130, 1003, 520), (257, 129, 40), (600, 5003, 136)]
-LARGE = [(48, 3001, 136), (64, 700, 64),       # the tile of 64 rows
+LARGE = [(48, 3001, 136), (64, 700, 64), (128, 900, 200),   # one tile of rows
          (600, 11008, 72),        # the 256 x 256 tiles
          (600, 23001, 520),       # whole rounds of them, and the rest apart
          (1100, 11001, 520),      # and for dX
@@ -91,7 +91,7 @@ def test_scale_and_z_loss(scale, z_loss):
           reference(X, W, labels=lab, dloss=dl, scale=scale, z_loss=z_loss), f"scale {scale} z {z_loss}")
 
 
-@pytest.mark.parametrize("T,V,D", [(30, 500, 72), (64, 500, 72), (130, 1003, 136), (600, 11008, 72)])
+@pytest.mark.parametrize("T,V,D", [(30, 500, 72), (64, 500, 72), (127, 500, 72), (130, 1003, 136), (600, 11008, 72)])
 @pytest.mark.parametrize("keep", [0.0, 0.03, 0.5])
 @pytest.mark.parametrize("kind", ["ce", "distill"])
 def test_rows_out(T, V, D, keep, kind):
