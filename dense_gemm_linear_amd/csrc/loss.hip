@@ -473,58 +473,133 @@ __global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p)
         p.loss[t] = p.flag[2 * t] == ROW_BAD ? NAN : part;
 }
 
+// What rounding took from a value kept in bf16.
+__device__ __forceinline__ float bf16_rest(float x) { return x - bf16_to_f32(bf16_rne(x)); }
+
 // Distillation: the sparse columns of the gradient piece, p - q in place of
-// p.  One wave a kept row.
-__global__ __launch_bounds__(256) void loss_sparse_kernel(const int* n_kept, const int* map,
-                                                          const RowInfo* rows, const int* leader,
-                                                          const float* qsum, const float* rest,
-                                                          const float* logp, int k, int64_t v0,
-                                                          int64_t vp, uint16_t* G, int64_t ldg)
+// p.  One wave a kept row.  What rounding them to bf16 takes away is kept for
+// dX where it counts (lost).
+struct SparseArgs {
+    const int* n_kept;
+    const int* map;
+    const RowInfo* rows;
+    const int* leader;
+    const float *qsum, *rest, *logp;
+    int k;
+    int64_t v0, vp;
+    uint16_t* G;
+    int64_t ldg, half_b;         // half_b 0: G has one half
+    float* lost;                 // [T][k]
+};
+__global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
 {
     const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= *n_kept)
+    if (row >= *p.n_kept)
         return;
-    const int64_t t = map[row];
-    const float g = rows[row].b;
-    for (int j = threadIdx.x & 63; j < k; j += 64) {
-        const int64_t col = leader[t * k + j];
-        if (col < v0 || col >= v0 + vp)
+    const int64_t t = p.map[row];
+    const float g = p.rows[row].b;
+    for (int j = threadIdx.x & 63; j < p.k; j += 64) {
+        const int64_t i = t * p.k + j, col = p.leader[i];
+        if (col < p.v0 || col >= p.v0 + p.vp)
             continue;
-        const float lp = logp[t * k + j], r = rest[t * k + j];
-        // q of the column: the sum of its slots' q is 1 - rest
+        const float lp = p.logp[i], r = p.rest[i];
         // p - q with q = 1 - rest: near p = q = 1 both sides are taken from 1
-        const float d = r < 0.5f ? expm1f(lp) + r : expf(lp) - qsum[t * k + j];
-        G[row * ldg + (col - v0)] = bf16_rne(g * d);
+        const float d = r < 0.5f ? expm1f(lp) + r : expf(lp) - p.qsum[i];
+        uint16_t* at = p.G + row * p.ldg + (col - p.v0);
+        *at = bf16_rne(g * d);
+        if (p.half_b)
+            at[p.half_b / 2] = bf16_rne(bf16_rest(g * d));
+        // columns below 1/64 leave less than 2^-14 of the row's weight
+        p.lost[i] = fabsf(d) >= 0.015625f ? bf16_rest(g * d) : 0.f;
     }
 }
 
 // dX: the sum of the K slices' planes in slice order, rounded once; zero for
 // rows that are out.  Four columns a thread, four planes' loads in flight.
-__global__ __launch_bounds__(256) void loss_dx_kernel(const float* planes, int splits, int64_t plane,
-                                                      int64_t ldplane, const int* pos, uint16_t* dX,
-                                                      int64_t lddx, int64_t D)
+// A row of dX is often little more than one or two columns' worth of W, the
+// target's: what rounding G to bf16 took from those is added here in fp32, rest
+// times the column's row of W.  (Without it the roundings of G and of dX
+// together are 1.4 times the latter, and up to 2.5 times where one target
+// makes up a row.)
+struct DxArgs {
+    const float* planes;
+    int splits;
+    int64_t plane, ldplane;
+    const int* pos;
+    const RowInfo* rows;
+    const uint16_t* W;
+    int64_t ldw;
+    int k;                       // distillation: slots, else 0
+    const int* leader;
+    const float* lost;
+    uint16_t* dX;
+    int64_t lddx, D;
+};
+__global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
 {
+    __shared__ int col[kMaxLossSlots];
+    __shared__ float rest[kMaxLossSlots];
+    __shared__ int used[4];
     const int64_t t = blockIdx.x;
-    const int at = pos[t];
-    for (int64_t d = threadIdx.x * 4; d < D; d += 1024) {
+    const int at = p.pos[t];
+    int n = 0;
+    if (at >= 0) {
+        if (p.k == 0) {
+            const RowInfo ri = p.rows[at];
+            if (threadIdx.x == 0) {
+                col[0] = ri.label;
+                rest[0] = bf16_rest(ri.b);
+            }
+            n = ri.label >= 0;
+        } else {
+            // the slots with something lost, in slot order
+            const int j = threadIdx.x;
+            const int c = j < p.k ? p.leader[t * p.k + j] : -1;
+            const float r = c >= 0 ? p.lost[t * p.k + j] : 0.f;
+            const uint64_t has = __ballot(r != 0.f);
+            if ((j & 63) == 0)
+                used[j >> 6] = __popcll(has);
+            __syncthreads();
+            int before = 0;
+            for (int w = 0; w < 4; ++w) {
+                before += w < (j >> 6) ? used[w] : 0;
+                n += used[w];
+            }
+            if (r != 0.f) {
+                const int to = before + __popcll(has & ((1ull << (j & 63)) - 1));
+                col[to] = c;
+                rest[to] = r;
+            }
+        }
+    }
+    __syncthreads();
+    for (int64_t d = threadIdx.x * 4; d < p.D; d += 1024) {
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
         if (at >= 0) {
-            const float* from = planes + at * ldplane + d;
-            for (int i = 0; i < splits; i += 4) {
+            const float* from = p.planes + at * p.ldplane + d;
+            for (int i = 0; i < p.splits; i += 4) {
                 f32x4 v[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    v[u] = i + u < splits ? *reinterpret_cast<const f32x4*>(from + (i + u) * plane)
-                                          : f32x4{0.f, 0.f, 0.f, 0.f};
+                    v[u] = i + u < p.splits ? *reinterpret_cast<const f32x4*>(from + (i + u) * p.plane)
+                                            : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                     s += v[u];
+            }
+            for (int i = 0; i < n; ++i) {
+                const uint2 w = *reinterpret_cast<const uint2*>(p.W + col[i] * p.ldw + d);
+                const float r = rest[i];
+                s[0] = fmaf(r, __uint_as_float(w.x << 16), s[0]);
+                s[1] = fmaf(r, __uint_as_float(w.x & 0xFFFF0000u), s[1]);
+                s[2] = fmaf(r, __uint_as_float(w.y << 16), s[2]);
+                s[3] = fmaf(r, __uint_as_float(w.y & 0xFFFF0000u), s[3]);
             }
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const float x = s[u];
-            dX[t * lddx + d + u] = bf16_rne(x);
+            p.dX[t * p.lddx + d + u] = bf16_rne(x);
         }
     }
 }
@@ -652,7 +727,7 @@ hipError_t go(const LossArgs& a, int64_t tiles_m, int cus, hipStream_t s)
                            dim3(S::THREADS), args, 0, s);
 }
 
-template <int ROLE>
+template <int ROLE, bool FEW = false>
 hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipStream_t s)
 {
     // (few rows' LSE has a launch of its own)
@@ -663,11 +738,11 @@ hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipS
             return go<Few, ROLE>(a, cdiv(rows, Few::TM), cus, s);
     }
     if (shape == SHAPE_BIG)
-        return go<Big, ROLE>(a, cdiv(rows, Big::TM), cus, s);
+        return go<Big, ROLE, FEW>(a, cdiv(rows, Big::TM), cus, s);
     if (shape == SHAPE_TALL)
-        return go<Tall, ROLE>(a, cdiv(rows, Tall::TM), cus, s);
+        return go<Tall, ROLE, FEW>(a, cdiv(rows, Tall::TM), cus, s);
     using Other = std::conditional_t<ROLE == ROLE_LSE || ROLE == ROLE_GRAD, Line, Mid>;
-    return go<Other, ROLE>(a, cdiv(rows, Other::TM), cus, s);
+    return go<Other, ROLE, FEW>(a, cdiv(rows, Other::TM), cus, s);
 }
 
 hipError_t last() { return hipGetLastError(); }
@@ -809,7 +884,8 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
                     p.splits = sp;
                 }
             }
-        p.off_g = take(p.rows_pad * piece * 2);
+        p.halves = T <= Line::TM;
+        p.off_g = take(p.rows_pad * piece * (p.halves ? 4 : 2));
         p.off_planes = take((int64_t)p.splits * T * D * 4);
         p.bytes = std::max(p.bytes, at);
     }
@@ -929,14 +1005,20 @@ hipError_t loss_backward(const LossCall& c)
     DG_TRY(select_rows(c, pl, src, true));
     const int* pos = reinterpret_cast<const int*>(ws + pl.off_pos);
     const int* map = reinterpret_cast<const int*>(ws + pl.off_map);
+    const RowInfo* rows = reinterpret_cast<const RowInfo*>(ws + pl.off_rows);
+    // few rows: G in two halves where dW is asked for
+    const int64_t half_b = pl.halves && c.dW ? pl.rows_pad * pl.piece * 2 : 0;
     uint16_t* G = reinterpret_cast<uint16_t*>(ws + pl.off_g);
     const uint8_t* Xc = ws + pl.off_x;
     float* planes = reinterpret_cast<float*>(ws + pl.off_planes);
     for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
         const int64_t vp = std::min(pl.piece, c.V - v0);
         const uint8_t* W = reinterpret_cast<const uint8_t*>(c.W) + v0 * c.ldw * 2;
-        const RangePlan gp = plan_range(c.T, vp, c.D, 0, false, c.cus);
+        RangePlan gp = plan_range(c.T, vp, c.D, 0, false, c.cus);
+        if (half_b)
+            gp = {c.T <= Low::TM ? SHAPE_LOW : c.T <= Few::TM ? SHAPE_FEW : SHAPE_LINE, 0, vp};
         for (int64_t u = 0; u < vp; u += gp.main) {
+            const int shape = u == 0 ? gp.shape : gp.rest_shape;
             LossArgs a = product_args(c, pl);
             a.A = Xc;
             a.lda_b = c.D * 2;
@@ -948,18 +1030,35 @@ hipError_t loss_backward(const LossCall& c)
             a.C = G + u;
             a.ldc = pl.piece;
             a.c_cols = (int)(pl.piece - u);
-            DG_TRY(launch_role<ROLE_GRAD>(u == 0 ? gp.shape : gp.rest_shape, a, c.T, c.cus, c.stream));
+            a.half_b = half_b;
+            if (!half_b)
+                DG_TRY(launch_role<ROLE_GRAD>(shape, a, c.T, c.cus, c.stream));
+            else if (shape == SHAPE_LOW)
+                DG_TRY((go<Low, ROLE_GRAD, true>(a, 1, c.cus, c.stream)));
+            else if (shape == SHAPE_FEW)
+                DG_TRY((go<Few, ROLE_GRAD, true>(a, 1, c.cus, c.stream)));
+            else
+                DG_TRY((go<Line, ROLE_GRAD, true>(a, 1, c.cus, c.stream)));
             if (u != 0)
                 break;
         }
         if (c.slots) {
-            loss_sparse_kernel<<<dim3((unsigned)cdiv(c.T, 4)), dim3(256), 0, c.stream>>>(
-                reinterpret_cast<const int*>(ws + pl.off_count), map,
-                reinterpret_cast<const RowInfo*>(ws + pl.off_rows),
-                reinterpret_cast<const int*>(ws + pl.off_lead),
-                reinterpret_cast<const float*>(ws + pl.off_qsum),
-                reinterpret_cast<const float*>(ws + pl.off_rest), c.logp_in, (int)c.slots, v0, vp, G,
-                pl.piece);
+            SparseArgs k;
+            k.n_kept = reinterpret_cast<const int*>(ws + pl.off_count);
+            k.map = map;
+            k.rows = rows;
+            k.leader = reinterpret_cast<const int*>(ws + pl.off_lead);
+            k.qsum = reinterpret_cast<const float*>(ws + pl.off_qsum);
+            k.rest = reinterpret_cast<const float*>(ws + pl.off_rest);
+            k.logp = c.logp_in;
+            k.k = (int)c.slots;
+            k.v0 = v0;
+            k.vp = vp;
+            k.G = G;
+            k.ldg = pl.piece;
+            k.half_b = half_b;
+            k.lost = reinterpret_cast<float*>(ws + pl.off_q);
+            loss_sparse_kernel<<<dim3((unsigned)cdiv(c.T, 4)), dim3(256), 0, c.stream>>>(k);
             DG_TRY(last());
         }
         if (c.dX) {
@@ -978,7 +1077,7 @@ hipError_t loss_backward(const LossCall& c)
             DG_TRY(launch_role<ROLE_DX>(pl.dx_shape, d, c.T, c.cus, c.stream));
         }
         if (c.dW) {
-            const RangePlan wp = plan_range(c.T, vp, c.T, c.D, true, c.cus);
+            const RangePlan wp = plan_range(c.T, vp, half_b ? 2 * c.T : c.T, c.D, true, c.cus);
             for (int64_t u = 0; u < vp; u += wp.main) {
                 LossArgs d = product_args(c, pl);
                 d.A = reinterpret_cast<const uint8_t*>(G + u);
@@ -990,15 +1089,34 @@ hipError_t loss_backward(const LossCall& c)
                 d.C = c.dW + (v0 + u) * c.lddw;
                 d.ldc = c.lddw;
                 d.c_vec = ((uintptr_t)c.dW & 15u) == 0 && c.lddw % 8 == 0;
-                DG_TRY(launch_role<ROLE_DW>(u == 0 ? wp.shape : wp.rest_shape, d, d.M, c.cus, c.stream));
+                d.half_b = half_b;
+                const int shape = u == 0 ? wp.shape : wp.rest_shape;
+                if (half_b)
+                    DG_TRY((launch_role<ROLE_DW, true>(shape, d, d.M, c.cus, c.stream)));
+                else
+                    DG_TRY(launch_role<ROLE_DW>(shape, d, d.M, c.cus, c.stream));
                 if (u != 0)
                     break;
             }
         }
     }
     if (c.dX) {
-        loss_dx_kernel<<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(
-            planes, pl.splits, c.T * c.D, c.D, pos, c.dX, c.lddx, c.D);
+        DxArgs d;
+        d.planes = planes;
+        d.splits = pl.splits;
+        d.plane = c.T * c.D;
+        d.ldplane = c.D;
+        d.pos = pos;
+        d.rows = rows;
+        d.W = c.W;
+        d.ldw = c.ldw;
+        d.k = (int)c.slots;
+        d.leader = reinterpret_cast<const int*>(ws + pl.off_lead);
+        d.lost = reinterpret_cast<const float*>(ws + pl.off_q);
+        d.dX = c.dX;
+        d.lddx = c.lddx;
+        d.D = c.D;
+        loss_dx_kernel<<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(d);
         DG_TRY(last());
     }
     return hipSuccess;

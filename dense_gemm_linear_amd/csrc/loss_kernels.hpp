@@ -67,6 +67,7 @@ struct LossArgs {
     int c_cols;            // GRAD: columns of G from C on that may be written (whole tiles)
     int64_t ldc;
     int c_vec;
+    int64_t half_b;        // few rows, GRAD and DW: bytes from G to its second half
 };
 
 // Tile shape: TM x TN outputs, WM x WN waves, ST stages of KTB bytes of K,
@@ -201,14 +202,22 @@ __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N
     });
 }
 
-// FEW: few rows, whose selection would take longer than what it saves.  A is X
-// itself and every row is computed (a row's X reaches its own logits only),
-// labels are read where they are needed, and W, read once, is loaded with the
-// non-temporal hint.
+// FEW: few rows (at most one tile of them).
+//   LSE   their selection would take longer than what it saves: A is X itself
+//         and every row is computed (a row's X reaches its own logits only),
+//         labels are read where they are needed, and W, read once, is loaded
+//         with the non-temporal hint.
+//   GRAD  G is stored in two bf16 halves, the rounded value and the rounded
+//         rest (16 bits of it together), and
+//   DW    sums both: with few rows one element's rounding can make up most of
+//         a row of dW (over many rows such errors average), and the product is
+//         bound by writing dW, not by its K.
 template <class S, int ROLE, bool FEW = false>
 __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs p)
 {
-    static_assert(!FEW || ROLE == ROLE_LSE, "the gradient needs its rows selected");
+    static_assert(!FEW || ROLE != ROLE_DX, "dX gets its rounding back row by row");
+    constexpr bool FEWX = FEW && ROLE == ROLE_LSE;        // X not selected
+    constexpr bool HALVES = FEW && ROLE == ROLE_DW;
     using AT = Atom<DT_BF16, 16>;
     using KTL = KTile<S::KTB>;
     using acc_t = AT::acc_t;
@@ -221,7 +230,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     static_assert(!TRB || TN >= 128, "a transposed operand's unit key needs 8 units a row");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
 
-    const int n = FEW ? p.n : *p.n_kept;
+    const int n = FEWX ? p.n : *p.n_kept;
     const int M = ROLE == ROLE_DW ? p.M : n;
     const int tiles_m = (M + TM - 1) / TM;
     // A persistent grid: workgroup b takes items b, b + gridDim, ...  The grid
@@ -275,7 +284,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     const int K = ROLE == ROLE_DW ? n : p.K;
     const int all_kt = (K + KT - 1) / KT;
     int slice = 0, m0 = 0, n0 = 0, rows = 0;
-    int kt0 = 0, nkt = all_kt, kb_end = K * 2, last_full = 0;
+    int kt0 = 0, nkt = HALVES ? 2 * all_kt : all_kt, kb_end = K * 2, last_full = 0;
     const uint8_t *a_base = nullptr, *b_base = nullptr;
     int64_t a_span = 0, b_span = 0;
     uint32_t a_bytes = 0, b_bytes = 0;
@@ -321,10 +330,12 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
         const int kt = kt0 + kt_local;
         const bool mask = kt >= last_full;
         uint8_t* base = lds + stage * STAGE;
-        const rsrc_t rat = TRA ? rebase(a_base, a_span, (int64_t)kt * KT * p.lda_b)
+        // the second half of G against the same rows of X
+        const bool second = HALVES && kt >= all_kt;
+        const int64_t row = (int64_t)(second ? kt - all_kt : kt) * KT;
+        const rsrc_t rat = TRA ? rebase(a_base + (second ? p.half_b : 0), a_span, row * p.lda_b)
                                : make_rsrc(a_base, a_bytes);
-        const rsrc_t rbt = TRB ? rebase(b_base, b_span, (int64_t)kt * KT * p.ldb_b)
-                               : make_rsrc(b_base, b_bytes);
+        const rsrc_t rbt = TRB ? rebase(b_base, b_span, row * p.ldb_b) : make_rsrc(b_base, b_bytes);
         auto one = [&](rsrc_t r, uint8_t* dst, uint32_t goff, uint32_t col, auto tr, auto nt)
                        __attribute__((always_inline)) {
             uint32_t off = goff, soff = 0;
@@ -350,7 +361,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
         for (int i = 0; i < B_DMA; ++i)
             if ((A_DMA + i) % nparts == part)
                 one(rbt, base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i], b_col[i],
-                    std::integral_constant<bool, TRB>{}, std::integral_constant<bool, FEW>{});
+                    std::integral_constant<bool, TRB>{}, std::integral_constant<bool, FEWX>{});
     };
 
     // ---- fragments.  Plain: one 16-byte read, K values 8 lg .. 8 lg + 7 of
@@ -472,7 +483,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                     }
                 // the label's column, in the one lane that holds it
                 int label;
-                if constexpr (FEW) {
+                if constexpr (FEWX) {
                     const int64_t at = min(m0 + r, n - 1);
                     const int64_t y = p.lead ? p.lead[2 * at + 1] : p.labels[at];
                     label = y >= 0 && y < (1 << 30) ? (int)y : -1;
@@ -563,6 +574,20 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
         store_bf16_block<MR, NR, 1, S::SROW>(p.C, p.ldc, p.c_cols, 1, acc,
                                                  out_lds + wave * (R * S::SROW), m0, rows,
                                                  (int)row0, col_w, ol);
+        if constexpr (FEW) {
+#pragma unroll
+            for (int mi = 0; mi < MR; ++mi)
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float g = acc[mi][j][e];
+                        acc[mi][j][e] = g - bf16_to_f32(bf16_rne(g));
+                    }
+            store_bf16_block<MR, NR, 1, S::SROW>(p.C + p.half_b / 2, p.ldc, p.c_cols, 1, acc,
+                                                 out_lds + wave * (R * S::SROW), m0, rows,
+                                                 (int)row0, col_w, ol);
+        }
     } else if constexpr (ROLE == ROLE_DX) {
         float* plane = p.planes + (int64_t)slice * p.plane + (int64_t)m0 * p.ldplane + n0;
         const rsrc_t rp = make_rsrc(plane, (uint32_t)(((int64_t)(rows - 1) * p.ldplane + (p.N - n0)) * 4));
@@ -603,7 +628,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
 #pragma unroll
         for (int t = 0; t < ST - 1; ++t)
             load(t, t, 0, 1, std::false_type{});
-        if constexpr ((ROLE == ROLE_LSE && !FEW) || ROLE == ROLE_GRAD)
+        if constexpr ((ROLE == ROLE_LSE && !FEWX) || ROLE == ROLE_GRAD)
             if (wave * 64 < TM)
                 dma16(make_rsrc(p.rows + m0, (uint32_t)rows * 16u),
                       lds + S::ROWS_AT + parity * S::ROWS_LDS + wave * 1024, (uint32_t)lane * 16u + (uint32_t)wave * 1024u, 0);

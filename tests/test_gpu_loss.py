@@ -147,6 +147,42 @@ def test_confident_rows_keep_their_digits():
     assert bool(((logp[:, 0].double() + want).abs() <= 2.0 ** -18 * want).all())
 
 
+@pytest.mark.parametrize("T,V,D,k", [(1, 4000, 256, 0), (6, 9001, 136, 0), (100, 2000, 512, 0),
+                                     (3, 4000, 256, 2), (128, 3000, 72, 5), (600, 3000, 256, 0),
+                                     (600, 3000, 256, 4)])
+def test_gradients_of_few_targets_are_rounded_once(T, V, D, k):
+    """Where one target makes up a row of dX, or a few rows make up dW, the
+    rounding of the logits' gradient to bf16 would show beside that of the
+    result.  A rounding to nearest of a value of mantissa m in [1, 2) is off by
+    at most 2^-8 / m, evenly: 2^-8 / (sqrt(3) m) root mean square, at most
+    2^-8 / sqrt(3).  dX: one such rounding, and those of the columns that are no
+    targets (independent, so the sum of their squares); dW of up to 128 rows:
+    one, the rest of G going into a second half."""
+    X, W, lab = problem(T, V, D, T + k, pull=8.0)
+    dl = _dloss(T, 5)
+    if k:
+        g = torch.Generator().manual_seed(k)
+        idx = torch.randint(0, V, (T, k), generator=g).cuda()
+        idx[:, 0] = lab
+        te = torch.randn(T, k, generator=g).cuda() * 3
+        got, ref = _run_di(X, W, idx, te, dl), reference(X, W, index=idx, teacher=te, dloss=dl)
+    else:
+        idx = lab[:, None]
+        got, ref = _run_ce(X, W, lab, dl), reference(X, W, labels=lab, dloss=dl)
+    z = X.double() @ W.double().t()
+    rest = torch.softmax(z, 1) * dl.double()[:, None]
+    rest = rest.scatter(1, idx, 0.0)
+    others = float(((rest * rest) @ (W.double() ** 2)).sum()) ** 0.5
+    once = 2.0 ** -8 / math.sqrt(3.0)
+    worst = {"dX": once * math.hypot(float(ref["dX"].norm()), others)}
+    if T <= 128:
+        worst["dW"] = once * float(ref["dW"].norm())
+    for name, bound in worst.items():
+        err = float((got[name].double() - ref[name]).norm())
+        # 5 %: fp32 sums, and targets below 1/64
+        assert err <= 1.05 * bound, f"{name}: {err:.3e} against {bound:.3e}"
+
+
 def test_large_logits_do_not_overflow():
     T, V, D = 33, 700, 64
     X, W, lab = problem(T, V, D, 10, spread=60.0)
