@@ -204,32 +204,35 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
     }
 }
 
-// Joins the tile columns' (reference, sum) pairs of each kept row and, with the
-// label's z, gives lse and the negative log-probability of the label.  R rows
-// a workgroup, 256 / R threads a row: 16 rows read whole 128-byte lines of
-// the table where there are many; few rows get all threads (one row of 393
-// pairs: 16 threads took 11 us, 256 take 3).
+struct JoinArgs {
+    const float2* part;          // [tiles_n][ldpart]
+    int64_t ldpart;
+    int tiles_n;
+    const int* n_kept;
+    const int* map;
+    RowSource src;               // few rows: their states
+    int few;                     // few rows: how many; none moved
+    const float* zlabel;
+    float scale, z_loss;         // scale without its sign
+    float* loss;
+    float* lse;
+};
+
+// Joins the tile columns' (reference, sum) pairs of one row (in the threads of
+// q = 0) by 256 threads, R rows in all; red: 256 pairs of LDS.
 template <int R>
-__global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, int64_t ldpart, int tiles_n,
-                                                        const int* n_kept, const int* map,
-                                                        RowSource src, int few, const float* zlabel, float scale, float z_loss,
-                                                        float* loss, float* lse)
+__device__ __forceinline__ float2 join_row(const JoinArgs& p, int row, bool valid, float2* red)
 {
     constexpr int Q = 256 / R;
-    __shared__ float2 red[256];
-    const int n = few ? few : *n_kept;       // few rows: all of them, none moved
-    const int r = threadIdx.x % R, q = threadIdx.x / R;
-    const int row = blockIdx.x * R + r;
-    if (blockIdx.x * R >= n)
-        return;
+    const int q = threadIdx.x / R;
     float2 acc = make_float2(-INFINITY, 0.f);
-    if (row < n)
-        for (int t = q; t < tiles_n; t += 4 * Q) {
+    if (valid)
+        for (int t = q; t < p.tiles_n; t += 4 * Q) {
             float2 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                v[u] = t + u * Q < tiles_n ? part[(int64_t)(t + u * Q) * ldpart + row]
-                                           : make_float2(-INFINITY, 0.f);
+                v[u] = t + u * Q < p.tiles_n ? p.part[(int64_t)(t + u * Q) * p.ldpart + row]
+                                             : make_float2(-INFINITY, 0.f);
             acc = lse_merge(acc, lse_merge(lse_merge(v[0], v[1]), lse_merge(v[2], v[3])));
         }
     red[threadIdx.x] = acc;
@@ -240,34 +243,56 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, int6
             red[threadIdx.x] = lse_merge(red[threadIdx.x], red[threadIdx.x + half * R]);
         __syncthreads();
     }
-    if (q != 0 || row >= n)
-        return;
-    // others = (reference + log2 sum) ln 2; its distance to the label's z from
-    // the label's own sum over d, so that what they share cancels before it is
-    // rounded
+    return red[threadIdx.x % R];
+}
+
+// lse and the label's negative log-probability from the joined pair and the
+// label's sum over d.  others = (reference + log2 sum) ln 2; its distance to the
+// label's z from the sum itself, so that what they share cancels before it is
+// rounded.
+__device__ __forceinline__ void lse_finish(float2 v, float xl, float scale, float& nll, float& lse)
+{
     constexpr float kLn2 = 0.69314718055994530942f;
-    const float ref = red[r].x, sum = red[r].y, logs = logf(sum);
-    const bool none = ref == -INFINITY && sum == 0.f;     // one column: no others
-    float xl = zlabel[row];
-    if (few) {
+    const float logs = logf(v.y), zl = xl * scale;
+    const bool none = v.x == -INFINITY && v.y == 0.f;     // one column: no others
+    const float others = none ? -INFINITY : fmaf(v.x, kLn2, logs);
+    const float d = none ? -INFINITY : fmaf(fmaf(-xl, scale * kLog2e, v.x), kLn2, logs);
+    nll = fmaxf(d, 0.f) + log1pf(expf(-fabsf(d))) + (d != d ? d : 0.f);
+    // no label column (NaN), or one of z = -inf: lse of all that was summed
+    lse = d != d || zl == -INFINITY ? others : zl + nll;
+}
+
+// Cross entropy's last step, and distillation's for many rows (loss: the lead's
+// negative log-probability then).  R rows a workgroup, 256 / R threads a row: 16
+// rows read whole 128-byte lines of the table where there are many; few rows
+// get all threads (one row of 393 pairs: 16 threads took 11 us, 256 take 4).
+template <int R>
+__global__ __launch_bounds__(256) void loss_join_kernel(JoinArgs p)
+{
+    __shared__ float2 red[256];
+    const int n = p.few ? p.few : *p.n_kept;
+    const int row = blockIdx.x * R + threadIdx.x % R;
+    if (blockIdx.x * R >= n)
+        return;
+    const float2 v = join_row<R>(p, row, row < n, red);
+    if (threadIdx.x >= R || row >= n)
+        return;
+    float xl = p.zlabel[row];
+    if (p.few) {
         int label;
-        const int st = row_state(src, row, label);
+        const int st = row_state(p.src, row, label);
         if (st == ROW_OUT) {
-            loss[row] = lse[row] = 0.f;
+            p.loss[row] = p.lse[row] = 0.f;
             return;
         }
         if (st == ROW_BAD)
             xl = NAN;
     }
-    const float zl = xl * scale;
-    const float others = none ? -INFINITY : fmaf(ref, kLn2, logs);
-    const float d = none ? -INFINITY : fmaf(fmaf(-xl, scale * kLog2e, ref), kLn2, logs);
-    const float nll = fmaxf(d, 0.f) + log1pf(expf(-fabsf(d))) + (d != d ? d : 0.f);
-    // no label column (NaN), or one of z = -inf: lse of all that was summed
-    const float l = d != d || zl == -INFINITY ? others : zl + nll;
-    const int t = few ? row : map[row];
-    loss[t] = nll + z_loss * l * l;
-    lse[t] = l;
+    float nll, l;
+    lse_finish(v, xl, p.scale, nll, l);
+    const int t = p.few ? row : p.map[row];
+    p.loss[t] = nll + p.z_loss * l * l;
+    p.lse[t] = l;
 }
 
 // ---------------------------------------------------------------------------
@@ -376,7 +401,6 @@ struct PickArgs {
     float scale;
     const float* zlabel;
     float* loss;                 // in: the lead's negative log-probability; out: the loss
-    const float* lse;
     float* logp;                 // [T][k]
 };
 
@@ -393,10 +417,13 @@ __device__ __forceinline__ float dot8(i32x4 a, i32x4 b, float s)
 
 // The student's log-probabilities at a row's slots, and the row's loss: a
 // workgroup of 4 waves a row, four slots at a time a wave, each a dot product of the
-// row of X with the slot's row of W.
-__global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p)
+// row of X with the slot's row of W.  JOIN (few rows): the row's join here too,
+// instead of in a launch of its own.
+template <bool JOIN>
+__global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p, JoinArgs jn)
 {
     __shared__ float z[kMaxLossSlots];
+    __shared__ float2 red[JOIN ? 256 : 1];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     // few rows: none moved
@@ -405,8 +432,13 @@ __global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p)
     if (at < 0) {
         for (int j = threadIdx.x; j < p.k; j += 256)
             out[j] = 0.f;
+        if (JOIN && threadIdx.x == 0)
+            p.loss[t] = jn.lse[t] = 0.f;
         return;
     }
+    float2 joined = make_float2(0.f, 0.f);
+    if constexpr (JOIN)
+        joined = join_row<1>(jn, (int)t, true, red);
     const uint8_t* x = p.Xc + at * p.ldx_b;
     const int lead = p.flag[2 * t + 1];
     for (int j0 = 4 * wave; j0 < p.k; j0 += 16) {
@@ -437,7 +469,16 @@ __global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p)
         return;
     // the lead's own log-probability is the well-conditioned one of the join;
     // the others' follow from their distance to it
-    const float lead_nll = p.loss[t], zl = p.zlabel[at] * fabsf(p.scale);
+    const float xl = p.zlabel[at], zl = xl * fabsf(p.scale);
+    float lead_nll;
+    if constexpr (JOIN) {
+        float lse;
+        lse_finish(joined, lead >= 0 ? xl : NAN, jn.scale, lead_nll, lse);
+        if (lane == 0)
+            jn.lse[t] = lse;
+    } else {
+        lead_nll = p.loss[t];
+    }
     float mx = -INFINITY;
     for (int j = lane; j < p.k; j += 64) {
         const int64_t i = p.index[t * p.ld_index + j];
@@ -959,17 +1000,28 @@ hipError_t loss_forward(const LossCall& c)
         if (v0 != 0)
             break;
     }
+    JoinArgs j;
+    j.part = a.part;
+    j.ldpart = a.ldpart;
+    j.tiles_n = (int)tiles;
+    j.n_kept = a.n_kept;
+    j.map = reinterpret_cast<const int*>(ws + pl.off_map);
+    j.src = src;
+    j.few = few ? (int)c.T : 0;
+    j.zlabel = a.zlabel;
+    j.scale = fabsf(c.scale);
+    j.z_loss = c.slots ? 0.f : c.z_loss;
+    j.loss = c.loss;
+    j.lse = c.lse;
     auto join = [&](auto r) {
         constexpr int R = decltype(r)::value;
-        loss_join_kernel<R><<<dim3((unsigned)cdiv(c.T, R)), dim3(256), 0, c.stream>>>(
-            a.part, a.ldpart, (int)tiles, a.n_kept,
-            reinterpret_cast<const int*>(ws + pl.off_map), src, few ? (int)c.T : 0, a.zlabel, fabsf(c.scale), c.slots ? 0.f : c.z_loss, c.loss,
-            c.lse);
+        loss_join_kernel<R><<<dim3((unsigned)cdiv(c.T, R)), dim3(256), 0, c.stream>>>(j);
         return last();
     };
-    DG_TRY(c.T >= 2048 ? join(std::integral_constant<int, 16>{})
-           : c.T >= 256 ? join(std::integral_constant<int, 4>{})
-                        : join(std::integral_constant<int, 1>{}));
+    if (!few || !c.slots)
+        DG_TRY(c.T >= 2048 ? join(std::integral_constant<int, 16>{})
+               : c.T >= 256 ? join(std::integral_constant<int, 4>{})
+                            : join(std::integral_constant<int, 1>{}));
     if (!c.slots)
         return hipSuccess;
     PickArgs k;
@@ -990,9 +1042,11 @@ hipError_t loss_forward(const LossCall& c)
     k.scale = c.scale;
     k.zlabel = a.zlabel;
     k.loss = c.loss;
-    k.lse = c.lse;
     k.logp = c.logp;
-    loss_pick_kernel<<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(k);
+    if (few)
+        loss_pick_kernel<true><<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(k, j);
+    else
+        loss_pick_kernel<false><<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(k, j);
     return last();
 }
 

@@ -289,12 +289,16 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     int64_t a_span = 0, b_span = 0;
     uint32_t a_bytes = 0, b_bytes = 0;
     auto set_item = [&](int it) __attribute__((always_inline)) {
-        int t = it, tm, tn;
+        // Each XCD a contiguous run of items.  dX: slices outermost, so that the
+        // tiles of a slice, which read the same columns of G and rows of W, share
+        // an L2 (1024 x 50257 x 512, gradient of X: 129 us against 155 with each
+        // slice's tiles spread over the XCDs, which read G four times from memory).
+        int t = xcd_remap(it, items), tm, tn;
         if constexpr (ROLE == ROLE_DX) {
-            slice = it / tiles;
+            slice = t / tiles;
             t -= slice * tiles;
         }
-        tile_raster<DG_GROUP_M>(xcd_remap(t, tiles), tiles_m, p.tiles_n, tm, tn);
+        tile_raster<DG_GROUP_M>(t, tiles_m, p.tiles_n, tm, tn);
         m0 = tm * TM;
         n0 = tn * TN;
         rows = min(TM, M - m0);
