@@ -13,6 +13,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <tuple>
+
 #include "internal.hpp"
 #include "loss_kernels.hpp"
 
@@ -575,6 +577,7 @@ struct DxArgs {
     const float* lost;
     uint16_t* dX;
     int64_t lddx, D;
+    int vec;                     // dX's rows start on 8 bytes
 };
 __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
 {
@@ -637,10 +640,16 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
                 s[3] = fmaf(r, __uint_as_float(w.y & 0xFFFF0000u), s[3]);
             }
         }
+        const float s0 = s[0], s1 = s[1], s2 = s[2], s3 = s[3];
+        const uint16_t o[4] = {bf16_rne(s0), bf16_rne(s1), bf16_rne(s2), bf16_rne(s3)};
+        uint16_t* to = p.dX + t * p.lddx + d;
+        if (p.vec) {
+            *reinterpret_cast<uint2*>(to) =
+                make_uint2((uint32_t)o[0] | (uint32_t)o[1] << 16, (uint32_t)o[2] | (uint32_t)o[3] << 16);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float x = s[u];
-            p.dX[t * p.lddx + d + u] = bf16_rne(x);
+            for (int u = 0; u < 4; ++u)
+                to[u] = o[u];
         }
     }
 }
@@ -786,7 +795,19 @@ hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipS
     return go<Other, ROLE, FEW>(a, cdiv(rows, Other::TM), cus, s);
 }
 
-hipError_t last() { return hipGetLastError(); }
+// Launches a kernel; the status of this launch, not an earlier sticky error.
+template <class... P, class... A>
+hipError_t launch(void (*kernel)(P...), int64_t grid, int block, hipStream_t s, A... args)
+{
+    std::tuple<P...> held(args...);
+    return std::apply(
+        [&](auto&... a) {
+            void* list[] = {&a...};
+            return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)grid),
+                                   dim3((unsigned)block), list, 0, s);
+        },
+        held);
+}
 
 #define DG_TRY(x)                    \
     do {                             \
@@ -817,8 +838,7 @@ hipError_t row_targets(const LossCall& c, const LossPlan& pl, RowSource* out)
         t.leader = reinterpret_cast<int*>(ws + pl.off_lead);
         t.flag = reinterpret_cast<int*>(ws + pl.off_flag);
         src.flag = t.flag;
-        loss_target_kernel<<<dim3((unsigned)c.T), dim3(64), 0, c.stream>>>(t);
-        DG_TRY(last());
+        DG_TRY(launch(loss_target_kernel, c.T, 64, c.stream, t));
     }
     return hipSuccess;
 }
@@ -829,8 +849,7 @@ hipError_t select_rows(const LossCall& c, const LossPlan& pl, const RowSource& s
     int* chunks = nullptr;
     if (c.T > kOwnCount) {
         chunks = reinterpret_cast<int*>(ws + pl.off_chunks);
-        loss_count_kernel<<<dim3((unsigned)cdiv(c.T, kChunk)), dim3(256), 0, c.stream>>>(src, c.T, chunks);
-        DG_TRY(last());
+        DG_TRY(launch(loss_count_kernel, cdiv(c.T, kChunk), 256, c.stream, src, c.T, chunks));
     }
     SelectArgs a;
     a.src = src;
@@ -853,8 +872,7 @@ hipError_t select_rows(const LossCall& c, const LossPlan& pl, const RowSource& s
     a.dloss_stride = c.dloss_stride;
     a.scale = c.scale;
     a.z_loss = c.z_loss;
-    loss_select_kernel<<<dim3((unsigned)cdiv(c.T, kSelRows)), dim3(256), 0, c.stream>>>(a);
-    return last();
+    return launch(loss_select_kernel, cdiv(c.T, kSelRows), 256, c.stream, a);
 }
 
 LossArgs product_args(const LossCall& c, const LossPlan& pl)
@@ -1015,8 +1033,7 @@ hipError_t loss_forward(const LossCall& c)
     j.lse = c.lse;
     auto join = [&](auto r) {
         constexpr int R = decltype(r)::value;
-        loss_join_kernel<R><<<dim3((unsigned)cdiv(c.T, R)), dim3(256), 0, c.stream>>>(j);
-        return last();
+        return launch(loss_join_kernel<R>, cdiv(c.T, R), 256, c.stream, j);
     };
     if (!few || !c.slots)
         DG_TRY(c.T >= 2048 ? join(std::integral_constant<int, 16>{})
@@ -1043,11 +1060,7 @@ hipError_t loss_forward(const LossCall& c)
     k.zlabel = a.zlabel;
     k.loss = c.loss;
     k.logp = c.logp;
-    if (few)
-        loss_pick_kernel<true><<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(k, j);
-    else
-        loss_pick_kernel<false><<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(k, j);
-    return last();
+    return launch(few ? loss_pick_kernel<true> : loss_pick_kernel<false>, c.T, 256, c.stream, k, j);
 }
 
 hipError_t loss_backward(const LossCall& c)
@@ -1112,8 +1125,7 @@ hipError_t loss_backward(const LossCall& c)
             k.ldg = pl.piece;
             k.half_b = half_b;
             k.lost = reinterpret_cast<float*>(ws + pl.off_q);
-            loss_sparse_kernel<<<dim3((unsigned)cdiv(c.T, 4)), dim3(256), 0, c.stream>>>(k);
-            DG_TRY(last());
+            DG_TRY(launch(loss_sparse_kernel, cdiv(c.T, 4), 256, c.stream, k));
         }
         if (c.dX) {
             LossArgs d = product_args(c, pl);
@@ -1170,8 +1182,8 @@ hipError_t loss_backward(const LossCall& c)
         d.dX = c.dX;
         d.lddx = c.lddx;
         d.D = c.D;
-        loss_dx_kernel<<<dim3((unsigned)c.T), dim3(256), 0, c.stream>>>(d);
-        DG_TRY(last());
+        d.vec = ((uintptr_t)c.dX & 7u) == 0 && c.lddx % 4 == 0;
+        DG_TRY(launch(loss_dx_kernel, c.T, 256, c.stream, d));
     }
     return hipSuccess;
 }

@@ -146,9 +146,9 @@ __device__ __forceinline__ float2 lse_merge(float2 a, float2 b)
     const float m = fmaxf(a.x, b.x);
     if (m == -INFINITY)
         return make_float2(m, a.y + b.y);
-    // 2^(reference - m): differences of integers; -inf converts to the least int
-    return make_float2(m, __builtin_amdgcn_ldexpf(a.y, (int)(a.x - m)) +
-                              __builtin_amdgcn_ldexpf(b.y, (int)(b.x - m)));
+    // 2^(reference - m): differences of integers, far below fp32's range at most
+    return make_float2(m, __builtin_amdgcn_ldexpf(a.y, (int)fmaxf(a.x - m, -4096.f)) +
+                              __builtin_amdgcn_ldexpf(b.y, (int)fmaxf(b.x - m, -4096.f)));
 }
 
 // A wave's (MR 16) x WCOLS block of accumulators as bf16 into rows of C from

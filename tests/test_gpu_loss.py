@@ -280,6 +280,15 @@ def test_no_rows():
     assert got["dW"].shape == (50, 64) and float(got["dW"].abs().sum()) == 0.0
 
 
+def test_most_rows():
+    """2^20 rows, a third of them out, in chunks of the row count."""
+    T, V, D = 1 << 20, 270, 8
+    X, W, lab = problem(T, V, D, 24)
+    lab[::3] = -100
+    dl = torch.full((1,), 1.0, device="cuda")
+    check(_run_ce(X, W, lab, dl), reference(X, W, labels=lab, dloss=dl), "2^20 rows")
+
+
 def test_repeats_bitwise_and_on_another_stream():
     T, V, D, k = 600, 11008, 136, 8
     X, W, lead = problem(T, V, D, 16)
@@ -294,6 +303,38 @@ def test_repeats_bitwise_and_on_another_stream():
     c = _run_di(X, W, idx, te, dl)
     for name in a:
         assert torch.equal(a[name], b[name]) and torch.equal(a[name], c[name]), name
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, at the same time:
+    the results of the calls one after the other."""
+    problems = []
+    for i, (T, V, D, k) in enumerate([(700, 9001, 264, 0), (300, 20011, 136, 7)]):
+        X, W, lead = problem(T, V, D, 40 + i)
+        tg = _slots(T, V, k, lead, 41) if k else (lead,)
+        run = _run_di if k else _run_ce
+        ws = torch.empty(dg.linear_loss_workspace_bytes(T, V, D, k, backward=True), dtype=torch.uint8,
+                         device="cuda")
+        dl = _dloss(T, 42)
+        want = run(X, W, *tg, dl)
+        problems.append((X, W, tg, dl, ws, bool(k), torch.cuda.Stream(), want))
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for i, (X, W, tg, dl, ws, di, s, _want) in enumerate(problems):
+            with torch.cuda.stream(s):
+                if di:
+                    loss, lse, logp = dg.linear_distillation(X, W, *tg, workspace=ws)
+                    dX, dW = dg.linear_distillation_grad(X, W, *tg, lse, logp, dl, workspace=ws)
+                    got[i] = dict(loss=loss, lse=lse, logp=logp, dX=dX, dW=dW)
+                else:
+                    loss, lse = dg.linear_cross_entropy(X, W, *tg, workspace=ws)
+                    dX, dW = dg.linear_cross_entropy_grad(X, W, *tg, loss, lse, dl, workspace=ws)
+                    got[i] = dict(loss=loss, lse=lse, dX=dX, dW=dW)
+    torch.cuda.synchronize()
+    for g, (*_rest, want) in zip(got, problems):
+        for name in want:
+            assert torch.equal(g[name], want[name]), name
 
 
 def test_captured_and_replayed():
