@@ -450,7 +450,10 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     // (with the rows in the elements they took 8 cross-lane steps for every row
     // of 4 values, and the log-sum-exp of a 256 x 256 tile 6 us), and the
     // stores take 8 or 16 bytes a lane.
-    auto output = [&](int m0, int n0, int rows, int slice, int parity) __attribute__((always_inline)) {
+    auto output = [&](int m0, int n0, int rows, int slice, int parity, bool idle)
+                      __attribute__((always_inline)) {
+    if (ROLE != ROLE_LSE && idle)
+        return;
     // the lane again, as a value of its own: what the outputs derive from it
     // would otherwise be kept in registers through the K loop
     int ol = lane;
@@ -531,10 +534,12 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                     red[wn * TM + r] = make_float2(none ? -INFINITY : m, s);
             }
         };
-        if (col_w + S::WCOLS <= p.N)
+        if (idle) {
+        } else if (col_w + S::WCOLS <= p.N) {
             rows_of(std::true_type{});
-        else
+        } else {
             rows_of(std::false_type{});
+        }
         // LDS only: the next item's loads stay in flight
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
@@ -625,6 +630,8 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     }
     };
 
+    auto nothing = [](int, int, int, int, int) {};
+
     // The first k-tiles of an item, and its rows' RowInfo (by LDS DMA too, so
     // that nothing waits for it before the first barrier; rows past n: zeros,
     // which reach no row that is kept).
@@ -645,8 +652,15 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
 #pragma unroll
             for (int j = 0; j < NR; ++j)
                 acc[mi][j] = zero_acc<AT>();
-        k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, min(nkt, last_full - kt0), load,
-                                                                read, mma);
+        // Waves whose rows all lie past the last one only load and keep the
+        // barriers' count: a row of tiles is half empty on average.
+        const bool idle = ROLE != ROLE_DW && (int)row0 >= rows;
+        if (!idle)
+            k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, min(nkt, last_full - kt0),
+                                                                    load, read, mma);
+        else
+            k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, min(nkt, last_full - kt0),
+                                                                    load, nothing, nothing);
         // the next item's loads go out before this one's outputs
         const int o_m0 = m0, o_n0 = n0, o_rows = rows, o_slice = slice;
         item += (int)gridDim.x;
@@ -655,7 +669,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
             set_item(item);
             preload(parity ^ 1);
         }
-        output(o_m0, o_n0, o_rows, o_slice, parity);
+        output(o_m0, o_n0, o_rows, o_slice, parity, idle);
         if (!more)
             break;
     }
