@@ -88,6 +88,11 @@ __device__ __forceinline__ void store16(rsrc_t r, uint32_t off, i32x4 v)
     __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, 0);
 }
 
+__device__ __forceinline__ void store16_nt(rsrc_t r, uint32_t off, i32x4 v)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, 2);
+}
+
 __device__ __forceinline__ void store4(rsrc_t r, uint32_t off, uint32_t v)
 {
     __builtin_amdgcn_raw_buffer_store_b32(v, r, (int)off, 0, 0);

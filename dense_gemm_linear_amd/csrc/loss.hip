@@ -558,7 +558,7 @@ __global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
 }
 
 // dX: the sum of the K slices' planes in slice order, rounded once; zero for
-// rows that are out.  Four columns a thread, four planes' loads in flight.
+// rows that are out.
 // A row of dX is often little more than one or two columns' worth of W, the
 // target's: what rounding G to bf16 took from those is added here in fp32, rest
 // times the column's row of W.  (Without it the roundings of G and of dX
@@ -579,12 +579,19 @@ struct DxArgs {
     int64_t lddx, D;
     int vec;                     // dX's rows start on 8 bytes
 };
+// A workgroup takes 1024 / P columns of a row, P threads each four of them: many
+// planes of few rows are summed by P threads side by side (48 rows of 2048 in
+// 24 planes: 14 us by one thread each).
+template <int P>
 __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
 {
+    constexpr int QUADS = 256 / P;
     __shared__ int col[kMaxLossSlots];
     __shared__ float rest[kMaxLossSlots];
     __shared__ int used[4];
-    const int64_t t = blockIdx.x;
+    __shared__ f32x4 sums[P > 1 ? 256 : 1];
+    const int blocks = (int)((p.D + 4 * QUADS - 1) / (4 * QUADS));
+    const int64_t t = blockIdx.x / blocks;
     const int at = p.pos[t];
     int n = 0;
     if (at >= 0) {
@@ -617,40 +624,52 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
         }
     }
     __syncthreads();
-    for (int64_t d = threadIdx.x * 4; d < p.D; d += 1024) {
-        f32x4 s = {0.f, 0.f, 0.f, 0.f};
-        if (at >= 0) {
-            const float* from = p.planes + at * p.ldplane + d;
-            for (int i = 0; i < p.splits; i += 4) {
-                f32x4 v[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    v[u] = i + u < p.splits ? *reinterpret_cast<const f32x4*>(from + (i + u) * p.plane)
-                                            : f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    s += v[u];
-            }
-            for (int i = 0; i < n; ++i) {
-                const uint2 w = *reinterpret_cast<const uint2*>(p.W + col[i] * p.ldw + d);
-                const float r = rest[i];
-                s[0] = fmaf(r, __uint_as_float(w.x << 16), s[0]);
-                s[1] = fmaf(r, __uint_as_float(w.x & 0xFFFF0000u), s[1]);
-                s[2] = fmaf(r, __uint_as_float(w.y << 16), s[2]);
-                s[3] = fmaf(r, __uint_as_float(w.y & 0xFFFF0000u), s[3]);
-            }
-        }
-        const float s0 = s[0], s1 = s[1], s2 = s[2], s3 = s[3];
-        const uint16_t o[4] = {bf16_rne(s0), bf16_rne(s1), bf16_rne(s2), bf16_rne(s3)};
-        uint16_t* to = p.dX + t * p.lddx + d;
-        if (p.vec) {
-            *reinterpret_cast<uint2*>(to) =
-                make_uint2((uint32_t)o[0] | (uint32_t)o[1] << 16, (uint32_t)o[2] | (uint32_t)o[3] << 16);
-        } else {
+    const int part = threadIdx.x / QUADS;
+    const int64_t d = (int64_t)(blockIdx.x % blocks) * 4 * QUADS + threadIdx.x % QUADS * 4;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (at >= 0 && d < p.D) {
+        const float* from = p.planes + at * p.ldplane + d;
+        for (int i = part; i < p.splits; i += 4 * P) {
+            f32x4 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                to[u] = o[u];
+                v[u] = i + u * P < p.splits ? *reinterpret_cast<const f32x4*>(from + (i + u * P) * p.plane)
+                                            : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                s += v[u];
         }
+    }
+    if constexpr (P > 1) {
+        sums[threadIdx.x] = s;
+        __syncthreads();
+        if (part != 0)
+            return;
+        for (int u = 1; u < P; ++u)
+            s += sums[threadIdx.x + u * QUADS];
+    }
+    if (d >= p.D)
+        return;
+    if (at >= 0) {
+        for (int i = 0; i < n; ++i) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p.W + col[i] * p.ldw + d);
+            const float r = rest[i];
+            s[0] = fmaf(r, __uint_as_float(w.x << 16), s[0]);
+            s[1] = fmaf(r, __uint_as_float(w.x & 0xFFFF0000u), s[1]);
+            s[2] = fmaf(r, __uint_as_float(w.y << 16), s[2]);
+            s[3] = fmaf(r, __uint_as_float(w.y & 0xFFFF0000u), s[3]);
+        }
+    }
+    const float s0 = s[0], s1 = s[1], s2 = s[2], s3 = s[3];
+    const uint16_t o[4] = {bf16_rne(s0), bf16_rne(s1), bf16_rne(s2), bf16_rne(s3)};
+    uint16_t* to = p.dX + t * p.lddx + d;
+    if (p.vec) {
+        *reinterpret_cast<uint2*>(to) =
+            make_uint2((uint32_t)o[0] | (uint32_t)o[1] << 16, (uint32_t)o[2] | (uint32_t)o[3] << 16);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            to[u] = o[u];
     }
 }
 
@@ -780,12 +799,12 @@ hipError_t go(const LossArgs& a, int64_t tiles_m, int cus, hipStream_t s)
 template <int ROLE, bool FEW = false>
 hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipStream_t s)
 {
-    // (few rows' LSE has a launch of its own)
-    if constexpr (ROLE == ROLE_GRAD || ROLE == ROLE_DX) {
+    // (few rows' logits have launches of their own)
+    if constexpr (ROLE == ROLE_DX) {
         if (shape == SHAPE_LOW)
-            return go<Low, ROLE>(a, cdiv(rows, Low::TM), cus, s);
+            return go<Low, ROLE, FEW>(a, cdiv(rows, Low::TM), cus, s);
         if (shape == SHAPE_FEW)
-            return go<Few, ROLE>(a, cdiv(rows, Few::TM), cus, s);
+            return go<Few, ROLE, FEW>(a, cdiv(rows, Few::TM), cus, s);
     }
     if (shape == SHAPE_BIG)
         return go<Big, ROLE, FEW>(a, cdiv(rows, Big::TM), cus, s);
@@ -943,8 +962,8 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
                     p.splits = sp;
                 }
             }
-        p.halves = T <= Line::TM;
-        p.off_g = take(p.rows_pad * piece * (p.halves ? 4 : 2));
+        p.few = T <= Line::TM;
+        p.off_g = take(p.rows_pad * piece * (p.few ? 4 : 2));
         p.off_planes = take((int64_t)p.splits * T * D * 4);
         p.bytes = std::max(p.bytes, at);
     }
@@ -1073,8 +1092,13 @@ hipError_t loss_backward(const LossCall& c)
     const int* pos = reinterpret_cast<const int*>(ws + pl.off_pos);
     const int* map = reinterpret_cast<const int*>(ws + pl.off_map);
     const RowInfo* rows = reinterpret_cast<const RowInfo*>(ws + pl.off_rows);
-    // few rows: G in two halves where dW is asked for
-    const int64_t half_b = pl.halves && c.dW ? pl.rows_pad * pl.piece * 2 : 0;
+    // few rows: G in two halves where dW is asked for; W past the Infinity Cache
+    // with the non-temporal hint (both gradients at 48 x 50257 x 4096, 412 MB: 275
+    // us against 302; 30 x 131072 x 4096: 562 against 635; but 48 x 50257 x 2048,
+    // 206 MB: 144 against 133)
+    const bool few = pl.few;
+    const int64_t half_b = few && c.dW ? pl.rows_pad * pl.piece * 2 : 0;
+    const int w_nt = few && c.V * c.D * 2 > (INT64_C(256) << 20);
     uint16_t* G = reinterpret_cast<uint16_t*>(ws + pl.off_g);
     const uint8_t* Xc = ws + pl.off_x;
     float* planes = reinterpret_cast<float*>(ws + pl.off_planes);
@@ -1082,7 +1106,7 @@ hipError_t loss_backward(const LossCall& c)
         const int64_t vp = std::min(pl.piece, c.V - v0);
         const uint8_t* W = reinterpret_cast<const uint8_t*>(c.W) + v0 * c.ldw * 2;
         RangePlan gp = plan_range(c.T, vp, c.D, 0, false, c.cus);
-        if (half_b)
+        if (few)
             gp = {c.T <= Low::TM ? SHAPE_LOW : c.T <= Few::TM ? SHAPE_FEW : SHAPE_LINE, 0, vp};
         for (int64_t u = 0; u < vp; u += gp.main) {
             const int shape = u == 0 ? gp.shape : gp.rest_shape;
@@ -1098,7 +1122,8 @@ hipError_t loss_backward(const LossCall& c)
             a.ldc = pl.piece;
             a.c_cols = (int)(pl.piece - u);
             a.half_b = half_b;
-            if (!half_b)
+            a.w_nt = w_nt;
+            if (!few)
                 DG_TRY(launch_role<ROLE_GRAD>(shape, a, c.T, c.cus, c.stream));
             else if (shape == SHAPE_LOW)
                 DG_TRY((go<Low, ROLE_GRAD, true>(a, 1, c.cus, c.stream)));
@@ -1140,7 +1165,11 @@ hipError_t loss_backward(const LossCall& c)
             d.plane = c.T * c.D;
             d.ldplane = c.D;
             d.first = v0 == 0;
-            DG_TRY(launch_role<ROLE_DX>(pl.dx_shape, d, c.T, c.cus, c.stream));
+            d.w_nt = w_nt;
+            if (w_nt)
+                DG_TRY((launch_role<ROLE_DX, true>(pl.dx_shape, d, c.T, c.cus, c.stream)));
+            else
+                DG_TRY(launch_role<ROLE_DX>(pl.dx_shape, d, c.T, c.cus, c.stream));
         }
         if (c.dW) {
             const RangePlan wp = plan_range(c.T, vp, half_b ? 2 * c.T : c.T, c.D, true, c.cus);
@@ -1155,6 +1184,12 @@ hipError_t loss_backward(const LossCall& c)
                 d.C = c.dW + (v0 + u) * c.lddw;
                 d.ldc = c.lddw;
                 d.c_vec = ((uintptr_t)c.dW & 15u) == 0 && c.lddw % 8 == 0;
+                // With few rows dW is bound by writing it; past half of the
+                // Infinity Cache the non-temporal hint helps (48 x 50257 x 2048,
+                // 206 MB: 112 us against 130), below it does not (1 x 50257 x
+                // 1024, 103 MB: 47 against 43).
+                if (half_b && d.c_vec && c.V * c.D * 2 > (INT64_C(128) << 20))
+                    d.c_vec = 2;
                 d.half_b = half_b;
                 const int shape = u == 0 ? wp.shape : wp.rest_shape;
                 if (half_b)
@@ -1183,7 +1218,10 @@ hipError_t loss_backward(const LossCall& c)
         d.lddx = c.lddx;
         d.D = c.D;
         d.vec = ((uintptr_t)c.dX & 7u) == 0 && c.lddx % 4 == 0;
-        DG_TRY(launch(loss_dx_kernel, c.T, 256, c.stream, d));
+        if (c.T <= Line::TM && pl.splits >= 8)
+            DG_TRY(launch(loss_dx_kernel<8>, c.T * cdiv(c.D, 128), 256, c.stream, d));
+        else
+            DG_TRY(launch(loss_dx_kernel<1>, c.T * cdiv(c.D, 1024), 256, c.stream, d));
     }
     return hipSuccess;
 }

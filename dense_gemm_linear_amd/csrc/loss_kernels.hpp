@@ -66,7 +66,8 @@ struct LossArgs {
     uint16_t* C;           // GRAD: G; DW: dW
     int c_cols;            // GRAD: columns of G from C on that may be written (whole tiles)
     int64_t ldc;
-    int c_vec;
+    int c_vec;             // DW: 1 C's rows take 16-byte stores, 2 and non-temporal ones
+    int w_nt;              // few rows, GRAD and DX: W with the non-temporal hint
     int64_t half_b;        // few rows, GRAD and DW: bytes from G to its second half
 };
 
@@ -155,7 +156,8 @@ __device__ __forceinline__ float2 lse_merge(float2 a, float2 b)
 // (row0, col_w) on, through its own LDS region, CH atom rows at a time: a lane
 // holds four consecutive columns (one 8-byte LDS write) and stores 16-byte
 // pieces of rows, or single elements where C's rows do not allow that.  Rows
-// past `rows` and columns past N are not stored.
+// past `rows` and columns past N are not stored.  c_vec: 16-byte pieces, 2 with
+// the non-temporal hint.
 template <int MR, int NR, int CH, int SROW>
 __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N, int c_vec,
                                                  const f32x4 (&acc)[MR][NR], uint8_t* stage, int m0,
@@ -188,7 +190,10 @@ __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N
                 const i32x4 v = *reinterpret_cast<const i32x4*>(stage + r * SROW + c * 2);
                 const uint32_t off = (uint32_t)(r0 + r) * pitch + (uint32_t)c * 2u;
                 // N is a multiple of 8 wherever c_vec is given
-                store16(rc, col_w + c < N ? off : kOOB, v);
+                if (c_vec == 2)
+                    store16_nt(rc, col_w + c < N ? off : kOOB, v);
+                else
+                    store16(rc, col_w + c < N ? off : kOOB, v);
             }
         } else {
             for (int q = lane; q < CH * 16 * WCOLS; q += 64) {
@@ -212,10 +217,11 @@ __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N
 //   DW    sums both: with few rows one element's rounding can make up most of
 //         a row of dW (over many rows such errors average), and the product is
 //         bound by writing dW, not by its K.
+//   GRAD, DX  load W with the non-temporal hint where it is larger than the
+//         Infinity Cache (w_nt), which then cannot hand it from one to the other.
 template <class S, int ROLE, bool FEW = false>
 __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs p)
 {
-    static_assert(!FEW || ROLE != ROLE_DX, "dX gets its rounding back row by row");
     constexpr bool FEWX = FEW && ROLE == ROLE_LSE;        // X not selected
     constexpr bool HALVES = FEW && ROLE == ROLE_DW;
     using AT = Atom<DT_BF16, 16>;
@@ -351,7 +357,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                 if (mask && (int)((uint32_t)kt * KTB + col) >= kb_end)
                     off = kOOB;
             }
-            if constexpr (decltype(nt)::value)
+            if (decltype(nt)::value && (FEWX || p.w_nt))
                 dma16_nt(r, dst, off, soff);
             else
                 dma16(r, dst, off, soff);
@@ -365,7 +371,8 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
         for (int i = 0; i < B_DMA; ++i)
             if ((A_DMA + i) % nparts == part)
                 one(rbt, base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i], b_col[i],
-                    std::integral_constant<bool, TRB>{}, std::integral_constant<bool, FEWX>{});
+                    std::integral_constant<bool, TRB>{},
+                    std::integral_constant<bool, FEW && ROLE != ROLE_DW>{});
     };
 
     // ---- fragments.  Plain: one 16-byte read, K values 8 lg .. 8 lg + 7 of
@@ -583,7 +590,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
         store_bf16_block<MR, NR, 1, S::SROW>(p.C, p.ldc, p.c_cols, 1, acc,
                                                  out_lds + wave * (R * S::SROW), m0, rows,
                                                  (int)row0, col_w, ol);
-        if constexpr (FEW) {
+        if (FEW && p.half_b) {
 #pragma unroll
             for (int mi = 0; mi < MR; ++mi)
 #pragma unroll
@@ -624,7 +631,8 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                 store16(rp, off[j], __builtin_bit_cast(i32x4, acc[mi][j]));
         }
     } else {
-        store_bf16_block<MR, NR, 1, S::SROW>(p.C, p.ldc, p.N, p.c_vec, acc,
+        // (only the few rows' instance has the non-temporal stores)
+        store_bf16_block<MR, NR, 1, S::SROW>(p.C, p.ldc, p.N, FEW ? p.c_vec : p.c_vec & 1, acc,
                                                  out_lds + wave * (R * S::SROW), m0, rows,
                                                  (int)row0, col_w, ol);
     }

@@ -15,6 +15,7 @@ pytestmark = pytest.mark.gpu
 SHAPES = [(1, 1, 8), (1, 50257, 64), (3, 7, 24), (17, 130, 64), (32, 1000, 136), (33, 257, 72),
           (130, 1003, 520), (257, 129, 40), (600, 5003, 136)]
 LARGE = [(48, 3001, 136), (64, 700, 64), (128, 900, 200),   # one tile of rows
+         (3, 70001, 1000), (40, 131072, 1032),    # dW and W past half and all of the Infinity Cache
          (600, 11008, 72),        # the 256 x 256 tiles
          (600, 23001, 520),       # whole rounds of them, and the rest apart
          (1100, 11001, 520),      # and for dX
