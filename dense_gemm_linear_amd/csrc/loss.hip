@@ -686,6 +686,9 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
 //         Against four of 64 bytes (Mid): 597 x 50257 x 4096 298 us : 357,
 //         100 x 50257 x 2048 41 : 46, 528 x 11007 x 1024 26 : 29.  Deeper
 //         rings of 64-byte k-tiles gained nothing (31 to 33 us there).
+//   Wide  for the logits where its tiles make one or two rounds: three stages of
+//         whole lines, one workgroup a CU (400 x 11008 x 1024 forward 21.7 us
+//         against 24.9 with Line, 300 x 30000 x 2048 48 against 55 with Big).
 //   Mid   for dX and dW, whose transposed operands are whole lines anyway.
 //   Few, Low  up to 64 and 32 rows, where the product is a read of W: the
 //         tile that just covers the rows keeps the most of it in flight (48 x
@@ -694,9 +697,10 @@ using Big = LossShape<256, 256, 2, 4, 4, 64, 1>;
 using Tall = LossShape<256, 128, 4, 2, 4, 64, 2>;
 using Mid = LossShape<128, 128, 2, 2, 4, 64, 2>;
 using Line = LossShape<128, 128, 2, 2, 2, 128, 2>;
+using Wide = LossShape<128, 192, 2, 4, 3, 128, 2>;
 using Few = LossShape<64, 128, 1, 4, 3, 128, 2>;
 using Low = LossShape<32, 128, 1, 4, 3, 128, 2>;
-enum { SHAPE_BIG = 0, SHAPE_TALL, SHAPE_MID, SHAPE_LINE, SHAPE_FEW, SHAPE_LOW };
+enum { SHAPE_BIG = 0, SHAPE_TALL, SHAPE_MID, SHAPE_LINE, SHAPE_WIDE, SHAPE_FEW, SHAPE_LOW };
 struct ShapeCost {
     int tm, tn, per_cu;
     double kt, kt1, epi;
@@ -705,6 +709,7 @@ constexpr ShapeCost kShapes[] = {{Big::TM, Big::TN, Big::PER_CU, 0.72, 0.72, 9.0
                                  {Tall::TM, Tall::TN, Tall::PER_CU, 0.48, 0.48, 4.5},
                                  {Mid::TM, Mid::TN, Mid::PER_CU, 0.64, 0.50, 0.5},
                                  {Line::TM, Line::TN, Line::PER_CU, 0.56, 0.47, 1.0},
+                                 {Wide::TM, Wide::TN, Wide::PER_CU, 0.36, 0.32, 2.0},
                                  {Few::TM, Few::TN, Few::PER_CU, 0.5, 0.4, 2.0},
                                  {Low::TM, Low::TN, Low::PER_CU, 0.5, 0.4, 2.0}};
 constexpr int kPlanCus = 256;            // the workspace must not depend on the device
@@ -728,7 +733,7 @@ int pick_shape(bool logits, int64_t rows, int64_t cols, int64_t k, int cus)
     if (logits && rows <= Few::TM)
         return rows <= Low::TM ? SHAPE_LOW : SHAPE_FEW;
     int best = SHAPE_BIG;
-    for (int i : {(int)SHAPE_TALL, logits ? (int)SHAPE_LINE : (int)SHAPE_MID})
+    for (int i : {SHAPE_TALL, logits ? SHAPE_LINE : SHAPE_MID, logits ? SHAPE_WIDE : SHAPE_MID})
         if (product_us(i, rows, cols, k, 1, cus) < product_us(best, rows, cols, k, 1, cus))
             best = i;
     return best;
@@ -810,6 +815,10 @@ hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipS
         return go<Big, ROLE, FEW>(a, cdiv(rows, Big::TM), cus, s);
     if (shape == SHAPE_TALL)
         return go<Tall, ROLE, FEW>(a, cdiv(rows, Tall::TM), cus, s);
+    if constexpr (ROLE == ROLE_LSE || ROLE == ROLE_GRAD) {
+        if (shape == SHAPE_WIDE)
+            return go<Wide, ROLE, FEW>(a, cdiv(rows, Wide::TM), cus, s);
+    }
     using Other = std::conditional_t<ROLE == ROLE_LSE || ROLE == ROLE_GRAD, Line, Mid>;
     return go<Other, ROLE, FEW>(a, cdiv(rows, Other::TM), cus, s);
 }

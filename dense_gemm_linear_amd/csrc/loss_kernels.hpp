@@ -186,7 +186,9 @@ __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N
         if (c_vec) {
 #pragma unroll
             for (int q0 = 0; q0 < CH * 16 * PPR; q0 += 64) {
-                const int q = q0 + lane, r = q / PPR, c = q % PPR * 8;
+                // (past the last piece: the last one again)
+                const int q = CH * 16 * PPR % 64 == 0 ? q0 + lane : min(q0 + lane, CH * 16 * PPR - 1);
+                const int r = q / PPR, c = q % PPR * 8;
                 const i32x4 v = *reinterpret_cast<const i32x4*>(stage + r * SROW + c * 2);
                 const uint32_t off = (uint32_t)(r0 + r) * pitch + (uint32_t)c * 2u;
                 // N is a multiple of 8 wherever c_vec is given

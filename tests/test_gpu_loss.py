@@ -17,6 +17,7 @@ SHAPES = [(1, 1, 8), (1, 50257, 64), (3, 7, 24), (17, 130, 64), (32, 1000, 136),
 LARGE = [(48, 3001, 136), (64, 700, 64), (128, 900, 200),   # one tile of rows
          (3, 70001, 1000), (40, 131072, 1032),    # dW and W past half and all of the Infinity Cache
          (600, 11008, 72),        # the 256 x 256 tiles
+         (400, 11007, 136), (300, 30011, 72),     # 128 x 192 tiles
          (600, 23001, 520),       # whole rounds of them, and the rest apart
          (1100, 11001, 520),      # and for dX
          (8192, 5003, 64), (20000, 7001, 16)]     # rows counted in chunks, two pieces of the vocabulary
