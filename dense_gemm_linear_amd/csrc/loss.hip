@@ -552,8 +552,9 @@ __global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
         *at = bf16_rne(g * d);
         if (p.half_b)
             at[p.half_b / 2] = bf16_rne(bf16_rest(g * d));
-        // columns below 1/64 leave less than 2^-14 of the row's weight
-        p.lost[i] = fabsf(d) >= 0.015625f ? bf16_rest(g * d) : 0.f;
+        // (smaller columns only make up a row together, at least sixteen of
+        // them, and their errors average)
+        p.lost[i] = fabsf(d) >= 0.0625f ? bf16_rest(g * d) : 0.f;
     }
 }
 
@@ -566,8 +567,9 @@ __global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
 // makes up a row.)
 struct DxArgs {
     const float* planes;
-    int splits;
-    int64_t plane, ldplane;
+    DxSlices slices;
+    const int* n_kept;
+    int64_t ldplane;
     const int* pos;
     const RowInfo* rows;
     const uint16_t* W;
@@ -628,16 +630,37 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
     const int64_t d = (int64_t)(blockIdx.x % blocks) * 4 * QUADS + threadIdx.x % QUADS * 4;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     if (at >= 0 && d < p.D) {
+        const int kept = *p.n_kept, slices = p.slices.count(kept);
+        const int64_t plane = kept * p.ldplane;
         const float* from = p.planes + at * p.ldplane + d;
-        for (int i = part; i < p.splits; i += 4 * P) {
+        for (int i = part; i < slices; i += 4 * P) {
             f32x4 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                v[u] = i + u * P < p.splits ? *reinterpret_cast<const f32x4*>(from + (i + u * P) * p.plane)
-                                            : f32x4{0.f, 0.f, 0.f, 0.f};
+                v[u] = i + u * P < slices ? *reinterpret_cast<const f32x4*>(from + (i + u * P) * plane)
+                                          : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 s += v[u];
+        }
+        for (int i = part; i < n; i += 4 * P) {
+            uint2 w[4];
+            float r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int at_i = min(i + u * P, n - 1);
+                r[u] = i + u * P < n ? rest[at_i] : 0.f;
+                w[u] = *reinterpret_cast<const uint2*>(p.W + col[at_i] * p.ldw + d);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (i + u * P >= n)
+                    continue;
+                s[0] = fmaf(r[u], __uint_as_float(w[u].x << 16), s[0]);
+                s[1] = fmaf(r[u], __uint_as_float(w[u].x & 0xFFFF0000u), s[1]);
+                s[2] = fmaf(r[u], __uint_as_float(w[u].y << 16), s[2]);
+                s[3] = fmaf(r[u], __uint_as_float(w[u].y & 0xFFFF0000u), s[3]);
+            }
         }
     }
     if constexpr (P > 1) {
@@ -650,16 +673,6 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
     }
     if (d >= p.D)
         return;
-    if (at >= 0) {
-        for (int i = 0; i < n; ++i) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p.W + col[i] * p.ldw + d);
-            const float r = rest[i];
-            s[0] = fmaf(r, __uint_as_float(w.x << 16), s[0]);
-            s[1] = fmaf(r, __uint_as_float(w.x & 0xFFFF0000u), s[1]);
-            s[2] = fmaf(r, __uint_as_float(w.y << 16), s[2]);
-            s[3] = fmaf(r, __uint_as_float(w.y & 0xFFFF0000u), s[3]);
-        }
-    }
     const float s0 = s[0], s1 = s[1], s2 = s[2], s3 = s[3];
     const uint16_t o[4] = {bf16_rne(s0), bf16_rne(s1), bf16_rne(s2), bf16_rne(s3)};
     uint16_t* to = p.dX + t * p.lddx + d;
@@ -689,18 +702,29 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
 //   Wide  for the logits where its tiles make one or two rounds: three stages of
 //         whole lines, one workgroup a CU (400 x 11008 x 1024 forward 21.7 us
 //         against 24.9 with Line, 300 x 30000 x 2048 48 against 55 with Big).
+//   Deep  for the logits where its tiles make one round: four stages of whole
+//         lines (215 x 9904 x 3832 forward 48 us against 54 with Wide).
 //   Mid   for dX and dW, whose transposed operands are whole lines anyway.
 //   Few, Low  up to 64 and 32 rows, where the product is a read of W: the
 //         tile that just covers the rows keeps the most of it in flight (48 x
 //         50257 x 4096, W cold: 141 us against 153 to 159 of the others).
+//   Slim, FewSlim, LowSlim  for up to 128, 64 and 32 rows of vocabularies that
+//         make no full round of the 128-column tiles: 64 columns and deeper
+//         rings (121 x 10399 x 3272 forward 41 us against 66, 48 x 16000 x 4096
+//         31 : 41, 1 x 5000 x 4096 19 : 31).
 using Big = LossShape<256, 256, 2, 4, 4, 64, 1>;
 using Tall = LossShape<256, 128, 4, 2, 4, 64, 2>;
 using Mid = LossShape<128, 128, 2, 2, 4, 64, 2>;
 using Line = LossShape<128, 128, 2, 2, 2, 128, 2>;
 using Wide = LossShape<128, 192, 2, 4, 3, 128, 2>;
+using Deep = LossShape<128, 128, 2, 2, 4, 128, 1>;
+using Slim = LossShape<128, 64, 2, 2, 6, 128, 1>;
+using FewSlim = LossShape<64, 64, 1, 4, 4, 128, 2>;
+using LowSlim = LossShape<32, 64, 1, 4, 5, 128, 2>;
 using Few = LossShape<64, 128, 1, 4, 3, 128, 2>;
 using Low = LossShape<32, 128, 1, 4, 3, 128, 2>;
-enum { SHAPE_BIG = 0, SHAPE_TALL, SHAPE_MID, SHAPE_LINE, SHAPE_WIDE, SHAPE_FEW, SHAPE_LOW };
+enum { SHAPE_BIG = 0, SHAPE_TALL, SHAPE_MID, SHAPE_LINE, SHAPE_WIDE, SHAPE_DEEP, SHAPE_FEW, SHAPE_LOW,
+       SHAPE_SLIM, SHAPE_FEW_SLIM, SHAPE_LOW_SLIM };
 struct ShapeCost {
     int tm, tn, per_cu;
     double kt, kt1, epi;
@@ -710,8 +734,12 @@ constexpr ShapeCost kShapes[] = {{Big::TM, Big::TN, Big::PER_CU, 0.72, 0.72, 9.0
                                  {Mid::TM, Mid::TN, Mid::PER_CU, 0.64, 0.50, 0.5},
                                  {Line::TM, Line::TN, Line::PER_CU, 0.56, 0.47, 1.0},
                                  {Wide::TM, Wide::TN, Wide::PER_CU, 0.36, 0.32, 2.0},
+                                 {Deep::TM, Deep::TN, Deep::PER_CU, 0.30, 0.29, 2.0},
                                  {Few::TM, Few::TN, Few::PER_CU, 0.5, 0.4, 2.0},
-                                 {Low::TM, Low::TN, Low::PER_CU, 0.5, 0.4, 2.0}};
+                                 {Low::TM, Low::TN, Low::PER_CU, 0.5, 0.4, 2.0},
+                                 {Slim::TM, Slim::TN, Slim::PER_CU, 0.3, 0.3, 2.0},
+                                 {FewSlim::TM, FewSlim::TN, FewSlim::PER_CU, 0.3, 0.3, 2.0},
+                                 {LowSlim::TM, LowSlim::TN, LowSlim::PER_CU, 0.3, 0.3, 2.0}};
 constexpr int kPlanCus = 256;            // the workspace must not depend on the device
 constexpr double kLaunchUs = 5.0;        // a further launch, start to start
 constexpr double kPlaneBytesPerUs = 2.0e6;
@@ -726,16 +754,26 @@ double product_us(int shape, int64_t rows, int64_t cols, int64_t k, int splits, 
     return full * (kts * s.kt + s.epi) + (left ? kts * (left > cus ? s.kt : s.kt1) + s.epi : 0.0);
 }
 
-// Shape of a product whose outputs are rows x cols: by the row count where it
-// is small (not for dW: its rows are W's), else by the estimate.
+// Shape of the logits of few rows (one tile of them).
+int few_shape(int64_t rows, int64_t cols, int cus)
+{
+    if (rows <= Low::TM)
+        return cols <= (int64_t)LowSlim::TN * LowSlim::PER_CU * cus ? SHAPE_LOW_SLIM : SHAPE_LOW;
+    if (rows <= Few::TM)
+        return cols <= (int64_t)FewSlim::TN * FewSlim::PER_CU * cus ? SHAPE_FEW_SLIM : SHAPE_FEW;
+    return cols <= (int64_t)Slim::TN * cus ? SHAPE_SLIM : cols <= (int64_t)Deep::TN * cus ? SHAPE_DEEP
+                                                                                        : SHAPE_LINE;
+}
+
+// Shape of a product whose outputs are rows x cols, by the estimate.
 int pick_shape(bool logits, int64_t rows, int64_t cols, int64_t k, int cus)
 {
-    if (logits && rows <= Few::TM)
-        return rows <= Low::TM ? SHAPE_LOW : SHAPE_FEW;
+    constexpr int kLogits[] = {SHAPE_TALL, SHAPE_LINE, SHAPE_WIDE, SHAPE_DEEP};
+    constexpr int kOthers[] = {SHAPE_TALL, SHAPE_MID};
     int best = SHAPE_BIG;
-    for (int i : {SHAPE_TALL, logits ? SHAPE_LINE : SHAPE_MID, logits ? SHAPE_WIDE : SHAPE_MID})
-        if (product_us(i, rows, cols, k, 1, cus) < product_us(best, rows, cols, k, 1, cus))
-            best = i;
+    for (const int* i = logits ? kLogits : kOthers; i != (logits ? kLogits + 4 : kOthers + 2); ++i)
+        if (product_us(*i, rows, cols, k, 1, cus) < product_us(best, rows, cols, k, 1, cus))
+            best = *i;
     return best;
 }
 
@@ -760,8 +798,6 @@ RangePlan plan_range(int64_t t, int64_t v, int64_t k, int64_t other, bool by_row
     RangePlan p;
     p.shape = p.rest_shape = pick(v);
     p.main = v;
-    if (p.shape >= SHAPE_FEW)
-        return p;
     double best = us(p.shape, v);
     const ShapeCost& b = kShapes[SHAPE_BIG];
     const int64_t across = by_rows ? cdiv(other, b.tn) : cdiv(t, b.tm);
@@ -788,11 +824,7 @@ hipError_t go(const LossArgs& a, int64_t tiles_m, int cus, hipStream_t s)
 {
     LossArgs copy = a;
     copy.tiles_n = (int)cdiv(a.N, S::TN);
-    if constexpr (ROLE == ROLE_DX) {
-        const int nkt = (int)cdiv(a.K, S::KT);
-        copy.kt_per = (int)cdiv(nkt, a.splits);
-    }
-    const int64_t items = tiles_m * copy.tiles_n * (ROLE == ROLE_DX ? a.splits : 1);
+    const int64_t items = tiles_m * copy.tiles_n * (ROLE == ROLE_DX ? a.slices.most : 1);
     if (items > INT32_MAX)
         return hipErrorInvalidValue;
     const int64_t grid = std::min<int64_t>(items, (int64_t)cus * S::PER_CU);
@@ -817,10 +849,33 @@ hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipS
         return go<Tall, ROLE, FEW>(a, cdiv(rows, Tall::TM), cus, s);
     if constexpr (ROLE == ROLE_LSE || ROLE == ROLE_GRAD) {
         if (shape == SHAPE_WIDE)
-            return go<Wide, ROLE, FEW>(a, cdiv(rows, Wide::TM), cus, s);
+            return go<Wide, ROLE>(a, cdiv(rows, Wide::TM), cus, s);
+        if (shape == SHAPE_DEEP)
+            return go<Deep, ROLE>(a, cdiv(rows, Deep::TM), cus, s);
     }
     using Other = std::conditional_t<ROLE == ROLE_LSE || ROLE == ROLE_GRAD, Line, Mid>;
     return go<Other, ROLE, FEW>(a, cdiv(rows, Other::TM), cus, s);
+}
+
+// The logits of few rows.
+template <int ROLE>
+hipError_t launch_few(int shape, const LossArgs& a, int cus, hipStream_t s)
+{
+    switch (shape) {
+    case SHAPE_LOW_SLIM:
+        return go<LowSlim, ROLE, true>(a, 1, cus, s);
+    case SHAPE_LOW:
+        return go<Low, ROLE, true>(a, 1, cus, s);
+    case SHAPE_FEW_SLIM:
+        return go<FewSlim, ROLE, true>(a, 1, cus, s);
+    case SHAPE_FEW:
+        return go<Few, ROLE, true>(a, 1, cus, s);
+    case SHAPE_SLIM:
+        return go<Slim, ROLE, true>(a, 1, cus, s);
+    case SHAPE_DEEP:
+        return go<Deep, ROLE, true>(a, 1, cus, s);
+    }
+    return go<Line, ROLE, true>(a, 1, cus, s);
 }
 
 // Launches a kernel; the status of this launch, not an earlier sticky error.
@@ -910,7 +965,6 @@ LossArgs product_args(const LossCall& c, const LossPlan& pl)
     a.n_kept = reinterpret_cast<const int*>(c.ws + pl.off_count);
     a.rows = reinterpret_cast<const RowInfo*>(c.ws + pl.off_rows);
     a.scale = c.scale;
-    a.splits = 1;
     return a;
 }
 
@@ -941,7 +995,7 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
         p.off_flag = take(T * 8);
     }
     const int64_t shared = at;
-    p.tiles_n_max = cdiv(V, 128);
+    p.tiles_n_max = cdiv(V, T <= Line::TM ? 64 : 128);
     p.off_part = take(p.tiles_n_max * p.rows_pad * 8);
     p.off_zlabel = take(p.rows_pad * 4);
     p.bytes = at;
@@ -1023,9 +1077,8 @@ hipError_t loss_forward(const LossCall& c)
     a.part = reinterpret_cast<float2*>(ws + pl.off_part);
     a.ldpart = pl.rows_pad;
     a.zlabel = reinterpret_cast<float*>(ws + pl.off_zlabel);
-    RangePlan rp = plan_range(c.T, c.V, c.D, 0, false, c.cus);
-    if (few)
-        rp = {c.T <= Low::TM ? SHAPE_LOW : c.T <= Few::TM ? SHAPE_FEW : SHAPE_LINE, 0, c.V};
+    const RangePlan rp = few ? RangePlan{few_shape(c.T, c.V, c.cus), 0, c.V}
+                             : plan_range(c.T, c.V, c.D, 0, false, c.cus);
     int64_t tiles = 0;                       // tile columns so far
     for (int64_t v0 = 0; v0 < c.V; v0 += rp.main) {
         const int shape = v0 == 0 ? rp.shape : rp.rest_shape;
@@ -1034,14 +1087,8 @@ hipError_t loss_forward(const LossCall& c)
         m.N = (int)(v0 == 0 ? rp.main : c.V - v0);
         m.B = a.B + v0 * a.ldb_b;
         m.part = a.part + tiles * a.ldpart;
-        if (c.T <= Low::TM)
-            DG_TRY((go<Low, ROLE_LSE, true>(m, 1, c.cus, c.stream)));
-        else if (c.T <= Few::TM)
-            DG_TRY((go<Few, ROLE_LSE, true>(m, 1, c.cus, c.stream)));
-        else if (few)
-            DG_TRY((go<Line, ROLE_LSE, true>(m, 1, c.cus, c.stream)));
-        else
-            DG_TRY(launch_role<ROLE_LSE>(shape, m, c.T, c.cus, c.stream));
+        DG_TRY(few ? launch_few<ROLE_LSE>(shape, m, c.cus, c.stream)
+                   : launch_role<ROLE_LSE>(shape, m, c.T, c.cus, c.stream));
         tiles += cdiv(m.N, kShapes[shape].tn);
         if (v0 != 0)
             break;
@@ -1109,14 +1156,21 @@ hipError_t loss_backward(const LossCall& c)
     const int64_t half_b = few && c.dW ? pl.rows_pad * pl.piece * 2 : 0;
     const int w_nt = few && c.V * c.D * 2 > (INT64_C(256) << 20);
     uint16_t* G = reinterpret_cast<uint16_t*>(ws + pl.off_g);
+    const ShapeCost& dxs = kShapes[pl.dx_shape];
+    DxSlices slices;
+    slices.S = pl.splits;
+    slices.T = (int)c.T;
+    slices.tm = dxs.tm;
+    slices.tiles_n = (int)cdiv(c.D, dxs.tn);
+    slices.workgroups = c.cus * dxs.per_cu;
+    slices.most = (int)std::max<int64_t>(pl.splits, pl.piece / 256);
     const uint8_t* Xc = ws + pl.off_x;
     float* planes = reinterpret_cast<float*>(ws + pl.off_planes);
     for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
         const int64_t vp = std::min(pl.piece, c.V - v0);
         const uint8_t* W = reinterpret_cast<const uint8_t*>(c.W) + v0 * c.ldw * 2;
-        RangePlan gp = plan_range(c.T, vp, c.D, 0, false, c.cus);
-        if (few)
-            gp = {c.T <= Low::TM ? SHAPE_LOW : c.T <= Few::TM ? SHAPE_FEW : SHAPE_LINE, 0, vp};
+        const RangePlan gp = few ? RangePlan{few_shape(c.T, vp, c.cus), 0, vp}
+                                 : plan_range(c.T, vp, c.D, 0, false, c.cus);
         for (int64_t u = 0; u < vp; u += gp.main) {
             const int shape = u == 0 ? gp.shape : gp.rest_shape;
             LossArgs a = product_args(c, pl);
@@ -1132,14 +1186,8 @@ hipError_t loss_backward(const LossCall& c)
             a.c_cols = (int)(pl.piece - u);
             a.half_b = half_b;
             a.w_nt = w_nt;
-            if (!few)
-                DG_TRY(launch_role<ROLE_GRAD>(shape, a, c.T, c.cus, c.stream));
-            else if (shape == SHAPE_LOW)
-                DG_TRY((go<Low, ROLE_GRAD, true>(a, 1, c.cus, c.stream)));
-            else if (shape == SHAPE_FEW)
-                DG_TRY((go<Few, ROLE_GRAD, true>(a, 1, c.cus, c.stream)));
-            else
-                DG_TRY((go<Line, ROLE_GRAD, true>(a, 1, c.cus, c.stream)));
+            DG_TRY(few ? launch_few<ROLE_GRAD>(shape, a, c.cus, c.stream)
+                       : launch_role<ROLE_GRAD>(shape, a, c.T, c.cus, c.stream));
             if (u != 0)
                 break;
         }
@@ -1169,9 +1217,8 @@ hipError_t loss_backward(const LossCall& c)
             d.ldb_b = c.ldw * 2;
             d.N = (int)c.D;
             d.K = (int)vp;
-            d.splits = pl.splits;
+            d.slices = slices;
             d.planes = planes;
-            d.plane = c.T * c.D;
             d.ldplane = c.D;
             d.first = v0 == 0;
             d.w_nt = w_nt;
@@ -1181,7 +1228,8 @@ hipError_t loss_backward(const LossCall& c)
                 DG_TRY(launch_role<ROLE_DX>(pl.dx_shape, d, c.T, c.cus, c.stream));
         }
         if (c.dW) {
-            const RangePlan wp = plan_range(c.T, vp, half_b ? 2 * c.T : c.T, c.D, true, c.cus);
+            const RangePlan wp = few ? RangePlan{SHAPE_MID, 0, vp}
+                                     : plan_range(c.T, vp, c.T, c.D, true, c.cus);
             for (int64_t u = 0; u < vp; u += wp.main) {
                 LossArgs d = product_args(c, pl);
                 d.A = reinterpret_cast<const uint8_t*>(G + u);
@@ -1201,10 +1249,8 @@ hipError_t loss_backward(const LossCall& c)
                     d.c_vec = 2;
                 d.half_b = half_b;
                 const int shape = u == 0 ? wp.shape : wp.rest_shape;
-                if (half_b)
-                    DG_TRY((launch_role<ROLE_DW, true>(shape, d, d.M, c.cus, c.stream)));
-                else
-                    DG_TRY(launch_role<ROLE_DW>(shape, d, d.M, c.cus, c.stream));
+                DG_TRY((few ? go<Mid, ROLE_DW, true>(d, cdiv(d.M, Mid::TM), c.cus, c.stream)
+                            : launch_role<ROLE_DW>(shape, d, d.M, c.cus, c.stream)));
                 if (u != 0)
                     break;
             }
@@ -1213,8 +1259,8 @@ hipError_t loss_backward(const LossCall& c)
     if (c.dX) {
         DxArgs d;
         d.planes = planes;
-        d.splits = pl.splits;
-        d.plane = c.T * c.D;
+        d.slices = slices;
+        d.n_kept = reinterpret_cast<const int*>(ws + pl.off_count);
         d.ldplane = c.D;
         d.pos = pos;
         d.rows = rows;

@@ -42,6 +42,23 @@ struct RowInfo {
     int label;    // column of W, -1: none
 };
 
+// K slices of dX.  The workspace holds S planes of T rows; where only n of the
+// rows are kept, the same memory holds S T / n planes of n, and the workgroups
+// that the missing tiles would leave idle take further slices (652 rows kept of
+// 6520: the slices chosen for 6520 rows left five sixths of the CUs without work).
+struct DxSlices {
+    int S, T;
+    int tm, tiles_n;       // tile rows, tile columns
+    int workgroups;        // that run at once
+    int most;              // slices of at least 8 k-tiles
+    __device__ __forceinline__ int count(int n) const
+    {
+        const int tiles = (n + tm - 1) / tm * tiles_n;
+        const int64_t room = (int64_t)S * T / max(n, 1);
+        return max(S, min(most, (int)min(room, (int64_t)(workgroups / max(tiles, 1)))));
+    }
+};
+
 struct LossArgs {
     const uint8_t* A;      // X compact [n, lda] (LSE, GRAD), G [n, lda] (DX, DW)
     const uint8_t* B;      // W [., ldb] from the piece's first row (LSE, GRAD, DX), X compact (DW)
@@ -52,15 +69,14 @@ struct LossArgs {
     const int* lead;       // columns of their largest targets, [n][2]; A is X itself then
     int M, N, K;           // M: DW only (the piece's rows of W); K: not for DW (n)
     int tiles_n;
-    int splits, kt_per;    // DX: K slices, k-tiles per slice
+    DxSlices slices;       // DX
     float scale;
     const RowInfo* rows;
     float2* part;          // LSE: [tiles_n][ldpart] (reference, sum)
     int64_t ldpart;
     float* zlabel;         // LSE: the label's sum over d, with scale's sign; compact rows
     int v0;                // LSE, GRAD: the vocabulary's column of B's first row
-    float* planes;         // DX: [splits][plane_rows][ldplane]
-    int64_t plane;         // elements of one plane
+    float* planes;         // DX: [slices][n][ldplane]
     int64_t ldplane;
     int first;             // DX: the first piece writes, later ones add
     uint16_t* C;           // GRAD: G; DW: dW
@@ -244,7 +260,8 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     // A persistent grid: workgroup b takes items b, b + gridDim, ...  The grid
     // is sized for every row of X; n may be less.
     const int tiles = tiles_m * p.tiles_n;
-    const int items = ROLE == ROLE_DX ? tiles * p.splits : tiles;
+    const int nslices = ROLE == ROLE_DX ? p.slices.count(n) : 1;
+    const int items = tiles * nslices;
     int item = (int)blockIdx.x;
     if (item >= items)
         return;
@@ -312,8 +329,9 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
         rows = min(TM, M - m0);
         int k_end = K;
         if constexpr (ROLE == ROLE_DX) {
-            kt0 = slice * p.kt_per;
-            const int kt_end = min(all_kt, kt0 + p.kt_per);
+            const int kt_per = (all_kt + nslices - 1) / nslices;
+            kt0 = slice * kt_per;
+            const int kt_end = min(all_kt, kt0 + kt_per);
             nkt = max(0, kt_end - kt0);
             k_end = min(K, kt_end * KT);
         }
@@ -607,7 +625,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                                                  (int)row0, col_w, ol);
         }
     } else if constexpr (ROLE == ROLE_DX) {
-        float* plane = p.planes + (int64_t)slice * p.plane + (int64_t)m0 * p.ldplane + n0;
+        float* plane = p.planes + ((int64_t)slice * n + m0) * p.ldplane + n0;
         const rsrc_t rp = make_rsrc(plane, (uint32_t)(((int64_t)(rows - 1) * p.ldplane + (p.N - n0)) * 4));
         const uint32_t pitch = (uint32_t)p.ldplane * 4u;
 #pragma unroll

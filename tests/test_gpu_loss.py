@@ -15,6 +15,8 @@ pytestmark = pytest.mark.gpu
 SHAPES = [(1, 1, 8), (1, 50257, 64), (3, 7, 24), (17, 130, 64), (32, 1000, 136), (33, 257, 72),
           (130, 1003, 520), (257, 129, 40), (600, 5003, 136)]
 LARGE = [(48, 3001, 136), (64, 700, 64), (128, 900, 200),   # one tile of rows
+         (1, 40000, 264), (20, 33000, 72), (60, 40000, 72), (100, 17000, 200), (110, 40000, 72),  # one tile of rows
+         (215, 9904, 264),        # 128 x 128 tiles of whole lines
          (3, 70001, 1000), (40, 131072, 1032),    # dW and W past half and all of the Infinity Cache
          (600, 11008, 72),        # the 256 x 256 tiles
          (400, 11007, 136), (300, 30011, 72),     # 128 x 192 tiles
@@ -93,7 +95,8 @@ def test_scale_and_z_loss(scale, z_loss):
           reference(X, W, labels=lab, dloss=dl, scale=scale, z_loss=z_loss), f"scale {scale} z {z_loss}")
 
 
-@pytest.mark.parametrize("T,V,D", [(30, 500, 72), (64, 500, 72), (127, 500, 72), (130, 1003, 136), (600, 11008, 72)])
+@pytest.mark.parametrize("T,V,D", [(30, 500, 72), (64, 500, 72), (127, 500, 72), (130, 1003, 136), (600, 11008, 72),
+                                   (3000, 5003, 264)])
 @pytest.mark.parametrize("keep", [0.0, 0.03, 0.5])
 @pytest.mark.parametrize("kind", ["ce", "distill"])
 def test_rows_out(T, V, D, keep, kind):
@@ -181,7 +184,7 @@ def test_gradients_of_few_targets_are_rounded_once(T, V, D, k):
         worst["dW"] = once * float(ref["dW"].norm())
     for name, bound in worst.items():
         err = float((got[name].double() - ref[name]).norm())
-        # 5 %: fp32 sums, and targets below 1/64
+        # 5 %: fp32 sums, and targets below 1/16
         assert err <= 1.05 * bound, f"{name}: {err:.3e} against {bound:.3e}"
 
 
