@@ -220,12 +220,12 @@ struct JoinArgs {
     float* lse;
 };
 
-// Joins the tile columns' (reference, sum) pairs of one row (in the threads of
-// q = 0) by 256 threads, R rows in all; red: 256 pairs of LDS.
-template <int R>
+// Joins the tile columns' (reference, sum) pairs of one row by a workgroup of
+// THREADS, R rows in all; red: a pair of LDS for each thread.
+template <int R, int THREADS = 256>
 __device__ __forceinline__ float2 join_row(const JoinArgs& p, int row, bool valid, float2* red)
 {
-    constexpr int Q = 256 / R;
+    constexpr int Q = THREADS / R;
     const int q = threadIdx.x / R;
     float2 acc = make_float2(-INFINITY, 0.f);
     if (valid)
@@ -318,10 +318,15 @@ struct TargetArgs {
 
 __global__ __launch_bounds__(64) void loss_target_kernel(TargetArgs p)
 {
-    __shared__ int idx[kMaxLossSlots];
-    __shared__ float qs[kMaxLossSlots];
+    __shared__ __attribute__((aligned(16))) int idx[kMaxLossSlots];
+    __shared__ __attribute__((aligned(16))) float qs[kMaxLossSlots];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x;
+    const int k4 = (p.k + 3) / 4;
+    if (lane < 4 * k4 - p.k) {               // fill the last group of four
+        idx[p.k + lane] = -2;
+        qs[p.k + lane] = 0.f;
+    }
     float m = -INFINITY;
     bool bad = false, any = false;
     for (int j = lane; j < p.k; j += 64) {
@@ -373,11 +378,20 @@ __global__ __launch_bounds__(64) void loss_target_kernel(TargetArgs p)
         const int me = idx[j];
         bool first = me >= 0;
         float rest = 0.f, sum = 0.f;
-        for (int i = 0; i < p.k; ++i) {
-            const bool same = idx[i] == me;
-            first = first && !(same && i < j);
-            rest += same ? 0.f : qs[i];
-            sum += same ? qs[i] : 0.f;
+        // every slot against every other, four to an LDS read (one at a time,
+        // 106 slots took 21 us)
+#pragma unroll 4
+        for (int i = 0; i < k4; ++i) {
+            const i32x4 c = reinterpret_cast<const i32x4*>(idx)[i];
+            const f32x4 v = reinterpret_cast<const f32x4*>(qs)[i];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool same = c[u] == me;
+                const float x = v[u];
+                first = first && !(same && 4 * i + u < j);
+                rest += same ? 0.f : x;
+                sum += same ? x : 0.f;
+            }
         }
         p.q[t * p.k + j] = qs[j];
         p.qsum[t * p.k + j] = sum;
@@ -418,21 +432,23 @@ __device__ __forceinline__ float dot8(i32x4 a, i32x4 b, float s)
 }
 
 // The student's log-probabilities at a row's slots, and the row's loss: a
-// workgroup of 4 waves a row, four slots at a time a wave, each a dot product of the
-// row of X with the slot's row of W.  JOIN (few rows): the row's join here too,
-// instead of in a launch of its own.
+// workgroup a row, four slots at a time a wave, each a dot product of the row of
+// X with the slot's row of W.  JOIN (few rows): the row's join here too, instead
+// of in a launch of its own, and 16 waves instead of 4, as few workgroups leave
+// the CUs to them (56 rows of 100 slots, D = 2656: 42 us with 4).
 template <bool JOIN>
-__global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p, JoinArgs jn)
+__global__ __launch_bounds__(JOIN ? 1024 : 256) void loss_pick_kernel(PickArgs p, JoinArgs jn)
 {
+    constexpr int THREADS = JOIN ? 1024 : 256;
     __shared__ float z[kMaxLossSlots];
-    __shared__ float2 red[JOIN ? 256 : 1];
+    __shared__ float2 red[JOIN ? THREADS : 1];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     // few rows: none moved
     const int at = p.pos ? p.pos[t] : p.flag[2 * t] == ROW_OUT ? -1 : (int)t;
     float* out = p.logp + t * p.k;
     if (at < 0) {
-        for (int j = threadIdx.x; j < p.k; j += 256)
+        for (int j = threadIdx.x; j < p.k; j += THREADS)
             out[j] = 0.f;
         if (JOIN && threadIdx.x == 0)
             p.loss[t] = jn.lse[t] = 0.f;
@@ -440,10 +456,10 @@ __global__ __launch_bounds__(256) void loss_pick_kernel(PickArgs p, JoinArgs jn)
     }
     float2 joined = make_float2(0.f, 0.f);
     if constexpr (JOIN)
-        joined = join_row<1>(jn, (int)t, true, red);
+        joined = join_row<1, THREADS>(jn, (int)t, true, red);
     const uint8_t* x = p.Xc + at * p.ldx_b;
     const int lead = p.flag[2 * t + 1];
-    for (int j0 = 4 * wave; j0 < p.k; j0 += 16) {
+    for (int j0 = 4 * wave; j0 < p.k; j0 += THREADS / 16) {
         const uint8_t* w[4];
         int use[4];
 #pragma unroll
@@ -1135,7 +1151,8 @@ hipError_t loss_forward(const LossCall& c)
     k.zlabel = a.zlabel;
     k.loss = c.loss;
     k.logp = c.logp;
-    return launch(few ? loss_pick_kernel<true> : loss_pick_kernel<false>, c.T, 256, c.stream, k, j);
+    return few ? launch(loss_pick_kernel<true>, c.T, 1024, c.stream, k, j)
+               : launch(loss_pick_kernel<false>, c.T, 256, c.stream, k, j);
 }
 
 hipError_t loss_backward(const LossCall& c)
