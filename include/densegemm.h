@@ -487,8 +487,8 @@ gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void
  * with X the hidden rows [T, D] and W the nn.Linear weight [V, D], bf16, sums
  * in fp32.  The entry points below take losses from z, and the gradients of X
  * and W, without storing z: the forward pass keeps one pair of floats per row
- * and 128 or 256 columns, the gradient one piece of the vocabulary at a time
- * (at most 256 MiB of bf16, or 256 columns), recomputed from X and W.
+ * and 64 to 256 columns, the gradient one piece of the vocabulary at a time (at
+ * most 256 MiB of bf16, or 256 columns), recomputed from X and W.
  *
  * Rows that are out -- an ignored label, no filled target slot -- have loss
  * 0, lse 0 and gradient 0, take no part in the products, and whatever their X
@@ -507,8 +507,10 @@ gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void
  *   dX  device bf16 [T, lddx], dW device bf16 [V, lddw], 2-byte aligned,
  *       pitches at least D; NULL leaves that gradient out (not both).  Every
  *       element of the T x D / V x D region is overwritten, nothing else is.
- *       Rounded once, to nearest even, from fp32 sums; the logits' gradient
- *       they are products of is rounded to bf16 first.
+ *       Rounded to nearest even from fp32 sums; the logits' gradient they are
+ *       products of is rounded to bf16 first, which is made good for dX's target
+ *       columns and for dW of at most 128 rows.  They must not overlap the
+ *       inputs or each other.
  *   workspace  device, 256-byte aligned, at least
  *       linear_loss_workspace_bytes(T, V, D, slots, backward) bytes (slots 0
  *       for cross entropy; backward 1 also serves the forward call).  Its
