@@ -597,9 +597,11 @@ struct DxArgs {
     int64_t lddx, D;
     int vec;                     // dX's rows start on 8 bytes
 };
-// A workgroup takes 1024 / P columns of a row, P threads each four of them: many
-// planes of few rows are summed by P threads side by side (48 rows of 2048 in
-// 24 planes: 14 us by one thread each).
+// P > 1: a workgroup takes 1024 / P columns of a row, and P threads share the
+// planes of each four of them (few rows in many planes: 48 x 2048 in 24 took 14
+// us by one thread, 56 x 2656 takes 4.9 by eight).  P = 1: a workgroup a row (4096
+// x 4096 in 2 planes takes 28 us; 39 where 1024 columns were a workgroup each,
+// which all read the row's targets again).
 template <int P>
 __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
 {
@@ -608,7 +610,7 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
     __shared__ float rest[kMaxLossSlots];
     __shared__ int used[4];
     __shared__ f32x4 sums[P > 1 ? 256 : 1];
-    const int blocks = (int)((p.D + 4 * QUADS - 1) / (4 * QUADS));
+    const int blocks = P > 1 ? (int)((p.D + 4 * QUADS - 1) / (4 * QUADS)) : 1;
     const int64_t t = blockIdx.x / blocks;
     const int at = p.pos[t];
     int n = 0;
@@ -643,62 +645,69 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
     }
     __syncthreads();
     const int part = threadIdx.x / QUADS;
-    const int64_t d = (int64_t)(blockIdx.x % blocks) * 4 * QUADS + threadIdx.x % QUADS * 4;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    if (at >= 0 && d < p.D) {
-        const int kept = *p.n_kept, slices = p.slices.count(kept);
-        const int64_t plane = kept * p.ldplane;
-        const float* from = p.planes + at * p.ldplane + d;
-        for (int i = part; i < slices; i += 4 * P) {
-            f32x4 v[4];
+    const int kept = *p.n_kept, slices = p.slices.count(kept);
+    const int64_t plane = kept * p.ldplane;
+    auto columns = [&](int64_t d) {
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        if (at >= 0 && d < p.D) {
+            const float* from = p.planes + at * p.ldplane + d;
+            for (int i = part; i < slices; i += 4 * P) {
+                f32x4 v[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                v[u] = i + u * P < slices ? *reinterpret_cast<const f32x4*>(from + (i + u * P) * plane)
-                                          : f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int u = 0; u < 4; ++u)
+                    v[u] = i + u * P < slices ? *reinterpret_cast<const f32x4*>(from + (i + u * P) * plane)
+                                              : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                s += v[u];
-        }
-        for (int i = part; i < n; i += 4 * P) {
-            uint2 w[4];
-            float r[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int at_i = min(i + u * P, n - 1);
-                r[u] = i + u * P < n ? rest[at_i] : 0.f;
-                w[u] = *reinterpret_cast<const uint2*>(p.W + col[at_i] * p.ldw + d);
+                for (int u = 0; u < 4; ++u)
+                    s += v[u];
             }
+            for (int i = part; i < n; i += 4 * P) {
+                uint2 w[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (i + u * P >= n)
-                    continue;
-                s[0] = fmaf(r[u], __uint_as_float(w[u].x << 16), s[0]);
-                s[1] = fmaf(r[u], __uint_as_float(w[u].x & 0xFFFF0000u), s[1]);
-                s[2] = fmaf(r[u], __uint_as_float(w[u].y << 16), s[2]);
-                s[3] = fmaf(r[u], __uint_as_float(w[u].y & 0xFFFF0000u), s[3]);
+                for (int u = 0; u < 4; ++u)
+                    if (i + u * P < n)
+                        w[u] = *reinterpret_cast<const uint2*>(p.W + col[i + u * P] * p.ldw + d);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (i + u * P >= n)
+                        continue;
+                    const float r = rest[i + u * P];
+                    s[0] = fmaf(r, __uint_as_float(w[u].x << 16), s[0]);
+                    s[1] = fmaf(r, __uint_as_float(w[u].x & 0xFFFF0000u), s[1]);
+                    s[2] = fmaf(r, __uint_as_float(w[u].y << 16), s[2]);
+                    s[3] = fmaf(r, __uint_as_float(w[u].y & 0xFFFF0000u), s[3]);
+                }
             }
         }
-    }
-    if constexpr (P > 1) {
-        sums[threadIdx.x] = s;
-        __syncthreads();
-        if (part != 0)
+        if constexpr (P > 1) {
+            sums[threadIdx.x] = s;
+            __syncthreads();
+            if (part != 0)
+                return;
+            for (int u = 1; u < P; ++u)
+                s += sums[threadIdx.x + u * QUADS];
+        }
+        if (d >= p.D)
             return;
-        for (int u = 1; u < P; ++u)
-            s += sums[threadIdx.x + u * QUADS];
-    }
-    if (d >= p.D)
-        return;
-    const float s0 = s[0], s1 = s[1], s2 = s[2], s3 = s[3];
-    const uint16_t o[4] = {bf16_rne(s0), bf16_rne(s1), bf16_rne(s2), bf16_rne(s3)};
-    uint16_t* to = p.dX + t * p.lddx + d;
-    if (p.vec) {
-        *reinterpret_cast<uint2*>(to) =
-            make_uint2((uint32_t)o[0] | (uint32_t)o[1] << 16, (uint32_t)o[2] | (uint32_t)o[3] << 16);
-    } else {
+        const float s0 = s[0], s1 = s[1], s2 = s[2], s3 = s[3];
+        const uint16_t o[4] = {bf16_rne(s0), bf16_rne(s1), bf16_rne(s2), bf16_rne(s3)};
+        uint16_t* to = p.dX + t * p.lddx + d;
+        if (p.vec) {
+            *reinterpret_cast<uint2*>(to) =
+                make_uint2((uint32_t)o[0] | (uint32_t)o[1] << 16, (uint32_t)o[2] | (uint32_t)o[3] << 16);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            to[u] = o[u];
+            for (int u = 0; u < 4; ++u)
+                to[u] = o[u];
+        }
+    };
+    // one group of columns a workgroup where the planes are shared out, else
+    // the whole row
+    if constexpr (P > 1) {
+        columns((int64_t)(blockIdx.x % blocks) * 4 * QUADS + threadIdx.x % QUADS * 4);
+    } else {
+        for (int64_t d = threadIdx.x * 4; d < p.D; d += 1024)
+            columns(d);
     }
 }
 
@@ -1179,7 +1188,7 @@ hipError_t loss_backward(const LossCall& c)
     slices.T = (int)c.T;
     slices.tm = dxs.tm;
     slices.tiles_n = (int)cdiv(c.D, dxs.tn);
-    slices.workgroups = c.cus * dxs.per_cu;
+    slices.items = (int)(cdiv(c.T, dxs.tm) * slices.tiles_n * pl.splits);
     slices.most = (int)std::max<int64_t>(pl.splits, pl.piece / 256);
     const uint8_t* Xc = ws + pl.off_x;
     float* planes = reinterpret_cast<float*>(ws + pl.off_planes);
@@ -1293,7 +1302,7 @@ hipError_t loss_backward(const LossCall& c)
         if (c.T <= Line::TM && pl.splits >= 8)
             DG_TRY(launch(loss_dx_kernel<8>, c.T * cdiv(c.D, 128), 256, c.stream, d));
         else
-            DG_TRY(launch(loss_dx_kernel<1>, c.T * cdiv(c.D, 1024), 256, c.stream, d));
+            DG_TRY(launch(loss_dx_kernel<1>, c.T, 256, c.stream, d));
     }
     return hipSuccess;
 }

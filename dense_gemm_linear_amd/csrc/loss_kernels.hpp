@@ -43,19 +43,19 @@ struct RowInfo {
 };
 
 // K slices of dX.  The workspace holds S planes of T rows; where only n of the
-// rows are kept, the same memory holds S T / n planes of n, and the workgroups
-// that the missing tiles would leave idle take further slices (652 rows kept of
-// 6520: the slices chosen for 6520 rows left five sixths of the CUs without work).
+// rows are kept, the same memory holds S T / n planes of n, and further slices
+// take the place of the missing tiles (652 rows kept of 6520: the slices chosen
+// for 6520 rows left five sixths of the CUs without work).
 struct DxSlices {
     int S, T;
     int tm, tiles_n;       // tile rows, tile columns
-    int workgroups;        // that run at once
+    int items;             // tiles x S of all T rows
     int most;              // slices of at least 8 k-tiles
     __device__ __forceinline__ int count(int n) const
     {
         const int tiles = (n + tm - 1) / tm * tiles_n;
         const int64_t room = (int64_t)S * T / max(n, 1);
-        return max(S, min(most, (int)min(room, (int64_t)(workgroups / max(tiles, 1)))));
+        return max(S, min(most, (int)min(room, (int64_t)(items / max(tiles, 1)))));
     }
 };
 
