@@ -774,7 +774,7 @@ def linear_cross_entropy_grad(X, W, labels, loss, lse, dloss, *, scale: float = 
     for the same arguments and dloss (float32, [T] or one value) the gradient
     with respect to each row's loss.  Returns (dX, dW), bf16, None for one that
     is not needed (need_dX, need_dW); dX / dW: views to write instead of new
-    tensors."""
+    tensors, which must not overlap the inputs or each other."""
     torch = _torch()
     fn = "linear_cross_entropy_grad"
     _loss_operands(fn, X, W, (("labels", labels, torch.int64), ("loss", loss, torch.float32),

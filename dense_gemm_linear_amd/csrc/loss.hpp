@@ -17,6 +17,7 @@ struct LossPlan {
     int64_t tiles_n_max;         // forward: tile columns of the narrowest tile
     int64_t piece;               // backward: columns of the vocabulary at a time
     int dx_shape, splits;        // backward: tile shape and K slices of the dX product
+    int pair;                    // backward: K slices of dX where it shares a launch with dW, 0: never
     bool few;                    // backward: at most one tile of rows, G in two halves
     int64_t off_count, off_chunks, off_map, off_pos, off_rows, off_x;
     int64_t off_part, off_zlabel;                       // forward

@@ -237,8 +237,9 @@ __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N
 //         bound by writing dW, not by its K.
 //   GRAD, DX  load W with the non-temporal hint where it is larger than the
 //         Infinity Cache (w_nt), which then cannot hand it from one to the other.
-template <class S, int ROLE, bool FEW = false>
-__global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs p)
+// Workgroup `block` of `blocks`; lds: S::LDS bytes.
+template <class S, int ROLE, bool FEW>
+__device__ __forceinline__ void loss_product(const LossArgs& p, uint8_t* lds, int block, int blocks)
 {
     constexpr bool FEWX = FEW && ROLE == ROLE_LSE;        // X not selected
     constexpr bool HALVES = FEW && ROLE == ROLE_DW;
@@ -252,17 +253,16 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
     constexpr bool TRA = ROLE == ROLE_DW, TRB = ROLE == ROLE_DX || ROLE == ROLE_DW;
     static_assert(!TRA || TM >= 128, "a transposed operand's unit key needs 8 units a row");
     static_assert(!TRB || TN >= 128, "a transposed operand's unit key needs 8 units a row");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
 
     const int n = FEWX ? p.n : *p.n_kept;
     const int M = ROLE == ROLE_DW ? p.M : n;
     const int tiles_m = (M + TM - 1) / TM;
-    // A persistent grid: workgroup b takes items b, b + gridDim, ...  The grid
+    // A persistent grid: workgroup b takes items b, b + blocks, ...  The grid
     // is sized for every row of X; n may be less.
     const int tiles = tiles_m * p.tiles_n;
     const int nslices = ROLE == ROLE_DX ? p.slices.count(n) : 1;
     const int items = tiles * nslices;
-    int item = (int)blockIdx.x;
+    int item = block;
     if (item >= items)
         return;
 
@@ -691,7 +691,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
                                                                     load, nothing, nothing);
         // the next item's loads go out before this one's outputs
         const int o_m0 = m0, o_n0 = n0, o_rows = rows, o_slice = slice;
-        item += (int)gridDim.x;
+        item += blocks;
         const bool more = item < items;
         if (more) {
             set_item(item);
@@ -701,6 +701,25 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
         if (!more)
             break;
     }
+}
+
+template <class S, int ROLE, bool FEW = false>
+__global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+    loss_product<S, ROLE, FEW>(p, lds, (int)blockIdx.x, (int)gridDim.x);
+}
+
+// dX and dW of the vocabulary in one launch, the first x_blocks workgroups for
+// dX.  They share nothing but the G they read.
+template <class S>
+__global__ __launch_bounds__(S::THREADS, S::OCC) void loss_pair_kernel(LossArgs x, LossArgs w, int x_blocks)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+    if ((int)blockIdx.x < x_blocks)
+        loss_product<S, ROLE_DX, false>(x, lds, (int)blockIdx.x, x_blocks);
+    else
+        loss_product<S, ROLE_DW, false>(w, lds, (int)blockIdx.x - x_blocks, (int)gridDim.x - x_blocks);
 }
 
 }  // namespace dg

@@ -517,15 +517,16 @@ gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void
  *       contents on entry are ignored and on return unspecified; calls that
  *       share one must not overlap in time.
  *
- * Every sum has a fixed order: a call's results are bitwise repeatable.  All
+ * Every sum has a fixed order: a call's results are bitwise repeatable (dX with
+ * and without dW may differ in its last bit: the sums are cut differently).  All
  * work is enqueued on `stream`, without allocation, synchronisation or memset
  * nodes, and may be captured in a graph.
  *
  * Errors: INVALID_VALUE for a null, misaligned or too small argument, V or D
  * below 1, T below 0, a scale or z_loss that is not finite, dloss_count other
  * than 1 or T; UNSUPPORTED for D % 8 != 0, D > 65536, T > 2^20, V > 2^24,
- * slots > 256 or a pitch above 2^21 elements; HIP.  T == 0: no row, no launch
- * but the zeros of dW; only W is looked at then.
+ * slots > 256 or a pitch of X, W or dW above 2^21 elements; HIP.  T == 0: no
+ * row, no launch but the zeros of dW; only W is looked at then.
  *
  * linear_cross_entropy -- with one label a row,
  *     loss[t] = lse[t] - z[t][labels[t]] + z_loss * lse[t]^2

@@ -247,6 +247,26 @@ def test_pitches_and_untouched_padding(T, V, D, px, pw, pdx, pdw):
         assert bool((b == s).all()), "wrote outside the output"
 
 
+@pytest.mark.parametrize("T,V,D", [(100, 3001, 136),        # one tile of rows
+                                   (400, 11007, 136), (1100, 11001, 520),  # dX and dW in one launch
+                                   (300, 60001, 264), (8192, 5003, 64)])   # in two, in pieces
+@pytest.mark.parametrize("keep", [0.0, 0.3, 1.0])
+def test_each_gradient_alone(T, V, D, keep):
+    """Each gradient within its bounds when asked for alone and together."""
+    _say("alone", T, V, D, keep)
+    X, W, lab = problem(T, V, D, 16)
+    g = torch.Generator().manual_seed(17)
+    lab = torch.where((torch.rand(T, generator=g) < keep).cuda(), lab, -100)
+    dl = _dloss(T, 18)
+    ref = reference(X, W, labels=lab, dloss=dl)
+    loss, lse = dg.linear_cross_entropy(X, W, lab)
+    dX, _ = dg.linear_cross_entropy_grad(X, W, lab, loss, lse, dl, need_dW=False)
+    _, dW = dg.linear_cross_entropy_grad(X, W, lab, loss, lse, dl, need_dX=False)
+    check(dict(dX=dX, dW=dW), ref, "alone")
+    dX, dW = dg.linear_cross_entropy_grad(X, W, lab, loss, lse, dl)
+    check(dict(dX=dX, dW=dW), ref, "together")
+
+
 def test_one_gradient_one_weight_and_workspace_reuse():
     T, V, D, k = 130, 1003, 136, 6
     X, W, lead = problem(T, V, D, 14)
