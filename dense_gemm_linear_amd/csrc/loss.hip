@@ -884,7 +884,7 @@ hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipS
 
 // dX and dW of the vocabulary in one launch, half of the workgroups for each.  In
 // launches of their own both mostly wait for memory, with one or two tiles a CU.
-template <class S>
+template <class S, bool FEW>
 hipError_t go_pair(const LossArgs& x, const LossArgs& w, int cus, hipStream_t s)
 {
     LossArgs xc = x, wc = w;
@@ -894,7 +894,7 @@ hipError_t go_pair(const LossArgs& x, const LossArgs& w, int cus, hipStream_t s)
     const int64_t w_items = cdiv(w.M, S::TM) * wc.tiles_n;
     const int64_t grid = half + std::min<int64_t>(w_items, (int64_t)cus * S::PER_CU - half);
     void* args[] = {&xc, &wc, &half};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&loss_pair_kernel<S>), dim3((unsigned)grid),
+    return hipLaunchKernel(reinterpret_cast<const void*>(&loss_pair_kernel<S, FEW>), dim3((unsigned)grid),
                            dim3(S::THREADS), args, 0, s);
 }
 
@@ -1072,9 +1072,12 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
         // at most 128 k-tiles: of 38 such sizes 37 then took 1 to 14 % less for
         // their gradients (400 x 11008 x 1024: 55.7 us, 50.1) and one 2 % more; with
         // longer slices 6 % less to 9 % more (148 x 57039 x 2896: 372, 405).
+        // Few rows, whose dW is stores more than sums: at most 16 k-tiles (14 of
+        // 38 sizes: 1 to 10 % less, 30 x 5000 x 512 30.5 us, 27.9; the others up
+        // to 13 % less, 1 x 43021 x 2160, and 9 % more, 100 x 11008 x 4096).
         const int64_t pair_tiles = cdiv(T, Mid::TM) * cdiv(D, Mid::TN);
         const int64_t pair_slices = std::min(kPlanCus / pair_tiles, piece / 256);
-        if (!p.few && V <= piece && pair_slices >= 1 && cdiv(cdiv(V, Mid::KT), pair_slices) <= 128)
+        if (V <= piece && pair_slices >= 1 && cdiv(cdiv(V, Mid::KT), pair_slices) <= (p.few ? 16 : 128))
             p.pair = (int)pair_slices;
         p.off_g = take(p.rows_pad * piece * (p.few ? 4 : 2));
         p.off_planes = take((int64_t)std::max(p.splits, p.pair) * T * D * 4);
@@ -1304,7 +1307,8 @@ hipError_t loss_backward(const LossCall& c)
                 d.half_b = half_b;
                 const int shape = u == 0 ? wp.shape : wp.rest_shape;
                 if (pair) {
-                    DG_TRY(go_pair<Mid>(dx, d, c.cus, c.stream));
+                    DG_TRY((few ? go_pair<Mid, true>(dx, d, c.cus, c.stream)
+                                : go_pair<Mid, false>(dx, d, c.cus, c.stream)));
                     break;
                 }
                 DG_TRY((few ? go<Mid, ROLE_DW, true>(d, cdiv(d.M, Mid::TM), c.cus, c.stream)
@@ -1331,7 +1335,7 @@ hipError_t loss_backward(const LossCall& c)
         d.lddx = c.lddx;
         d.D = c.D;
         d.vec = ((uintptr_t)c.dX & 7u) == 0 && c.lddx % 4 == 0;
-        if (c.T <= Line::TM && pl.splits >= 8)
+        if (c.T <= Line::TM && splits >= 8)
             DG_TRY(launch(loss_dx_kernel<8>, c.T * cdiv(c.D, 128), 256, c.stream, d));
         else
             DG_TRY(launch(loss_dx_kernel<1>, c.T, 256, c.stream, d));

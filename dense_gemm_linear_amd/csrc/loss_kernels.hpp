@@ -712,14 +712,14 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_gemm_kernel(LossArgs 
 
 // dX and dW of the vocabulary in one launch, the first x_blocks workgroups for
 // dX.  They share nothing but the G they read.
-template <class S>
+template <class S, bool FEW>
 __global__ __launch_bounds__(S::THREADS, S::OCC) void loss_pair_kernel(LossArgs x, LossArgs w, int x_blocks)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
     if ((int)blockIdx.x < x_blocks)
         loss_product<S, ROLE_DX, false>(x, lds, (int)blockIdx.x, x_blocks);
     else
-        loss_product<S, ROLE_DW, false>(w, lds, (int)blockIdx.x - x_blocks, (int)gridDim.x - x_blocks);
+        loss_product<S, ROLE_DW, FEW>(w, lds, (int)blockIdx.x - x_blocks, (int)gridDim.x - x_blocks);
 }
 
 }  // namespace dg

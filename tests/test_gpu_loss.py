@@ -247,7 +247,8 @@ def test_pitches_and_untouched_padding(T, V, D, px, pw, pdx, pdw):
         assert bool((b == s).all()), "wrote outside the output"
 
 
-@pytest.mark.parametrize("T,V,D", [(100, 3001, 136),        # one tile of rows
+@pytest.mark.parametrize("T,V,D", [(100, 3001, 136), (20, 5003, 264),      # one tile of rows, in
+                                   (100, 40000, 520),        # one launch and in two
                                    (400, 11007, 136), (1100, 11001, 520),  # dX and dW in one launch
                                    (300, 60001, 264), (8192, 5003, 64)])   # in two, in pieces
 @pytest.mark.parametrize("keep", [0.0, 0.3, 1.0])
