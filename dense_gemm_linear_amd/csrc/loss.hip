@@ -30,6 +30,12 @@ constexpr int kChunk = 1024;
 constexpr int64_t kOwnCount = 4096;
 constexpr int kSelRows = 4;      // rows one workgroup of the selection moves, one a wave
 
+// dW of more rows than one tile wants them in the order of their target's group
+// of columns (kRestCols).  Up to kOwnCount rows each workgroup counts, for its
+// rows, those that come before; of more, a table holds how many rows of each chunk
+// of kOwnCount lie in each group, and what lies in front of those (place).
+constexpr int kGroupPass = 4096; // groups one workgroup of that count holds in LDS
+
 // Row state: out, kept, or kept with a target outside the vocabulary (loss
 // and gradient NaN).
 enum { ROW_OUT = 0, ROW_KEPT = 1, ROW_BAD = 2 };
@@ -77,6 +83,9 @@ __device__ __forceinline__ float wave_max(float x)
     return x;
 }
 
+// What rounding took from a value kept in bf16.
+__device__ __forceinline__ float bf16_rest(float x) { return x - bf16_to_f32(bf16_rne(x)); }
+
 // Kept rows in [t0, t1), counted by a workgroup of 256 threads.
 __device__ __forceinline__ int count_kept(const RowSource& src, int64_t t0, int64_t t1, int* red)
 {
@@ -89,6 +98,78 @@ __device__ __forceinline__ int count_kept(const RowSource& src, int64_t t0, int6
         red[threadIdx.x >> 6] = c;
     __syncthreads();
     return red[0] + red[1] + red[2] + red[3];
+}
+
+// The group of a kept row's target (no target in the vocabulary: the first).
+__device__ __forceinline__ int row_group(int label) { return max(label, 0) / kRestCols; }
+
+// place[group][chunk]: kept rows of one chunk of kOwnCount rows in each group.
+// Integer sums in LDS: their order does not matter.
+__global__ __launch_bounds__(1024) void loss_group_count_kernel(RowSource src, int64_t T, int groups, int* place)
+{
+    __shared__ int found[kGroupPass];
+    const int64_t t0 = (int64_t)blockIdx.x * kOwnCount, t1 = min(T, t0 + kOwnCount);
+    const int g0 = blockIdx.y * kGroupPass, n = min(groups - g0, kGroupPass);
+    for (int g = threadIdx.x; g < n; g += 1024)
+        found[g] = 0;
+    __syncthreads();
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += 1024) {
+        int label;
+        const bool kept = row_state(src, t, label) != ROW_OUT;
+        const int g = row_group(label) - g0;
+        if (kept && g >= 0 && g < n)
+            atomicAdd(&found[g], 1);
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < n; g += 1024)
+        place[(int64_t)(g0 + g) * gridDim.x + blockIdx.x] = found[g];
+}
+
+// The counts -> what lies in front of them, by one workgroup, 8 a thread at a
+// time; and the groups' first rows.
+__global__ __launch_bounds__(1024) void loss_group_place_kernel(int* place, int64_t n, int chunks, int* group,
+                                                                int groups, int* n_kept)
+{
+    __shared__ int sums[16];
+    int before = 0;
+    for (int64_t i0 = 0; i0 < n; i0 += 8192) {
+        int v[8], mine = 0;
+        const int64_t i = i0 + (int64_t)threadIdx.x * 8;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            v[u] = i + u < n ? place[i + u] : 0;
+            mine += v[u];
+        }
+        int run = mine;                        // up to and with this lane
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(run, d);
+            run += (int)(threadIdx.x & 63) >= d ? o : 0;
+        }
+        if ((threadIdx.x & 63) == 63)
+            sums[threadIdx.x >> 6] = run;
+        __syncthreads();
+        int at = before + run - mine;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            at += w < (int)(threadIdx.x >> 6) ? sums[w] : 0;
+            before += sums[w];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (i + u < n) {
+                place[i + u] = at;
+                if ((i + u) % chunks == 0)
+                    group[(i + u) / chunks] = at;
+            }
+            at += v[u];
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        group[groups] = before;
+        *n_kept = before;
+    }
 }
 
 __global__ __launch_bounds__(256) void loss_count_kernel(RowSource src, int64_t T, int* chunks)
@@ -122,17 +203,80 @@ struct SelectArgs {
     const float* dloss;
     int64_t dloss_stride;
     float scale, z_loss;
+    // BY_GROUP
+    const int* place;            // [groups][chunks], or null: count them here
+    int n_chunks, groups;
+    int* group;                  // [groups + 1]: first rows
+    uint8_t* rest;               // G's columns of rests
+    int64_t rest_b;              // G's pitch
 };
 
 // 4 rows a workgroup: how many kept rows lie in front of them, each row's
-// place, what the row's gradient needs, and the copy of the kept rows.
+// place, what the row's gradient needs, and the copy of the kept rows.  BY_GROUP:
+// in the order of the targets' groups, and the rests of G there; without a table
+// the workgroups past those of the rows find the groups' first rows, four each.
+template <bool BY_GROUP>
 __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
 {
     __shared__ int red[4];
     __shared__ int place[kSelRows];
+    __shared__ int front[4][kSelRows + 1];
+    __shared__ uint32_t left[kSelRows];      // the row's rest, bf16, and its column in the group
+    __shared__ int column[kSelRows];
     const int64_t t0 = (int64_t)blockIdx.x * kSelRows;
-    int before;
-    if (p.chunks) {
+    int before = 0;
+    if constexpr (BY_GROUP) {
+        // rows that come before (group, row) of each of the four
+        const int64_t row_blocks = (p.T + kSelRows - 1) / kSelRows;
+        const bool firsts = (int64_t)blockIdx.x >= row_blocks;
+        int g[kSelRows], c[kSelRows + 1] = {0, 0, 0, 0, 0};
+        int64_t upto[kSelRows];
+#pragma unroll
+        for (int r = 0; r < kSelRows; ++r) {
+            if (firsts) {
+                g[r] = (int)((int64_t)blockIdx.x - row_blocks) * kSelRows + r;
+                upto[r] = 0;
+            } else {
+                int label = -1;
+                if (t0 + r < p.T)
+                    row_state(p.src, t0 + r, label);
+                g[r] = row_group(label);
+                upto[r] = t0 + r;
+            }
+        }
+        const int64_t c0 = p.place ? t0 / kOwnCount * kOwnCount : 0, c1 = p.place ? t0 + kSelRows : p.T;
+        for (int64_t t = c0 + threadIdx.x; t < min(p.T, c1); t += 256) {
+            int label;
+            const bool kept = row_state(p.src, t, label) != ROW_OUT;
+            const int at = row_group(label);
+#pragma unroll
+            for (int r = 0; r < kSelRows; ++r)
+                c[r] += kept && ((at == g[r] && t < upto[r]) || (!p.place && at < g[r]));
+            c[kSelRows] += kept;
+        }
+#pragma unroll
+        for (int r = 0; r <= kSelRows; ++r) {
+            c[r] = wave_sum(c[r]);
+            if ((threadIdx.x & 63) == 0)
+                front[threadIdx.x >> 6][r] = c[r];
+        }
+        __syncthreads();
+        const int r = threadIdx.x;
+        if (firsts) {
+            const int at = (int)((int64_t)blockIdx.x - row_blocks) * kSelRows + r;
+            if (r < kSelRows && at <= p.groups)
+                p.group[at] = front[0][r] + front[1][r] + front[2][r] + front[3][r];
+            return;
+        }
+        if (r < kSelRows) {
+            before = front[0][r] + front[1][r] + front[2][r] + front[3][r];
+            if (p.place)
+                before += p.place[(r == 0 ? g[0] : r == 1 ? g[1] : r == 2 ? g[2] : g[3]) * (int64_t)p.n_chunks +
+                                  t0 / kOwnCount];
+        }
+        if (r == 0 && blockIdx.x == 0 && !p.place)
+            *p.n_kept = front[0][kSelRows] + front[1][kSelRows] + front[2][kSelRows] + front[3][kSelRows];
+    } else if (p.chunks) {
         const int64_t c0 = t0 / kChunk;
         int c = 0;
         for (int64_t i = threadIdx.x; i < c0; i += 256)
@@ -152,7 +296,7 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
         int label = -1;
         const int st = mine ? row_state(p.src, t, label) : ROW_OUT;
         const uint64_t kept = __ballot(st != ROW_OUT);
-        const int at = before + __popcll(kept & ((1ull << threadIdx.x) - 1));
+        const int at = BY_GROUP ? before : before + __popcll(kept & ((1ull << threadIdx.x) - 1));
         if (mine) {
             place[threadIdx.x] = st != ROW_OUT ? at : -1;
             p.pos[t] = st != ROW_OUT ? at : -1;
@@ -174,6 +318,8 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
                     }
                     if (st == ROW_BAD)
                         ri.a = ri.b = NAN;
+                    if (BY_GROUP)
+                        left[threadIdx.x] = ri.label >= 0 ? bf16_rne(bf16_rest(ri.b)) : 0u;
                 }
                 if (p.zlabel)
                     p.zlabel[at] = NAN;        // stays for a target outside the vocabulary
@@ -184,13 +330,22 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
                 p.lse_out[t] = 0.f;
             }
         }
-        if (threadIdx.x == 0 && t0 + kSelRows >= p.T)
+        if (BY_GROUP && mine)
+            column[threadIdx.x] = max(label, 0) % kRestCols;
+        if (!BY_GROUP && threadIdx.x == 0 && t0 + kSelRows >= p.T)
             *p.n_kept = before + __popcll(kept);
     }
     __syncthreads();
     const int r = threadIdx.x >> 6;
     if (t0 + r >= p.T || place[r] < 0)
         return;
+    if constexpr (BY_GROUP) {
+        // (distillation's come with its sparse columns)
+        const int lane = threadIdx.x & 63, c = column[r];
+        const uint32_t v = left[r] << (c & 1) * 16;
+        const uint2 w = make_uint2(c / 4 == lane && !(c & 2) ? v : 0u, c / 4 == lane && c & 2 ? v : 0u);
+        *reinterpret_cast<uint2*>(p.rest + place[r] * p.rest_b + lane * 8) = w;
+    }
     const uint8_t* from = p.X + (t0 + r) * p.ldx_b;
     uint8_t* to = p.Xc + place[r] * p.row_b;
     for (int64_t b = (threadIdx.x & 63) * 16; b < p.row_b; b += 4096) {
@@ -302,7 +457,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(JoinArgs p)
 // row's filled slots; slots that name one column together count once, in the
 // first of them (the leader); the row's lead is the column of the largest q.
 // For a leader, rest = 1 - (its q) is the sum of the other slots' q, so that
-// p - q of a column that both sides are sure of keeps its digits.
+// p - q of a column that both sides are sure of keeps its digits.  With logp the lead
+// is the column of the largest |p - q|.
 struct TargetArgs {
     const int64_t* index;
     const float* teacher;
@@ -314,7 +470,28 @@ struct TargetArgs {
     float* rest;                 // [T][k]: 1 - qsum
     int* leader;                 // [T][k]: column, or -1: empty or not the first
     int* flag;                   // [T][2]: row state, lead column
+    const float* logp;           // gradient, dW of more rows: [T][k], else null
 };
+
+// p - q with q = 1 - rest: near p = q = 1 both sides are taken from 1.
+__device__ __forceinline__ float target_dz(float logp, float qsum, float rest)
+{
+    return rest < 0.5f ? expm1f(logp) + rest : expf(logp) - qsum;
+}
+
+// The wave's largest value and its slot, the lowest among equals.
+__device__ __forceinline__ void first_largest(float& best, int& slot)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const float ob = __shfl_xor(best, d);
+        const int os = __shfl_xor(slot, d);
+        if (ob > best || (ob == best && os < slot)) {
+            best = ob;
+            slot = os;
+        }
+    }
+}
 
 __global__ __launch_bounds__(64) void loss_target_kernel(TargetArgs p)
 {
@@ -361,18 +538,14 @@ __global__ __launch_bounds__(64) void loss_target_kernel(TargetArgs p)
             best = qs[j];
             slot = j;
         }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const float ob = __shfl_xor(best, d);
-        const int os = __shfl_xor(slot, d);
-        if (ob > best || (ob == best && os < slot)) {
-            best = ob;
-            slot = os;
-        }
-    }
+    first_largest(best, slot);
     if (lane == 0) {
         p.flag[2 * t] = !any ? ROW_OUT : bad ? ROW_BAD : ROW_KEPT;
         p.flag[2 * t + 1] = slot < p.k ? idx[slot] : -1;
+    }
+    if (p.logp) {
+        best = -1.f;
+        slot = p.k;
     }
     for (int j = lane; j < p.k; j += 64) {
         const int me = idx[j];
@@ -397,6 +570,18 @@ __global__ __launch_bounds__(64) void loss_target_kernel(TargetArgs p)
         p.qsum[t * p.k + j] = sum;
         p.rest[t * p.k + j] = rest;
         p.leader[t * p.k + j] = first ? me : -1;
+        if (p.logp && first) {
+            const float d = fabsf(target_dz(p.logp[t * p.k + j], sum, rest));
+            if (d > best) {
+                best = d;
+                slot = j;
+            }
+        }
+    }
+    if (p.logp) {
+        first_largest(best, slot);
+        if (lane == 0)
+            p.flag[2 * t + 1] = slot < p.k ? idx[slot] : -1;
     }
 }
 
@@ -532,9 +717,6 @@ __global__ __launch_bounds__(JOIN ? 1024 : 256) void loss_pick_kernel(PickArgs p
         p.loss[t] = p.flag[2 * t] == ROW_BAD ? NAN : part;
 }
 
-// What rounding took from a value kept in bf16.
-__device__ __forceinline__ float bf16_rest(float x) { return x - bf16_to_f32(bf16_rne(x)); }
-
 // Distillation: the sparse columns of the gradient piece, p - q in place of
 // p.  One wave a kept row.  What rounding them to bf16 takes away is kept for
 // dX where it counts (lost).
@@ -549,6 +731,8 @@ struct SparseArgs {
     uint16_t* G;
     int64_t ldg, half_b;         // half_b 0: G has one half
     float* lost;                 // [T][k]
+    const int* flag;             // dW of more rows: the lead's column,
+    uint16_t* lead_rest;         // and G's columns of rests; else null
 };
 __global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
 {
@@ -561,13 +745,13 @@ __global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
         const int64_t i = t * p.k + j, col = p.leader[i];
         if (col < p.v0 || col >= p.v0 + p.vp)
             continue;
-        const float lp = p.logp[i], r = p.rest[i];
-        // p - q with q = 1 - rest: near p = q = 1 both sides are taken from 1
-        const float d = r < 0.5f ? expm1f(lp) + r : expf(lp) - p.qsum[i];
+        const float d = target_dz(p.logp[i], p.qsum[i], p.rest[i]);
         uint16_t* at = p.G + row * p.ldg + (col - p.v0);
         *at = bf16_rne(g * d);
         if (p.half_b)
             at[p.half_b / 2] = bf16_rne(bf16_rest(g * d));
+        if (p.lead_rest && col == p.flag[2 * t + 1])
+            p.lead_rest[row * p.ldg + col % kRestCols] = bf16_rne(bf16_rest(g * d));
         // (smaller columns only make up a row together, at least sixteen of
         // them, and their errors average)
         p.lost[i] = fabsf(d) >= 0.0625f ? bf16_rest(g * d) : 0.f;
@@ -921,16 +1105,21 @@ hipError_t launch_few(int shape, const LossArgs& a, int cus, hipStream_t s)
 
 // Launches a kernel; the status of this launch, not an earlier sticky error.
 template <class... P, class... A>
-hipError_t launch(void (*kernel)(P...), int64_t grid, int block, hipStream_t s, A... args)
+hipError_t launch(void (*kernel)(P...), dim3 grid, int block, hipStream_t s, A... args)
 {
     std::tuple<P...> held(args...);
     return std::apply(
         [&](auto&... a) {
             void* list[] = {&a...};
-            return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)grid),
-                                   dim3((unsigned)block), list, 0, s);
+            return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3((unsigned)block), list,
+                                   0, s);
         },
         held);
+}
+template <class... P, class... A>
+hipError_t launch(void (*kernel)(P...), int64_t grid, int block, hipStream_t s, A... args)
+{
+    return launch(kernel, dim3((unsigned)grid), block, s, args...);
 }
 
 #define DG_TRY(x)                    \
@@ -941,7 +1130,7 @@ hipError_t launch(void (*kernel)(P...), int64_t grid, int block, hipStream_t s, 
     } while (0)
 
 // Distillation: the targets' kernel.  Returns where the rows' states are.
-hipError_t row_targets(const LossCall& c, const LossPlan& pl, RowSource* out)
+hipError_t row_targets(const LossCall& c, const LossPlan& pl, bool by_group, RowSource* out)
 {
     uint8_t* ws = c.ws;
     RowSource& src = *out;
@@ -961,17 +1150,28 @@ hipError_t row_targets(const LossCall& c, const LossPlan& pl, RowSource* out)
         t.rest = reinterpret_cast<float*>(ws + pl.off_rest);
         t.leader = reinterpret_cast<int*>(ws + pl.off_lead);
         t.flag = reinterpret_cast<int*>(ws + pl.off_flag);
+        t.logp = by_group ? c.logp_in : nullptr;
         src.flag = t.flag;
         DG_TRY(launch(loss_target_kernel, c.T, 64, c.stream, t));
     }
     return hipSuccess;
 }
 
-hipError_t select_rows(const LossCall& c, const LossPlan& pl, const RowSource& src, bool backward)
+hipError_t select_rows(const LossCall& c, const LossPlan& pl, const RowSource& src, bool backward, bool by_group)
 {
     uint8_t* ws = c.ws;
     int* chunks = nullptr;
-    if (c.T > kOwnCount) {
+    int* n_kept = reinterpret_cast<int*>(ws + pl.off_count);
+    int* group = reinterpret_cast<int*>(ws + pl.off_group);
+    int* place = nullptr;
+    const int groups = (int)pl.groups, n_chunks = (int)cdiv(c.T, kOwnCount);
+    if (by_group && c.T > kOwnCount) {
+        place = reinterpret_cast<int*>(ws + pl.off_place);
+        DG_TRY(launch(loss_group_count_kernel, dim3((unsigned)n_chunks, (unsigned)cdiv(groups, kGroupPass)), 1024,
+                      c.stream, src, c.T, groups, place));
+        DG_TRY(launch(loss_group_place_kernel, dim3(1), 1024, c.stream, place, (int64_t)groups * n_chunks, n_chunks,
+                      group, groups, n_kept));
+    } else if (c.T > kOwnCount) {
         chunks = reinterpret_cast<int*>(ws + pl.off_chunks);
         DG_TRY(launch(loss_count_kernel, cdiv(c.T, kChunk), 256, c.stream, src, c.T, chunks));
     }
@@ -983,7 +1183,7 @@ hipError_t select_rows(const LossCall& c, const LossPlan& pl, const RowSource& s
     a.ldx_b = c.ldx * 2;
     a.Xc = ws + pl.off_x;
     a.row_b = c.D * 2;
-    a.n_kept = reinterpret_cast<int*>(ws + pl.off_count);
+    a.n_kept = n_kept;
     a.map = reinterpret_cast<int*>(ws + pl.off_map);
     a.pos = reinterpret_cast<int*>(ws + pl.off_pos);
     a.rows = reinterpret_cast<RowInfo*>(ws + pl.off_rows);
@@ -996,7 +1196,15 @@ hipError_t select_rows(const LossCall& c, const LossPlan& pl, const RowSource& s
     a.dloss_stride = c.dloss_stride;
     a.scale = c.scale;
     a.z_loss = c.z_loss;
-    return launch(loss_select_kernel, cdiv(c.T, kSelRows), 256, c.stream, a);
+    a.place = place;
+    a.n_chunks = n_chunks;
+    a.groups = groups;
+    a.group = group;
+    a.rest = ws + pl.off_g + pl.piece * 2;
+    a.rest_b = pl.ldg * 2;
+    const int64_t firsts = place ? 0 : cdiv(groups + 1, kSelRows);
+    return by_group ? launch(loss_select_kernel<true>, cdiv(c.T, kSelRows) + firsts, 256, c.stream, a)
+                    : launch(loss_select_kernel<false>, cdiv(c.T, kSelRows), 256, c.stream, a);
 }
 
 LossArgs product_args(const LossCall& c, const LossPlan& pl)
@@ -1079,7 +1287,13 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
         const int64_t pair_slices = std::min(kPlanCus / pair_tiles, piece / 256);
         if (V <= piece && pair_slices >= 1 && cdiv(cdiv(V, Mid::KT), pair_slices) <= (p.few ? 16 : 128))
             p.pair = (int)pair_slices;
-        p.off_g = take(p.rows_pad * piece * (p.few ? 4 : 2));
+        p.ldg = piece + (p.few ? 0 : kRestCols);
+        p.off_g = take(p.rows_pad * p.ldg * (p.few ? 4 : 2));
+        if (!p.few) {
+            p.groups = cdiv(V, kRestCols);
+            p.off_group = take((p.groups + 1) * 4);
+            p.off_place = take(T > kOwnCount ? p.groups * cdiv(T, kOwnCount) * 4 : 0);
+        }
         p.off_planes = take((int64_t)std::max(p.splits, p.pair) * T * D * 4);
         p.bytes = std::max(p.bytes, at);
     }
@@ -1110,13 +1324,13 @@ hipError_t loss_forward(const LossCall& c)
     const LossPlan pl = loss_plan(c.T, c.V, c.D, c.slots, false);
     uint8_t* ws = c.ws;
     RowSource src;
-    DG_TRY(row_targets(c, pl, &src));
+    DG_TRY(row_targets(c, pl, false, &src));
     // Rows that one tile holds are not selected: W is read for one of them as
     // for all, and the launch takes longer than the rest could save (one row of
     // 50257 x 512: 20 us with it, 16 without).
     const bool few = c.T <= Line::TM;
     if (!few)
-        DG_TRY(select_rows(c, pl, src, false));
+        DG_TRY(select_rows(c, pl, src, false, false));
     LossArgs a = product_args(c, pl);
     a.A = few ? reinterpret_cast<const uint8_t*>(c.X) : ws + pl.off_x;
     a.lda_b = few ? c.ldx * 2 : c.D * 2;
@@ -1197,8 +1411,9 @@ hipError_t loss_backward(const LossCall& c)
     const LossPlan pl = loss_plan(c.T, c.V, c.D, c.slots, true);
     uint8_t* ws = c.ws;
     RowSource src;
-    DG_TRY(row_targets(c, pl, &src));
-    DG_TRY(select_rows(c, pl, src, true));
+    const bool by_group = c.dW && !pl.few;
+    DG_TRY(row_targets(c, pl, by_group, &src));
+    DG_TRY(select_rows(c, pl, src, true, by_group));
     const int* pos = reinterpret_cast<const int*>(ws + pl.off_pos);
     const int* map = reinterpret_cast<const int*>(ws + pl.off_map);
     const RowInfo* rows = reinterpret_cast<const RowInfo*>(ws + pl.off_rows);
@@ -1238,7 +1453,7 @@ hipError_t loss_backward(const LossCall& c)
             a.K = (int)c.D;
             a.v0 = (int)(v0 + u);
             a.C = G + u;
-            a.ldc = pl.piece;
+            a.ldc = pl.ldg;
             a.c_cols = (int)(pl.piece - u);
             a.half_b = half_b;
             a.w_nt = w_nt;
@@ -1260,16 +1475,18 @@ hipError_t loss_backward(const LossCall& c)
             k.v0 = v0;
             k.vp = vp;
             k.G = G;
-            k.ldg = pl.piece;
+            k.ldg = pl.ldg;
             k.half_b = half_b;
             k.lost = reinterpret_cast<float*>(ws + pl.off_q);
+            k.flag = src.flag;
+            k.lead_rest = by_group ? G + pl.piece : nullptr;
             DG_TRY(launch(loss_sparse_kernel, cdiv(c.T, 4), 256, c.stream, k));
         }
         LossArgs dx = product_args(c, pl);
         if (c.dX) {
             LossArgs& d = dx;
             d.A = reinterpret_cast<const uint8_t*>(G);
-            d.lda_b = pl.piece * 2;
+            d.lda_b = pl.ldg * 2;
             d.B = W;
             d.ldb_b = c.ldw * 2;
             d.N = (int)c.D;
@@ -1290,10 +1507,13 @@ hipError_t loss_backward(const LossCall& c)
             for (int64_t u = 0; u < vp; u += wp.main) {
                 LossArgs d = product_args(c, pl);
                 d.A = reinterpret_cast<const uint8_t*>(G + u);
-                d.lda_b = pl.piece * 2;
+                d.lda_b = pl.ldg * 2;
                 d.B = Xc;
                 d.ldb_b = c.D * 2;
                 d.M = (int)(u == 0 ? wp.main : vp - u);
+                d.v0 = (int)(v0 + u);        // (whole groups)
+                d.rest = reinterpret_cast<const uint8_t*>(G + pl.piece);
+                d.group = reinterpret_cast<const int*>(ws + pl.off_group);
                 d.N = (int)c.D;
                 d.C = c.dW + (v0 + u) * c.lddw;
                 d.ldc = c.lddw;

@@ -16,6 +16,7 @@ struct LossPlan {
     int64_t rows_pad;            // T rounded up to 256
     int64_t tiles_n_max;         // forward: tile columns of the narrowest tile
     int64_t piece;               // backward: columns of the vocabulary at a time
+    int64_t ldg;                 // backward: pitch of G
     int dx_shape, splits;        // backward: tile shape and K slices of the dX product
     int pair;                    // backward: K slices of dX where it shares a launch with dW, 0: never
     bool few;                    // backward: at most one tile of rows, G in two halves
@@ -23,6 +24,8 @@ struct LossPlan {
     int64_t off_part, off_zlabel;                       // forward
     int64_t off_q, off_qsum, off_rest, off_lead, off_flag;        // distillation targets
     int64_t off_g, off_planes;                          // backward
+    int64_t groups;              // backward of more rows: the vocabulary's groups of columns
+    int64_t off_group, off_place;
     int64_t bytes;
 };
 LossPlan loss_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool backward);

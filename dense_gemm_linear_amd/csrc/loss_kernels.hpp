@@ -34,6 +34,11 @@ namespace dg {
 
 enum { ROLE_LSE = 0, ROLE_GRAD = 1, ROLE_DX = 2, ROLE_DW = 3 };
 
+// dW of more rows than one tile: rows are in the order of their target's group of
+// this many columns, and G's rows end in as many more, the rest of the row's target
+// at the target's column of its group.
+constexpr int kRestCols = 256;
+
 // One kept row: what its gradient needs, in compact row order.
 struct RowInfo {
     float lse2;   // lse / ln 2
@@ -75,7 +80,7 @@ struct LossArgs {
     float2* part;          // LSE: [tiles_n][ldpart] (reference, sum)
     int64_t ldpart;
     float* zlabel;         // LSE: the label's sum over d, with scale's sign; compact rows
-    int v0;                // LSE, GRAD: the vocabulary's column of B's first row
+    int v0;                // LSE, GRAD: the vocabulary's column of B's first row; DW: of M's
     float* planes;         // DX: [slices][n][ldplane]
     int64_t ldplane;
     int first;             // DX: the first piece writes, later ones add
@@ -85,6 +90,9 @@ struct LossArgs {
     int c_vec;             // DW: 1 C's rows take 16-byte stores, 2 and non-temporal ones
     int w_nt;              // few rows, GRAD and DX: W with the non-temporal hint
     int64_t half_b;        // few rows, GRAD and DW: bytes from G to its second half
+    // DW of more rows: G's columns of rests, and the first row of each group
+    const uint8_t* rest;
+    const int* group;
 };
 
 // Tile shape: TM x TN outputs, WM x WN waves, ST stages of KTB bytes of K,
@@ -232,9 +240,18 @@ __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N
 //         with the non-temporal hint.
 //   GRAD  G is stored in two bf16 halves, the rounded value and the rounded
 //         rest (16 bits of it together), and
-//   DW    sums both: with few rows one element's rounding can make up most of
-//         a row of dW (over many rows such errors average), and the product is
-//         bound by writing dW, not by its K.
+//   DW    sums both: the product is bound by writing dW, not by its K.
+// With more rows the second half's products would take as long as the first's
+// again.  Rounding G to bf16 is as large an error as rounding dW itself, over any
+// number of rows, as the errors and the products add up alike, and nearly all of it
+// comes from the columns that are some row's target, where |dz| is largest.  DW
+// takes the rests of those alone (p.rest): rows lie in the order of their target's
+// group of 256 columns, so the ones with a target in a tile's columns are a
+// range of rows, further k-tiles of the same loop with the rests at the targets and
+// zeros elsewhere (3686 rows: 115 k-tiles, and 19 rows a tile on average).  The norm of
+// dW's error at 1100 x 11001 x 520 is that of one rounding, and 1.44 times it
+// without; gradients and loss of 1024 x 50257 x 512 take 283 us, 287 without, of
+// 528 x 11007 x 1024 77, 74.
 //   GRAD, DX  load W with the non-temporal hint where it is larger than the
 //         Infinity Cache (w_nt), which then cannot hand it from one to the other.
 // Workgroup `block` of `blocks`; lds: S::LDS bytes.
@@ -242,7 +259,7 @@ template <class S, int ROLE, bool FEW>
 __device__ __forceinline__ void loss_product(const LossArgs& p, uint8_t* lds, int block, int blocks)
 {
     constexpr bool FEWX = FEW && ROLE == ROLE_LSE;        // X not selected
-    constexpr bool HALVES = FEW && ROLE == ROLE_DW;
+    constexpr bool HALVES = FEW && ROLE == ROLE_DW, RESTS = !FEW && ROLE == ROLE_DW;
     using AT = Atom<DT_BF16, 16>;
     using KTL = KTile<S::KTB>;
     using acc_t = AT::acc_t;
@@ -312,6 +329,9 @@ __device__ __forceinline__ void loss_product(const LossArgs& p, uint8_t* lds, in
     int kt0 = 0, nkt = HALVES ? 2 * all_kt : all_kt, kb_end = K * 2, last_full = 0;
     const uint8_t *a_base = nullptr, *b_base = nullptr;
     int64_t a_span = 0, b_span = 0;
+    const uint8_t* e_base = nullptr;                 // RESTS: the tile's rows of rests
+    int64_t e_span = 0;
+    int e_row = 0;
     uint32_t a_bytes = 0, b_bytes = 0;
     auto set_item = [&](int it) __attribute__((always_inline)) {
         // Each XCD a contiguous run of items.  dX: slices outermost, so that the
@@ -345,14 +365,26 @@ __device__ __forceinline__ void loss_product(const LossArgs& p, uint8_t* lds, in
             a_span = (int64_t)(k_end - 1) * p.lda_b + (int64_t)(p.M - m0 + 7) / 8 * 16;
         else
             a_bytes = (uint32_t)((int64_t)(rows - 1) * p.lda_b + (int64_t)(K + 7) / 8 * 16);
+        if constexpr (RESTS) {
+            const int v = p.v0 + m0;                   // tiles do not cross groups
+            e_row = __builtin_amdgcn_readfirstlane(p.group[v / kRestCols]);
+            const int e_rows = __builtin_amdgcn_readfirstlane(p.group[v / kRestCols + 1]) - e_row;
+            e_base = p.rest + e_row * p.lda_b + v % kRestCols * 2;
+            e_span = (e_rows - 1) * p.lda_b + TM * 2;
+            nkt = all_kt + (e_rows + KT - 1) / KT;
+        }
         if constexpr (TRB)
             b_span = (int64_t)(k_end - 1) * p.ldb_b + (int64_t)(p.N - n0) * 2;
         else
             b_bytes = (uint32_t)((int64_t)(min(TN, p.N - n0) - 1) * p.ldb_b + (int64_t)K * 2);
     };
     auto rebase = [&](const uint8_t* base, int64_t span, int64_t off) __attribute__((always_inline)) {
+        // (in 32-bit halves, which stay in scalar registers: 64-bit compares take
+        // vector ones, and the 256 x 256 tile has none left)
         const int64_t left = span - off;
-        return make_rsrc(base + off, left <= 0 ? 0u : (uint32_t)min(left, (int64_t)0x7FFFFFFF));
+        const int hi = (int)(left >> 32);
+        const uint32_t lo = min((uint32_t)left, 0x7FFFFFFFu);
+        return make_rsrc(base + off, hi < 0 ? 0u : hi > 0 ? 0x7FFFFFFFu : lo);
     };
     auto load = [&](int kt_local, int stage, int part, int nparts, auto nomask_c)
                     __attribute__((always_inline)) {
@@ -360,12 +392,16 @@ __device__ __forceinline__ void loss_product(const LossArgs& p, uint8_t* lds, in
         const int kt = kt0 + kt_local;
         const bool mask = kt >= last_full;
         uint8_t* base = lds + stage * STAGE;
-        // the second half of G against the same rows of X
-        const bool second = HALVES && kt >= all_kt;
+        // the second half of G against the same rows of X, or the rests against
+        // the rows of the tile's targets (past the last of them: zeros)
+        const bool second = (HALVES || RESTS) && kt >= all_kt;
         const int64_t row = (int64_t)(second ? kt - all_kt : kt) * KT;
-        const rsrc_t rat = TRA ? rebase(a_base + (second ? p.half_b : 0), a_span, row * p.lda_b)
-                               : make_rsrc(a_base, a_bytes);
-        const rsrc_t rbt = TRB ? rebase(b_base, b_span, row * p.ldb_b) : make_rsrc(b_base, b_bytes);
+        const rsrc_t rat =
+            TRA ? rebase(RESTS && second ? e_base : a_base + (HALVES && second ? p.half_b : 0),
+                         RESTS && second ? e_span : a_span, row * p.lda_b)
+                : make_rsrc(a_base, a_bytes);
+        const rsrc_t rbt = TRB ? rebase(b_base, b_span, ((RESTS && second ? e_row : 0) + row) * p.ldb_b)
+                               : make_rsrc(b_base, b_bytes);
         auto one = [&](rsrc_t r, uint8_t* dst, uint32_t goff, uint32_t col, auto tr, auto nt)
                        __attribute__((always_inline)) {
             uint32_t off = goff, soff = 0;

@@ -488,7 +488,8 @@ gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void
  * in fp32.  The entry points below take losses from z, and the gradients of X
  * and W, without storing z: the forward pass keeps one pair of floats per row
  * and 64 to 256 columns, the gradient one piece of the vocabulary at a time (at
- * most 256 MiB of bf16, or 256 columns), recomputed from X and W.
+ * most 256 MiB of bf16, or 256 columns; and 256 columns for what rounding it
+ * left over), recomputed from X and W.
  *
  * Rows that are out -- an ignored label, no filled target slot -- have loss
  * 0, lse 0 and gradient 0, take no part in the products, and whatever their X
@@ -509,8 +510,9 @@ gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void
  *       element of the T x D / V x D region is overwritten, nothing else is.
  *       Rounded to nearest even from fp32 sums; the logits' gradient they are
  *       products of is rounded to bf16 first, which is made good for dX's target
- *       columns and for dW of at most 128 rows.  They must not overlap the
- *       inputs or each other.
+ *       columns, for all of dW of at most 128 rows, and for dW of more rows at each
+ *       row's label or, of a teacher's columns, the one of the largest
+ *       |softmax(z) - q|.  They must not overlap the inputs or each other.
  *   workspace  device, 256-byte aligned, at least
  *       linear_loss_workspace_bytes(T, V, D, slots, backward) bytes (slots 0
  *       for cross entropy; backward 1 also serves the forward call).  Its
