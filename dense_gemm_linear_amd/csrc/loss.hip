@@ -741,20 +741,34 @@ __global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
         return;
     const int64_t t = p.map[row];
     const float g = p.rows[row].b;
-    for (int j = threadIdx.x & 63; j < p.k; j += 64) {
-        const int64_t i = t * p.k + j, col = p.leader[i];
+    constexpr int U = kMaxLossSlots / 64;
+    const int lane = threadIdx.x & 63;
+    int cols[U];
+    float d[U], most = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int j = lane + 64 * u;
+        const int64_t i = t * p.k + j;
+        cols[u] = j < p.k ? p.leader[i] : -1;
+        d[u] = cols[u] >= 0 ? target_dz(p.logp[i], p.qsum[i], p.rest[i]) : 0.f;
+        most = fmaxf(most, fabsf(d[u]));
+    }
+    most = wave_max(most);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = t * p.k + lane + 64 * u, col = cols[u];
         if (col < p.v0 || col >= p.v0 + p.vp)
             continue;
-        const float d = target_dz(p.logp[i], p.qsum[i], p.rest[i]);
         uint16_t* at = p.G + row * p.ldg + (col - p.v0);
-        *at = bf16_rne(g * d);
+        *at = bf16_rne(g * d[u]);
         if (p.half_b)
-            at[p.half_b / 2] = bf16_rne(bf16_rest(g * d));
+            at[p.half_b / 2] = bf16_rne(bf16_rest(g * d[u]));
         if (p.lead_rest && col == p.flag[2 * t + 1])
-            p.lead_rest[row * p.ldg + col % kRestCols] = bf16_rne(bf16_rest(g * d));
-        // (smaller columns only make up a row together, at least sixteen of
-        // them, and their errors average)
-        p.lost[i] = fabsf(d) >= 0.0625f ? bf16_rest(g * d) : 0.f;
+            p.lead_rest[row * p.ldg + col % kRestCols] = bf16_rne(bf16_rest(g * d[u]));
+        // Below 1 / (4 sqrt k) of the row's largest: all of them together hold at
+        // most 1/16 of its square, and their roundings add 3 % to the error's
+        // norm at most; each one more is a row of W to read.
+        p.lost[i] = d[u] * d[u] * (16.f * p.k) >= most * most ? bf16_rest(g * d[u]) : 0.f;
     }
 }
 
