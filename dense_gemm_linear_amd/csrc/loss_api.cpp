@@ -53,7 +53,8 @@ gemm_status check_slots(const int64_t* index, int64_t ld_index, const float* tea
 gemm_status check_grad(const float* lse, const float* dloss, int64_t dloss_count, int64_t T, int64_t D,
                        const uint16_t* dX, int64_t lddx, const uint16_t* dW, int64_t lddw)
 {
-    if (!dX && !dW)
+    // (without rows dX holds nothing and its pointer says nothing)
+    if (!dX && !dW && T > 0)
         return GEMM_ERR_INVALID_VALUE;
     if (dW && (!aligned(dW, 2) || lddw < D))
         return GEMM_ERR_INVALID_VALUE;

@@ -530,7 +530,7 @@ gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void
  * below 1, T below 0, a scale or z_loss that is not finite, dloss_count other
  * than 1 or T; UNSUPPORTED for D % 8 != 0, D > 65536, T > 2^20, V > 2^24,
  * slots > 256 or a pitch of X, W or dW above 2^21 elements; HIP.  T == 0: no
- * row, no launch but the zeros of dW; only W is looked at then.
+ * row, no launch but the zeros of dW; only W and dW are looked at then.
  *
  * linear_cross_entropy -- with one label a row,
  *     loss[t] = lse[t] - z[t][labels[t]] + z_loss * lse[t]^2
