@@ -1244,6 +1244,10 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
         return o;
     };
     p.rows_pad = round_up(T, 256);
+    p.few = T <= Line::TM;
+    // Rows of the large tables: stores and reads stop at the last kept row, so
+    // that few rows need no more (one row of 50257 x 512 asks for 1 MB, 49 with 256)
+    p.rows = p.few ? T : p.rows_pad;
     p.off_count = take(256);
     p.off_chunks = take(cdiv(T, kChunk) * 4);
     p.off_map = take(p.rows_pad * 4);
@@ -1259,17 +1263,20 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
     }
     const int64_t shared = at;
     p.tiles_n_max = cdiv(V, T <= Line::TM ? 64 : 128);
-    p.off_part = take(p.tiles_n_max * p.rows_pad * 8);
+    p.off_part = take(p.tiles_n_max * p.rows * 8);
     p.off_zlabel = take(p.rows_pad * 4);
     p.bytes = at;
     if (backward) {
         at = shared;
-        // G of one piece: at most 256 MiB (the Infinity Cache's size), at
-        // least 256 columns.  Fewer pieces make fuller rounds of tiles and
+        // G of one piece, or its two halves: at most 256 MiB (the Infinity Cache's
+        // size), at least 256 columns; at most 2^21 columns, as the pitches of X
+        // and W (a tile's rows stay within a 31-bit offset).  Fewer pieces make fuller rounds of tiles and
         // fewer passes over dX's planes: 2048 x 131072 x 4096 measured 5351,
         // 5316, 5222 and 5172 us with 64, 128, 256 and 512 MiB.
-        int64_t piece = (INT64_C(256) << 20) / 2 / p.rows_pad / 256 * 256;
+        const int64_t row_b = p.rows * (p.few ? 4 : 2);
+        int64_t piece = (INT64_C(256) << 20) / row_b / 256 * 256;
         piece = std::max<int64_t>(piece, 256);
+        piece = std::min<int64_t>(piece, INT64_C(1) << 21);
         piece = std::min(piece, round_up(V, 256));
         p.piece = piece;
         // dX: shape and K slices by the estimate, the planes' traffic included
@@ -1288,7 +1295,6 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
                     p.splits = sp;
                 }
             }
-        p.few = T <= Line::TM;
         // Both gradients of a small vocabulary in one launch, dX in as many
         // slices as give half of the workgroups one tile each, when a slice is
         // at most 128 k-tiles: of 38 such sizes 37 then took 1 to 14 % less for
@@ -1302,7 +1308,7 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
         if (V <= piece && pair_slices >= 1 && cdiv(cdiv(V, Mid::KT), pair_slices) <= (p.few ? 16 : 128))
             p.pair = (int)pair_slices;
         p.ldg = piece + (p.few ? 0 : kRestCols);
-        p.off_g = take(p.rows_pad * p.ldg * (p.few ? 4 : 2));
+        p.off_g = take(row_b * p.ldg);
         if (!p.few) {
             p.groups = cdiv(V, kRestCols);
             p.off_group = take((p.groups + 1) * 4);
@@ -1356,7 +1362,7 @@ hipError_t loss_forward(const LossCall& c)
     a.N = (int)c.V;
     a.K = (int)c.D;
     a.part = reinterpret_cast<float2*>(ws + pl.off_part);
-    a.ldpart = pl.rows_pad;
+    a.ldpart = pl.rows;
     a.zlabel = reinterpret_cast<float*>(ws + pl.off_zlabel);
     const RangePlan rp = few ? RangePlan{few_shape(c.T, c.V, c.cus), 0, c.V}
                              : plan_range(c.T, c.V, c.D, 0, false, c.cus);
@@ -1436,7 +1442,7 @@ hipError_t loss_backward(const LossCall& c)
     // us against 302; 30 x 131072 x 4096: 562 against 635; but 48 x 50257 x 2048,
     // 206 MB: 144 against 133)
     const bool few = pl.few;
-    const int64_t half_b = few && c.dW ? pl.rows_pad * pl.piece * 2 : 0;
+    const int64_t half_b = few && c.dW ? pl.rows * pl.piece * 2 : 0;
     const int w_nt = few && c.V * c.D * 2 > (INT64_C(256) << 20);
     uint16_t* G = reinterpret_cast<uint16_t*>(ws + pl.off_g);
     const bool pair = pl.pair && c.dX && c.dW;

@@ -14,12 +14,13 @@ constexpr int kMaxLossSlots = 256;
 // them.  Everything follows from (T, V, D, slots, backward).
 struct LossPlan {
     int64_t rows_pad;            // T rounded up to 256
+    int64_t rows;                // rows of the large tables: T of few rows, else rows_pad
     int64_t tiles_n_max;         // forward: tile columns of the narrowest tile
     int64_t piece;               // backward: columns of the vocabulary at a time
     int64_t ldg;                 // backward: pitch of G
     int dx_shape, splits;        // backward: tile shape and K slices of the dX product
     int pair;                    // backward: K slices of dX where it shares a launch with dW, 0: never
-    bool few;                    // backward: at most one tile of rows, G in two halves
+    bool few;                    // at most one tile of rows; backward: G in two halves
     int64_t off_count, off_chunks, off_map, off_pos, off_rows, off_x;
     int64_t off_part, off_zlabel;                       // forward
     int64_t off_q, off_qsum, off_rest, off_lead, off_flag;        // distillation targets
