@@ -1066,8 +1066,10 @@ hipError_t launch_role(int shape, const LossArgs& a, int64_t rows, int cus, hipS
         if (shape == SHAPE_FEW)
             return go<Few, ROLE, FEW>(a, cdiv(rows, Few::TM), cus, s);
     }
-    if (shape == SHAPE_BIG)
-        return go<Big, ROLE, FEW>(a, cdiv(rows, Big::TM), cus, s);
+    if constexpr (!FEW) {
+        if (shape == SHAPE_BIG)
+            return go<Big, ROLE>(a, cdiv(rows, Big::TM), cus, s);
+    }
     if (shape == SHAPE_TALL)
         return go<Tall, ROLE, FEW>(a, cdiv(rows, Tall::TM), cus, s);
     if constexpr (ROLE == ROLE_LSE || ROLE == ROLE_GRAD) {
@@ -1283,8 +1285,10 @@ static LossPlan make_plan(int64_t T, int64_t V, int64_t D, int64_t slots, bool b
         // (each slice writes one, the last kernel reads them, and every
         // further piece reads and writes them again)
         const int64_t passes = 2 * cdiv(V, piece);
+        // (One tile of rows never takes Big: a round of Mid holds as many columns of
+        // outputs, two tiles a CU, and costs less.)
         double best = 0.0;
-        for (int sh = T <= 32 ? SHAPE_LOW : T <= 64 ? SHAPE_FEW : SHAPE_BIG;
+        for (int sh = T <= 32 ? SHAPE_LOW : T <= 64 ? SHAPE_FEW : p.few ? SHAPE_TALL : SHAPE_BIG;
              sh <= (T <= 32 ? SHAPE_LOW : T <= 64 ? SHAPE_FEW : SHAPE_MID); ++sh)
             for (int sp = 1; sp <= 64 && (sp == 1 || piece / sp >= 256); ++sp) {
                 const double us = cdiv(V, piece) * product_us(sh, T, D, piece, sp, kPlanCus) +
