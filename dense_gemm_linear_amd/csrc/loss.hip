@@ -1520,10 +1520,13 @@ hipError_t loss_backward(const LossCall& c)
             d.ldplane = c.D;
             d.first = v0 == 0;
             d.w_nt = w_nt;
-            if (w_nt)
+            if (pair) {
+                // with dW, below
+            } else if (w_nt) {
                 DG_TRY((launch_role<ROLE_DX, true>(pl.dx_shape, d, c.T, c.cus, c.stream)));
-            else if (!pair)
+            } else {
                 DG_TRY(launch_role<ROLE_DX>(pl.dx_shape, d, c.T, c.cus, c.stream));
+            }
         }
         if (c.dW) {
             const RangePlan wp = few || pair ? RangePlan{SHAPE_MID, 0, vp}
