@@ -915,6 +915,10 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
 // Tile shapes.  kt and epi are what one round (every CU holding its fill of
 // workgroups) measured on MI355X, in microseconds: kt for each 32 values of K,
 // epi for the rest of a tile; kt1 where there is at most one workgroup a CU.
+// Those of Few and Low are one guess for both, which dX's K slices alone go by:
+// over 32 sizes of 16 to 64 rows dX then takes at most 8.5 % more than with the
+// best of 12 numbers of slices, 3 % on average.  few_shape takes Slim, FewSlim and
+// LowSlim by size, so they have none.
 //   Big   taken where its tiles fill the CUs: twice the work of Tall, four
 //         times that of the others, in 1.0 to 1.6 times their time (4095 x
 //         50257 x 4096 logits: 1291 us; the next best shape 1414).
@@ -929,8 +933,9 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(DxArgs p)
 //         lines (215 x 9904 x 3832 forward 48 us against 54 with Wide).
 //   Mid   for dX and dW, whose transposed operands are whole lines anyway.
 //   Few, Low  up to 64 and 32 rows, where the product is a read of W: the
-//         tile that just covers the rows keeps the most of it in flight (48 x
-//         50257 x 4096, W cold: 141 us against 153 to 159 of the others).
+//         tile that just covers the rows keeps the most of it in flight (forward
+//         of 48 x 50257 x 4096, whose W no cache holds: 82 us against 93 to 109 of
+//         the others; 30 rows 78 against 79 to 87).
 //   Slim, FewSlim, LowSlim  for up to 128, 64 and 32 rows of vocabularies that
 //         make no full round of the 128-column tiles: 64 columns and deeper
 //         rings (121 x 10399 x 3272 forward 41 us against 66, 48 x 16000 x 4096
@@ -950,7 +955,7 @@ enum { SHAPE_BIG = 0, SHAPE_TALL, SHAPE_MID, SHAPE_LINE, SHAPE_WIDE, SHAPE_DEEP,
        SHAPE_SLIM, SHAPE_FEW_SLIM, SHAPE_LOW_SLIM };
 struct ShapeCost {
     int tm, tn, per_cu;
-    double kt, kt1, epi;
+    double kt = 0.0, kt1 = 0.0, epi = 0.0;
 };
 constexpr ShapeCost kShapes[] = {{Big::TM, Big::TN, Big::PER_CU, 0.72, 0.72, 9.0},
                                  {Tall::TM, Tall::TN, Tall::PER_CU, 0.48, 0.48, 4.5},
@@ -960,9 +965,9 @@ constexpr ShapeCost kShapes[] = {{Big::TM, Big::TN, Big::PER_CU, 0.72, 0.72, 9.0
                                  {Deep::TM, Deep::TN, Deep::PER_CU, 0.30, 0.29, 2.0},
                                  {Few::TM, Few::TN, Few::PER_CU, 0.5, 0.4, 2.0},
                                  {Low::TM, Low::TN, Low::PER_CU, 0.5, 0.4, 2.0},
-                                 {Slim::TM, Slim::TN, Slim::PER_CU, 0.3, 0.3, 2.0},
-                                 {FewSlim::TM, FewSlim::TN, FewSlim::PER_CU, 0.3, 0.3, 2.0},
-                                 {LowSlim::TM, LowSlim::TN, LowSlim::PER_CU, 0.3, 0.3, 2.0}};
+                                 {Slim::TM, Slim::TN, Slim::PER_CU},
+                                 {FewSlim::TM, FewSlim::TN, FewSlim::PER_CU},
+                                 {LowSlim::TM, LowSlim::TN, LowSlim::PER_CU}};
 constexpr int kPlanCus = 256;            // the workspace must not depend on the device
 constexpr double kLaunchUs = 5.0;        // a further launch, start to start
 constexpr double kPlaneBytesPerUs = 2.0e6;
