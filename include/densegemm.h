@@ -16,8 +16,10 @@
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *     Work is enqueued on it and the call returns without synchronising.
  *     Faults inside a kernel surface at the caller's next synchronisation.
- *   - The caller owns every buffer.  The library allocates no device memory,
- *     keeps no per-call state and is safe to call from several host threads.
+ *   - The caller owns every buffer.  The library allocates no device memory
+ *     and keeps nothing of a call but host tables by size: tile choices, and per
+ *     thread the last few workspace layouts of the losses.  It is safe to call
+ *     from several host threads.
  *   - Errors are reported by return value; nothing throws across this ABI.
  *     Argument checks run before any HIP call, so invalid arguments are
  *     rejected without touching the device.
