@@ -732,7 +732,7 @@ struct SparseArgs {
     int64_t ldg, half_b;         // half_b 0: G has one half
     float* lost;                 // [T][k]
     const int* flag;             // dW of more rows: the lead's column,
-    uint16_t* lead_rest;         // and G's columns of rests; else null
+    uint16_t* lead_rest;         // and G's columns of rests, of the lead's group; else null
 };
 __global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
 {
@@ -763,7 +763,8 @@ __global__ __launch_bounds__(256) void loss_sparse_kernel(SparseArgs p)
         *at = bf16_rne(g * d[u]);
         if (p.half_b)
             at[p.half_b / 2] = bf16_rne(bf16_rest(g * d[u]));
-        if (p.lead_rest && col == p.flag[2 * t + 1])
+        // (the row lies with its lead's group, whose other targets come for nothing)
+        if (p.lead_rest && col / kRestCols == row_group(p.flag[2 * t + 1]))
             p.lead_rest[row * p.ldg + col % kRestCols] = bf16_rne(bf16_rest(g * d[u]));
         // Below 1 / (4 sqrt k) of the row's largest: all of them together hold at
         // most 1/16 of its square, and their roundings add 3 % to the error's

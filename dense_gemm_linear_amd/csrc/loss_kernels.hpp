@@ -35,8 +35,8 @@ namespace dg {
 enum { ROLE_LSE = 0, ROLE_GRAD = 1, ROLE_DX = 2, ROLE_DW = 3 };
 
 // dW of more rows than one tile: rows are in the order of their target's group of
-// this many columns, and G's rows end in as many more, the rest of the row's target
-// at the target's column of its group.
+// this many columns, and G's rows end in as many more, the rests of the row's
+// targets in that group.
 constexpr int kRestCols = 256;
 
 // One kept row: what its gradient needs, in compact row order.

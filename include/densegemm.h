@@ -515,8 +515,8 @@ gemm_status gemm_read_probe(const void* buf, uint64_t bytes, uint32_t* out, void
  *       columns (but for such of a teacher's as together hold at most 1/16 of
  *       the square of the row's largest |softmax(z) - q|), for all of dW of at most
  *       128 rows, and for dW of more rows at each row's label or, of a teacher's
- *       columns, the one of that largest.  They must not overlap the inputs or each
- *       other.
+ *       columns, at those in the same 256 columns (from a multiple of 256 on) as
+ *       that largest.  They must not overlap the inputs or each other.
  *   workspace  device, 256-byte aligned, at least
  *       linear_loss_workspace_bytes(T, V, D, slots, backward) bytes (slots 0
  *       for cross entropy; backward 1 also serves the forward call).  Its
