@@ -245,21 +245,30 @@ __global__ __launch_bounds__(256) void loss_select_kernel(SelectArgs p)
             }
         }
         const int64_t c0 = p.place ? t0 / kOwnCount * kOwnCount : 0, c1 = p.place ? t0 + kSelRows : p.T;
-        for (int64_t t = c0 + threadIdx.x; t < min(p.T, c1); t += 256) {
-            int label;
-            const bool kept = row_state(p.src, t, label) != ROW_OUT;
-            const int at = row_group(label);
+        const int64_t c_end = min(p.T, c1);
+        for (int64_t t1 = c0 + threadIdx.x; t1 - threadIdx.x < c_end; t1 += 1024) {
+            int at[4];                       // four rows a lane at once; -1: none
 #pragma unroll
-            for (int r = 0; r < kSelRows; ++r)
-                c[r] += kept && ((at == g[r] && t < upto[r]) || (!p.place && at < g[r]));
-            c[kSelRows] += kept;
+            for (int u = 0; u < 4; ++u) {
+                const int64_t t = t1 + u * 256;
+                int label = -1;
+                const bool kept = t < c_end && row_state(p.src, t, label) != ROW_OUT;
+                at[u] = kept ? row_group(label) : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t t = t1 + u * 256;
+#pragma unroll
+                for (int r = 0; r < kSelRows; ++r)
+                    c[r] += __popcll(__ballot((at[u] == g[r] && t < upto[r]) ||
+                                              (!p.place && at[u] >= 0 && at[u] < g[r])));
+                c[kSelRows] += __popcll(__ballot(at[u] >= 0));
+            }
         }
+        if ((threadIdx.x & 63) == 0)
 #pragma unroll
-        for (int r = 0; r <= kSelRows; ++r) {
-            c[r] = wave_sum(c[r]);
-            if ((threadIdx.x & 63) == 0)
+            for (int r = 0; r <= kSelRows; ++r)
                 front[threadIdx.x >> 6][r] = c[r];
-        }
         __syncthreads();
         const int r = threadIdx.x;
         if (firsts) {
