@@ -250,8 +250,8 @@ __device__ __forceinline__ void store_bf16_block(uint16_t* C, int64_t ldc, int N
 // range of rows, further k-tiles of the same loop with the rests at the targets and
 // zeros elsewhere (3686 rows: 115 k-tiles, and 19 rows a tile on average).  The norm of
 // dW's error at 1100 x 11001 x 520 is that of one rounding, and 1.44 times it
-// without; gradients and loss of 1024 x 50257 x 512 take 283 us, 287 without, of
-// 528 x 11007 x 1024 77, 74.
+// without; gradients and loss of 1024 x 50257 x 512 take 281 us, 276 without, of
+// 528 x 11007 x 1024 with half of the rows kept 77, 73.
 //   GRAD, DX  load W with the non-temporal hint where it is larger than the
 //         Infinity Cache (w_nt), which then cannot hand it from one to the other.
 // Workgroup `block` of `blocks`; lds: S::LDS bytes.
