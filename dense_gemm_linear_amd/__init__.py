@@ -16,6 +16,13 @@ Functions mirror the C entry points:
   linear_cross_entropy_grad(X, W, labels, loss, lse, dloss, ...) -> (dX, dW)
   linear_distillation(X, W, index, teacher, ...) -> (loss, lse, logp)
   linear_distillation_grad(X, W, index, teacher, lse, logp, dloss, ...) -> (dX, dW)
+  group_sort(ids, groups) -> (offsets, order, place)
+  group_gather(X, place) -> Xs
+  group_combine(Y, place, weights=None) -> out
+  group_combine_grad(dout, Y, place, weights) -> (dY, dweights)
+  group_linear(X, W, offsets, order=None, ...) -> Y
+  group_linear_grad(dY, X, W, offsets, order=None, ...) -> (dX, dW)
+  linear_adapters(X, W, A, B, offsets, order, ...) -> Y
   gemm_status_string(code) -> str
 """
 from __future__ import annotations
@@ -49,7 +56,10 @@ EXPORTS = ("select_tile", "shuffle_b_bytes", "shuffle_b", "gemm_bf16", "gemm_fp8
            "gemm_bf16_ws", "gemm_fp8_scaled_ws", "gemm_bf16_ex", "gemm_fp8_scaled_ex", "shuffle_b_t",
            "transpose_2d", "gemm_plan", "gemm_bf16_noalloc", "gemm_read_probe",
            "linear_loss_workspace_bytes", "linear_cross_entropy", "linear_cross_entropy_grad",
-           "linear_distillation", "linear_distillation_grad")
+           "linear_distillation", "linear_distillation_grad", "group_sort_workspace_bytes", "group_sort",
+           "group_gather", "group_combine", "group_combine_grad", "group_linear",
+           "group_linear_grad_workspace_bytes", "group_linear_grad", "linear_adapters_workspace_bytes",
+           "linear_adapters")
 
 # gemm_activation
 GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_SILU, GEMM_ACT_GELU_ERF, GEMM_ACT_GELU_TANH = 0, 1, 2, 3, 4
@@ -278,6 +288,29 @@ def _load_lib():
     lib.linear_distillation_grad.argtypes = head + [P, I64, P, I64, I64, I64, I64, I64, F, P, P] + \
         grads + space
     lib.linear_distillation_grad.restype = ctypes.c_int
+    stack = [P, I64, I64]                                         # pointer, pitch, group stride
+    lib.group_sort_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.group_sort_workspace_bytes.restype = ctypes.c_size_t
+    lib.group_sort.argtypes = [P, I64, I64, I64, I64, P, P, P] + space
+    lib.group_sort.restype = ctypes.c_int
+    lib.group_gather.argtypes = [P, I64, P, I64, I64, I64, ctypes.c_int32, P, I64, P]
+    lib.group_gather.restype = ctypes.c_int
+    lib.group_combine.argtypes = [P, I64, P, P, I64, I64, I64, I64, P, I64, P]
+    lib.group_combine.restype = ctypes.c_int
+    lib.group_combine_grad.argtypes = [P, I64, P, I64, P, P, I64, I64, I64, I64, P, I64, P, P]
+    lib.group_combine_grad.restype = ctypes.c_int
+    lib.group_linear.argtypes = [P, I64] + stack + [P, P, I64, I64, I64, I64, I64, ctypes.c_int32, P, I64,
+                                                    P, I64, P]
+    lib.group_linear.restype = ctypes.c_int
+    lib.group_linear_grad_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.group_linear_grad_workspace_bytes.restype = ctypes.c_size_t
+    lib.group_linear_grad.argtypes = [P, I64, P, I64] + stack + [P, P, I64, I64, I64, I64, I64, P, I64] + \
+        stack + space
+    lib.group_linear_grad.restype = ctypes.c_int
+    lib.linear_adapters_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.linear_adapters_workspace_bytes.restype = ctypes.c_size_t
+    lib.linear_adapters.argtypes = head + stack + stack + [P, P, P, I64, I64, I64, I64, I64, P, I64] + space
+    lib.linear_adapters.restype = ctypes.c_int
     lib.gemm_status_string.argtypes = [ctypes.c_int]
     lib.gemm_status_string.restype = ctypes.c_char_p
     return lib
@@ -831,3 +864,303 @@ def linear_distillation_grad(X, W, index, teacher, lse, logp, dloss, *, scale: f
                        lse.data_ptr(), logp.data_ptr(), dloss.data_ptr(), count,
                        *_grad_pointers(dX, dW)), ws, nbytes)
     return dX, dW
+
+
+# ------------------------- linear layers whose weight depends on the row
+def group_sort_workspace_bytes(T: int, slots: int, groups: int) -> int:
+    """Workspace of group_sort for ids [T, slots]: 0 up to 8192 slots."""
+    return int(lib.group_sort_workspace_bytes(T, slots, groups))
+
+
+def group_linear_grad_workspace_bytes(T: int, slots: int, K: int) -> int:
+    """Workspace of group_linear_grad for X [T, K] with an order, where dW is asked for."""
+    return int(lib.group_linear_grad_workspace_bytes(T, slots, K))
+
+
+def linear_adapters_workspace_bytes(T: int, R: int, groups: int) -> int:
+    """Workspace of linear_adapters for T rows and adapters of rank R."""
+    return int(lib.linear_adapters_workspace_bytes(T, R, groups))
+
+
+def _typed(fn: str, name: str, t, *dtypes):
+    if not isinstance(t, _torch().Tensor) or t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} must be a {' or '.join(str(d) for d in dtypes)} tensor")
+
+
+def _rows_of(fn: str, name: str, t, shape):
+    """A 2-D view of this shape (None: any extent) with contiguous rows."""
+    if t.dim() != 2 or any(w is not None and n != w for n, w in zip(t.shape, shape)) or \
+            (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        want = ", ".join("any" if w is None else str(w) for w in shape)
+        raise ValueError(f"{fn}: {name} must be a [{want}] tensor with contiguous rows")
+
+
+def _vector(fn: str, name: str, t, n: int):
+    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{fn}: {name} must be a contiguous vector of {n} values")
+
+
+def _stack_of(fn: str, name: str, t, shape):
+    """A 3-D view of this shape with contiguous rows, matrix after matrix."""
+    if t.dim() != 3 or any(w is not None and n != w for n, w in zip(t.shape, shape)) or \
+            (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) < t.shape[2]):
+        want = ", ".join("any" if w is None else str(w) for w in shape)
+        raise ValueError(f"{fn}: {name} must be a [{want}] tensor with contiguous rows")
+
+
+def _stack_args(t):
+    """Pointer, pitch and group stride; an extent of one says nothing by its stride."""
+    G, rows, width = t.shape
+    pitch = t.stride(1) if rows > 1 else (width + 7) // 8 * 8
+    return t.data_ptr(), pitch, (t.stride(0) if G > 1 else rows * pitch)
+
+
+def _same_device(fn: str, first, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device != first.device):
+            raise ValueError(f"{fn}: {name} must be a device tensor on {first.device}")
+
+
+def _group_workspace(fn: str, like, need: int, workspace):
+    torch = _torch()
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        # freed on return: the caching allocator reuses it on this stream only
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous device tensor on {like.device}")
+    nbytes = workspace.numel() * workspace.element_size()
+    if nbytes < need:
+        raise ValueError(f"{fn}: workspace holds {nbytes} bytes, {need} are needed")
+    return workspace, nbytes
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _group_call(fn: str, device_of, *args):
+    # launches go to the operands' device, whichever device is current
+    with _torch().cuda.device(device_of.device):
+        st = getattr(lib, fn)(*args, _stream_ptr(device_of))
+    if st != GEMM_OK:
+        raise GemmError(fn, st)
+
+
+def group_sort(ids, groups: int, *, workspace=None):
+    """Sort the slots of ids (int64 [T, slots], or [T]) by group id, stable.
+    Returns int32 (offsets [groups + 1], order [T * slots], place [T, slots]):
+    group g's rows are the sorted positions offsets[g] .. offsets[g + 1] - 1,
+    order[p] is the slot t * slots + j at position p, place[t, j] the position of a
+    slot.  An id outside [0, groups) takes no part: its place is -1, and it
+    stands in order behind the others."""
+    torch = _torch()
+    fn = "group_sort"
+    _typed(fn, "ids", ids, torch.int64)
+    if ids.dim() == 1:
+        ids = ids[:, None]
+    _rows_of(fn, "ids", ids, (None, None))
+    _same_device(fn, ids, ids=ids)
+    T, k = ids.shape
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device=ids.device)
+    order = torch.empty(T * k, dtype=torch.int32, device=ids.device)
+    place = torch.empty((T, k), dtype=torch.int32, device=ids.device)
+    ws, nbytes = _group_workspace(fn, ids, group_sort_workspace_bytes(T, k, groups), workspace)
+    _group_call(fn, ids, ids.data_ptr(), _pitch(ids), T, k, groups, offsets.data_ptr(), order.data_ptr(),
+                place.data_ptr(), _ptr(ws), nbytes)
+    return offsets, order, place
+
+
+def _place(fn: str, place, T=None):
+    _typed(fn, "place", place, _torch().int32)
+    _rows_of(fn, "place", place, (T, None))
+    if not place.is_contiguous():
+        raise ValueError(f"{fn}: place must be contiguous")
+    return place.shape
+
+
+def _group_out(fn: str, name: str, out, shape, dtype, like):
+    if out is None:
+        return _torch().empty(shape, dtype=dtype, device=like.device)
+    _typed(fn, name, out, dtype)
+    (_rows_of if len(shape) == 2 else _stack_of)(fn, name, out, shape)
+    return out
+
+
+def group_gather(X, place, out=None):
+    """Xs [T * slots, D] with Xs[place[t, j]] = X[t]: the rows of X (elements of 1, 2
+    or 4 bytes) in sorted order.  Rows behind the last slot that takes part are
+    not written.  The gradient of X is group_combine(dXs, place)."""
+    fn = "group_gather"
+    if not isinstance(X, _torch().Tensor) or X.element_size() not in (1, 2, 4):
+        raise ValueError(f"{fn}: X must be a tensor of 1-, 2- or 4-byte elements")
+    _rows_of(fn, "X", X, (None, None))
+    T, k = _place(fn, place, X.shape[0])
+    out = _group_out(fn, "out", out, (T * k, X.shape[1]), X.dtype, X)
+    _same_device(fn, X, X=X, place=place, out=out)
+    _group_call(fn, X, X.data_ptr(), _pitch(X), place.data_ptr(), T, k, X.shape[1], X.element_size(),
+                out.data_ptr(), _pitch(out))
+    return out
+
+
+def _weights(fn: str, weights, T: int, k: int):
+    if weights is None:
+        return None, 0
+    _typed(fn, "weights", weights, _torch().float32)
+    _rows_of(fn, "weights", weights, (T, k))
+    return weights.data_ptr(), _pitch(weights)
+
+
+def group_combine(Y, place, weights=None, out=None):
+    """out [T, D] with out[t] = sum_j weights[t, j] * Y[place[t, j]] (Y bf16 [T * slots,
+    D], weights float32 [T, slots] or None for 1), in fp32, rounded once; slots that
+    take no part are left out."""
+    torch = _torch()
+    fn = "group_combine"
+    _typed(fn, "Y", Y, torch.bfloat16)
+    T, k = _place(fn, place)
+    _rows_of(fn, "Y", Y, (T * k, None))
+    w, ldw = _weights(fn, weights, T, k)
+    out = _group_out(fn, "out", out, (T, Y.shape[1]), torch.bfloat16, Y)
+    _same_device(fn, Y, Y=Y, place=place, weights=weights, out=out)
+    _group_call(fn, Y, Y.data_ptr(), _pitch(Y), place.data_ptr(), w, ldw, T, k, Y.shape[1], out.data_ptr(),
+                _pitch(out))
+    return out
+
+
+def group_combine_grad(dout, Y, place, weights=None, *, need_dY: bool = True, need_dweights: bool = True,
+                       dY=None):
+    """The gradients of group_combine for dout bf16 [T, D]: (dY bf16 [T * slots, D],
+    dweights float32 [T, slots]), None for one that is not needed.  Rows of dY
+    behind the last slot that takes part are not written; dY may be Y itself.  Y is
+    used for dweights only (None if not needed)."""
+    torch = _torch()
+    fn = "group_combine_grad"
+    _typed(fn, "dout", dout, torch.bfloat16)
+    T, k = _place(fn, place)
+    _rows_of(fn, "dout", dout, (T, None))
+    D = dout.shape[1]
+    if need_dweights or Y is not None:
+        _typed(fn, "Y", Y, torch.bfloat16)
+        _rows_of(fn, "Y", Y, (T * k, D))
+    if not need_dY and not need_dweights:
+        raise ValueError(f"{fn}: neither dY nor dweights is asked for")
+    if not need_dY and dY is not None:
+        raise ValueError(f"{fn}: dY given, but need_dY is false")
+    w, ldw = _weights(fn, weights, T, k)
+    if need_dY:
+        dY = _group_out(fn, "dY", dY, (T * k, D), torch.bfloat16, dout)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device) if need_dweights else None
+    _same_device(fn, dout, dout=dout, Y=Y, place=place, weights=weights, dY=dY)
+    _group_call(fn, dout, dout.data_ptr(), _pitch(dout), _ptr(Y), 0 if Y is None else _pitch(Y),
+                place.data_ptr(), w, ldw, T, k, D, _ptr(dY), 0 if dY is None else _pitch(dY), _ptr(dweights))
+    return dY, dweights
+
+
+def _group_operands(fn: str, X, W, offsets, order, slots: int):
+    """(T, k, S) of a grouped product, its operands checked."""
+    torch = _torch()
+    _typed(fn, "X", X, torch.bfloat16)
+    _typed(fn, "W", W, torch.bfloat16)
+    _typed(fn, "offsets", offsets, torch.int32)
+    _rows_of(fn, "X", X, (None, None))
+    _stack_of(fn, "W", W, (None, None, X.shape[1]))
+    _vector(fn, "offsets", offsets, W.shape[0] + 1)
+    T = X.shape[0]
+    if order is None:
+        if slots != 1:
+            raise ValueError(f"{fn}: slots needs an order")
+    else:
+        _typed(fn, "order", order, torch.int32)
+        if slots < 1:
+            raise ValueError(f"{fn}: slots must be at least 1")
+        _vector(fn, "order", order, T * slots)
+    _same_device(fn, X, X=X, W=W, offsets=offsets, order=order)
+    return T, slots, T * slots
+
+
+def group_linear(X, W, offsets, order=None, *, slots: int = 1, activation=None, mul=None, out=None):
+    """Y [S, N] with Y[p] = act(x W[g]^T) * mul[p] for the rows p of group g, offsets[g] <=
+    p < offsets[g + 1]; W bf16 [groups, N, K] as it lies in memory.  x is X[order[p] //
+    slots] (X bf16 [T, K], S = T * slots; no sorted copy is made), or X[p] without an
+    order (X sorted, S = T).  activation: one of ACTIVATIONS; mul bf16 [S, N], which
+    may be `out` itself.  Rows from offsets[-1] on are not written."""
+    torch = _torch()
+    fn = "group_linear"
+    T, k, S = _group_operands(fn, X, W, offsets, order, slots)
+    G, N, K = W.shape
+    act = ACTIVATIONS[activation] if not isinstance(activation, int) else activation
+    if mul is not None:
+        _typed(fn, "mul", mul, torch.bfloat16)
+        _rows_of(fn, "mul", mul, (S, N))
+    out = _group_out(fn, "out", out, (S, N), torch.bfloat16, X)
+    _same_device(fn, X, mul=mul, out=out)
+    _group_call(fn, X, X.data_ptr(), _row_pitch8(X), *_stack_args(W), offsets.data_ptr(), _ptr(order), T, k, G,
+                N, K, act, _ptr(mul), 0 if mul is None else _pitch(mul), out.data_ptr(), _pitch(out))
+    return out
+
+
+def group_linear_grad(dY, X, W, offsets, order=None, *, slots: int = 1, need_dX: bool = True,
+                      need_dW: bool = True, dX=None, dW=None, workspace=None):
+    """The gradients of group_linear without activation and mul, for dY bf16 [S, N] in
+    sorted order: (dX bf16 [S, K], sorted, dW bf16 like W), None for one that is not
+    needed.  group_combine(dX, place) joins the rows of a token.  Rows of dX from
+    offsets[-1] on are not written; dW is zero for a group without rows.  workspace:
+    a uint8 tensor of group_linear_grad_workspace_bytes bytes (with an order, for dW)."""
+    torch = _torch()
+    fn = "group_linear_grad"
+    T, k, S = _group_operands(fn, X, W, offsets, order, slots)
+    G, N, K = W.shape
+    _typed(fn, "dY", dY, torch.bfloat16)
+    _rows_of(fn, "dY", dY, (S, N))
+    if not need_dX and not need_dW:
+        raise ValueError(f"{fn}: neither dX nor dW is asked for")
+    for name, need, given in (("dX", need_dX, dX), ("dW", need_dW, dW)):
+        if given is not None and not need:
+            raise ValueError(f"{fn}: {name} given, but need_{name} is false")
+    if need_dX:
+        dX = _group_out(fn, "dX", dX, (S, K), torch.bfloat16, X)
+    if need_dW:
+        dW = _group_out(fn, "dW", dW, (G, N, K), torch.bfloat16, X)
+    _same_device(fn, X, dY=dY, dX=dX, dW=dW)
+    need = group_linear_grad_workspace_bytes(T, k, K) if need_dW and order is not None else 0
+    ws, nbytes = _group_workspace(fn, X, need, workspace)
+    _group_call(fn, X, dY.data_ptr(), _row_pitch8(dY), X.data_ptr(), _row_pitch8(X), *_stack_args(W),
+                offsets.data_ptr(), _ptr(order), T, k, G, N, K, _ptr(dX), 0 if dX is None else _pitch(dX),
+                *((None, 0, 0) if dW is None else _stack_args(dW)), _ptr(ws), nbytes)
+    return dX, dW
+
+
+def linear_adapters(X, W, A, B, offsets, order, *, scale=None, out=None, workspace=None):
+    """Y [T, N] = X W^T, plus scale[g] * (X A[g]^T) B[g]^T in the rows of group g: one
+    shared projection (W bf16 [N, K]) and the low-rank adapters of many requests
+    (A bf16 [groups, R, K], B bf16 [groups, N, R], scale float32 [groups] or None for 1).
+    offsets and order as group_sort(adapter of each row, groups) gives them; rows of
+    no adapter get the projection alone.  workspace: a uint8 tensor of
+    linear_adapters_workspace_bytes bytes."""
+    torch = _torch()
+    fn = "linear_adapters"
+    for name, t in (("X", X), ("W", W), ("A", A), ("B", B)):
+        _typed(fn, name, t, torch.bfloat16)
+    _typed(fn, "offsets", offsets, torch.int32)
+    _typed(fn, "order", order, torch.int32)
+    _rows_of(fn, "X", X, (None, None))
+    T, K = X.shape
+    _rows_of(fn, "W", W, (None, K))
+    N = W.shape[0]
+    _stack_of(fn, "A", A, (None, None, K))
+    G, R = A.shape[:2]
+    _stack_of(fn, "B", B, (G, N, R))
+    _vector(fn, "offsets", offsets, G + 1)
+    _vector(fn, "order", order, T)
+    if scale is not None:
+        _typed(fn, "scale", scale, torch.float32)
+        _vector(fn, "scale", scale, G)
+    out = _group_out(fn, "out", out, (T, N), torch.bfloat16, X)
+    _same_device(fn, X, X=X, W=W, A=A, B=B, offsets=offsets, order=order, scale=scale, out=out)
+    ws, nbytes = _group_workspace(fn, X, linear_adapters_workspace_bytes(T, R, G), workspace)
+    _group_call(fn, X, X.data_ptr(), _row_pitch8(X), W.data_ptr(), _row_pitch8(W), *_stack_args(A),
+                *_stack_args(B), _ptr(scale), offsets.data_ptr(), order.data_ptr(), T, N, K, R, G,
+                out.data_ptr(), _pitch(out), _ptr(ws), nbytes)
+    return out

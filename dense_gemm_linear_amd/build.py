@@ -22,7 +22,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 # (element type, kernel variant, ladder family), so the instances build in
 # parallel translation units
 SOURCES = [("api.cpp", "api", []), ("select_tile.cpp", "select_tile", []), ("misc.hip", "misc", []),
-           ("skinny.hip", "skinny", []), ("loss_api.cpp", "loss_api", []), ("loss.hip", "loss", [])] + \
+           ("skinny.hip", "skinny", []), ("loss_api.cpp", "loss_api", []), ("loss.hip", "loss", []),
+           ("group_api.cpp", "group_api", []), ("group.hip", "group", [])] + \
+    [("group_product.hip", f"group_product{r}", [f"-DDG_GROUP_ROLE={r}"]) for r in range(5)] + \
     [("tiled_inst.hip", f"tiled_d{d}_m{m}_f{f}",
       [f"-DDG_INST_DT={d}", f"-DDG_INST_MODE={m}", f"-DDG_INST_FAMILY={f}"])
      for d in (0, 1) for m in (0, 1, 2, 3) for f in (0, 1)]

@@ -1,0 +1,489 @@
+// Rows sorted by group and back: the slots' stable sort, the rows' copy into
+// that order, their weighted join and its gradient.  All of it moves memory;
+// nothing is multiplied but by a weight.
+#include "group.hpp"
+#include "kernels.hpp"
+
+#include <algorithm>
+
+namespace dg {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Sort.  A stable counting sort of S slots by group id, ids outside [0, groups)
+// behind the rest as a group of their own (`none`).  One workgroup of 16 waves
+// takes a chunk of slots, every wave a contiguous part of it, 64 slots at a
+// time:
+//   1. each wave counts its slots by group;
+//   2. thread g turns group g's counts into the position of each wave's first
+//      slot of it: rows of all lower groups, then of the waves (and chunks)
+//      before;
+//   3. each wave walks its slots again; a slot's position is its group's next
+//      one plus the number of lower lanes with the same group, which log2(groups)
+//      ballots tell.
+// Integers only: the result does not depend on any order of execution.
+constexpr int kSortWaves = 16;
+constexpr int kSortOne = 8192;         // slots up to which one workgroup takes all
+constexpr int kSortChunks = 256;       // at most
+
+struct SortArgs {
+    const int64_t* ids;
+    int64_t ld;
+    int k;
+    uint32_t k_mul;        // 2^32 / k rounded up; 0: k is 1
+    int dense;             // the pitch of ids is k
+    int S, groups;
+    int chunk;
+    int* counts;           // [chunks][groups + 1], null: one chunk
+    int* offsets;
+    int* order;
+    int* place;
+};
+
+__device__ __forceinline__ int slot_group(const SortArgs& p, int s)
+{
+    int64_t at = s;
+    if (!p.dense) {
+        const int t = p.k_mul ? (int)__umulhi((uint32_t)s, p.k_mul) : s;
+        at = t * p.ld + (s - t * p.k);
+    }
+    const int64_t id = p.ids[at];
+    return id >= 0 && id < p.groups ? (int)id : p.groups;
+}
+
+__device__ __forceinline__ int wave_scan(int x, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int y = __shfl_up(x, d);
+        x += lane >= d ? y : 0;
+    }
+    return x;
+}
+
+__global__ __launch_bounds__(1024) void group_count_kernel(SortArgs p)
+{
+    __shared__ int found[kMaxGroups + 1];
+    for (int g = threadIdx.x; g <= p.groups; g += 1024)
+        found[g] = 0;
+    __syncthreads();
+    const int s0 = (int)blockIdx.x * p.chunk, s1 = min(p.S, s0 + p.chunk);
+    for (int s = s0 + (int)threadIdx.x; s < s1; s += 1024)
+        atomicAdd(&found[slot_group(p, s)], 1);
+    __syncthreads();
+    for (int g = threadIdx.x; g <= p.groups; g += 1024)
+        p.counts[(int64_t)blockIdx.x * (p.groups + 1) + g] = found[g];
+}
+
+__global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
+{
+    __shared__ int next[kSortWaves][kMaxGroups + 1];
+    __shared__ int sums[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int G = p.groups;
+    for (int g = lane; g <= G; g += 64)
+        next[wave][g] = 0;
+    wave_lds_order();
+    const int s0 = (int)blockIdx.x * p.chunk, s1 = min(p.S, s0 + p.chunk);
+    const int part = (s1 - s0 + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
+    const int w0 = min(s1, s0 + wave * part), w1 = min(s1, w0 + part);
+    for (int s = w0 + lane; s < w1; s += 64)
+        atomicAdd(&next[wave][slot_group(p, s)], 1);
+    __syncthreads();
+    // thread g: rows of group g in all (the group none: thread 0, last)
+    auto totals = [&](int g, int& before) {
+        int total = 0;
+        before = 0;
+        if (p.counts) {
+            for (int c = 0; c < (int)gridDim.x; ++c) {
+                const int n = p.counts[(int64_t)c * (G + 1) + g];
+                before += c < (int)blockIdx.x ? n : 0;
+                total += n;
+            }
+        } else {
+            for (int w = 0; w < kSortWaves; ++w)
+                total += next[w][g];
+        }
+        return total;
+    };
+    auto starts = [&](int g, int at) {
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int n = next[w][g];
+            next[w][g] = at;
+            at += n;
+        }
+    };
+    int before = 0;
+    const int total = tid < G ? totals(tid, before) : 0;
+    const int upto = wave_scan(total, lane);
+    if (lane == 63)
+        sums[wave] = upto;
+    __syncthreads();
+    int base = 0, all = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        base += w < wave ? sums[w] : 0;
+        all += sums[w];
+    }
+    if (tid < G) {
+        const int first = base + upto - total;
+        starts(tid, first + before);
+        if (blockIdx.x == 0)
+            p.offsets[tid] = first;
+    }
+    if (tid == 0) {
+        int none_before = 0;
+        if (p.counts)
+            for (int c = 0; c < (int)blockIdx.x; ++c)
+                none_before += p.counts[(int64_t)c * (G + 1) + G];
+        starts(G, all + none_before);
+        if (blockIdx.x == 0)
+            p.offsets[G] = all;
+    }
+    __syncthreads();
+    const int bits = 32 - __clz(G);
+    for (int s = w0; s < w1; s += 64) {
+        const bool in = s + lane < w1;
+        const int g = in ? slot_group(p, s + lane) : 0;
+        uint64_t same = __ballot(in);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t set = __ballot((g >> b) & 1);
+            same &= (g >> b) & 1 ? set : ~set;
+        }
+        const int rank = __popcll(same & ((UINT64_C(1) << lane) - 1));
+        const int at = next[wave][g] + rank;
+        wave_lds_order();
+        if (in && rank == 0)
+            next[wave][g] = at + __popcll(same);
+        wave_lds_order();
+        if (in) {
+            p.order[at] = s + lane;
+            p.place[s + lane] = g < G ? at : -1;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Rows.  Pieces of 16 bytes; rows and their starts may have any alignment (the
+// hardware takes unaligned vector accesses).  The last piece of a row whose
+// length is no multiple of 16 bytes begins 16 bytes before its end: both
+// pieces write the same values where they overlap.
+typedef i32x4 i32x4_u __attribute__((aligned(1)));
+
+__device__ __forceinline__ i32x4 load_piece(const void* p) { return *static_cast<const i32x4_u*>(p); }
+__device__ __forceinline__ void store_piece(void* p, i32x4 v) { *static_cast<i32x4_u*>(p) = v; }
+
+struct GatherArgs {
+    const uint8_t* X;
+    int64_t ldx_b;
+    const int* place;
+    int T, k, S;
+    int row_b, pieces;
+    uint8_t* Xs;
+    int64_t ldxs_b;
+};
+
+// TPR threads a row.  A token's row is read once and written to each of its
+// slots' places (a copy by sorted position reads it k times).
+template <int TPR>
+__global__ __launch_bounds__(256) void group_gather_kernel(GatherArgs p)
+{
+    const int t = (int)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+    if (t >= p.T)
+        return;
+    const uint8_t* from = p.X + t * p.ldx_b;
+    const int* place = p.place + (int64_t)t * p.k;
+    if (p.row_b < 16) {
+        for (int j = 0; j < p.k; ++j)
+            if ((uint32_t)place[j] < (uint32_t)p.S)
+                for (int b = (int)threadIdx.x % TPR; b < p.row_b; b += TPR)
+                    p.Xs[place[j] * p.ldxs_b + b] = from[b];
+        return;
+    }
+    for (int q = (int)threadIdx.x % TPR; q < p.pieces; q += TPR) {
+        const int at = min(q * 16, p.row_b - 16);
+        const i32x4 v = load_piece(from + at);
+        for (int j = 0; j < p.k; ++j) {
+            const int to = place[j];
+            if ((uint32_t)to < (uint32_t)p.S)
+                store_piece(p.Xs + to * p.ldxs_b + at, v);
+        }
+    }
+}
+
+struct PickArgs {
+    const uint16_t* X;
+    int64_t ldx;
+    const int* offsets;
+    const int* order;
+    uint32_t k_mul;
+    int S, groups, K;
+    uint16_t* Xs;
+};
+
+// The same by sorted position, for whom the places are not at hand: rows of K
+// (a multiple of 8) values, 16-byte aligned.
+template <int TPR>
+__global__ __launch_bounds__(256) void group_pick_kernel(PickArgs p)
+{
+    const int at = (int)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+    if (at >= min(p.S, p.offsets[p.groups]))
+        return;
+    const uint32_t slot = (uint32_t)p.order[at];
+    if (slot >= (uint32_t)p.S)
+        return;
+    const int64_t row = p.k_mul ? __umulhi(slot, p.k_mul) : slot;
+    const i32x4* from = reinterpret_cast<const i32x4*>(p.X + row * p.ldx);
+    i32x4* to = reinterpret_cast<i32x4*>(p.Xs + (int64_t)at * p.K);
+    for (int q = (int)threadIdx.x % TPR; q < p.K / 8; q += TPR)
+        to[q] = from[q];
+}
+
+struct CombineArgs {
+    const uint16_t* Y;
+    int64_t ldy;
+    const int* place;
+    const float* weights;
+    int64_t ldw;
+    int T, k, S, D, pieces;
+    uint16_t* out;
+    int64_t ldo;
+    const uint16_t* dout;
+    int64_t lddo;
+    uint16_t* dY;
+    int64_t lddy;
+    float* dweights;
+};
+
+__device__ __forceinline__ void unpack8(i32x4 v, float (&f)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float((uint32_t)v[i] << 16);
+        f[2 * i + 1] = __uint_as_float((uint32_t)v[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ i32x4 pack8(const float (&f)[8])
+{
+    i32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (int)((uint32_t)bf16_rne(f[2 * i]) | (uint32_t)bf16_rne(f[2 * i + 1]) << 16);
+    return v;
+}
+
+// out[t] = sum_j w[t][j] Y[place[t][j]], j ascending, in fp32, rounded once.
+template <int TPR>
+__global__ __launch_bounds__(256) void group_combine_kernel(CombineArgs p)
+{
+    const int t = (int)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+    if (t >= p.T)
+        return;
+    const int* place = p.place + (int64_t)t * p.k;
+    const float* w = p.weights ? p.weights + t * p.ldw : nullptr;
+    uint16_t* out = p.out + t * p.ldo;
+    if (p.D < 8) {
+        for (int d = (int)threadIdx.x % TPR; d < p.D; d += TPR) {
+            float s = 0.f;
+            for (int j = 0; j < p.k; ++j)
+                if ((uint32_t)place[j] < (uint32_t)p.S)
+                    s = fmaf(w ? w[j] : 1.f, bf16_to_f32(p.Y[place[j] * p.ldy + d]), s);
+            out[d] = bf16_rne(s);
+        }
+        return;
+    }
+    for (int q = (int)threadIdx.x % TPR; q < p.pieces; q += TPR) {
+        const int at = min(q * 8, p.D - 8);
+        float sum[8] = {};
+        for (int j = 0; j < p.k; ++j) {
+            const int from = place[j];
+            if ((uint32_t)from >= (uint32_t)p.S)
+                continue;
+            float y[8];
+            unpack8(load_piece(p.Y + from * p.ldy + at), y);
+            const float wj = w ? w[j] : 1.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sum[i] = fmaf(wj, y[i], sum[i]);
+        }
+        store_piece(out + at, pack8(sum));
+    }
+}
+
+// One wave a slot (t, j): dY[place] = w dout[t], dw = <dout[t], Y[place]>.  The
+// slots of a token share a workgroup, and its dout comes from the L1.
+__global__ __launch_bounds__(256) void group_combine_grad_kernel(CombineArgs p, uint32_t k_mul)
+{
+    const int s = (int)blockIdx.x * 4 + (int)threadIdx.x / 64;
+    const int lane = threadIdx.x & 63;
+    if (s >= p.T * p.k)
+        return;
+    const int t = k_mul ? (int)__umulhi((uint32_t)s, k_mul) : s;
+    const int at = p.place[s];
+    if ((uint32_t)at >= (uint32_t)p.S) {
+        if (p.dweights && lane == 0)
+            p.dweights[s] = 0.f;
+        return;
+    }
+    const float w = p.weights ? p.weights[t * p.ldw + (s - t * p.k)] : 1.f;
+    const uint16_t* dout = p.dout + t * p.lddo;
+    const uint16_t* y = p.Y + at * p.ldy;
+    uint16_t* dy = p.dY ? p.dY + at * p.lddy : nullptr;
+    float sum = 0.f;
+    if (p.D < 8) {
+        if (lane < p.D) {
+            const float d = bf16_to_f32(dout[lane]);
+            if (p.dweights)
+                sum = d * bf16_to_f32(y[lane]);
+            if (dy)
+                dy[lane] = bf16_rne(w * d);
+        }
+    } else {
+        for (int q = lane; q < p.pieces; q += 64) {
+            // (the last piece counts what the one before it has not)
+            const int c = min(q * 8, p.D - 8);
+            float d[8], r[8];
+            unpack8(load_piece(dout + c), d);
+            if (p.dweights) {
+                unpack8(load_piece(y + c), r);
+                float part = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    part = c + i >= q * 8 ? fmaf(d[i], r[i], part) : part;
+                sum += part;
+            }
+            if (dy) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    r[i] = w * d[i];
+                store_piece(dy + c, pack8(r));
+            }
+        }
+    }
+    if (!p.dweights)
+        return;
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        sum += __shfl_xor(sum, d);
+    if (lane == 0)
+        p.dweights[s] = sum;
+}
+
+
+template <class Args, class... More>
+hipError_t launch(void (*kernel)(Args, More...), int64_t grid, int block, hipStream_t s, Args a, More... more)
+{
+    void* list[] = {&a, &more...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)grid), dim3((unsigned)block),
+                           list, 0, s);
+}
+
+}  // namespace
+
+SortPlan sort_plan(int64_t S, int64_t groups)
+{
+    SortPlan p = {S, 1, 0};
+    if (S > kSortOne) {
+        p.chunk = std::max<int64_t>(4096, cdiv(cdiv(S, kSortChunks), 1024) * 1024);
+        p.chunks = cdiv(S, p.chunk);
+        p.bytes = p.chunks * (groups + 1) * 4;
+    }
+    return p;
+}
+
+hipError_t group_sort(const SortCall& c)
+{
+    const SortPlan pl = sort_plan(c.T * c.k, c.groups);
+    SortArgs a;
+    a.ids = c.ids;
+    a.ld = c.ld_ids;
+    a.k = (int)c.k;
+    a.k_mul = divide_by(c.k);
+    a.dense = c.ld_ids == c.k;
+    a.S = (int)(c.T * c.k);
+    a.groups = (int)c.groups;
+    a.chunk = (int)pl.chunk;
+    a.counts = pl.chunks > 1 ? static_cast<int*>(c.ws) : nullptr;
+    a.offsets = c.offsets;
+    a.order = c.order;
+    a.place = c.place;
+    if (pl.chunks > 1) {
+        const hipError_t e = launch(group_count_kernel, pl.chunks, 1024, c.stream, a);
+        if (e != hipSuccess)
+            return e;
+    }
+    return launch(group_place_kernel, pl.chunks, 1024, c.stream, a);
+}
+
+hipError_t group_gather(const GatherCall& c)
+{
+    GatherArgs a;
+    a.X = c.X;
+    a.ldx_b = c.ldx_b;
+    a.place = c.place;
+    a.T = (int)c.T;
+    a.k = (int)c.k;
+    a.S = (int)(c.T * c.k);
+    a.row_b = (int)c.row_b;
+    a.pieces = (int)cdiv(c.row_b, 16);
+    a.Xs = c.Xs;
+    a.ldxs_b = c.ldxs_b;
+    if (a.pieces <= 64)
+        return launch(group_gather_kernel<64>, cdiv(c.T, 4), 256, c.stream, a);
+    return launch(group_gather_kernel<256>, c.T, 256, c.stream, a);
+}
+
+hipError_t group_pick(const PickCall& c)
+{
+    PickArgs a;
+    a.X = c.X;
+    a.ldx = c.ldx;
+    a.offsets = c.offsets;
+    a.order = c.order;
+    a.k_mul = divide_by(c.k);
+    a.S = (int)c.S;
+    a.groups = (int)c.groups;
+    a.K = (int)c.K;
+    a.Xs = c.Xs;
+    if (c.K <= 1024)
+        return launch(group_pick_kernel<64>, cdiv(c.S, 4), 256, c.stream, a);
+    return launch(group_pick_kernel<256>, c.S, 256, c.stream, a);
+}
+
+static CombineArgs combine_args(const CombineCall& c)
+{
+    CombineArgs a;
+    a.Y = c.Y;
+    a.ldy = c.ldy;
+    a.place = c.place;
+    a.weights = c.weights;
+    a.ldw = c.ld_weights;
+    a.T = (int)c.T;
+    a.k = (int)c.k;
+    a.S = (int)(c.T * c.k);
+    a.D = (int)c.D;
+    a.pieces = (int)cdiv(c.D, 8);
+    a.out = c.out;
+    a.ldo = c.ldo;
+    a.dout = c.dout;
+    a.lddo = c.lddo;
+    a.dY = c.dY;
+    a.lddy = c.lddy;
+    a.dweights = c.dweights;
+    return a;
+}
+
+hipError_t group_combine(const CombineCall& c)
+{
+    const CombineArgs a = combine_args(c);
+    if (a.pieces <= 64)
+        return launch(group_combine_kernel<64>, cdiv(c.T, 4), 256, c.stream, a);
+    return launch(group_combine_kernel<256>, c.T, 256, c.stream, a);
+}
+
+hipError_t group_combine_grad(const CombineCall& c)
+{
+    return launch(group_combine_grad_kernel, cdiv(c.T * c.k, 4), 256, c.stream, combine_args(c),
+                  divide_by(c.k));
+}
+
+}  // namespace dg

@@ -1,0 +1,730 @@
+// Products of rows that lie sorted by group, each group with a weight of its
+// own, and of all rows with one weight beside each group's low-rank pair.
+// With rows p of group g at offsets[g] <= p < offsets[g + 1]:
+//
+//   GROUP_FWD    Y[p] = act(W_g x) * mul[p], x = X[p] or X[order[p] / k]
+//   GROUP_DX     dX[p] = sum_n dY[p][n] W_g[n]
+//   GROUP_DW     dW_g = sum over its p of dY[p] x^T; zeros for a group of no row
+//   GROUP_ADAPT  Y[order[p]] = W x + B_g u[p], u = scale_g A_g x in two bf16
+//                halves from the kernel before
+//
+// Operands are taken as they lie in memory and staged in LDS k-tile by k-tile
+// (k_loop): one whose contraction axis is contiguous as gemm_ab_kernel stages
+// A, the others as rows that gfx950's transposing LDS read turns (dX's W, both
+// of dW's; see loss_kernels.hpp).  Rows of X are picked up by the loads
+// themselves: every lane of an LDS DMA has an offset of its own, so that rows in
+// any order cost what sorted ones cost, and no sorted copy of X is made.
+//
+// How many rows a group has is known on the device only.  Every workgroup
+// turns the offsets into the groups' first tiles (a scan over at most 1024
+// groups in LDS, under 2 us) and walks a persistent range of tiles; no host
+// synchronisation, no table from another launch.
+#pragma once
+
+#include "group.hpp"
+#include "loss_kernels.hpp"
+
+namespace dg {
+
+// FWD without act and mul is an instance of its own (GATED has them).
+enum { GROUP_FWD = 0, GROUP_DX = 1, GROUP_DW = 2, GROUP_ADAPT = 3, GROUP_GATED = 4 };
+
+struct GroupArgs {
+    const uint8_t* A;      // X (FWD, ADAPT), dY (DX, DW)
+    int64_t lda_b;         // pitches in bytes
+    const uint8_t* B;      // W (FWD, DX, ADAPT), sorted X (DW)
+    int64_t ldb_b, b_group;// bytes between two groups' W
+    const int* offsets;    // [groups + 1]
+    int groups;
+    int S;                 // sorted rows that the buffers hold
+    const int* order;      // FWD: null, A's rows are sorted
+    uint32_t k_mul;        // slot -> row of X (divide_by)
+    uint32_t a_bytes;      // order given: bytes of X
+    int M, N, K;           // M: DW's rows; N: columns of the output; K: not for DW
+    int tiles_n;
+    uint16_t* C;
+    int64_t ldc, c_group;  // c_group: DW, elements between two groups' dW
+    int c_vec;             // 16-byte stores of C's rows, 2: non-temporal
+    int b_nt;              // B is read once: non-temporal loads
+    int act;               // GATED
+    const uint16_t* mul;
+    int64_t ld_mul;
+    int mul_vec;           // mul's rows take 8-byte loads
+    const uint8_t* U;      // ADAPT: [S][2][R]
+    const uint8_t* LB;     // ADAPT: [groups][N][ldlb]
+    int64_t ldlb_b, lb_group;
+    int R;
+};
+
+constexpr int kTableLds = ((int)kMaxGroups + 4) * 4 + 64;
+
+// Tile shape: TM x TN outputs, WM x WN waves, ST stages of KTB bytes of K, OCC
+// waves per SIMD to leave registers for.
+template <int TM_, int TN_, int WM_, int WN_, int ST_, int KTB_, int OCC_>
+struct GroupShape {
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, ST = ST_, KTB = KTB_, OCC = OCC_;
+    static constexpr int R = 16;
+    static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    static constexpr int MR = TM / WM / R, NR = TN / WN / R;
+    static constexpr int A_BUF = TM * KTB, B_BUF = TN * KTB, STAGE = A_BUF + B_BUF;
+    static constexpr int A_DMA = A_BUF / 1024 / WAVES, B_DMA = B_BUF / 1024 / WAVES;
+    static constexpr int LOADS = A_DMA + B_DMA;
+    static constexpr int KT = KTB / 2;
+    static constexpr int WCOLS = TN / WN;
+    static constexpr int SROW = WCOLS * 2 + 16;
+    // after the stages: the waves' output blocks, the groups' table
+    static constexpr int OUT_AT = ST * STAGE, OUT_LDS = WAVES * R * SROW;
+    static constexpr int TABLE_AT = OUT_AT + OUT_LDS;
+    static constexpr int TABLE_LDS = kTableLds;
+    static constexpr int LDS = TABLE_AT + TABLE_LDS;
+    static constexpr int PER_CU = (160 * 1024 / LDS < 4 * OCC / WAVES || OCC == 1) ? 160 * 1024 / LDS
+                                                                                  : 4 * OCC / WAVES;
+    static_assert(MR >= 1 && NR >= 1 && MR * WM * R == TM && NR * WN * R == TN, "tile shape");
+    static_assert(A_DMA >= 1 && B_DMA >= 1 && A_DMA * 1024 * WAVES == A_BUF &&
+                      B_DMA * 1024 * WAVES == B_BUF, "DMA split");
+    static_assert(LDS <= 160 * 1024, "LDS budget");
+};
+
+// The groups' table in LDS.  first(i): where entry i begins, counted in units of
+// `unit` rows (rounded up per group); first(count): the end.  With COMPACT only
+// groups that have rows are entries, id(i) says which group entry i is, and the
+// unit is a row; else entry i is group i.  Offsets that are not ascending or lie
+// outside [0, S] are taken as the nearest that are, so that no index derived
+// from them leaves the buffers.
+struct GroupTable {
+    int* entry;            // [kMaxGroups + 1], COMPACT: first << 10 | id
+    int* sums;             // [16]
+    int count, shift;
+    __device__ __forceinline__ void at(uint8_t* lds)
+    {
+        entry = reinterpret_cast<int*>(lds);
+        sums = entry + kMaxGroups + 4;
+    }
+    __device__ __forceinline__ int first(int i) const { return (int)((uint32_t)entry[i] >> shift); }
+    __device__ __forceinline__ int id(int i) const { return entry[i] & 1023; }
+};
+
+// Rows of group g: [lo, hi).
+__device__ __forceinline__ int2 group_rows(const int* offsets, int g, int S)
+{
+    const int lo = min(max(offsets[g], 0), S);
+    return make_int2(lo, min(max(offsets[g + 1], lo), S));
+}
+
+template <int THREADS, bool COMPACT>
+__device__ __forceinline__ void build_table(GroupTable& t, const int* offsets, int groups, int S, int unit)
+{
+    constexpr int WAVES = THREADS / 64;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int each = (groups + THREADS - 1) / THREADS;
+    const int g0 = min(groups, tid * each), g1 = min(groups, g0 + each);
+    auto units = [&](int g) {
+        const int2 r = group_rows(offsets, g, S);
+        return COMPACT ? (int)(r.y > r.x) : (r.y - r.x + unit - 1) / unit;
+    };
+    int n = 0;
+    for (int g = g0; g < g1; ++g)
+        n += units(g);
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int y = __shfl_up(upto, d);
+        upto += lane >= d ? y : 0;
+    }
+    if (lane == 63)
+        t.sums[wave] = upto;
+    __syncthreads();
+    int at = upto - n, all = 0;
+    for (int w = 0; w < WAVES; ++w) {
+        at += w < wave ? t.sums[w] : 0;
+        all += t.sums[w];
+    }
+    for (int g = g0; g < g1; ++g) {
+        if constexpr (COMPACT) {
+            const int2 r = group_rows(offsets, g, S);
+            if (r.y > r.x) {
+                t.entry[at] = r.x << 10 | g;
+                ++at;
+                // (an entry ends where the next begins, the last at its own end)
+                if (at == all)
+                    t.entry[all] = r.y << 10;
+            }
+        } else {
+            t.entry[g] = at;
+            at += units(g);
+        }
+    }
+    if (!COMPACT && tid == 0)
+        t.entry[groups] = all;
+    t.shift = COMPACT ? 10 : 0;
+    t.count = COMPACT ? all : groups;
+    __syncthreads();
+}
+
+// The last entry i with first(i) <= x, for first(0) <= x < first(count) (the
+// same x in every lane).  Two ballots over 64 entries at most.
+__device__ __forceinline__ int find_entry(const GroupTable& t, int x, int lane)
+{
+    const int step = t.count / 64 + 1;
+    int i = min(lane * step, t.count);
+    const int block = __popcll(__ballot(lane * step <= t.count && t.first(i) <= x)) - 1;
+    if (step == 1)
+        return block;
+    i = min(block * step + lane, t.count);
+    return block * step + __popcll(__ballot(lane < step && block * step + lane <= t.count && t.first(i) <= x)) - 1;
+}
+
+// A wave's block of accumulators as bf16 into rows of C, through its own LDS
+// region, 16 rows at a time: a lane holds four consecutive columns of one row
+// (one 8-byte LDS write) and stores 16-byte pieces of rows, or single elements
+// where C's rows do not allow that.  finish(r, col, v) turns the four sums of row
+// r of the tile, columns col .. col + 3, into outputs; row_of(r) is C's row, or
+// negative: not stored.
+template <int MR, int NR, int SROW, class Finish, class RowOf>
+__device__ __forceinline__ void store_group_block(uint16_t* C, int64_t ldc, int N, int c_vec,
+                                                  const f32x4 (&acc)[MR][NR], uint8_t* stage, int row0,
+                                                  int col_w, int lane, Finish&& finish, RowOf&& row_of)
+{
+    constexpr int WCOLS = NR * 16, PPR = WCOLS / 8;
+    const int lc = lane & 15, lg = lane >> 4;
+    static_for<MR>([&](auto mi_c) __attribute__((always_inline)) {
+        constexpr int mi = decltype(mi_c)::value;
+        const int r0 = row0 + mi * 16;
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            f32x4 v = acc[mi][j];
+            finish(r0 + lc, col_w + j * 16 + 4 * lg, v);
+            uint2 o;
+            const float v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
+            o.x = (uint32_t)bf16_rne(v0) | (uint32_t)bf16_rne(v1) << 16;
+            o.y = (uint32_t)bf16_rne(v2) | (uint32_t)bf16_rne(v3) << 16;
+            *reinterpret_cast<uint2*>(stage + lc * SROW + (j * 16 + 4 * lg) * 2) = o;
+        }
+        wave_lds_order();
+        if (c_vec) {
+#pragma unroll
+            for (int q0 = 0; q0 < 16 * PPR; q0 += 64) {
+                const int q = q0 + lane;
+                const int r = q / PPR, c = q % PPR * 8;
+                const int to = q < 16 * PPR ? row_of(r0 + r) : -1;
+                if (to >= 0 && col_w + c < N) {
+                    const i32x4 v = *reinterpret_cast<const i32x4*>(stage + r * SROW + c * 2);
+                    *reinterpret_cast<i32x4*>(C + to * ldc + col_w + c) = v;
+                }
+            }
+        } else {
+            for (int q = lane; q < 16 * WCOLS; q += 64) {
+                const int r = q / WCOLS, c = q % WCOLS;
+                const int to = row_of(r0 + r);
+                if (to >= 0 && col_w + c < N)
+                    C[to * ldc + col_w + c] = *reinterpret_cast<const uint16_t*>(stage + r * SROW + c * 2);
+            }
+        }
+        wave_lds_order();
+    });
+}
+
+template <class S, int ROLE>
+__global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+    using AT = Atom<DT_BF16, 16>;
+    using KTL = KTile<S::KTB>;
+    using acc_t = AT::acc_t;
+    constexpr int TM = S::TM, TN = S::TN, WN = S::WN, R = 16, KTB = S::KTB, KT = S::KT;
+    constexpr int MR = S::MR, NR = S::NR, A_DMA = S::A_DMA, B_DMA = S::B_DMA;
+    constexpr int A_BUF = S::A_BUF, STAGE = S::STAGE, WAVES = S::WAVES, ST = S::ST;
+    constexpr int STEPS = KTB / 64, CHUNKS = KTB / 16;
+    constexpr bool TRA = ROLE == GROUP_DW, TRB = ROLE == GROUP_DX || ROLE == GROUP_DW;
+    constexpr bool ADAPT = ROLE == GROUP_ADAPT, GATHER = ROLE == GROUP_FWD || ROLE == GROUP_GATED || ADAPT;
+    static_assert(!TRA || TM >= 128, "a transposed operand's unit key needs 8 units a row");
+    static_assert(!TRB || TN >= 128, "a transposed operand's unit key needs 8 units a row");
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int lc = lane & 15, lg = lane >> 4;
+
+    // ---- the tiles
+    GroupTable table;
+    table.at(lds + S::TABLE_AT);
+    if constexpr (ROLE != GROUP_DW)
+        build_table<S::THREADS, ADAPT>(table, p.offsets, p.groups, p.S, TM);
+    const int w_tiles = ROLE == GROUP_DW ? (p.M + TM - 1) / TM * p.tiles_n : 0;   // DW: tiles of a group
+    const int items = __builtin_amdgcn_readfirstlane(
+        ROLE == GROUP_DW ? p.groups * w_tiles
+                         : (ADAPT ? (p.S + TM - 1) / TM : table.first(p.groups)) * p.tiles_n);
+    int item = (int)blockIdx.x;
+    if (item >= items)
+        return;
+
+    // ---- loads.  Plain operand: rows of K, KTB bytes a k-tile, chunk c of row
+    // r at c ^ key(r); rows past the bound read zero, chunks past K go out of
+    // range.  Transposed operand: the k-tile's KT rows, the descriptor rebased
+    // to them, rows past K read zero; columns past the matrix hold other rows'
+    // values and only reach outputs that are not stored.
+    uint32_t a_goff[A_DMA], b_goff[B_DMA], a_col[A_DMA], b_col[B_DMA];
+#pragma unroll
+    for (int i = 0; i < A_DMA; ++i) {
+        if constexpr (TRA) {
+            const uint32_t at = (uint32_t)(wave + WAVES * i) * 1024u + (uint32_t)lane * 16u;
+            const uint32_t r = at / (TM * 2), c = at % (TM * 2) / 16;
+            a_goff[i] = r * (uint32_t)p.lda_b + ((c ^ (tr_key(r) << 1)) << 4);
+            a_col[i] = 0;
+        } else {
+            const ADma d = a_dma_lane<KTB>(wave + WAVES * i, lane, p.lda_b);
+            a_goff[i] = d.goff;
+            a_col[i] = d.col;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < B_DMA; ++i) {
+        if constexpr (TRB) {
+            const uint32_t at = (uint32_t)(wave + WAVES * i) * 1024u + (uint32_t)lane * 16u;
+            const uint32_t r = at / (TN * 2), c = at % (TN * 2) / 16;
+            b_goff[i] = r * (uint32_t)p.ldb_b + ((c ^ (tr_key(r) << 1)) << 4);
+            b_col[i] = 0;
+        } else {
+            const ADma d = a_dma_lane<KTB>(wave + WAVES * i, lane, p.ldb_b);
+            b_goff[i] = d.goff;
+            b_col[i] = d.col;
+        }
+    }
+    // ---- the item: its group, output tile, K range, operands
+    const int plain_kt = (p.K + KT - 1) / KT;          // not DW
+    int group = 0, m0 = 0, n0 = 0, rows = 0, nkt = plain_kt;
+    const int kb_end = ROLE == GROUP_DW ? 0 : p.K * 2;
+    const int last_full = ROLE == GROUP_DW ? 0 : kb_end / KTB;
+    const uint8_t *a_base = nullptr, *b_base = nullptr;
+    int64_t a_span = 0, b_span = 0;
+    uint32_t a_bytes = 0, b_bytes = 0;
+    // ADAPT: the entries of the table that the tile's rows touch, k-tiles of
+    // ranks per entry, and the entry of the k-tile being loaded
+    const int rank_kts = ADAPT ? (p.R + KT / 2 - 1) / (KT / 2) : 0;
+    int entry0 = 0, x_group = 0, x_lo = 0, x_hi = 0, x_rank = 0;
+    auto set_item = [&](int it) __attribute__((always_inline)) {
+        int t = xcd_remap(it, items), tm, tn;
+        int last_row;
+        if constexpr (ROLE == GROUP_DW) {
+            group = t / w_tiles;
+            tile_raster<DG_GROUP_M>(t - group * w_tiles, w_tiles / p.tiles_n, p.tiles_n, tm, tn);
+            const int2 r = group_rows(p.offsets, group, p.S);
+            const int lo = __builtin_amdgcn_readfirstlane(r.x);
+            const int n = __builtin_amdgcn_readfirstlane(r.y) - lo;
+            m0 = tm * TM;
+            rows = min(TM, p.M - m0);
+            nkt = (n + KT - 1) / KT;
+            a_base = p.A + lo * p.lda_b + (int64_t)m0 * 2;
+            a_span = n ? (int64_t)(n - 1) * p.lda_b + (int64_t)(p.M - m0) * 2 : 0;
+            b_base = p.B + lo * p.ldb_b;
+            b_span = n ? (int64_t)(n - 1) * p.ldb_b : 0;
+            last_row = 0;
+        } else if constexpr (ADAPT) {
+            tile_raster<DG_GROUP_M>(t, items / p.tiles_n, p.tiles_n, tm, tn);
+            m0 = tm * TM;
+            last_row = p.S;
+        } else {
+            group = __builtin_amdgcn_readfirstlane(find_entry(table, t / p.tiles_n, lane));
+            const int first = __builtin_amdgcn_readfirstlane(table.first(group));
+            const int tiles = __builtin_amdgcn_readfirstlane(table.first(group + 1)) - first;
+            const int2 r = group_rows(p.offsets, group, p.S);
+            tile_raster<DG_GROUP_M>(t - first * p.tiles_n, tiles, p.tiles_n, tm, tn);
+            m0 = __builtin_amdgcn_readfirstlane(r.x) + tm * TM;
+            last_row = __builtin_amdgcn_readfirstlane(r.y);
+        }
+        n0 = tn * TN;
+        if constexpr (ROLE != GROUP_DW) {
+            rows = min(TM, last_row - m0);
+            a_base = p.A + (int64_t)m0 * p.lda_b;
+            a_bytes = (uint32_t)((int64_t)(rows - 1) * p.lda_b + (int64_t)p.K * 2);
+            b_base = p.B + group * p.b_group;
+        }
+        if constexpr (GATHER) {
+            if (ADAPT || p.order) {
+                a_base = p.A;
+                a_bytes = p.a_bytes;
+#pragma unroll
+                for (int i = 0; i < A_DMA; ++i) {
+                    const int r = KTL::ROWS_PER_LOAD * (wave + WAVES * i) + lane / CHUNKS;
+                    const uint32_t slot = (uint32_t)p.order[m0 + min(r, rows - 1)];
+                    const uint32_t row = p.k_mul ? __umulhi(slot, p.k_mul) : slot;
+                    a_goff[i] = r < rows && slot < (uint32_t)p.S ? row * (uint32_t)p.lda_b + a_col[i] : kOOB;
+                }
+            }
+        }
+        if constexpr (ADAPT) {
+            entry0 = 0;
+            int over = 0;
+            if (table.count > 0 && m0 < table.first(table.count)) {
+                const int end = min(m0 + rows, table.first(table.count));
+                entry0 = max(0, find_entry(table, max(m0, table.first(0)), lane));
+                over = end > table.first(0) ? find_entry(table, end - 1, lane) - entry0 + 1 : 0;
+            }
+            entry0 = __builtin_amdgcn_readfirstlane(entry0);
+            nkt = plain_kt + __builtin_amdgcn_readfirstlane(over) * rank_kts;
+        }
+        if constexpr (TRB) {
+            b_base += (int64_t)n0 * 2;
+            if constexpr (ROLE == GROUP_DX)
+                b_span = (int64_t)(p.K - 1) * p.ldb_b;
+            b_span += (ROLE == GROUP_DX || b_span || nkt) ? (int64_t)(p.N - n0) * 2 : 0;
+        } else {
+            b_base += (int64_t)n0 * p.ldb_b;
+            b_bytes = (uint32_t)((int64_t)(min(TN, p.N - n0) - 1) * p.ldb_b + (int64_t)p.K * 2);
+        }
+    };
+    auto rebase = [&](const uint8_t* base, int64_t span, int64_t off) __attribute__((always_inline)) {
+        // (in 32-bit halves, which stay in scalar registers)
+        const int64_t left = span - off;
+        const int hi = (int)(left >> 32);
+        const uint32_t lo = min((uint32_t)left, 0x7FFFFFFFu);
+        return make_rsrc(base + off, hi < 0 ? 0u : hi > 0 ? 0x7FFFFFFFu : lo);
+    };
+    auto load = [&](int kt, int stage, int part, int nparts, auto nomask_c) __attribute__((always_inline)) {
+        constexpr bool NOMASK = decltype(nomask_c)::value;
+        const bool mask = kt >= last_full;
+        uint8_t* base = lds + stage * STAGE;
+        if constexpr (ADAPT && !NOMASK) {
+            if (kt >= plain_kt) {
+                // ranks of one adapter: the rows' inner values, upper halves in the
+                // first chunks and lower ones in the others, against the same
+                // columns of B twice; rows of other adapters are out of range
+                if (part == 0) {
+                    const int e = kt - plain_kt, i = e / rank_kts;
+                    const int at = entry0 + i;
+                    if (kt < nkt) {
+                        x_group = __builtin_amdgcn_readfirstlane(table.id(at));
+                        x_lo = __builtin_amdgcn_readfirstlane(table.first(at)) - m0;
+                        x_hi = __builtin_amdgcn_readfirstlane(table.first(at + 1)) - m0;
+                        x_rank = (e - i * rank_kts) * (KT / 2);
+                    } else {
+                        x_hi = x_lo;               // past the last one: zeros
+                    }
+                }
+                const rsrc_t ru = make_rsrc(p.U + (int64_t)m0 * p.R * 4, (uint32_t)(rows * p.R * 4));
+                const rsrc_t rl = make_rsrc(p.LB + x_group * p.lb_group + (int64_t)n0 * p.ldlb_b,
+                                            (uint32_t)((int64_t)(min(TN, p.N - n0) - 1) * p.ldlb_b + p.R * 2));
+                auto chunk = [&](int n, int& r, int& rank, int& half) __attribute__((always_inline)) {
+                    r = KTL::ROWS_PER_LOAD * n + lane / CHUNKS;
+                    const int c = (int)((uint32_t)(lane % CHUNKS) ^ KTL::key((uint32_t)r));
+                    half = c / (CHUNKS / 2);
+                    rank = x_rank + c % (CHUNKS / 2) * 8;
+                };
+#pragma unroll
+                for (int i = 0; i < A_DMA; ++i)
+                    if (i % nparts == part) {
+                        int r, rank, half;
+                        chunk(wave + WAVES * i, r, rank, half);
+                        const bool in = r >= x_lo && r < x_hi && rank < p.R;
+                        dma16(ru, base + (wave + WAVES * i) * 1024,
+                              in ? (uint32_t)((r * 2 + half) * p.R + rank) * 2u : kOOB, 0);
+                    }
+#pragma unroll
+                for (int i = 0; i < B_DMA; ++i)
+                    if ((A_DMA + i) % nparts == part) {
+                        int r, rank, half;
+                        chunk(wave + WAVES * i, r, rank, half);
+                        const bool in = x_hi > x_lo && rank < p.R;
+                        dma16(rl, base + A_BUF + (wave + WAVES * i) * 1024,
+                              in ? (uint32_t)r * (uint32_t)p.ldlb_b + (uint32_t)rank * 2u : kOOB, 0);
+                    }
+                return;
+            }
+        }
+        const int64_t row = (int64_t)kt * KT;
+        const rsrc_t rat = TRA ? rebase(a_base, a_span, row * p.lda_b) : make_rsrc(a_base, a_bytes);
+        const rsrc_t rbt = TRB ? rebase(b_base, b_span, row * p.ldb_b) : make_rsrc(b_base, b_bytes);
+        auto one = [&](rsrc_t r, uint8_t* dst, uint32_t goff, uint32_t col, auto tr, int nt)
+                       __attribute__((always_inline)) {
+            uint32_t off = goff, soff = 0;
+            if constexpr (decltype(tr)::value) {
+            } else if constexpr (NOMASK) {
+                soff = (uint32_t)kt * KTB;
+            } else {
+                off = goff + (uint32_t)kt * KTB;
+                if (mask && (int)((uint32_t)kt * KTB + col) >= kb_end)
+                    off = kOOB;
+            }
+            if (nt)
+                dma16_nt(r, dst, off, soff);
+            else
+                dma16(r, dst, off, soff);
+        };
+#pragma unroll
+        for (int i = 0; i < A_DMA; ++i)
+            if (i % nparts == part)
+                one(rat, base + (wave + WAVES * i) * 1024, a_goff[i], a_col[i],
+                    std::integral_constant<bool, TRA>{}, 0);
+#pragma unroll
+        for (int i = 0; i < B_DMA; ++i)
+            if ((A_DMA + i) % nparts == part)
+                one(rbt, base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i], b_col[i],
+                    std::integral_constant<bool, TRB>{}, TM <= 64 && !TRA ? p.b_nt : 0);
+    };
+
+    // ---- fragments, as in loss_product
+    const uint32_t swz = KTL::key((uint32_t)lc);
+    const uint32_t row0 = (uint32_t)(wm * (TM / S::WM)), col0 = (uint32_t)(wn * S::WCOLS);
+    constexpr int PA = TRA ? 1 : STEPS, PB = TRB ? 1 : STEPS;
+    LdsBases<S::LDS> a_at[PA], b_at[PB];
+    const uint32_t key = tr_key((uint32_t)(8 * lg + (lc >> 2)));
+    if constexpr (TRA) {
+        a_at[0].init((uint32_t)(8 * lg + (lc >> 2)) * (TM * 2) + (((row0 >> 4) ^ key) << 5) +
+                     (uint32_t)(lc & 3) * 8);
+    } else {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            a_at[s].init((row0 + (uint32_t)lc) * KTB + (((uint32_t)AT::a_chunk(s, lane, 0) ^ swz) << 4));
+    }
+    if constexpr (TRB) {
+        b_at[0].init((uint32_t)(8 * lg + (lc >> 2)) * (TN * 2) + (((col0 >> 4) ^ key) << 5) +
+                     (uint32_t)(lc & 3) * 8);
+    } else {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            b_at[s].init((col0 + (uint32_t)lc) * KTB + (((uint32_t)AT::a_chunk(s, lane, 0) ^ swz) << 4));
+    }
+    auto tr_frag = [&](const LdsBases<S::LDS>& at, uint32_t c, int i, int pitch)
+                       __attribute__((always_inline)) {
+        i32x4 v;
+        const uint32_t c1 = c + 4u * (uint32_t)pitch;
+        const s16x4 lo = lds_read_tr16(
+            (lds_s16x4*)(lds + (at.b[c >> 16] ^ ((uint32_t)i << 5)) + (c & 0xFFFFu)));
+        const s16x4 hi = lds_read_tr16(
+            (lds_s16x4*)(lds + (at.b[c1 >> 16] ^ ((uint32_t)i << 5)) + (c1 & 0xFFFFu)));
+        typedef int i32x2 __attribute__((ext_vector_type(2)));
+        const i32x2 l2 = __builtin_bit_cast(i32x2, lo), h2 = __builtin_bit_cast(i32x2, hi);
+        v[0] = l2[0];
+        v[1] = l2[1];
+        v[2] = h2[0];
+        v[3] = h2[1];
+        return v;
+    };
+
+    i32x4 af[frag_sets(ST, STEPS)][MR], bf[frag_sets(ST, STEPS)][NR];
+    acc_t acc[MR][NR];
+    auto read = [&](int stage, int s, int set, int g, int G) __attribute__((always_inline)) {
+        constexpr int NF = MR + NR;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            if (f * G / NF != g)
+                continue;
+            if (f < NR) {
+                if constexpr (TRB)
+                    bf[set][f] = tr_frag(b_at[0], (uint32_t)(stage * STAGE + A_BUF + s * 32 * TN * 2), f,
+                                         TN * 2);
+                else
+                    bf[set][f] = *reinterpret_cast<const i32x4*>(
+                        lds + b_at[s % PB].at((uint32_t)(stage * STAGE + A_BUF + f * R * KTB)));
+            } else {
+                const int mi = f - NR;
+                if constexpr (TRA)
+                    af[set][mi] = tr_frag(a_at[0], (uint32_t)(stage * STAGE + s * 32 * TM * 2), mi, TM * 2);
+                else
+                    af[set][mi] = *reinterpret_cast<const i32x4*>(
+                        lds + a_at[s % PA].at((uint32_t)(stage * STAGE + mi * R * KTB)));
+            }
+        }
+    };
+    // operands exchanged: a lane holds four consecutive columns of one row
+    auto mma = [&](int, int, int set, int g, int G) __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < MR * NR; ++a) {
+            if (a * G / (MR * NR) != g)
+                continue;
+            const int mi = a / NR, j = a % NR;
+            acc[mi][j] = mfma_bf16(bf[set][j], af[set][mi], acc[mi][j]);
+        }
+    };
+    auto output = [&](int group, int m0, int n0, int rows) __attribute__((always_inline)) {
+        // the lane again, as a value of its own, so that what the outputs derive
+        // from it is not kept in registers through the K loop
+        int ol = lane;
+        asm volatile("" : "+v"(ol));
+        const int col_w = n0 + (int)col0;
+        uint8_t* stage = lds + S::OUT_AT + wave * (R * S::SROW);
+        if constexpr (ADAPT) {
+            store_group_block<MR, NR, S::SROW>(
+                p.C, p.ldc, p.N, p.c_vec, acc, stage, (int)row0, col_w, ol, [](int, int, f32x4&) {},
+                [&](int r) __attribute__((always_inline)) {
+                    const int to = r < rows ? p.order[m0 + r] : -1;
+                    return to < p.S ? to : -1;
+                });
+        } else if constexpr (ROLE == GROUP_GATED) {
+            auto gated = [&](auto cls) __attribute__((always_inline)) {
+                store_group_block<MR, NR, S::SROW>(
+                    p.C + (int64_t)m0 * p.ldc, p.ldc, p.N, p.c_vec, acc, stage, (int)row0, col_w, ol,
+                    [&](int r, int col, f32x4& v) __attribute__((always_inline)) {
+                        float f[4] = {1.f, 1.f, 1.f, 1.f};
+                        if (p.mul && r < rows && col < p.N) {
+                            const uint16_t* from = p.mul + (int64_t)(m0 + r) * p.ld_mul + col;
+                            if (p.mul_vec) {
+                                const uint2 u = *reinterpret_cast<const uint2*>(from);
+                                f[0] = __uint_as_float(u.x << 16);
+                                f[1] = __uint_as_float(u.x & 0xFFFF0000u);
+                                f[2] = __uint_as_float(u.y << 16);
+                                f[3] = __uint_as_float(u.y & 0xFFFF0000u);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    f[e] = bf16_to_f32(from[min(e, p.N - 1 - col)]);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = activate_c<decltype(cls)::value>(p.act, v[e]);
+                            v[e] = p.mul ? a * f[e] : a;
+                        }
+                    },
+                    [&](int r) __attribute__((always_inline)) { return r < rows ? r : -1; });
+            };
+            switch (act_class(p.act)) {
+            case 1:
+                gated(std::integral_constant<int, 1>{});
+                break;
+            case 2:
+                gated(std::integral_constant<int, 2>{});
+                break;
+            default:
+                gated(std::integral_constant<int, 0>{});
+            }
+        } else {
+            store_bf16_block<MR, NR, 1, S::SROW>(p.C + group * p.c_group, p.ldc, p.N, p.c_vec, acc, stage,
+                                                 m0, rows, (int)row0, col_w, ol);
+        }
+    };
+
+    auto nothing = [](int, int, int, int, int) {};
+    auto preload = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < ST - 1; ++t)
+            load(t, t, 0, 1, std::false_type{});
+    };
+    set_item(item);
+    preload();
+    for (;;) {
+#pragma unroll
+        for (int mi = 0; mi < MR; ++mi)
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+                acc[mi][j] = zero_acc<AT>();
+        // waves whose rows all lie past the last one only load
+        const bool idle = (int)row0 >= rows;
+        const int nomask = min(nkt, last_full);
+        if (!idle)
+            k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, nomask, load, read, mma);
+        else
+            k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, nomask, load, nothing, nothing);
+        // the next item's loads go out before this one's outputs
+        const int o_group = group, o_m0 = m0, o_n0 = n0, o_rows = rows;
+        item += (int)gridDim.x;
+        const bool more = item < items;
+        if (more) {
+            set_item(item);
+            preload();
+        }
+        if (!idle)
+            output(o_group, o_m0, o_n0, o_rows);
+        if (!more)
+            break;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Adapters' inner values: u[p] = scale_g A_g x for every sorted row p of a
+// group, as two bf16 halves (the rounded value and the rounded rest: 16 bits of
+// it together, so that what rounding takes from u is far below the rounding of
+// Y).  One workgroup takes 16 rows of one group and 16 NR ranks; its 8 waves
+// split K 32 values at a time, take both operands straight from memory in the
+// fragments' layout, and add their sums in LDS in a fixed order.
+struct InnerArgs {
+    const uint8_t* X;
+    int64_t ldx_b;
+    uint32_t x_bytes;
+    const int* offsets;
+    const int* order;
+    int groups, S;
+    const uint8_t* A;      // [groups][R][lda]
+    int64_t lda_b, a_group;
+    const float* scale;
+    int R, K;
+    uint16_t* U;           // [S][2][R]
+};
+
+template <int NR, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void adapter_inner_kernel(InnerArgs p)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t
+        lds[WAVES * NR * 1024 + kTableLds];
+    f32x4* part = reinterpret_cast<f32x4*>(lds);                     // [WAVES][NR][64]
+    GroupTable table;
+    table.at(lds + WAVES * NR * 1024);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lc = lane & 15, lg = lane >> 4;
+    build_table<64 * WAVES, false>(table, p.offsets, p.groups, p.S, 16);
+    const int block = (int)blockIdx.x;
+    if (block >= table.first(p.groups))
+        return;
+    const int group = __builtin_amdgcn_readfirstlane(find_entry(table, block, lane));
+    const int2 gr = group_rows(p.offsets, group, p.S);
+    const int m0 = __builtin_amdgcn_readfirstlane(gr.x + (block - table.first(group)) * 16);
+    const int rows = min(16, __builtin_amdgcn_readfirstlane(gr.y) - m0);
+    const int r0 = (int)blockIdx.y * 16 * NR;
+
+    const uint32_t row = (uint32_t)p.order[m0 + min(lc, rows - 1)];
+    const rsrc_t rx = make_rsrc(p.X, p.x_bytes);
+    const rsrc_t ra = make_rsrc(p.A + group * p.a_group + r0 * p.lda_b,
+                                (uint32_t)((int64_t)(min(16 * NR, p.R - r0) - 1) * p.lda_b + p.K * 2));
+    const uint32_t x_off = lc < rows && row < (uint32_t)p.S ? row * (uint32_t)p.ldx_b : kOOB;
+    f32x4 acc[NR];
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+        acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int steps = (p.K + 31) / 32;
+    constexpr int UN = 4;
+    for (int s0 = wave; s0 < steps; s0 += WAVES * UN) {
+        i32x4 x[UN], a[UN][NR];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int k = (s0 + u * WAVES) * 32 + lg * 8;
+            const bool in = k < p.K;
+            x[u] = load16(rx, in ? x_off + (uint32_t)k * 2u : kOOB);
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+                a[u][j] = load16(ra, in ? (uint32_t)(16 * j + lc) * (uint32_t)p.lda_b + (uint32_t)k * 2u : kOOB);
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+                acc[j] = mfma_bf16(x[u], a[u][j], acc[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+        part[(wave * NR + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    const float scale = p.scale ? p.scale[group] : 1.f;
+    for (int j = wave; j < NR; j += WAVES) {
+        f32x4 sum = part[j * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w)
+            sum += part[(w * NR + j) * 64 + lane];
+        const int rank = r0 + 16 * j + lc;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 4 * lg + e;
+            if (r < rows && rank < p.R) {
+                const float v = sum[e] * scale;
+                const uint16_t hi = bf16_rne(v);
+                const float rest = v - bf16_to_f32(hi);      // infinite v: none
+                uint16_t* to = p.U + (int64_t)(m0 + r) * 2 * p.R + rank;
+                to[0] = hi;
+                to[p.R] = fabsf(rest) < INFINITY ? bf16_rne(rest) : 0;
+            }
+        }
+    }
+}
+
+}  // namespace dg

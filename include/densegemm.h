@@ -586,6 +586,125 @@ gemm_status linear_distillation_grad(const uint16_t* X, int64_t ldx, const uint1
                                      int64_t lddx, uint16_t* dW, int64_t lddw, void* workspace,
                                      size_t workspace_bytes, void* stream);
 
+/*
+ * Linear layers whose weight depends on the row: a mixture of experts, the
+ * adapters of many requests.  T tokens have k slots each (the k experts a
+ * router chose for them; one adapter a token: k = 1).  The work runs over the
+ * S = T k slots sorted by group (expert, adapter).
+ *
+ * Common arguments:
+ *   groups   1 to 512.  k up to 64, T k up to 2^24 (linear_adapters: T up to 2^20).
+ *   offsets  device int32 [groups + 1]: group g's rows are the sorted positions
+ *            offsets[g] .. offsets[g + 1] - 1, n = offsets[groups] rows in all.
+ *   order    device int32 [S]: the slot t k + j at each sorted position.
+ *   place    device int32 [T][k]: the sorted position of each slot, -1 for a slot
+ *            that takes no part.
+ * group_sort writes the three; they may also come from elsewhere.  Offsets that
+ * are not ascending, and an order or place outside [0, S), give unspecified rows
+ * but reach no memory outside the buffers described.
+ *
+ * Buffers of sorted rows hold S rows.  Rows from n on (there are some if slots
+ * take no part) are not written and not read.  Outputs must not overlap inputs
+ * unless it is said.  Sums have a fixed order: results are bitwise repeatable.
+ * Work is enqueued on `stream` without allocation, synchronisation or memset
+ * nodes, and may be captured in a graph; how many rows a group has is read on the
+ * device when it runs.
+ *
+ * group_sort -- a stable sort of the slots by ids (device int64 [T, ld_ids]): in
+ * each group the slots keep their order.  An id outside [0, groups) takes no
+ * part: its slot has place -1 and stands in order behind the n others.
+ *   workspace  16-byte aligned, group_sort_workspace_bytes(T, k, groups) bytes (0 up
+ *              to 8192 slots: may be NULL); contents unspecified before and after.
+ *   T == 0: offsets are zeros.
+ *
+ * group_gather -- Xs[place[t][j]] = X[t]: the rows of X [T, ldx] by sorted
+ * position, D elements of 1, 2 or 4 bytes, pitches in elements.  Any alignment of
+ * rows; a row of X is read once however many slots it has.  Its gradient is
+ * group_combine without weights.
+ *
+ * group_combine -- out[t] = sum_j weights[t][j] Y[place[t][j]], bf16 rows, fp32
+ * weights (NULL: 1), the sum in fp32 in the order of j, rounded once; slots that
+ * take no part are left out (zeros for a token of none).
+ *
+ * group_combine_grad -- for dout [T, ld_dout] bf16:
+ *     dY[place[t][j]] = bf16(weights[t][j] dout[t])
+ *     dweights[t][j]  = sum_d dout[t][d] Y[place[t][j]][d]   fp32 [T][k], dense;
+ *                       0 for a slot that takes no part
+ * dY or dweights may be NULL (not both); Y is read for dweights only, and dY may be
+ * Y itself.
+ *
+ * Errors of these: INVALID_VALUE for a null or misaligned pointer, a size below
+ * its minimum, a pitch below the row's length, a workspace too small; UNSUPPORTED
+ * past the limits above or for D > 2^20; HIP.
+ */
+size_t group_sort_workspace_bytes(int64_t T, int64_t k, int64_t groups);
+gemm_status group_sort(const int64_t* ids, int64_t ld_ids, int64_t T, int64_t k, int64_t groups,
+                       int32_t* offsets, int32_t* order, int32_t* place, void* workspace,
+                       size_t workspace_bytes, void* stream);
+gemm_status group_gather(const void* X, int64_t ldx, const int32_t* place, int64_t T, int64_t k,
+                         int64_t D, int32_t elem_bytes, void* Xs, int64_t ldxs, void* stream);
+gemm_status group_combine(const uint16_t* Y, int64_t ldy, const int32_t* place, const float* weights,
+                          int64_t ld_weights, int64_t T, int64_t k, int64_t D, uint16_t* out,
+                          int64_t ldo, void* stream);
+gemm_status group_combine_grad(const uint16_t* dout, int64_t ld_dout, const uint16_t* Y, int64_t ldy,
+                               const int32_t* place, const float* weights, int64_t ld_weights,
+                               int64_t T, int64_t k, int64_t D, uint16_t* dY, int64_t lddy,
+                               float* dweights, void* stream);
+
+/*
+ * group_linear -- every sorted row times its group's weight:
+ *     Y[p] = act(x W_g^T) * mul[p],  offsets[g] <= p < offsets[g + 1]
+ * with x = X[order[p] / k], X [T, ldx] (order given), or x = X[p], X [T, ldx] sorted
+ * already (order NULL, k 1, T = S).  fp32 sums; act a gemm_activation, mul bf16
+ * [S, ld_mul] in sorted order or NULL, both in fp32 as in gemm_epilogue; rounded once.
+ * mul may be Y itself (same pointer and pitch).
+ *   X   device bf16, 16-byte aligned, ldx a multiple of 8.
+ *   W   device bf16 [groups][N][ldw], nn.Linear weights as they lie in memory, 16-byte
+ *       aligned, ldw and the distance w_stride between groups multiples of 8.
+ *   Y   device bf16 [S, ldy], 2-byte aligned.
+ *
+ * group_linear_grad -- its gradients without act and mul, for dY [S, lddy] bf16
+ * (laid out as X) in sorted order:
+ *     dX[p] = dY[p] W_g              bf16 [S, lddx], sorted; group_combine joins them
+ *     dW_g  = sum_p dY[p]^T x        bf16 [groups][N][lddw], dw_stride between groups;
+ *                                    all of it is written, zeros for a group of no row
+ * dX or dW may be NULL (not both).  W is read for dX, X and order for dW.
+ *   workspace  256-byte aligned, group_linear_grad_workspace_bytes(T, k, K) bytes, for dW
+ *              with an order (else NULL is allowed).
+ *
+ * linear_adapters -- one shared projection and a low-rank pair for each group:
+ *     Y[t] = X[t] W^T + scale[g] (X[t] A_g^T) B_g^T
+ * for the slots t = order[p] of group g, and Y[t] = X[t] W^T for the others: order is
+ * a permutation of the T tokens, as group_sort writes it for k = 1.  The inner values
+ * X A^T are kept in two bf16 halves (16 bits); sums in fp32, rounded once.
+ *   W   device bf16 [N, ldw], A [groups][R][lda], B [groups][N][ldb], as W above; R a
+ *       multiple of 8 up to 256 (adapters of lower rank end in zeros).
+ *   scale  device fp32 [groups], NULL: 1.
+ *   workspace  256-byte aligned, linear_adapters_workspace_bytes(T, R, groups) bytes.
+ *
+ * Errors of these: as above, and INVALID_VALUE for a misaligned operand or pitch;
+ * UNSUPPORTED for K (grad: or N) not a multiple of 8, K > 2^16, N > 2^20 (grad: 2^16), R
+ * not a multiple of 8 or > 256, a pitch above 2^21 elements, and with an order for rows
+ * of X that span 2 GiB or more (group_gather sorts those).
+ */
+gemm_status group_linear(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                         int64_t w_stride, const int32_t* offsets, const int32_t* order, int64_t T,
+                         int64_t k, int64_t groups, int64_t N, int64_t K, int32_t activation,
+                         const uint16_t* mul, int64_t ld_mul, uint16_t* Y, int64_t ldy, void* stream);
+size_t group_linear_grad_workspace_bytes(int64_t T, int64_t k, int64_t K);
+gemm_status group_linear_grad(const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx,
+                              const uint16_t* W, int64_t ldw, int64_t w_stride, const int32_t* offsets,
+                              const int32_t* order, int64_t T, int64_t k, int64_t groups, int64_t N,
+                              int64_t K, uint16_t* dX, int64_t lddx, uint16_t* dW, int64_t lddw,
+                              int64_t dw_stride, void* workspace, size_t workspace_bytes, void* stream);
+size_t linear_adapters_workspace_bytes(int64_t T, int64_t R, int64_t groups);
+gemm_status linear_adapters(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
+                            const uint16_t* A, int64_t lda, int64_t a_stride, const uint16_t* B,
+                            int64_t ldb, int64_t b_stride, const float* scale, const int32_t* offsets,
+                            const int32_t* order, int64_t T, int64_t N, int64_t K, int64_t R,
+                            int64_t groups, uint16_t* Y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code ("GEMM_OK", ...). */
 const char* gemm_status_string(gemm_status status);
 
