@@ -882,68 +882,99 @@ def linear_adapters_workspace_bytes(T: int, R: int, groups: int) -> int:
     return int(lib.linear_adapters_workspace_bytes(T, R, groups))
 
 
-def _typed(fn: str, name: str, t, *dtypes):
-    if not isinstance(t, _torch().Tensor) or t.dtype not in dtypes:
-        raise ValueError(f"{fn}: {name} must be a {' or '.join(str(d) for d in dtypes)} tensor")
+def _refuse(fn: str, name: str, what: str):
+    raise ValueError(f"{fn}: {name} must be {what}")
 
 
-def _rows_of(fn: str, name: str, t, shape):
-    """A 2-D view of this shape (None: any extent) with contiguous rows."""
-    if t.dim() != 2 or any(w is not None and n != w for n, w in zip(t.shape, shape)) or \
-            (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        want = ", ".join("any" if w is None else str(w) for w in shape)
-        raise ValueError(f"{fn}: {name} must be a [{want}] tensor with contiguous rows")
+def _extent(shape) -> str:
+    return "[" + ", ".join("any" if n is None else str(n) for n in shape) + "]"
 
 
-def _vector(fn: str, name: str, t, n: int):
-    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{fn}: {name} must be a contiguous vector of {n} values")
+def _matrix(fn: str, name: str, t, dtype, rows=None, cols=None):
+    """A 2-D view (rows, cols None: any) with contiguous rows: (rows, columns, pitch).
+    A single row's stride says nothing; its pitch is the columns in whole 8."""
+    if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
+        _refuse(fn, name, f"a {dtype} tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        n, w = shape
+        if (rows is None or n == rows) and (cols is None or w == cols) and (w < 2 or stride[1] == 1):
+            if n < 2:
+                return n, w, (w + 7) // 8 * 8
+            if stride[0] >= w:
+                return n, w, stride[0]
+    _refuse(fn, name, f"a {_extent((rows, cols))} tensor with contiguous rows")
 
 
-def _stack_of(fn: str, name: str, t, shape):
-    """A 3-D view of this shape with contiguous rows, matrix after matrix."""
-    if t.dim() != 3 or any(w is not None and n != w for n, w in zip(t.shape, shape)) or \
-            (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) < t.shape[2]):
-        want = ", ".join("any" if w is None else str(w) for w in shape)
-        raise ValueError(f"{fn}: {name} must be a [{want}] tensor with contiguous rows")
+def _stack(fn: str, name: str, t, dtype, groups=None, rows=None, cols=None):
+    """A 3-D view with contiguous rows: (groups, rows, columns, pitch, group stride)."""
+    if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
+        _refuse(fn, name, f"a {dtype} tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        g, n, w = shape
+        if (groups is None or g == groups) and (rows is None or n == rows) and \
+                (cols is None or w == cols) and (w < 2 or stride[2] == 1) and (n < 2 or stride[1] >= w):
+            pitch = stride[1] if n > 1 else (w + 7) // 8 * 8
+            return g, n, w, pitch, (stride[0] if g > 1 else n * pitch)
+    _refuse(fn, name, f"a {_extent((groups, rows, cols))} tensor with contiguous rows")
 
 
-def _stack_args(t):
-    """Pointer, pitch and group stride; an extent of one says nothing by its stride."""
-    G, rows, width = t.shape
-    pitch = t.stride(1) if rows > 1 else (width + 7) // 8 * 8
-    return t.data_ptr(), pitch, (t.stride(0) if G > 1 else rows * pitch)
+def _vector(fn: str, name: str, t, dtype, n: int):
+    if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
+        _refuse(fn, name, f"a {dtype} tensor")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        _refuse(fn, name, f"a contiguous vector of {n} values")
 
 
-def _same_device(fn: str, first, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device != first.device):
-            raise ValueError(f"{fn}: {name} must be a device tensor on {first.device}")
+def _place(fn: str, place, T=None):
+    T, k, _ = _matrix(fn, "place", place, _torch().int32, T)
+    if not place.is_contiguous():
+        _refuse(fn, "place", "contiguous")
+    return T, k
 
 
-def _group_workspace(fn: str, like, need: int, workspace):
-    torch = _torch()
+def _one_device(fn: str, names: str, *tensors) -> int:
+    """The device of the first tensor, which the others (None: absent) share."""
+    dev = tensors[0].get_device()
+    for i, t in enumerate(tensors):
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            _refuse(fn, names.split()[i], "a device tensor" if i == 0 or dev < 0 else f"on cuda:{dev}")
+    return dev
+
+
+def _group_workspace(fn: str, device, need: int, workspace):
+    """(tensor, pointer, bytes): the caller's, or one made for the call."""
     if workspace is None:
         if need == 0:
-            return None, 0
+            return None, None, 0
         # freed on return: the caching allocator reuses it on this stream only
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    elif not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be a contiguous device tensor on {like.device}")
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        _refuse(fn, "workspace", f"a contiguous device tensor on {device}")
     nbytes = workspace.numel() * workspace.element_size()
     if nbytes < need:
         raise ValueError(f"{fn}: workspace holds {nbytes} bytes, {need} are needed")
-    return workspace, nbytes
+    return workspace, workspace.data_ptr(), nbytes
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _group_call(fn: str, device_of, *args):
-    # launches go to the operands' device, whichever device is current
-    with _torch().cuda.device(device_of.device):
-        st = getattr(lib, fn)(*args, _stream_ptr(device_of))
+def _group_call(fn: str, dev: int, *args):
+    """The C call on the current stream of the operands' device, whichever device is
+    current.  (The stream's handle without the Stream object, and no device guard
+    where none is needed: together 3 of 13 us a call.)"""
+    torch = _torch()
+    call = getattr(lib, fn)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        st = call(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, stream)
     if st != GEMM_OK:
         raise GemmError(fn, st)
 
@@ -957,59 +988,39 @@ def group_sort(ids, groups: int, *, workspace=None):
     stands in order behind the others."""
     torch = _torch()
     fn = "group_sort"
-    _typed(fn, "ids", ids, torch.int64)
-    if ids.dim() == 1:
+    if isinstance(ids, torch.Tensor) and ids.dim() == 1:
         ids = ids[:, None]
-    _rows_of(fn, "ids", ids, (None, None))
-    _same_device(fn, ids, ids=ids)
-    T, k = ids.shape
-    offsets = torch.empty(groups + 1, dtype=torch.int32, device=ids.device)
-    order = torch.empty(T * k, dtype=torch.int32, device=ids.device)
-    place = torch.empty((T, k), dtype=torch.int32, device=ids.device)
-    ws, nbytes = _group_workspace(fn, ids, group_sort_workspace_bytes(T, k, groups), workspace)
-    _group_call(fn, ids, ids.data_ptr(), _pitch(ids), T, k, groups, offsets.data_ptr(), order.data_ptr(),
-                place.data_ptr(), _ptr(ws), nbytes)
+    T, k, ld = _matrix(fn, "ids", ids, torch.int64)
+    dev = _one_device(fn, "ids", ids)
+    if groups < 1:
+        raise ValueError(f"{fn}: groups must be at least 1")
+    device = ids.device
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device=device)
+    order = torch.empty(T * k, dtype=torch.int32, device=device)
+    place = torch.empty((T, k), dtype=torch.int32, device=device)
+    need = lib.group_sort_workspace_bytes(T, k, groups)
+    ws, at, nbytes = _group_workspace(fn, device, need, workspace) if need else (None, None, 0)
+    _group_call(fn, dev, ids.data_ptr(), ld, T, k, groups, offsets.data_ptr(), order.data_ptr(),
+                place.data_ptr(), at, nbytes)
     return offsets, order, place
-
-
-def _place(fn: str, place, T=None):
-    _typed(fn, "place", place, _torch().int32)
-    _rows_of(fn, "place", place, (T, None))
-    if not place.is_contiguous():
-        raise ValueError(f"{fn}: place must be contiguous")
-    return place.shape
-
-
-def _group_out(fn: str, name: str, out, shape, dtype, like):
-    if out is None:
-        return _torch().empty(shape, dtype=dtype, device=like.device)
-    _typed(fn, name, out, dtype)
-    (_rows_of if len(shape) == 2 else _stack_of)(fn, name, out, shape)
-    return out
 
 
 def group_gather(X, place, out=None):
     """Xs [T * slots, D] with Xs[place[t, j]] = X[t]: the rows of X (elements of 1, 2
     or 4 bytes) in sorted order.  Rows behind the last slot that takes part are
     not written.  The gradient of X is group_combine(dXs, place)."""
+    torch = _torch()
     fn = "group_gather"
-    if not isinstance(X, _torch().Tensor) or X.element_size() not in (1, 2, 4):
-        raise ValueError(f"{fn}: X must be a tensor of 1-, 2- or 4-byte elements")
-    _rows_of(fn, "X", X, (None, None))
-    T, k = _place(fn, place, X.shape[0])
-    out = _group_out(fn, "out", out, (T * k, X.shape[1]), X.dtype, X)
-    _same_device(fn, X, X=X, place=place, out=out)
-    _group_call(fn, X, X.data_ptr(), _pitch(X), place.data_ptr(), T, k, X.shape[1], X.element_size(),
-                out.data_ptr(), _pitch(out))
+    if not isinstance(X, torch.Tensor) or X.element_size() not in (1, 2, 4):
+        _refuse(fn, "X", "a tensor of 1-, 2- or 4-byte elements")
+    T, D, ldx = _matrix(fn, "X", X, X.dtype)
+    T, k = _place(fn, place, T)
+    if out is None:
+        out = torch.empty((T * k, D), dtype=X.dtype, device=X.device)
+    _, _, ldo = _matrix(fn, "out", out, X.dtype, T * k, D)
+    dev = _one_device(fn, "X place out", X, place, out)
+    _group_call(fn, dev, X.data_ptr(), ldx, place.data_ptr(), T, k, D, X.element_size(), out.data_ptr(), ldo)
     return out
-
-
-def _weights(fn: str, weights, T: int, k: int):
-    if weights is None:
-        return None, 0
-    _typed(fn, "weights", weights, _torch().float32)
-    _rows_of(fn, "weights", weights, (T, k))
-    return weights.data_ptr(), _pitch(weights)
 
 
 def group_combine(Y, place, weights=None, out=None):
@@ -1018,14 +1029,14 @@ def group_combine(Y, place, weights=None, out=None):
     take no part are left out."""
     torch = _torch()
     fn = "group_combine"
-    _typed(fn, "Y", Y, torch.bfloat16)
     T, k = _place(fn, place)
-    _rows_of(fn, "Y", Y, (T * k, None))
-    w, ldw = _weights(fn, weights, T, k)
-    out = _group_out(fn, "out", out, (T, Y.shape[1]), torch.bfloat16, Y)
-    _same_device(fn, Y, Y=Y, place=place, weights=weights, out=out)
-    _group_call(fn, Y, Y.data_ptr(), _pitch(Y), place.data_ptr(), w, ldw, T, k, Y.shape[1], out.data_ptr(),
-                _pitch(out))
+    _, D, ldy = _matrix(fn, "Y", Y, torch.bfloat16, T * k)
+    ldw = 0 if weights is None else _matrix(fn, "weights", weights, torch.float32, T, k)[2]
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.bfloat16, device=Y.device)
+    _, _, ldo = _matrix(fn, "out", out, torch.bfloat16, T, D)
+    dev = _one_device(fn, "Y place weights out", Y, place, weights, out)
+    _group_call(fn, dev, Y.data_ptr(), ldy, place.data_ptr(), _ptr(weights), ldw, T, k, D, out.data_ptr(), ldo)
     return out
 
 
@@ -1037,47 +1048,37 @@ def group_combine_grad(dout, Y, place, weights=None, *, need_dY: bool = True, ne
     used for dweights only (None if not needed)."""
     torch = _torch()
     fn = "group_combine_grad"
-    _typed(fn, "dout", dout, torch.bfloat16)
     T, k = _place(fn, place)
-    _rows_of(fn, "dout", dout, (T, None))
-    D = dout.shape[1]
+    _, D, ldd = _matrix(fn, "dout", dout, torch.bfloat16, T)
+    ldy = 0
     if need_dweights or Y is not None:
-        _typed(fn, "Y", Y, torch.bfloat16)
-        _rows_of(fn, "Y", Y, (T * k, D))
+        ldy = _matrix(fn, "Y", Y, torch.bfloat16, T * k, D)[2]
+    ldw = 0 if weights is None else _matrix(fn, "weights", weights, torch.float32, T, k)[2]
     if not need_dY and not need_dweights:
         raise ValueError(f"{fn}: neither dY nor dweights is asked for")
-    if not need_dY and dY is not None:
-        raise ValueError(f"{fn}: dY given, but need_dY is false")
-    w, ldw = _weights(fn, weights, T, k)
+    lddy, dweights = 0, None
     if need_dY:
-        dY = _group_out(fn, "dY", dY, (T * k, D), torch.bfloat16, dout)
-    dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device) if need_dweights else None
-    _same_device(fn, dout, dout=dout, Y=Y, place=place, weights=weights, dY=dY)
-    _group_call(fn, dout, dout.data_ptr(), _pitch(dout), _ptr(Y), 0 if Y is None else _pitch(Y),
-                place.data_ptr(), w, ldw, T, k, D, _ptr(dY), 0 if dY is None else _pitch(dY), _ptr(dweights))
+        if dY is None:
+            dY = torch.empty((T * k, D), dtype=torch.bfloat16, device=dout.device)
+        lddy = _matrix(fn, "dY", dY, torch.bfloat16, T * k, D)[2]
+    elif dY is not None:
+        raise ValueError(f"{fn}: dY given, but need_dY is false")
+    dev = _one_device(fn, "dout Y place weights dY", dout, Y, place, weights, dY)
+    if need_dweights:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+    _group_call(fn, dev, dout.data_ptr(), ldd, _ptr(Y), ldy, place.data_ptr(), _ptr(weights), ldw, T, k, D,
+                _ptr(dY), lddy, _ptr(dweights))
     return dY, dweights
 
 
-def _group_operands(fn: str, X, W, offsets, order, slots: int):
-    """(T, k, S) of a grouped product, its operands checked."""
-    torch = _torch()
-    _typed(fn, "X", X, torch.bfloat16)
-    _typed(fn, "W", W, torch.bfloat16)
-    _typed(fn, "offsets", offsets, torch.int32)
-    _rows_of(fn, "X", X, (None, None))
-    _stack_of(fn, "W", W, (None, None, X.shape[1]))
-    _vector(fn, "offsets", offsets, W.shape[0] + 1)
-    T = X.shape[0]
+def _group_order(fn: str, order, T: int, slots: int):
     if order is None:
         if slots != 1:
             raise ValueError(f"{fn}: slots needs an order")
     else:
-        _typed(fn, "order", order, torch.int32)
         if slots < 1:
             raise ValueError(f"{fn}: slots must be at least 1")
-        _vector(fn, "order", order, T * slots)
-    _same_device(fn, X, X=X, W=W, offsets=offsets, order=order)
-    return T, slots, T * slots
+        _vector(fn, "order", order, _torch().int32, T * slots)
 
 
 def group_linear(X, W, offsets, order=None, *, slots: int = 1, activation=None, mul=None, out=None):
@@ -1088,16 +1089,19 @@ def group_linear(X, W, offsets, order=None, *, slots: int = 1, activation=None, 
     may be `out` itself.  Rows from offsets[-1] on are not written."""
     torch = _torch()
     fn = "group_linear"
-    T, k, S = _group_operands(fn, X, W, offsets, order, slots)
-    G, N, K = W.shape
+    T, K, ldx = _matrix(fn, "X", X, torch.bfloat16)
+    G, N, _, ldw, strw = _stack(fn, "W", W, torch.bfloat16, None, None, K)
+    _vector(fn, "offsets", offsets, torch.int32, G + 1)
+    _group_order(fn, order, T, slots)
+    S = T * slots
     act = ACTIVATIONS[activation] if not isinstance(activation, int) else activation
-    if mul is not None:
-        _typed(fn, "mul", mul, torch.bfloat16)
-        _rows_of(fn, "mul", mul, (S, N))
-    out = _group_out(fn, "out", out, (S, N), torch.bfloat16, X)
-    _same_device(fn, X, mul=mul, out=out)
-    _group_call(fn, X, X.data_ptr(), _row_pitch8(X), *_stack_args(W), offsets.data_ptr(), _ptr(order), T, k, G,
-                N, K, act, _ptr(mul), 0 if mul is None else _pitch(mul), out.data_ptr(), _pitch(out))
+    ldm = 0 if mul is None else _matrix(fn, "mul", mul, torch.bfloat16, S, N)[2]
+    if out is None:
+        out = torch.empty((S, N), dtype=torch.bfloat16, device=X.device)
+    ldo = _matrix(fn, "out", out, torch.bfloat16, S, N)[2]
+    dev = _one_device(fn, "X W offsets order mul out", X, W, offsets, order, mul, out)
+    _group_call(fn, dev, X.data_ptr(), ldx, W.data_ptr(), ldw, strw, offsets.data_ptr(), _ptr(order), T, slots, G,
+                N, K, act, _ptr(mul), ldm, out.data_ptr(), ldo)
     return out
 
 
@@ -1110,25 +1114,31 @@ def group_linear_grad(dY, X, W, offsets, order=None, *, slots: int = 1, need_dX:
     a uint8 tensor of group_linear_grad_workspace_bytes bytes (with an order, for dW)."""
     torch = _torch()
     fn = "group_linear_grad"
-    T, k, S = _group_operands(fn, X, W, offsets, order, slots)
-    G, N, K = W.shape
-    _typed(fn, "dY", dY, torch.bfloat16)
-    _rows_of(fn, "dY", dY, (S, N))
+    T, K, ldx = _matrix(fn, "X", X, torch.bfloat16)
+    G, N, _, ldw, strw = _stack(fn, "W", W, torch.bfloat16, None, None, K)
+    _vector(fn, "offsets", offsets, torch.int32, G + 1)
+    _group_order(fn, order, T, slots)
+    S = T * slots
+    lddy = _matrix(fn, "dY", dY, torch.bfloat16, S, N)[2]
     if not need_dX and not need_dW:
         raise ValueError(f"{fn}: neither dX nor dW is asked for")
     for name, need, given in (("dX", need_dX, dX), ("dW", need_dW, dW)):
         if given is not None and not need:
             raise ValueError(f"{fn}: {name} given, but need_{name} is false")
+    lddx, ld_dw = 0, (0, 0)
     if need_dX:
-        dX = _group_out(fn, "dX", dX, (S, K), torch.bfloat16, X)
+        if dX is None:
+            dX = torch.empty((S, K), dtype=torch.bfloat16, device=X.device)
+        lddx = _matrix(fn, "dX", dX, torch.bfloat16, S, K)[2]
     if need_dW:
-        dW = _group_out(fn, "dW", dW, (G, N, K), torch.bfloat16, X)
-    _same_device(fn, X, dY=dY, dX=dX, dW=dW)
-    need = group_linear_grad_workspace_bytes(T, k, K) if need_dW and order is not None else 0
-    ws, nbytes = _group_workspace(fn, X, need, workspace)
-    _group_call(fn, X, dY.data_ptr(), _row_pitch8(dY), X.data_ptr(), _row_pitch8(X), *_stack_args(W),
-                offsets.data_ptr(), _ptr(order), T, k, G, N, K, _ptr(dX), 0 if dX is None else _pitch(dX),
-                *((None, 0, 0) if dW is None else _stack_args(dW)), _ptr(ws), nbytes)
+        if dW is None:
+            dW = torch.empty((G, N, K), dtype=torch.bfloat16, device=X.device)
+        ld_dw = _stack(fn, "dW", dW, torch.bfloat16, G, N, K)[3:]
+    dev = _one_device(fn, "X W offsets order dY dX dW", X, W, offsets, order, dY, dX, dW)
+    need = lib.group_linear_grad_workspace_bytes(T, slots, K) if need_dW and order is not None else 0
+    ws, at, nbytes = _group_workspace(fn, X.device, need, workspace) if need else (None, None, 0)
+    _group_call(fn, dev, dY.data_ptr(), lddy, X.data_ptr(), ldx, W.data_ptr(), ldw, strw, offsets.data_ptr(),
+                _ptr(order), T, slots, G, N, K, _ptr(dX), lddx, _ptr(dW), *ld_dw, at, nbytes)
     return dX, dW
 
 
@@ -1141,26 +1151,19 @@ def linear_adapters(X, W, A, B, offsets, order, *, scale=None, out=None, workspa
     linear_adapters_workspace_bytes bytes."""
     torch = _torch()
     fn = "linear_adapters"
-    for name, t in (("X", X), ("W", W), ("A", A), ("B", B)):
-        _typed(fn, name, t, torch.bfloat16)
-    _typed(fn, "offsets", offsets, torch.int32)
-    _typed(fn, "order", order, torch.int32)
-    _rows_of(fn, "X", X, (None, None))
-    T, K = X.shape
-    _rows_of(fn, "W", W, (None, K))
-    N = W.shape[0]
-    _stack_of(fn, "A", A, (None, None, K))
-    G, R = A.shape[:2]
-    _stack_of(fn, "B", B, (G, N, R))
-    _vector(fn, "offsets", offsets, G + 1)
-    _vector(fn, "order", order, T)
+    T, K, ldx = _matrix(fn, "X", X, torch.bfloat16)
+    N, _, ldw = _matrix(fn, "W", W, torch.bfloat16, None, K)
+    G, R, _, lda, stra = _stack(fn, "A", A, torch.bfloat16, None, None, K)
+    _, _, _, ldb, strb = _stack(fn, "B", B, torch.bfloat16, G, N, R)
+    _vector(fn, "offsets", offsets, torch.int32, G + 1)
+    _vector(fn, "order", order, torch.int32, T)
     if scale is not None:
-        _typed(fn, "scale", scale, torch.float32)
-        _vector(fn, "scale", scale, G)
-    out = _group_out(fn, "out", out, (T, N), torch.bfloat16, X)
-    _same_device(fn, X, X=X, W=W, A=A, B=B, offsets=offsets, order=order, scale=scale, out=out)
-    ws, nbytes = _group_workspace(fn, X, linear_adapters_workspace_bytes(T, R, G), workspace)
-    _group_call(fn, X, X.data_ptr(), _row_pitch8(X), W.data_ptr(), _row_pitch8(W), *_stack_args(A),
-                *_stack_args(B), _ptr(scale), offsets.data_ptr(), order.data_ptr(), T, N, K, R, G,
-                out.data_ptr(), _pitch(out), _ptr(ws), nbytes)
+        _vector(fn, "scale", scale, torch.float32, G)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=X.device)
+    ldo = _matrix(fn, "out", out, torch.bfloat16, T, N)[2]
+    dev = _one_device(fn, "X W A B offsets order scale out", X, W, A, B, offsets, order, scale, out)
+    ws, at, nbytes = _group_workspace(fn, X.device, lib.linear_adapters_workspace_bytes(T, R, G), workspace)
+    _group_call(fn, dev, X.data_ptr(), ldx, W.data_ptr(), ldw, A.data_ptr(), lda, stra, B.data_ptr(), ldb, strb,
+                _ptr(scale), offsets.data_ptr(), order.data_ptr(), T, N, K, R, G, out.data_ptr(), ldo, at, nbytes)
     return out

@@ -51,6 +51,15 @@ __device__ __forceinline__ int slot_group(const SortArgs& p, int s)
     return id >= 0 && id < p.groups ? (int)id : p.groups;
 }
 
+// The groups of slots s, s + step, ... below s1, the ids' loads all in flight.
+constexpr int kBatch = 8;
+__device__ __forceinline__ void batch_groups(const SortArgs& p, int s, int s1, int step, int (&id)[kBatch])
+{
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+        id[i] = s + i * step < s1 ? slot_group(p, s + i * step) : 0;
+}
+
 __device__ __forceinline__ int wave_scan(int x, int lane)
 {
 #pragma unroll
@@ -68,8 +77,14 @@ __global__ __launch_bounds__(1024) void group_count_kernel(SortArgs p)
         found[g] = 0;
     __syncthreads();
     const int s0 = (int)blockIdx.x * p.chunk, s1 = min(p.S, s0 + p.chunk);
-    for (int s = s0 + (int)threadIdx.x; s < s1; s += 1024)
-        atomicAdd(&found[slot_group(p, s)], 1);
+    for (int s = s0 + (int)threadIdx.x; s < s1; s += 1024 * kBatch) {
+        int id[kBatch];
+        batch_groups(p, s, s1, 1024, id);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (s + i * 1024 < s1)
+                atomicAdd(&found[id[i]], 1);
+    }
     __syncthreads();
     for (int g = threadIdx.x; g <= p.groups; g += 1024)
         p.counts[(int64_t)blockIdx.x * (p.groups + 1) + g] = found[g];
@@ -87,14 +102,21 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
     const int s0 = (int)blockIdx.x * p.chunk, s1 = min(p.S, s0 + p.chunk);
     const int part = (s1 - s0 + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
     const int w0 = min(s1, s0 + wave * part), w1 = min(s1, w0 + part);
-    for (int s = w0 + lane; s < w1; s += 64)
-        atomicAdd(&next[wave][slot_group(p, s)], 1);
+    for (int s = w0 + lane; s < w1; s += 64 * kBatch) {
+        int id[kBatch];
+        batch_groups(p, s, w1, 64, id);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (s + i * 64 < w1)
+                atomicAdd(&next[wave][id[i]], 1);
+    }
     __syncthreads();
     // thread g: rows of group g in all (the group none: thread 0, last)
     auto totals = [&](int g, int& before) {
         int total = 0;
         before = 0;
         if (p.counts) {
+#pragma unroll 8
             for (int c = 0; c < (int)gridDim.x; ++c) {
                 const int n = p.counts[(int64_t)c * (G + 1) + g];
                 before += c < (int)blockIdx.x ? n : 0;
@@ -141,23 +163,30 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
     }
     __syncthreads();
     const int bits = 32 - __clz(G);
-    for (int s = w0; s < w1; s += 64) {
-        const bool in = s + lane < w1;
-        const int g = in ? slot_group(p, s + lane) : 0;
-        uint64_t same = __ballot(in);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot((g >> b) & 1);
-            same &= (g >> b) & 1 ? set : ~set;
-        }
-        const int rank = __popcll(same & ((UINT64_C(1) << lane) - 1));
-        const int at = next[wave][g] + rank;
-        wave_lds_order();
-        if (in && rank == 0)
-            next[wave][g] = at + __popcll(same);
-        wave_lds_order();
-        if (in) {
-            p.order[at] = s + lane;
-            p.place[s + lane] = g < G ? at : -1;
+    for (int s = w0; s < w1; s += 64 * kBatch) {
+        int id[kBatch];
+        batch_groups(p, s + lane, w1, 64, id);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (s + i * 64 >= w1)
+                break;
+            const int slot = s + i * 64 + lane, g = id[i];
+            const bool in = slot < w1;
+            uint64_t same = __ballot(in);
+            for (int b = 0; b < bits; ++b) {
+                const uint64_t set = __ballot((g >> b) & 1);
+                same &= (g >> b) & 1 ? set : ~set;
+            }
+            const int rank = __popcll(same & ((UINT64_C(1) << lane) - 1));
+            const int at = next[wave][g] + rank;
+            wave_lds_order();
+            if (in && rank == 0)
+                next[wave][g] = at + __popcll(same);
+            wave_lds_order();
+            if (in) {
+                p.order[at] = slot;
+                p.place[slot] = g < G ? at : -1;
+            }
         }
     }
 }
@@ -294,16 +323,29 @@ __global__ __launch_bounds__(256) void group_combine_kernel(CombineArgs p)
     for (int q = (int)threadIdx.x % TPR; q < p.pieces; q += TPR) {
         const int at = min(q * 8, p.D - 8);
         float sum[8] = {};
-        for (int j = 0; j < p.k; ++j) {
-            const int from = place[j];
-            if ((uint32_t)from >= (uint32_t)p.S)
-                continue;
-            float y[8];
-            unpack8(load_piece(p.Y + from * p.ldy + at), y);
-            const float wj = w ? w[j] : 1.f;
+        // four rows' loads in flight; a slot that takes no part reads the first
+        // row and counts zeros
+        for (int j0 = 0; j0 < p.k; j0 += 4) {
+            i32x4 v[4];
+            float wj[4];
+            bool in[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                sum[i] = fmaf(wj, y[i], sum[i]);
+            for (int i = 0; i < 4; ++i) {
+                const int j = min(j0 + i, p.k - 1);
+                const int from = place[j];
+                in[i] = j0 + i < p.k && (uint32_t)from < (uint32_t)p.S;
+                v[i] = load_piece(p.Y + (in[i] ? from : 0) * p.ldy + at);
+                wj[i] = w ? w[j] : 1.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y[8];
+                unpack8(v[i], y);
+                if (in[i])
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sum[e] = fmaf(wj[i], y[e], sum[e]);
+            }
         }
         store_piece(out + at, pack8(sum));
     }

@@ -6,7 +6,7 @@
 //   GROUP_DX     dX[p] = sum_n dY[p][n] W_g[n]
 //   GROUP_DW     dW_g = sum over its p of dY[p] x^T; zeros for a group of no row
 //   GROUP_ADAPT  Y[order[p]] = W x + B_g u[p], u = scale_g A_g x in two bf16
-//                halves from the kernel before
+//                halves from the kernel before; the second term as further k-tiles
 //
 // Operands are taken as they lie in memory and staged in LDS k-tile by k-tile
 // (k_loop): one whose contraction axis is contiguous as gemm_ab_kernel stages
@@ -224,6 +224,14 @@ __device__ __forceinline__ void store_group_block(uint16_t* C, int64_t ldc, int 
     });
 }
 
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p)
+{
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return (const uint8_t*)((uint64_t)hi << 32 | lo);
+}
+
 template <class S, int ROLE>
 __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArgs p)
 {
@@ -302,7 +310,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
     // ADAPT: the entries of the table that the tile's rows touch, k-tiles of
     // ranks per entry, and the entry of the k-tile being loaded
     const int rank_kts = ADAPT ? (p.R + KT / 2 - 1) / (KT / 2) : 0;
-    int entry0 = 0, x_group = 0, x_lo = 0, x_hi = 0, x_rank = 0;
+    int xkt = 0, entry0 = 0, x_group = 0, x_lo = 0, x_hi = 0, x_rank = 0;
     auto set_item = [&](int it) __attribute__((always_inline)) {
         int t = xcd_remap(it, items), tm, tn;
         int last_row;
@@ -362,7 +370,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                 over = end > table.first(0) ? find_entry(table, end - 1, lane) - entry0 + 1 : 0;
             }
             entry0 = __builtin_amdgcn_readfirstlane(entry0);
-            nkt = plain_kt + __builtin_amdgcn_readfirstlane(over) * rank_kts;
+            xkt = __builtin_amdgcn_readfirstlane(over) * rank_kts;
         }
         if constexpr (TRB) {
             b_base += (int64_t)n0 * 2;
@@ -373,6 +381,12 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             b_base += (int64_t)n0 * p.ldb_b;
             b_bytes = (uint32_t)((int64_t)(min(TN, p.N - n0) - 1) * p.ldb_b + (int64_t)p.K * 2);
         }
+        // Said to be uniform, which they are: where the compiler computed one of
+        // them in vector registers, every load would run a loop over its values.
+        a_base = uniform(a_base);
+        b_base = uniform(b_base);
+        a_bytes = (uint32_t)__builtin_amdgcn_readfirstlane((int)a_bytes);
+        b_bytes = (uint32_t)__builtin_amdgcn_readfirstlane((int)b_bytes);
     };
     auto rebase = [&](const uint8_t* base, int64_t span, int64_t off) __attribute__((always_inline)) {
         // (in 32-bit halves, which stay in scalar registers)
@@ -385,53 +399,6 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         constexpr bool NOMASK = decltype(nomask_c)::value;
         const bool mask = kt >= last_full;
         uint8_t* base = lds + stage * STAGE;
-        if constexpr (ADAPT && !NOMASK) {
-            if (kt >= plain_kt) {
-                // ranks of one adapter: the rows' inner values, upper halves in the
-                // first chunks and lower ones in the others, against the same
-                // columns of B twice; rows of other adapters are out of range
-                if (part == 0) {
-                    const int e = kt - plain_kt, i = e / rank_kts;
-                    const int at = entry0 + i;
-                    if (kt < nkt) {
-                        x_group = __builtin_amdgcn_readfirstlane(table.id(at));
-                        x_lo = __builtin_amdgcn_readfirstlane(table.first(at)) - m0;
-                        x_hi = __builtin_amdgcn_readfirstlane(table.first(at + 1)) - m0;
-                        x_rank = (e - i * rank_kts) * (KT / 2);
-                    } else {
-                        x_hi = x_lo;               // past the last one: zeros
-                    }
-                }
-                const rsrc_t ru = make_rsrc(p.U + (int64_t)m0 * p.R * 4, (uint32_t)(rows * p.R * 4));
-                const rsrc_t rl = make_rsrc(p.LB + x_group * p.lb_group + (int64_t)n0 * p.ldlb_b,
-                                            (uint32_t)((int64_t)(min(TN, p.N - n0) - 1) * p.ldlb_b + p.R * 2));
-                auto chunk = [&](int n, int& r, int& rank, int& half) __attribute__((always_inline)) {
-                    r = KTL::ROWS_PER_LOAD * n + lane / CHUNKS;
-                    const int c = (int)((uint32_t)(lane % CHUNKS) ^ KTL::key((uint32_t)r));
-                    half = c / (CHUNKS / 2);
-                    rank = x_rank + c % (CHUNKS / 2) * 8;
-                };
-#pragma unroll
-                for (int i = 0; i < A_DMA; ++i)
-                    if (i % nparts == part) {
-                        int r, rank, half;
-                        chunk(wave + WAVES * i, r, rank, half);
-                        const bool in = r >= x_lo && r < x_hi && rank < p.R;
-                        dma16(ru, base + (wave + WAVES * i) * 1024,
-                              in ? (uint32_t)((r * 2 + half) * p.R + rank) * 2u : kOOB, 0);
-                    }
-#pragma unroll
-                for (int i = 0; i < B_DMA; ++i)
-                    if ((A_DMA + i) % nparts == part) {
-                        int r, rank, half;
-                        chunk(wave + WAVES * i, r, rank, half);
-                        const bool in = x_hi > x_lo && rank < p.R;
-                        dma16(rl, base + A_BUF + (wave + WAVES * i) * 1024,
-                              in ? (uint32_t)r * (uint32_t)p.ldlb_b + (uint32_t)rank * 2u : kOOB, 0);
-                    }
-                return;
-            }
-        }
         const int64_t row = (int64_t)kt * KT;
         const rsrc_t rat = TRA ? rebase(a_base, a_span, row * p.lda_b) : make_rsrc(a_base, a_bytes);
         const rsrc_t rbt = TRB ? rebase(b_base, b_span, row * p.ldb_b) : make_rsrc(b_base, b_bytes);
@@ -461,6 +428,52 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             if ((A_DMA + i) % nparts == part)
                 one(rbt, base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i], b_col[i],
                     std::integral_constant<bool, TRB>{}, TM <= 64 && !TRA ? p.b_nt : 0);
+    };
+
+    // ADAPT, behind the k-tiles of X and W: k-tiles of one adapter's ranks.  The
+    // rows' inner values, upper halves in the first chunks and lower ones in the
+    // others, against the same columns of B twice; rows of other adapters are out
+    // of range and read zero.
+    auto load_ranks = [&](int kt, int stage, int part, int nparts, auto) __attribute__((always_inline)) {
+        if (part == 0) {
+            const int i = kt / rank_kts;
+            x_hi = x_lo = 0;                       // past the last one: zeros
+            if (kt < xkt) {
+                const int at = entry0 + i;
+                x_group = __builtin_amdgcn_readfirstlane(table.id(at));
+                x_lo = __builtin_amdgcn_readfirstlane(table.first(at)) - m0;
+                x_hi = __builtin_amdgcn_readfirstlane(table.first(at + 1)) - m0;
+                x_rank = (kt - i * rank_kts) * (KT / 2);
+            }
+        }
+        uint8_t* base = lds + stage * STAGE;
+        const rsrc_t ru = make_rsrc(p.U + (int64_t)m0 * p.R * 4, (uint32_t)(rows * p.R * 4));
+        const rsrc_t rl = make_rsrc(p.LB + x_group * p.lb_group + (int64_t)n0 * p.ldlb_b,
+                                    (uint32_t)((int64_t)(min(TN, p.N - n0) - 1) * p.ldlb_b + p.R * 2));
+        auto chunk = [&](int n, int& r, int& rank, int& half) __attribute__((always_inline)) {
+            r = KTL::ROWS_PER_LOAD * n + lane / CHUNKS;
+            const int c = (int)((uint32_t)(lane % CHUNKS) ^ KTL::key((uint32_t)r));
+            half = c / (CHUNKS / 2);
+            rank = x_rank + c % (CHUNKS / 2) * 8;
+        };
+#pragma unroll
+        for (int i = 0; i < A_DMA; ++i)
+            if (i % nparts == part) {
+                int r, rank, half;
+                chunk(wave + WAVES * i, r, rank, half);
+                const bool in = r >= x_lo && r < x_hi && rank < p.R;
+                dma16(ru, base + (wave + WAVES * i) * 1024,
+                      in ? (uint32_t)((r * 2 + half) * p.R + rank) * 2u : kOOB, 0);
+            }
+#pragma unroll
+        for (int i = 0; i < B_DMA; ++i)
+            if ((A_DMA + i) % nparts == part) {
+                int r, rank, half;
+                chunk(wave + WAVES * i, r, rank, half);
+                const bool in = x_hi > x_lo && rank < p.R;
+                dma16(rl, base + A_BUF + (wave + WAVES * i) * 1024,
+                      in ? (uint32_t)r * (uint32_t)p.ldlb_b + (uint32_t)rank * 2u : kOOB, 0);
+            }
     };
 
     // ---- fragments, as in loss_product
@@ -616,6 +629,12 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, nomask, load, read, mma);
         else
             k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, nomask, load, nothing, nothing);
+        if (ADAPT && xkt > 0) {
+            if (!idle)
+                k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR)>(xkt, 0, load_ranks, read, mma);
+            else
+                k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR)>(xkt, 0, load_ranks, nothing, nothing);
+        }
         // the next item's loads go out before this one's outputs
         const int o_group = group, o_m0 = m0, o_n0 = n0, o_rows = rows;
         item += (int)gridDim.x;
@@ -635,9 +654,10 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
 // Adapters' inner values: u[p] = scale_g A_g x for every sorted row p of a
 // group, as two bf16 halves (the rounded value and the rounded rest: 16 bits of
 // it together, so that what rounding takes from u is far below the rounding of
-// Y).  One workgroup takes 16 rows of one group and 16 NR ranks; its 8 waves
-// split K 32 values at a time, take both operands straight from memory in the
-// fragments' layout, and add their sums in LDS in a fixed order.
+// Y).  One workgroup takes 16 MB rows of one group and 16 NR ranks; its waves
+// split K in chunks of 64 values (a whole line of every row), take both operands
+// straight from memory in the fragments' layout, UN chunks in flight, and add
+// their sums in LDS in a fixed order.
 struct InnerArgs {
     const uint8_t* X;
     int64_t ldx_b;
@@ -652,69 +672,97 @@ struct InnerArgs {
     uint16_t* U;           // [S][2][R]
 };
 
-template <int NR, int WAVES>
+template <int NR, int MB, int WAVES, int UN>
 __global__ __launch_bounds__(64 * WAVES) void adapter_inner_kernel(InnerArgs p)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t
-        lds[WAVES * NR * 1024 + kTableLds];
-    f32x4* part = reinterpret_cast<f32x4*>(lds);                     // [WAVES][NR][64]
+    __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * MB * NR * 1024 + kTableLds];
+    f32x4* part = reinterpret_cast<f32x4*>(lds);                     // [WAVES][MB * NR][64]
     GroupTable table;
-    table.at(lds + WAVES * NR * 1024);
+    table.at(lds + WAVES * MB * NR * 1024);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lc = lane & 15, lg = lane >> 4;
-    build_table<64 * WAVES, false>(table, p.offsets, p.groups, p.S, 16);
+    build_table<64 * WAVES, false>(table, p.offsets, p.groups, p.S, 16 * MB);
     const int block = (int)blockIdx.x;
     if (block >= table.first(p.groups))
         return;
     const int group = __builtin_amdgcn_readfirstlane(find_entry(table, block, lane));
     const int2 gr = group_rows(p.offsets, group, p.S);
-    const int m0 = __builtin_amdgcn_readfirstlane(gr.x + (block - table.first(group)) * 16);
-    const int rows = min(16, __builtin_amdgcn_readfirstlane(gr.y) - m0);
+    const int m0 = __builtin_amdgcn_readfirstlane(gr.x + (block - table.first(group)) * 16 * MB);
+    const int rows = min(16 * MB, __builtin_amdgcn_readfirstlane(gr.y) - m0);
     const int r0 = (int)blockIdx.y * 16 * NR;
 
-    const uint32_t row = (uint32_t)p.order[m0 + min(lc, rows - 1)];
+    uint32_t x_off[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+        x_off[m] = (uint32_t)p.order[m0 + min(16 * m + lc, rows - 1)];
     const rsrc_t rx = make_rsrc(p.X, p.x_bytes);
-    const rsrc_t ra = make_rsrc(p.A + group * p.a_group + r0 * p.lda_b,
+    const rsrc_t ra = make_rsrc(uniform(p.A + group * p.a_group + r0 * p.lda_b),
                                 (uint32_t)((int64_t)(min(16 * NR, p.R - r0) - 1) * p.lda_b + p.K * 2));
-    const uint32_t x_off = lc < rows && row < (uint32_t)p.S ? row * (uint32_t)p.ldx_b : kOOB;
-    f32x4 acc[NR];
+    f32x4 acc[MB][NR];
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
-        acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int steps = (p.K + 31) / 32;
-    constexpr int UN = 4;
-    for (int s0 = wave; s0 < steps; s0 += WAVES * UN) {
-        i32x4 x[UN], a[UN][NR];
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int k = (s0 + u * WAVES) * 32 + lg * 8;
-            const bool in = k < p.K;
-            x[u] = load16(rx, in ? x_off + (uint32_t)k * 2u : kOOB);
+        for (int j = 0; j < NR; ++j)
+            acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int chunks = (p.K + 63) / 64;
+    bool first = true;
+    for (int c0 = wave; c0 < chunks || first; c0 += WAVES * UN) {
+        i32x4 x[UN][2][MB], a[UN][2][NR];
+        // A's loads first: those of X wait for the rows' numbers
 #pragma unroll
-            for (int j = 0; j < NR; ++j)
-                a[u][j] = load16(ra, in ? (uint32_t)(16 * j + lc) * (uint32_t)p.lda_b + (uint32_t)k * 2u : kOOB);
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = (c0 + u * WAVES) * 64 + h * 32 + lg * 8;
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+                    a[u][h][j] = load16(ra, k < p.K ? (uint32_t)(16 * j + lc) * (uint32_t)p.lda_b + (uint32_t)k * 2u
+                                                    : kOOB);
+            }
+        if (first) {
+            first = false;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                x_off[m] = 16 * m + lc < rows && x_off[m] < (uint32_t)p.S ? x_off[m] * (uint32_t)p.ldx_b : kOOB;
         }
 #pragma unroll
         for (int u = 0; u < UN; ++u)
 #pragma unroll
-            for (int j = 0; j < NR; ++j)
-                acc[j] = mfma_bf16(x[u], a[u][j], acc[j]);
+            for (int h = 0; h < 2; ++h) {
+                const int k = (c0 + u * WAVES) * 64 + h * 32 + lg * 8;
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+                    x[u][h][m] = load16(rx, k < p.K ? x_off[m] + (uint32_t)k * 2u : kOOB);
+            }
+        // (all of them in flight before the first product)
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+                        acc[m][j] = mfma_bf16(x[u][h][m], a[u][h][j], acc[m][j]);
     }
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
-        part[(wave * NR + j) * 64 + lane] = acc[j];
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+            part[(wave * MB * NR + m * NR + j) * 64 + lane] = acc[m][j];
     __syncthreads();
     const float scale = p.scale ? p.scale[group] : 1.f;
-    for (int j = wave; j < NR; j += WAVES) {
-        f32x4 sum = part[j * 64 + lane];
+    for (int b = wave; b < MB * NR; b += WAVES) {
+        f32x4 sum = part[b * 64 + lane];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w)
-            sum += part[(w * NR + j) * 64 + lane];
-        const int rank = r0 + 16 * j + lc;
+            sum += part[(w * MB * NR + b) * 64 + lane];
+        const int rank = r0 + 16 * (b % NR) + lc;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int r = 4 * lg + e;
+            const int r = 16 * (b / NR) + 4 * lg + e;
             if (r < rows && rank < p.R) {
                 const float v = sum[e] * scale;
                 const uint16_t hi = bf16_rne(v);

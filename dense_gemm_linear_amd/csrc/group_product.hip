@@ -147,6 +147,8 @@ double tiles_us(const Cost& c, double tiles, int64_t cols, int64_t k, int cus)
 // a tile a group is empty on average.
 double row_tiles(int64_t rows, int64_t used, int tm)
 {
+    if (used == 1)
+        return (double)cdiv(rows, tm);
     return (double)used * std::max(1.0, (double)rows / (double)used / tm + 0.5);
 }
 
@@ -314,15 +316,21 @@ hipError_t adapters_forward(const ProductCall& c)
         i.R = (int)c.R;
         i.K = (int)c.K;
         i.U = reinterpret_cast<uint16_t*>(c.ws);
-        const int64_t blocks = T / 16 + std::min(c.groups, T);
-        const int nr = (int)std::min<int64_t>(4, cdiv(c.R, 16));
+        // 16 rows a workgroup; 32, which read A half as often, where 16 make more
+        // than one round
+        const int64_t cols = c.R > 32 ? 64 : c.R > 16 ? 32 : 16, wide = cdiv(c.R, cols);
+        const bool two = (T / 16 + std::min(c.groups, T)) * wide > c.cus;
+        const int64_t blocks = T / (two ? 32 : 16) + std::min(c.groups, T);
         void* args[] = {&i};
-        const void* kernel = nr == 1   ? reinterpret_cast<const void*>(&adapter_inner_kernel<1, 8>)
-                             : nr == 2 ? reinterpret_cast<const void*>(&adapter_inner_kernel<2, 8>)
-                                       : reinterpret_cast<const void*>(&adapter_inner_kernel<4, 8>);
-        const int cols = nr == 1 ? 16 : nr == 2 ? 32 : 64;
-        const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)blocks, (unsigned)cdiv(c.R, cols)), dim3(512),
-                                             args, 0, c.stream);
+        const void* kernel =
+            two ? (cols == 64   ? reinterpret_cast<const void*>(&adapter_inner_kernel<4, 2, 8, 2>)
+                   : cols == 32 ? reinterpret_cast<const void*>(&adapter_inner_kernel<2, 2, 8, 4>)
+                                : reinterpret_cast<const void*>(&adapter_inner_kernel<1, 2, 8, 4>))
+                : (cols == 64   ? reinterpret_cast<const void*>(&adapter_inner_kernel<4, 1, 16, 2>)
+                   : cols == 32 ? reinterpret_cast<const void*>(&adapter_inner_kernel<2, 1, 16, 2>)
+                                : reinterpret_cast<const void*>(&adapter_inner_kernel<1, 1, 16, 4>));
+        const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)blocks, (unsigned)wide),
+                                             dim3(two ? 512 : 1024), args, 0, c.stream);
         if (e != hipSuccess)
             return e;
     }
@@ -343,7 +351,13 @@ hipError_t adapters_forward(const ProductCall& c)
     a.ldlb_b = c.ldb * 2;
     a.lb_group = c.ldb_group * 2;
     a.R = (int)c.R;
-    return launch_group_adapt(plain_shape(T, 1, c.N, c.K, c.cus), a, 0, c.cus, c.stream);
+    // one group of T rows: the number is known
+    const bool narrow = cdiv(c.N, 128) <= 2 * c.cus;
+    const int shape = T <= 16 && cdiv(c.N, 32) <= 8 * c.cus ? G_ONE
+                      : T <= 32 ? (narrow ? G_LOW_SLIM : G_LOW)
+                      : T <= 64 ? (narrow ? G_FEW_SLIM : G_FEW)
+                                : pick({0, 1, 3, 4}, T, 1, c.N, c.K, c.cus);
+    return launch_group_adapt(shape, a, 0, c.cus, c.stream);
 }
 
 #endif
