@@ -72,6 +72,7 @@ struct GroupShape {
     static constexpr int KT = KTB / 2;
     static constexpr int WCOLS = TN / WN;
     static constexpr int SROW = WCOLS * 2 + 16;
+    static constexpr int REST_KT = TM * TN >= 256 * 256 ? 14 : 8;    // DW, see there
     // after the stages: the waves' output blocks, the groups' table
     static constexpr int OUT_AT = ST * STAGE, OUT_LDS = WAVES * R * SROW;
     static constexpr int TABLE_AT = OUT_AT + OUT_LDS;
@@ -86,7 +87,7 @@ struct GroupShape {
 };
 
 // The groups' table in LDS.  first(i): where entry i begins, counted in units of
-// `unit` rows (rounded up per group); first(count): the end.  With COMPACT only
+// `unit` rows (rounded up per group, and `more` of them each); first(count): the end.  With COMPACT only
 // groups that have rows are entries, id(i) says which group entry i is, and the
 // unit is a row; else entry i is group i.  Offsets that are not ascending or lie
 // outside [0, S] are taken as the nearest that are, so that no index derived
@@ -112,7 +113,7 @@ __device__ __forceinline__ int2 group_rows(const int* offsets, int g, int S)
 }
 
 template <int THREADS, bool COMPACT>
-__device__ __forceinline__ void build_table(GroupTable& t, const int* offsets, int groups, int S, int unit)
+__device__ __forceinline__ void build_table(GroupTable& t, const int* offsets, int groups, int S, int unit, int more)
 {
     constexpr int WAVES = THREADS / 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -120,7 +121,7 @@ __device__ __forceinline__ void build_table(GroupTable& t, const int* offsets, i
     const int g0 = min(groups, tid * each), g1 = min(groups, g0 + each);
     auto units = [&](int g) {
         const int2 r = group_rows(offsets, g, S);
-        return COMPACT ? (int)(r.y > r.x) : (r.y - r.x + unit - 1) / unit;
+        return COMPACT ? (int)(r.y > r.x) : (r.y - r.x + unit - 1) / unit + more;
     };
     int n = 0;
     for (int g = g0; g < g1; ++g)
@@ -232,6 +233,18 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p)
     return (const uint8_t*)((uint64_t)hi << 32 | lo);
 }
 
+// The kernel's arguments, read again from memory where they are used: as values of
+// the start they would stay in scalar registers through the K loop, which has none
+// left (the 256 x 256 tiles spilled 90 of them to vector registers, and those to
+// memory inside the loop).
+typedef const __attribute__((address_space(4))) GroupArgs* KernelArgs;
+__device__ __forceinline__ KernelArgs kernel_args()
+{
+    KernelArgs a = (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(a));
+    return a;
+}
+
 template <class S, int ROLE>
 __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArgs p)
 {
@@ -257,14 +270,36 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
     // ---- the tiles
     GroupTable table;
     table.at(lds + S::TABLE_AT);
-    if constexpr (ROLE != GROUP_DW)
-        build_table<S::THREADS, ADAPT>(table, p.offsets, p.groups, p.S, TM);
+    build_table<S::THREADS, ADAPT>(table, p.offsets, p.groups, p.S, ROLE == GROUP_DW ? KT : TM,
+                                   ROLE == GROUP_DW ? S::REST_KT : 0);
     const int w_tiles = ROLE == GROUP_DW ? (p.M + TM - 1) / TM * p.tiles_n : 0;   // DW: tiles of a group
     const int items = __builtin_amdgcn_readfirstlane(
         ROLE == GROUP_DW ? p.groups * w_tiles
                          : (ADAPT ? (p.S + TM - 1) / TM : table.first(p.groups)) * p.tiles_n);
-    int item = (int)blockIdx.x;
-    if (item >= items)
+    // DW: a tile takes as long as its group has rows.  Each XCD has a run of tiles
+    // of the same cost, counted in k-tiles (with REST_KT for a tile's start and its
+    // output), which its workgroups take in turn.  (Items b, b + G, ... as for the
+    // others gave an XCD one group: 8 groups of 342 to 2185 rows, 8192 in all, of 4096 x
+    // 4096 took 419 us where equal groups took 262; a run of equal cost for each
+    // workgroup 337, but equal groups 313, as tiles that share operands are apart.)
+    int item = (int)blockIdx.x, end = items, step = (int)gridDim.x;
+    if constexpr (ROLE == GROUP_DW) {
+        const int parts = step % 8 == 0 ? 8 : 1;
+        const int64_t all = (int64_t)__builtin_amdgcn_readfirstlane(table.first(p.groups)) * w_tiles;
+        auto start = [&](int i) __attribute__((always_inline)) {
+            if (i >= parts)
+                return items;
+            const int64_t x = all / parts * i + all % parts * i / parts;      // i / parts of all
+            const int g = __builtin_amdgcn_readfirstlane(find_entry(table, (int)(x / w_tiles), lane));
+            const int first = __builtin_amdgcn_readfirstlane(table.first(g));
+            const int cost = __builtin_amdgcn_readfirstlane(table.first(g + 1)) - first;
+            return g * w_tiles + (int)((x - (int64_t)first * w_tiles + cost - 1) / cost);
+        };
+        end = start(item % parts + 1);
+        item = start(item % parts) + item / parts;
+        step /= parts;
+    }
+    if (item >= end)
         return;
 
     // ---- loads.  Plain operand: rows of K, KTB bytes a k-tile, chunk c of row
@@ -272,92 +307,117 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
     // range.  Transposed operand: the k-tile's KT rows, the descriptor rebased
     // to them, rows past K read zero; columns past the matrix hold other rows'
     // values and only reach outputs that are not stored.
-    uint32_t a_goff[A_DMA], b_goff[B_DMA], a_col[A_DMA], b_col[B_DMA];
+    // Chunk i of a wave lies A_ROWS i (B_ROWS i) rows further: a multiple of 16, so
+    // that the swizzles are the first chunk's.  For a plain operand one offset in a
+    // vector register serves all, with the descriptor's base moved; rows picked up
+    // by order, and those of a transposed operand, whose descriptor moves with the
+    // k-tiles, have an offset each.  (With offsets for all, the 256 x 256 tiles
+    // spilled them into the K loop.)
+    constexpr int A_ROWS = WAVES * 1024 / (TRA ? TM * 2 : KTB), B_ROWS = WAVES * 1024 / (TRB ? TN * 2 : KTB);
+    static_assert(A_ROWS % 16 == 0 && B_ROWS % 16 == 0, "swizzles repeat");
+    constexpr int A_OFFS = GATHER || TRA ? A_DMA : 1, B_OFFS = TRB ? B_DMA : 1;
+    uint32_t a_goff[A_OFFS], b_goff[B_OFFS], a_col = 0, b_col = 0;
+    auto tr_offset = [&](int width, int64_t ld_b) __attribute__((always_inline)) {
+        const uint32_t at = (uint32_t)wave * 1024u + (uint32_t)lane * 16u;
+        const uint32_t r = at / (uint32_t)(width * 2), c = at % (uint32_t)(width * 2) / 16;
+        return r * (uint32_t)ld_b + ((c ^ (tr_key(r) << 1)) << 4);
+    };
+    if constexpr (TRA) {
+        a_goff[0] = tr_offset(TM, p.lda_b);
 #pragma unroll
-    for (int i = 0; i < A_DMA; ++i) {
-        if constexpr (TRA) {
-            const uint32_t at = (uint32_t)(wave + WAVES * i) * 1024u + (uint32_t)lane * 16u;
-            const uint32_t r = at / (TM * 2), c = at % (TM * 2) / 16;
-            a_goff[i] = r * (uint32_t)p.lda_b + ((c ^ (tr_key(r) << 1)) << 4);
-            a_col[i] = 0;
-        } else {
-            const ADma d = a_dma_lane<KTB>(wave + WAVES * i, lane, p.lda_b);
-            a_goff[i] = d.goff;
-            a_col[i] = d.col;
-        }
-    }
+        for (int i = 1; i < A_OFFS; ++i)
+            a_goff[i] = a_goff[0] + (uint32_t)(i * A_ROWS) * (uint32_t)p.lda_b;
+    } else {
+        const ADma d = a_dma_lane<KTB>(wave, lane, p.lda_b);
+        a_goff[0] = d.goff;
+        a_col = d.col;
 #pragma unroll
-    for (int i = 0; i < B_DMA; ++i) {
-        if constexpr (TRB) {
-            const uint32_t at = (uint32_t)(wave + WAVES * i) * 1024u + (uint32_t)lane * 16u;
-            const uint32_t r = at / (TN * 2), c = at % (TN * 2) / 16;
-            b_goff[i] = r * (uint32_t)p.ldb_b + ((c ^ (tr_key(r) << 1)) << 4);
-            b_col[i] = 0;
-        } else {
-            const ADma d = a_dma_lane<KTB>(wave + WAVES * i, lane, p.ldb_b);
-            b_goff[i] = d.goff;
-            b_col[i] = d.col;
-        }
+        for (int i = 1; i < A_OFFS; ++i)
+            a_goff[i] = a_goff[0] + (uint32_t)(i * A_ROWS) * (uint32_t)p.lda_b;
     }
+    if constexpr (TRB) {
+        b_goff[0] = tr_offset(TN, p.ldb_b);
+#pragma unroll
+        for (int i = 1; i < B_OFFS; ++i)
+            b_goff[i] = b_goff[0] + (uint32_t)(i * B_ROWS) * (uint32_t)p.ldb_b;
+    } else {
+        const ADma d = a_dma_lane<KTB>(wave, lane, p.ldb_b);
+        b_goff[0] = d.goff;
+        b_col = d.col;
+    }
+    // (as values of their own: where they are the low halves of 64-bit products, the
+    // compiler keeps both halves)
+#pragma unroll
+    for (int i = 0; i < A_OFFS; ++i)
+        asm volatile("" : "+v"(a_goff[i]));
+#pragma unroll
+    for (int i = 0; i < B_OFFS; ++i)
+        asm volatile("" : "+v"(b_goff[i]));
     // ---- the item: its group, output tile, K range, operands
     const int plain_kt = (p.K + KT - 1) / KT;          // not DW
     int group = 0, m0 = 0, n0 = 0, rows = 0, nkt = plain_kt;
     const int kb_end = ROLE == GROUP_DW ? 0 : p.K * 2;
     const int last_full = ROLE == GROUP_DW ? 0 : kb_end / KTB;
     const uint8_t *a_base = nullptr, *b_base = nullptr;
-    int64_t a_span = 0, b_span = 0;
-    uint32_t a_bytes = 0, b_bytes = 0;
+    // plain: bytes of the tile's rows; transposed: bytes of the last k-tile
+    int a_span = 0, b_span = 0;
+    const int a_step = KT * (int)p.lda_b, b_step = KT * (int)p.ldb_b;         // TRA, TRB
+    const int a_rows = A_ROWS * (int)p.lda_b, b_rows = B_ROWS * (int)p.ldb_b;
+    uint32_t a_bytes = 0;                                                     // GATHER
     // ADAPT: the entries of the table that the tile's rows touch, k-tiles of
     // ranks per entry, and the entry of the k-tile being loaded
     const int rank_kts = ADAPT ? (p.R + KT / 2 - 1) / (KT / 2) : 0;
     int xkt = 0, entry0 = 0, x_group = 0, x_lo = 0, x_hi = 0, x_rank = 0;
     auto set_item = [&](int it) __attribute__((always_inline)) {
-        int t = xcd_remap(it, items), tm, tn;
+        const KernelArgs q = kernel_args();
+        int t = ROLE == GROUP_DW ? it : xcd_remap(it, items), tm, tn;
+
         int last_row;
         if constexpr (ROLE == GROUP_DW) {
             group = t / w_tiles;
-            tile_raster<DG_GROUP_M>(t - group * w_tiles, w_tiles / p.tiles_n, p.tiles_n, tm, tn);
-            const int2 r = group_rows(p.offsets, group, p.S);
+            tile_raster<DG_GROUP_M>(t - group * w_tiles, w_tiles / q->tiles_n, q->tiles_n, tm, tn);
+            const int2 r = group_rows(q->offsets, group, q->S);
             const int lo = __builtin_amdgcn_readfirstlane(r.x);
             const int n = __builtin_amdgcn_readfirstlane(r.y) - lo;
             m0 = tm * TM;
-            rows = min(TM, p.M - m0);
+            rows = min(TM, q->M - m0);
             nkt = (n + KT - 1) / KT;
-            a_base = p.A + lo * p.lda_b + (int64_t)m0 * 2;
-            a_span = n ? (int64_t)(n - 1) * p.lda_b + (int64_t)(p.M - m0) * 2 : 0;
-            b_base = p.B + lo * p.ldb_b;
-            b_span = n ? (int64_t)(n - 1) * p.ldb_b : 0;
+            a_base = q->A + lo * q->lda_b + (int64_t)m0 * 2;
+            a_span = (n - 1) % KT * (int)q->lda_b + (q->M - m0) * 2;
+            b_base = q->B + lo * q->ldb_b;
+            b_span = (n - 1) % KT * (int)q->ldb_b;
             last_row = 0;
         } else if constexpr (ADAPT) {
-            tile_raster<DG_GROUP_M>(t, items / p.tiles_n, p.tiles_n, tm, tn);
+            tile_raster<DG_GROUP_M>(t, items / q->tiles_n, q->tiles_n, tm, tn);
             m0 = tm * TM;
-            last_row = p.S;
+            last_row = q->S;
         } else {
-            group = __builtin_amdgcn_readfirstlane(find_entry(table, t / p.tiles_n, lane));
+            group = __builtin_amdgcn_readfirstlane(find_entry(table, t / q->tiles_n, lane));
             const int first = __builtin_amdgcn_readfirstlane(table.first(group));
             const int tiles = __builtin_amdgcn_readfirstlane(table.first(group + 1)) - first;
-            const int2 r = group_rows(p.offsets, group, p.S);
-            tile_raster<DG_GROUP_M>(t - first * p.tiles_n, tiles, p.tiles_n, tm, tn);
+            const int2 r = group_rows(q->offsets, group, q->S);
+            tile_raster<8>(t - first * q->tiles_n, tiles, q->tiles_n, tm, tn);
             m0 = __builtin_amdgcn_readfirstlane(r.x) + tm * TM;
             last_row = __builtin_amdgcn_readfirstlane(r.y);
         }
         n0 = tn * TN;
         if constexpr (ROLE != GROUP_DW) {
             rows = min(TM, last_row - m0);
-            a_base = p.A + (int64_t)m0 * p.lda_b;
-            a_bytes = (uint32_t)((int64_t)(rows - 1) * p.lda_b + (int64_t)p.K * 2);
-            b_base = p.B + group * p.b_group;
+            a_base = q->A + (int64_t)m0 * q->lda_b;
+            a_span = (rows - 1) * (int)q->lda_b + q->K * 2;
+            a_bytes = (uint32_t)a_span;
+            b_base = q->B + group * q->b_group;
         }
         if constexpr (GATHER) {
-            if (ADAPT || p.order) {
-                a_base = p.A;
-                a_bytes = p.a_bytes;
+            if (ADAPT || q->order) {
+                a_base = q->A;
+                a_bytes = q->a_bytes;
 #pragma unroll
                 for (int i = 0; i < A_DMA; ++i) {
                     const int r = KTL::ROWS_PER_LOAD * (wave + WAVES * i) + lane / CHUNKS;
-                    const uint32_t slot = (uint32_t)p.order[m0 + min(r, rows - 1)];
-                    const uint32_t row = p.k_mul ? __umulhi(slot, p.k_mul) : slot;
-                    a_goff[i] = r < rows && slot < (uint32_t)p.S ? row * (uint32_t)p.lda_b + a_col[i] : kOOB;
+                    const uint32_t slot = (uint32_t)q->order[m0 + min(r, rows - 1)];
+                    const uint32_t row = q->k_mul ? __umulhi(slot, q->k_mul) : slot;
+                    a_goff[i] = r < rows && slot < (uint32_t)q->S ? row * (uint32_t)q->lda_b + a_col : kOOB;
                 }
             }
         }
@@ -375,33 +435,34 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         if constexpr (TRB) {
             b_base += (int64_t)n0 * 2;
             if constexpr (ROLE == GROUP_DX)
-                b_span = (int64_t)(p.K - 1) * p.ldb_b;
-            b_span += (ROLE == GROUP_DX || b_span || nkt) ? (int64_t)(p.N - n0) * 2 : 0;
+                b_span = (q->K - 1) % KT * (int)q->ldb_b;
+            b_span += (q->N - n0) * 2;
         } else {
-            b_base += (int64_t)n0 * p.ldb_b;
-            b_bytes = (uint32_t)((int64_t)(min(TN, p.N - n0) - 1) * p.ldb_b + (int64_t)p.K * 2);
+            b_base += (int64_t)n0 * q->ldb_b;
+            b_span = (min(TN, q->N - n0) - 1) * (int)q->ldb_b + q->K * 2;
         }
         // Said to be uniform, which they are: where the compiler computed one of
         // them in vector registers, every load would run a loop over its values.
         a_base = uniform(a_base);
         b_base = uniform(b_base);
         a_bytes = (uint32_t)__builtin_amdgcn_readfirstlane((int)a_bytes);
-        b_bytes = (uint32_t)__builtin_amdgcn_readfirstlane((int)b_bytes);
+        a_span = __builtin_amdgcn_readfirstlane(a_span);
+        b_span = __builtin_amdgcn_readfirstlane(b_span);
+        if constexpr (ROLE == GROUP_DW)
+            nkt = __builtin_amdgcn_readfirstlane(nkt);
     };
-    auto rebase = [&](const uint8_t* base, int64_t span, int64_t off) __attribute__((always_inline)) {
-        // (in 32-bit halves, which stay in scalar registers)
-        const int64_t left = span - off;
-        const int hi = (int)(left >> 32);
-        const uint32_t lo = min((uint32_t)left, 0x7FFFFFFFu);
-        return make_rsrc(base + off, hi < 0 ? 0u : hi > 0 ? 0x7FFFFFFFu : lo);
+    // Rows i rows_b bytes behind the tile's first; or the rows of k-tile kt, all
+    // there before the last k-tile and none behind it.
+    auto plain_rsrc = [&](const uint8_t* base, int span, int behind) __attribute__((always_inline)) {
+        return make_rsrc(base + behind, (uint32_t)max(span - behind, 0));
+    };
+    auto tr_rsrc = [&](const uint8_t* base, int span, int kt) __attribute__((always_inline)) {
+        return make_rsrc(base, kt + 1 < nkt ? 0x7FFFFFFFu : kt + 1 == nkt ? (uint32_t)span : 0u);
     };
     auto load = [&](int kt, int stage, int part, int nparts, auto nomask_c) __attribute__((always_inline)) {
         constexpr bool NOMASK = decltype(nomask_c)::value;
         const bool mask = kt >= last_full;
         uint8_t* base = lds + stage * STAGE;
-        const int64_t row = (int64_t)kt * KT;
-        const rsrc_t rat = TRA ? rebase(a_base, a_span, row * p.lda_b) : make_rsrc(a_base, a_bytes);
-        const rsrc_t rbt = TRB ? rebase(b_base, b_span, row * p.ldb_b) : make_rsrc(b_base, b_bytes);
         auto one = [&](rsrc_t r, uint8_t* dst, uint32_t goff, uint32_t col, auto tr, int nt)
                        __attribute__((always_inline)) {
             uint32_t off = goff, soff = 0;
@@ -421,13 +482,25 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
 #pragma unroll
         for (int i = 0; i < A_DMA; ++i)
             if (i % nparts == part)
-                one(rat, base + (wave + WAVES * i) * 1024, a_goff[i], a_col[i],
+                one(GATHER ? make_rsrc(a_base, a_bytes)
+                    : TRA  ? tr_rsrc(a_base, a_span, kt)
+                           : plain_rsrc(a_base, a_span, i * a_rows),
+                    base + (wave + WAVES * i) * 1024, a_goff[i % A_OFFS], a_col,
                     std::integral_constant<bool, TRA>{}, 0);
 #pragma unroll
         for (int i = 0; i < B_DMA; ++i)
             if ((A_DMA + i) % nparts == part)
-                one(rbt, base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i], b_col[i],
+                one(TRB ? tr_rsrc(b_base, b_span, kt) : plain_rsrc(b_base, b_span, i * b_rows),
+                    base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i % B_OFFS], b_col,
                     std::integral_constant<bool, TRB>{}, TM <= 64 && !TRA ? p.b_nt : 0);
+        // a transposed operand's base goes on with the k-tiles (part by part, then
+        // tile by tile: load is called in that order)
+        if (part == nparts - 1) {
+            if constexpr (TRA)
+                a_base += a_step;
+            if constexpr (TRB)
+                b_base += b_step;
+        }
     };
 
     // ADAPT, behind the k-tiles of X and W: k-tiles of one adapter's ranks.  The
@@ -502,10 +575,16 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                        __attribute__((always_inline)) {
         i32x4 v;
         const uint32_t c1 = c + 4u * (uint32_t)pitch;
-        const s16x4 lo = lds_read_tr16(
-            (lds_s16x4*)(lds + (at.b[c >> 16] ^ ((uint32_t)i << 5)) + (c & 0xFFFFu)));
-        const s16x4 hi = lds_read_tr16(
-            (lds_s16x4*)(lds + (at.b[c1 >> 16] ^ ((uint32_t)i << 5)) + (c1 & 0xFFFFu)));
+        // (formed at the read: hoisted out of the K loop, the 12 fragments' addresses
+        // in two halves of LDS took 24 registers and others were spilled for them)
+        uint32_t x = at.b[c >> 16], y = at.b[c1 >> 16];
+        asm volatile("" : "+v"(x));
+        if (c1 >> 16 != c >> 16)
+            asm volatile("" : "+v"(y));
+        else
+            y = x;
+        const s16x4 lo = lds_read_tr16((lds_s16x4*)(lds + (x ^ ((uint32_t)i << 5)) + (c & 0xFFFFu)));
+        const s16x4 hi = lds_read_tr16((lds_s16x4*)(lds + (y ^ ((uint32_t)i << 5)) + (c1 & 0xFFFFu)));
         typedef int i32x2 __attribute__((ext_vector_type(2)));
         const i32x2 l2 = __builtin_bit_cast(i32x2, lo), h2 = __builtin_bit_cast(i32x2, hi);
         v[0] = l2[0];
@@ -551,6 +630,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         }
     };
     auto output = [&](int group, int m0, int n0, int rows) __attribute__((always_inline)) {
+        const KernelArgs q = kernel_args();
         // the lane again, as a value of its own, so that what the outputs derive
         // from it is not kept in registers through the K loop
         int ol = lane;
@@ -559,20 +639,20 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         uint8_t* stage = lds + S::OUT_AT + wave * (R * S::SROW);
         if constexpr (ADAPT) {
             store_group_block<MR, NR, S::SROW>(
-                p.C, p.ldc, p.N, p.c_vec, acc, stage, (int)row0, col_w, ol, [](int, int, f32x4&) {},
+                q->C, q->ldc, q->N, q->c_vec, acc, stage, (int)row0, col_w, ol, [](int, int, f32x4&) {},
                 [&](int r) __attribute__((always_inline)) {
-                    const int to = r < rows ? p.order[m0 + r] : -1;
-                    return to < p.S ? to : -1;
+                    const int to = r < rows ? q->order[m0 + r] : -1;
+                    return to < q->S ? to : -1;
                 });
         } else if constexpr (ROLE == GROUP_GATED) {
             auto gated = [&](auto cls) __attribute__((always_inline)) {
                 store_group_block<MR, NR, S::SROW>(
-                    p.C + (int64_t)m0 * p.ldc, p.ldc, p.N, p.c_vec, acc, stage, (int)row0, col_w, ol,
+                    q->C + (int64_t)m0 * q->ldc, q->ldc, q->N, q->c_vec, acc, stage, (int)row0, col_w, ol,
                     [&](int r, int col, f32x4& v) __attribute__((always_inline)) {
                         float f[4] = {1.f, 1.f, 1.f, 1.f};
-                        if (p.mul && r < rows && col < p.N) {
-                            const uint16_t* from = p.mul + (int64_t)(m0 + r) * p.ld_mul + col;
-                            if (p.mul_vec) {
+                        if (q->mul && r < rows && col < q->N) {
+                            const uint16_t* from = q->mul + (int64_t)(m0 + r) * q->ld_mul + col;
+                            if (q->mul_vec) {
                                 const uint2 u = *reinterpret_cast<const uint2*>(from);
                                 f[0] = __uint_as_float(u.x << 16);
                                 f[1] = __uint_as_float(u.x & 0xFFFF0000u);
@@ -581,18 +661,18 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                             } else {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    f[e] = bf16_to_f32(from[min(e, p.N - 1 - col)]);
+                                    f[e] = bf16_to_f32(from[min(e, q->N - 1 - col)]);
                             }
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float a = activate_c<decltype(cls)::value>(p.act, v[e]);
-                            v[e] = p.mul ? a * f[e] : a;
+                            const float a = activate_c<decltype(cls)::value>(q->act, v[e]);
+                            v[e] = q->mul ? a * f[e] : a;
                         }
                     },
                     [&](int r) __attribute__((always_inline)) { return r < rows ? r : -1; });
             };
-            switch (act_class(p.act)) {
+            switch (act_class(q->act)) {
             case 1:
                 gated(std::integral_constant<int, 1>{});
                 break;
@@ -603,11 +683,31 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                 gated(std::integral_constant<int, 0>{});
             }
         } else {
-            store_bf16_block<MR, NR, 1, S::SROW>(p.C + group * p.c_group, p.ldc, p.N, p.c_vec, acc, stage,
+            store_bf16_block<MR, NR, 1, S::SROW>(q->C + group * q->c_group, q->ldc, q->N, q->c_vec, acc, stage,
                                                  m0, rows, (int)row0, col_w, ol);
         }
     };
 
+    // (but DW:) Round r of the grid takes items r G .. r G + G - 1, rotated by 8 r: a group's
+    // last, partly filled row of tiles comes up every few items, and without the
+    // rotation the same workgroups would get it in every round.  (8: an XCD's
+    // workgroups keep to its run of tiles.)
+    int round = 0;
+    auto next_item = [&]() __attribute__((always_inline)) {
+        if constexpr (ROLE == GROUP_DW)
+            return (item += step) < end;
+        const int G = (int)gridDim.x;
+        ++round;
+        const int left = items - round * G;
+        if (left <= 0)
+            return false;
+        if (left >= G && G % 8 == 0) {
+            item = round * G + ((int)blockIdx.x + 8 * round) % G;
+            return true;
+        }
+        item = round * G + (int)blockIdx.x;
+        return item < items;
+    };
     auto nothing = [](int, int, int, int, int) {};
     auto preload = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -623,7 +723,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             for (int j = 0; j < NR; ++j)
                 acc[mi][j] = zero_acc<AT>();
         // waves whose rows all lie past the last one only load
-        const bool idle = (int)row0 >= rows;
+        const bool idle = ROLE != GROUP_DW && (int)row0 >= rows;
         const int nomask = min(nkt, last_full);
         if (!idle)
             k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, nomask, load, read, mma);
@@ -637,8 +737,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         }
         // the next item's loads go out before this one's outputs
         const int o_group = group, o_m0 = m0, o_n0 = n0, o_rows = rows;
-        item += (int)gridDim.x;
-        const bool more = item < items;
+        const bool more = next_item();
         if (more) {
             set_item(item);
             preload();
@@ -682,7 +781,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_inner_kernel(InnerArgs p)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lc = lane & 15, lg = lane >> 4;
-    build_table<64 * WAVES, false>(table, p.offsets, p.groups, p.S, 16 * MB);
+    build_table<64 * WAVES, false>(table, p.offsets, p.groups, p.S, 16 * MB, 0);
     const int block = (int)blockIdx.x;
     if (block >= table.first(p.groups))
         return;
