@@ -868,7 +868,7 @@ def linear_distillation_grad(X, W, index, teacher, lse, logp, dloss, *, scale: f
 
 # ------------------------- linear layers whose weight depends on the row
 def group_sort_workspace_bytes(T: int, slots: int, groups: int) -> int:
-    """Workspace of group_sort for ids [T, slots]: 0 up to 8192 slots."""
+    """Workspace of group_sort for ids [T, slots]: 0 up to 4096 slots."""
     return int(lib.group_sort_workspace_bytes(T, slots, groups))
 
 
@@ -934,12 +934,15 @@ def _place(fn: str, place, T=None):
     return T, k
 
 
-def _one_device(fn: str, names: str, *tensors) -> int:
+def _one_device(fn: str, names: str, first, *others) -> int:
     """The device of the first tensor, which the others (None: absent) share."""
-    dev = tensors[0].get_device()
-    for i, t in enumerate(tensors):
-        if t is not None and (dev < 0 or t.get_device() != dev):
-            _refuse(fn, names.split()[i], "a device tensor" if i == 0 or dev < 0 else f"on cuda:{dev}")
+    dev = first.get_device()
+    if dev < 0:
+        _refuse(fn, names.split()[0], "a device tensor")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            name = next(n for n, o in zip(names.split()[1:], others) if o is t)
+            _refuse(fn, name, f"a device tensor on cuda:{dev}")
     return dev
 
 
@@ -970,7 +973,7 @@ def _group_call(fn: str, dev: int, *args):
     torch = _torch()
     call = getattr(lib, fn)
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = call(*args, stream)
     else:
         with torch.cuda.device(dev):

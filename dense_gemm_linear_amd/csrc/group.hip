@@ -12,19 +12,25 @@ namespace {
 // ---------------------------------------------------------------------------
 // Sort.  A stable counting sort of S slots by group id, ids outside [0, groups)
 // behind the rest as a group of their own (`none`).  One workgroup of 16 waves
-// takes a chunk of slots, every wave a contiguous part of it, 64 slots at a
-// time:
-//   1. each wave counts its slots by group;
-//   2. thread g turns group g's counts into the position of each wave's first
-//      slot of it: rows of all lower groups, then of the waves (and chunks)
-//      before;
-//   3. each wave walks its slots again; a slot's position is its group's next
-//      one plus the number of lower lanes with the same group, which log2(groups)
-//      ballots tell.
-// Integers only: the result does not depend on any order of execution.
+// takes a chunk of up to 8192 slots, every wave a contiguous part of it, 64 slots
+// at a time:
+//   1. a slot's number among its wave's slots of the same group: those of the
+//      steps before (a count per wave and group in LDS) and those of the lower
+//      lanes, which log2(groups) ballots tell (LDS atomics on the counts took
+//      longer the fewer groups there were: 12 us for 8190 slots of 8 groups, 8 now);
+//   2. thread g adds up group g's counts: rows of all lower groups, then of the
+//      chunks and waves before;
+//   3. each slot's position is the sum of both.
+// Integers only: the result does not depend on any order of execution.  More
+// chunks than one get their counts from a launch before, and many chunks the sums
+// over the chunks before from one between.
 constexpr int kSortWaves = 16;
-constexpr int kSortOne = 8192;         // slots up to which one workgroup takes all
-constexpr int kSortChunks = 256;       // at most
+constexpr int kSortBatch = 8;          // slots a lane at most
+constexpr int kSortMost = kSortWaves * 64 * kSortBatch;
+// Slots that one workgroup takes: 2048 in 4.6 us, 4096 in 6.2, 8192 in 9 to 14; two
+// launches over chunks of 1024 take 7 to 8.
+constexpr int kSortOne = 4096;
+constexpr int kSortScan = 32;          // chunks from which on their counts are summed apart
 
 struct SortArgs {
     const int64_t* ids;
@@ -35,6 +41,7 @@ struct SortArgs {
     int S, groups;
     int chunk;
     int* counts;           // [chunks][groups + 1], null: one chunk
+    int* totals;           // [groups + 1], counts are sums already; null: they are not
     int* offsets;
     int* order;
     int* place;
@@ -51,15 +58,6 @@ __device__ __forceinline__ int slot_group(const SortArgs& p, int s)
     return id >= 0 && id < p.groups ? (int)id : p.groups;
 }
 
-// The groups of slots s, s + step, ... below s1, the ids' loads all in flight.
-constexpr int kBatch = 8;
-__device__ __forceinline__ void batch_groups(const SortArgs& p, int s, int s1, int step, int (&id)[kBatch])
-{
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-        id[i] = s + i * step < s1 ? slot_group(p, s + i * step) : 0;
-}
-
 __device__ __forceinline__ int wave_scan(int x, int lane)
 {
 #pragma unroll
@@ -70,24 +68,92 @@ __device__ __forceinline__ int wave_scan(int x, int lane)
     return x;
 }
 
+// A wave's slots: [w0, w1) of the workgroup's chunk.
+struct WavePart {
+    int w0, w1;
+};
+__device__ __forceinline__ WavePart wave_part(const SortArgs& p, int wave)
+{
+    const int s0 = (int)blockIdx.x * p.chunk, s1 = min(p.S, s0 + p.chunk);
+    const int part = (s1 - s0 + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
+    WavePart w;
+    w.w0 = min(s1, s0 + wave * part);
+    w.w1 = min(s1, w.w0 + part);
+    return w;
+}
+
+// Step 1: the groups of a wave's slots and their numbers; `count` is the wave's
+// counts, zeros before.
+__device__ __forceinline__ void number_slots(const SortArgs& p, const WavePart& w, int lane, int* count,
+                                             int (&id)[kSortBatch], int (&number)[kSortBatch])
+{
+#pragma unroll
+    for (int i = 0; i < kSortBatch; ++i)
+        id[i] = w.w0 + i * 64 + lane < w.w1 ? slot_group(p, w.w0 + i * 64 + lane) : 0;
+    const int bits = 32 - __clz(p.groups);
+#pragma unroll
+    for (int i = 0; i < kSortBatch; ++i) {
+        if (w.w0 + i * 64 >= w.w1)
+            break;
+        const bool in = w.w0 + i * 64 + lane < w.w1;
+        const int g = id[i];
+        uint64_t same = __ballot(in);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t set = __ballot((g >> b) & 1);
+            same &= (g >> b) & 1 ? set : ~set;
+        }
+        const int rank = __popcll(same & ((UINT64_C(1) << lane) - 1));
+        number[i] = count[g] + rank;
+        wave_lds_order();
+        if (in && rank == 0)
+            count[g] = number[i] + __popcll(same);
+        wave_lds_order();
+    }
+}
+
 __global__ __launch_bounds__(1024) void group_count_kernel(SortArgs p)
 {
-    __shared__ int found[kMaxGroups + 1];
-    for (int g = threadIdx.x; g <= p.groups; g += 1024)
-        found[g] = 0;
+    __shared__ int count[kSortWaves][kMaxGroups + 1];
+    const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    for (int g = lane; g <= p.groups; g += 64)
+        count[wave][g] = 0;
+    wave_lds_order();
+    int id[kSortBatch], number[kSortBatch];
+    number_slots(p, wave_part(p, wave), lane, count[wave], id, number);
     __syncthreads();
-    const int s0 = (int)blockIdx.x * p.chunk, s1 = min(p.S, s0 + p.chunk);
-    for (int s = s0 + (int)threadIdx.x; s < s1; s += 1024 * kBatch) {
-        int id[kBatch];
-        batch_groups(p, s, s1, 1024, id);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (s + i * 1024 < s1)
-                atomicAdd(&found[id[i]], 1);
+    for (int g = threadIdx.x; g <= p.groups; g += 1024) {
+        int n = 0;
+        for (int w = 0; w < kSortWaves; ++w)
+            n += count[w][g];
+        p.counts[(int64_t)blockIdx.x * (p.groups + 1) + g] = n;
     }
-    __syncthreads();
-    for (int g = threadIdx.x; g <= p.groups; g += 1024)
-        p.counts[(int64_t)blockIdx.x * (p.groups + 1) + g] = found[g];
+}
+
+// One workgroup a group: its chunks' counts become the sums of those before.
+__global__ __launch_bounds__(256) void group_scan_kernel(SortArgs p, int chunks)
+{
+    __shared__ int sums[4];
+    const int g = (int)blockIdx.x, lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    int total = 0;
+    for (int c0 = 0; c0 < chunks; c0 += 256) {
+        const int c = c0 + (int)threadIdx.x;
+        int* at = p.counts + (int64_t)c * (p.groups + 1) + g;
+        const int n = c < chunks ? *at : 0;
+        const int upto = wave_scan(n, lane);
+        if (lane == 63)
+            sums[wave] = upto;
+        __syncthreads();
+        int before = total + upto - n;
+        for (int w = 0; w < 4; ++w) {
+            before += w < wave ? sums[w] : 0;
+            total += sums[w];
+        }
+        if (c < chunks)
+            *at = before;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        p.totals[g] = total;
 }
 
 __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
@@ -99,42 +165,44 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
     for (int g = lane; g <= G; g += 64)
         next[wave][g] = 0;
     wave_lds_order();
-    const int s0 = (int)blockIdx.x * p.chunk, s1 = min(p.S, s0 + p.chunk);
-    const int part = (s1 - s0 + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
-    const int w0 = min(s1, s0 + wave * part), w1 = min(s1, w0 + part);
-    for (int s = w0 + lane; s < w1; s += 64 * kBatch) {
-        int id[kBatch];
-        batch_groups(p, s, w1, 64, id);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (s + i * 64 < w1)
-                atomicAdd(&next[wave][id[i]], 1);
-    }
+    const WavePart w = wave_part(p, wave);
+    int id[kSortBatch], number[kSortBatch];
+    number_slots(p, w, lane, next[wave], id, number);
     __syncthreads();
-    // thread g: rows of group g in all (the group none: thread 0, last)
+    // rows of group g in all, and in the chunks before
     auto totals = [&](int g, int& before) {
         int total = 0;
         before = 0;
+        if (p.totals) {
+            before = p.counts[(int64_t)blockIdx.x * (G + 1) + g];
+            return p.totals[g];
+        }
         if (p.counts) {
-#pragma unroll 8
+#pragma unroll 16
             for (int c = 0; c < (int)gridDim.x; ++c) {
                 const int n = p.counts[(int64_t)c * (G + 1) + g];
                 before += c < (int)blockIdx.x ? n : 0;
                 total += n;
             }
         } else {
-            for (int w = 0; w < kSortWaves; ++w)
-                total += next[w][g];
+#pragma unroll
+            for (int v = 0; v < kSortWaves; ++v)
+                total += next[v][g];
         }
         return total;
     };
     auto starts = [&](int g, int at) {
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int n = next[w][g];
-            next[w][g] = at;
-            at += n;
+        int n[kSortWaves];
+#pragma unroll
+        for (int v = 0; v < kSortWaves; ++v)
+            n[v] = next[v][g];
+#pragma unroll
+        for (int v = 0; v < kSortWaves; ++v) {
+            next[v][g] = at;
+            at += n[v];
         }
     };
+    // thread g: group g (and thread 0 `none`, behind all)
     int before = 0;
     const int total = tid < G ? totals(tid, before) : 0;
     const int upto = wave_scan(total, lane);
@@ -142,9 +210,9 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
         sums[wave] = upto;
     __syncthreads();
     int base = 0, all = 0;
-    for (int w = 0; w < kSortWaves; ++w) {
-        base += w < wave ? sums[w] : 0;
-        all += sums[w];
+    for (int v = 0; v < kSortWaves; ++v) {
+        base += v < wave ? sums[v] : 0;
+        all += sums[v];
     }
     if (tid < G) {
         const int first = base + upto - total;
@@ -153,40 +221,20 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
             p.offsets[tid] = first;
     }
     if (tid == 0) {
-        int none_before = 0;
-        if (p.counts)
-            for (int c = 0; c < (int)blockIdx.x; ++c)
-                none_before += p.counts[(int64_t)c * (G + 1) + G];
+        int none_before;
+        totals(G, none_before);
         starts(G, all + none_before);
         if (blockIdx.x == 0)
             p.offsets[G] = all;
     }
     __syncthreads();
-    const int bits = 32 - __clz(G);
-    for (int s = w0; s < w1; s += 64 * kBatch) {
-        int id[kBatch];
-        batch_groups(p, s + lane, w1, 64, id);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (s + i * 64 >= w1)
-                break;
-            const int slot = s + i * 64 + lane, g = id[i];
-            const bool in = slot < w1;
-            uint64_t same = __ballot(in);
-            for (int b = 0; b < bits; ++b) {
-                const uint64_t set = __ballot((g >> b) & 1);
-                same &= (g >> b) & 1 ? set : ~set;
-            }
-            const int rank = __popcll(same & ((UINT64_C(1) << lane) - 1));
-            const int at = next[wave][g] + rank;
-            wave_lds_order();
-            if (in && rank == 0)
-                next[wave][g] = at + __popcll(same);
-            wave_lds_order();
-            if (in) {
-                p.order[at] = slot;
-                p.place[slot] = g < G ? at : -1;
-            }
+    for (int i = 0; i < kSortBatch; ++i) {
+        const int slot = w.w0 + i * 64 + lane;
+        if (slot < w.w1) {
+            const int at = next[wave][id[i]] + number[i];
+            p.order[at] = slot;
+            p.place[slot] = id[i] < G ? at : -1;
         }
     }
 }
@@ -198,8 +246,39 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
 // pieces write the same values where they overlap.
 typedef i32x4 i32x4_u __attribute__((aligned(1)));
 
+// The row of this thread, TPR (64 or 256) of which take one: the same in a whole
+// wave, so that what hangs on it alone is loaded by scalar loads.
+template <int TPR>
+__device__ __forceinline__ int my_row()
+{
+    static_assert(TPR == 64 || TPR == 256, "whole waves");
+    return TPR == 256 ? (int)blockIdx.x
+                      : (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+}
+
 __device__ __forceinline__ i32x4 load_piece(const void* p) { return *static_cast<const i32x4_u*>(p); }
 __device__ __forceinline__ void store_piece(void* p, i32x4 v) { *static_cast<i32x4_u*>(p) = v; }
+// Non-temporal accesses.  Loads of the experts' rows in the join and its gradient,
+// their last use: as good in a layer (8190 rows of 4096: gather, two products and
+// join 383 us, 385 without), and the rows that other kernels left in the caches are
+// not pushed out (gather and join alone 40 us against 42, 65536 rows of 2048 120
+// against 140).  Stores of sorted rows where these fill the Infinity Cache, so that
+// the product that reads them would not find them there: 120 -> 105 us, the layer even
+// (755 -> 750); below that they cost the product more than they save (8190 rows of
+// 4096: 393 us against 385).
+constexpr int64_t kCacheBytes = INT64_C(256) << 20;
+__device__ __forceinline__ i32x4 load_piece_nt(const void* p)
+{
+    return __builtin_nontemporal_load(static_cast<const i32x4_u*>(p));
+}
+template <bool NT>
+__device__ __forceinline__ void store_sorted(void* p, i32x4 v)
+{
+    if constexpr (NT)
+        __builtin_nontemporal_store(v, static_cast<i32x4_u*>(p));
+    else
+        store_piece(p, v);
+}
 
 struct GatherArgs {
     const uint8_t* X;
@@ -213,10 +292,10 @@ struct GatherArgs {
 
 // TPR threads a row.  A token's row is read once and written to each of its
 // slots' places (a copy by sorted position reads it k times).
-template <int TPR>
+template <int TPR, bool NT>
 __global__ __launch_bounds__(256) void group_gather_kernel(GatherArgs p)
 {
-    const int t = (int)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+    const int t = my_row<TPR>();
     if (t >= p.T)
         return;
     const uint8_t* from = p.X + t * p.ldx_b;
@@ -234,7 +313,7 @@ __global__ __launch_bounds__(256) void group_gather_kernel(GatherArgs p)
         for (int j = 0; j < p.k; ++j) {
             const int to = place[j];
             if ((uint32_t)to < (uint32_t)p.S)
-                store_piece(p.Xs + to * p.ldxs_b + at, v);
+                store_sorted<NT>(p.Xs + to * p.ldxs_b + at, v);
         }
     }
 }
@@ -254,7 +333,7 @@ struct PickArgs {
 template <int TPR>
 __global__ __launch_bounds__(256) void group_pick_kernel(PickArgs p)
 {
-    const int at = (int)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+    const int at = my_row<TPR>();
     if (at >= min(p.S, p.offsets[p.groups]))
         return;
     const uint32_t slot = (uint32_t)p.order[at];
@@ -300,18 +379,21 @@ __device__ __forceinline__ i32x4 pack8(const float (&f)[8])
     return v;
 }
 
-// out[t] = sum_j w[t][j] Y[place[t][j]], j ascending, in fp32, rounded once.
-template <int TPR>
+// out[t] = sum_j w[t][j] Y[place[t][j]], j ascending, in fp32, rounded once.  TPR
+// threads a row; B slots of P pieces at a time, whose loads are all in flight: with
+// one after the other (8192 x 8 slots of 2048) the rows came at 3 TB/s.
+template <int TPR, int B, int P>
 __global__ __launch_bounds__(256) void group_combine_kernel(CombineArgs p)
 {
-    const int t = (int)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+    const int t = my_row<TPR>();
     if (t >= p.T)
         return;
     const int* place = p.place + (int64_t)t * p.k;
     const float* w = p.weights ? p.weights + t * p.ldw : nullptr;
     uint16_t* out = p.out + t * p.ldo;
+    const int q0 = (int)threadIdx.x % TPR;
     if (p.D < 8) {
-        for (int d = (int)threadIdx.x % TPR; d < p.D; d += TPR) {
+        for (int d = q0; d < p.D; d += TPR) {
             float s = 0.f;
             for (int j = 0; j < p.k; ++j)
                 if ((uint32_t)place[j] < (uint32_t)p.S)
@@ -320,42 +402,60 @@ __global__ __launch_bounds__(256) void group_combine_kernel(CombineArgs p)
         }
         return;
     }
-    for (int q = (int)threadIdx.x % TPR; q < p.pieces; q += TPR) {
-        const int at = min(q * 8, p.D - 8);
-        float sum[8] = {};
-        // four rows' loads in flight; a slot that takes no part reads the first
-        // row and counts zeros
-        for (int j0 = 0; j0 < p.k; j0 += 4) {
-            i32x4 v[4];
-            float wj[4];
-            bool in[4];
+    for (int q = q0; q < p.pieces; q += TPR * P) {
+        float sum[P][8] = {};
+        // a slot that takes no part reads the first row and counts nothing; a piece
+        // past the row is its last one again
+        for (int j0 = 0; j0 < p.k; j0 += B) {
+            i32x4 v[B][P];
+            float wj[B];
+            bool in[B];
+            int from[B];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = min(j0 + i, p.k - 1);
-                const int from = place[j];
-                in[i] = j0 + i < p.k && (uint32_t)from < (uint32_t)p.S;
-                v[i] = load_piece(p.Y + (in[i] ? from : 0) * p.ldy + at);
-                wj[i] = w ? w[j] : 1.f;
+            for (int i = 0; i < B; ++i)
+                from[i] = place[min(j0 + i, p.k - 1)];
+            if (w) {
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+                    wj[i] = w[min(j0 + i, p.k - 1)];
+            } else {
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+                    wj[i] = 1.f;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y[8];
-                unpack8(v[i], y);
+            for (int i = 0; i < B; ++i) {
+                in[i] = j0 + i < p.k && (uint32_t)from[i] < (uint32_t)p.S;
+                const uint16_t* y = p.Y + (in[i] ? from[i] : 0) * p.ldy;
+#pragma unroll
+                for (int u = 0; u < P; ++u)
+                    v[i][u] = load_piece_nt(y + min((q + u * TPR) * 8, p.D - 8));
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i)
                 if (in[i])
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum[e] = fmaf(wj[i], y[e], sum[e]);
-            }
+                    for (int u = 0; u < P; ++u) {
+                        float y[8];
+                        unpack8(v[i][u], y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            sum[u][e] = fmaf(wj[i], y[e], sum[u][e]);
+                    }
         }
-        store_piece(out + at, pack8(sum));
+#pragma unroll
+        for (int u = 0; u < P; ++u)
+            if (q + u * TPR < p.pieces)
+                store_piece(out + min((q + u * TPR) * 8, p.D - 8), pack8(sum[u]));
     }
 }
 
 // One wave a slot (t, j): dY[place] = w dout[t], dw = <dout[t], Y[place]>.  The
 // slots of a token share a workgroup, and its dout comes from the L1.
+template <bool NT>
 __global__ __launch_bounds__(256) void group_combine_grad_kernel(CombineArgs p, uint32_t k_mul)
 {
-    const int s = (int)blockIdx.x * 4 + (int)threadIdx.x / 64;
+    const int s = my_row<64>();
     const int lane = threadIdx.x & 63;
     if (s >= p.T * p.k)
         return;
@@ -386,7 +486,7 @@ __global__ __launch_bounds__(256) void group_combine_grad_kernel(CombineArgs p, 
             float d[8], r[8];
             unpack8(load_piece(dout + c), d);
             if (p.dweights) {
-                unpack8(load_piece(y + c), r);
+                unpack8(load_piece_nt(y + c), r);
                 float part = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -397,7 +497,7 @@ __global__ __launch_bounds__(256) void group_combine_grad_kernel(CombineArgs p, 
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     r[i] = w * d[i];
-                store_piece(dy + c, pack8(r));
+                store_sorted<NT>(dy + c, pack8(r));
             }
         }
     }
@@ -425,9 +525,10 @@ SortPlan sort_plan(int64_t S, int64_t groups)
 {
     SortPlan p = {S, 1, 0};
     if (S > kSortOne) {
-        p.chunk = std::max<int64_t>(4096, cdiv(cdiv(S, kSortChunks), 1024) * 1024);
+        // chunks of 1024 to 8192 slots, fewer than kSortScan of them if that does
+        p.chunk = std::min<int64_t>(kSortMost, cdiv(cdiv(S, kSortScan - 1), 1024) * 1024);
         p.chunks = cdiv(S, p.chunk);
-        p.bytes = p.chunks * (groups + 1) * 4;
+        p.bytes = (p.chunks + 1) * (groups + 1) * 4;
     }
     return p;
 }
@@ -448,8 +549,13 @@ hipError_t group_sort(const SortCall& c)
     a.offsets = c.offsets;
     a.order = c.order;
     a.place = c.place;
+    a.totals = nullptr;
     if (pl.chunks > 1) {
-        const hipError_t e = launch(group_count_kernel, pl.chunks, 1024, c.stream, a);
+        hipError_t e = launch(group_count_kernel, pl.chunks, 1024, c.stream, a);
+        if (e == hipSuccess && pl.chunks >= kSortScan) {
+            a.totals = a.counts + pl.chunks * (c.groups + 1);
+            e = launch(group_scan_kernel, c.groups + 1, 256, c.stream, a, (int)pl.chunks);
+        }
         if (e != hipSuccess)
             return e;
     }
@@ -470,8 +576,10 @@ hipError_t group_gather(const GatherCall& c)
     a.Xs = c.Xs;
     a.ldxs_b = c.ldxs_b;
     if (a.pieces <= 64)
-        return launch(group_gather_kernel<64>, cdiv(c.T, 4), 256, c.stream, a);
-    return launch(group_gather_kernel<256>, c.T, 256, c.stream, a);
+        return launch(group_gather_kernel<64, false>, cdiv(c.T, 4), 256, c.stream, a);
+    if (c.T * c.k * c.row_b < kCacheBytes)
+        return launch(group_gather_kernel<256, false>, c.T, 256, c.stream, a);
+    return launch(group_gather_kernel<256, true>, c.T, 256, c.stream, a);
 }
 
 hipError_t group_pick(const PickCall& c)
@@ -518,13 +626,19 @@ hipError_t group_combine(const CombineCall& c)
 {
     const CombineArgs a = combine_args(c);
     if (a.pieces <= 64)
-        return launch(group_combine_kernel<64>, cdiv(c.T, 4), 256, c.stream, a);
-    return launch(group_combine_kernel<256>, c.T, 256, c.stream, a);
+        return c.k <= 2 ? launch(group_combine_kernel<64, 2, 1>, cdiv(c.T, 4), 256, c.stream, a)
+                        : launch(group_combine_kernel<64, 8, 1>, cdiv(c.T, 4), 256, c.stream, a);
+    return c.k <= 2   ? launch(group_combine_kernel<256, 2, 2>, c.T, 256, c.stream, a)
+           : c.k <= 4 ? launch(group_combine_kernel<256, 4, 2>, c.T, 256, c.stream, a)
+                      : launch(group_combine_kernel<256, 8, 1>, c.T, 256, c.stream, a);
 }
 
 hipError_t group_combine_grad(const CombineCall& c)
 {
-    return launch(group_combine_grad_kernel, cdiv(c.T * c.k, 4), 256, c.stream, combine_args(c),
+    if (c.T * c.k * c.D * 2 < kCacheBytes)
+        return launch(group_combine_grad_kernel<false>, cdiv(c.T * c.k, 4), 256, c.stream, combine_args(c),
+                      divide_by(c.k));
+    return launch(group_combine_grad_kernel<true>, cdiv(c.T * c.k, 4), 256, c.stream, combine_args(c),
                   divide_by(c.k));
 }
 

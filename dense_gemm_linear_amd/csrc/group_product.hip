@@ -39,6 +39,12 @@ hipError_t go(const GroupArgs& a, int64_t extra, int cus, hipStream_t s)
 {
     GroupArgs copy = a;
     copy.tiles_n = (int)cdiv(a.N, S::TN);
+    if (ROLE == GROUP_ADAPT) {
+        // adapters that share a k-tile are told apart by 32-bit offsets into B; else an
+        // adapter's units fill whole k-tiles
+        copy.pack = a.groups * a.lb_group < (INT64_C(1) << 31);
+        copy.units = (int)(copy.pack ? cdiv(a.R, 16) : cdiv(a.R, S::KT / 2) * (S::KT / 32));
+    }
     const int64_t tiles_m = ROLE == GROUP_DW ? a.groups * cdiv(a.M, S::TM)
                                              : ROLE == GROUP_ADAPT ? cdiv(a.S, S::TM) : a.S / S::TM + extra;
     const int64_t items = tiles_m * copy.tiles_n;
@@ -66,8 +72,6 @@ hipError_t go_plain(int shape, const GroupArgs& a, int64_t extra, int cus, hipSt
         return go<GFew, ROLE>(a, extra, cus, s);
     case G_FEW_SLIM:
         return go<GFewSlim, ROLE>(a, extra, cus, s);
-    case G_LOW:
-        return go<GLow, ROLE>(a, extra, cus, s);
     case G_LOW_SLIM:
         return go<GLowSlim, ROLE>(a, extra, cus, s);
     case G_ONE:
@@ -111,13 +115,9 @@ hipError_t launch_group_dx(int shape, const GroupArgs& a, int64_t extra, int cus
 #elif DG_GROUP_ROLE == 2
 hipError_t launch_group_dw(int shape, const GroupArgs& a, int64_t extra, int cus, hipStream_t s)
 {
-    switch (shape) {
-    case G_BIG:
-        return go<GBig, GROUP_DW>(a, extra, cus, s);
-    case G_TALL:
-        return go<GTall, GROUP_DW>(a, extra, cus, s);
-    }
-    return go<GMid, GROUP_DW>(a, extra, cus, s);
+    // (256 x 256 tiles spill registers into the K loop here, and took 368 us where 256 x
+    // 128 ones took 299)
+    return shape == G_TALL ? go<GTall, GROUP_DW>(a, extra, cus, s) : go<GMid, GROUP_DW>(a, extra, cus, s);
 }
 #endif
 
@@ -125,59 +125,69 @@ hipError_t launch_group_dw(int shape, const GroupArgs& a, int64_t extra, int cus
 
 namespace {
 
+// What one round of tiles (every CU holding its fill of workgroups) takes, in
+// microseconds: kt for each 32 values of K, epi for the rest; kt1 where there is at
+// most one workgroup a CU.  Fitted to the times of all shapes at 61 sizes (1 to 8192
+// tokens, 1 to 8 choices, 4 to 128 groups, N 520 to 11008, K 512 to 11008, with
+// adapters and without): the shape chosen then took 1.5 % longer than the best on
+// average, 16 % at most.
 struct Cost {
     int shape, tm, tn, per_cu;
-    double kt, kt1, epi;         // as ShapeCost in loss.hip: us a round for 32 of K, and its rest
+    double kt, kt1, epi;
 };
-constexpr Cost kCosts[] = {{G_BIG, GBig::TM, GBig::TN, GBig::PER_CU, 0.72, 0.72, 9.0},
-                           {G_TALL, GTall::TM, GTall::TN, GTall::PER_CU, 0.48, 0.48, 4.5},
-                           {G_MID, GMid::TM, GMid::TN, GMid::PER_CU, 0.64, 0.50, 0.5},
-                           {G_LINE, GLine::TM, GLine::TN, GLine::PER_CU, 0.56, 0.47, 1.0},
-                           {G_DEEP, GDeep::TM, GDeep::TN, GDeep::PER_CU, 0.30, 0.29, 2.0}};
+template <class S>
+constexpr Cost cost_of(int shape, double kt, double kt1, double epi)
+{
+    return {shape, S::TM, S::TN, S::PER_CU, kt, kt1, epi};
+}
+constexpr Cost kPlain[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5),          cost_of<GTall>(G_TALL, 0.48, 0.42, 3.8),
+                           cost_of<GLine>(G_LINE, 0.56, 0.38, 2.5),        cost_of<GDeep>(G_DEEP, 0.28, 0.27, 2.3),
+                           cost_of<GSlim>(G_SLIM, 0.20, 0.16, 2.0),        cost_of<GFew>(G_FEW, 0.41, 0.19, 4.6),
+                           cost_of<GFewSlim>(G_FEW_SLIM, 0.21, 0.11, 4.0), cost_of<GLowSlim>(G_LOW_SLIM, 0.17, 0.12, 2.7),
+                           cost_of<GOne>(G_ONE, 0.12, 0.08, 1.9)};
+constexpr Cost kDx[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5), cost_of<GTall>(G_TALL, 0.48, 0.42, 3.8),
+                        cost_of<GMid>(G_MID, 0.64, 0.50, 0.5), cost_of<GFew>(G_FEW, 0.41, 0.19, 4.6),
+                        cost_of<GLow>(G_LOW, 0.40, 0.20, 1.3)};
+// dW: the rest of a tile is its output (4096 rows of K a group and tile would be
+// alike; of the two the wider tile takes longer to start and store)
+constexpr Cost kDw[] = {cost_of<GTall>(G_TALL, 0.48, 0.48, 7.3), cost_of<GMid>(G_MID, 0.64, 0.64, 5.6)};
 
-// Estimated time of `tiles` rows of tiles over `cols` columns and k values.
-double tiles_us(const Cost& c, double tiles, int64_t cols, int64_t k, int cus)
+// Estimated time of `tiles` rows of tiles over `cols` columns and `kts` times 32
+// values of K.
+double tiles_us(const Cost& c, double tiles, int64_t cols, double kts, int cus)
 {
     const double items = tiles * (double)cdiv(cols, c.tn), round = (double)cus * c.per_cu;
-    const double full = (double)(int64_t)(items / round), left = items - full * round, kts = (double)cdiv(k, 32);
+    const double full = (double)(int64_t)(items / round), left = items - full * round;
     return full * (kts * c.kt + c.epi) + (left > 0.5 ? kts * (left > cus ? c.kt : c.kt1) + c.epi : 0.0);
 }
 
-// Tiles of tm rows that `rows` rows in `used` groups are expected to make: half
-// a tile a group is empty on average.
+// Tiles of tm rows that `rows` rows in `used` groups are expected to make: a group's
+// last tile is half empty on average, and groups are uneven.
 double row_tiles(int64_t rows, int64_t used, int tm)
 {
-    if (used == 1)
-        return (double)cdiv(rows, tm);
-    return (double)used * std::max(1.0, (double)rows / (double)used / tm + 0.5);
+    const double mean = (double)rows / (double)used;
+    return (double)used * std::max(mean > 1.5 ? 1.1 : 1.0, mean / tm + 0.55);
 }
 
-int pick(std::initializer_list<int> of, int64_t rows, int64_t used, int64_t cols, int64_t k, int cus)
+// The shape of the least estimate, us(cost).  The smallest tiles only where they
+// make no second round: what bounds such a product is reading W, which they do
+// less well (16 x 2 rows of 8 groups of 4096 x 4096: 51 us against 44).
+template <int N, class Tiles>
+int pick(const Cost (&of)[N], int64_t cols, double kts, int cus, Tiles&& tiles)
 {
     int best = -1;
-    double us = 0.0;
-    for (int i : of) {
-        const double t = tiles_us(kCosts[i], row_tiles(rows, used, kCosts[i].tm), cols, k, cus);
-        if (best < 0 || t < us) {
-            best = kCosts[i].shape;
-            us = t;
+    double least = 0.0;
+    for (const Cost& c : of) {
+        const double t = tiles(c.tm);
+        if (c.shape == G_ONE && t * (double)cdiv(cols, c.tn) > (double)cus * c.per_cu)
+            continue;
+        const double us = tiles_us(c, t, cols, kts, cus);
+        if (best < 0 || us < least) {
+            best = c.shape;
+            least = us;
         }
     }
     return best;
-}
-
-// Shape of a product whose W rows are read as they lie.  Few rows a group: the
-// tile that covers twice their mean, narrow where wide tiles make no full round.
-int plain_shape(int64_t rows, int64_t used, int64_t cols, int64_t k, int cus)
-{
-    const int64_t mean = cdiv(rows, used);
-    if (mean <= 2 && used * cdiv(cols, 32) <= 8 * cus)
-        return G_ONE;
-    if (mean <= 16)
-        return used * cdiv(cols, 128) <= 2 * cus ? G_LOW_SLIM : G_LOW;
-    if (mean <= 40)
-        return used * cdiv(cols, 128) <= 2 * cus ? G_FEW_SLIM : G_FEW;
-    return pick({0, 1, 3, 4}, rows, used, cols, k, cus);
 }
 
 GroupArgs base_args(const ProductCall& c)
@@ -223,7 +233,8 @@ hipError_t group_forward(const ProductCall& c)
     a.ld_mul = c.ld_mul;
     a.mul_vec = ((uintptr_t)c.mul & 7u) == 0 && c.ld_mul % 4 == 0 && c.N % 4 == 0;
     a.b_nt = 1;
-    const int shape = plain_shape(S, used, c.N, c.K, c.cus);
+    const int shape = pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus,
+                           [&](int tm) { return row_tiles(S, used, tm); });
     return c.act || c.mul ? launch_group_gated(shape, a, used, c.cus, c.stream)
                           : launch_group_fwd(shape, a, used, c.cus, c.stream);
 }
@@ -244,8 +255,8 @@ hipError_t group_backward(const ProductCall& c)
         a.ldc = c.lddx;
         a.c_vec = vec_of(c.dX, c.lddx, c.K);
         a.b_nt = 1;
-        const int64_t mean = cdiv(S, used);
-        const int shape = mean <= 16 ? G_LOW : mean <= 40 ? G_FEW : pick({0, 1, 2}, S, used, c.K, c.N, c.cus);
+        const int shape = pick(kDx, c.K, (double)cdiv(c.N, 32), c.cus,
+                               [&](int tm) { return row_tiles(S, used, tm); });
         const hipError_t e = launch_group_dx(shape, a, used, c.cus, c.stream);
         if (e != hipSuccess)
             return e;
@@ -283,57 +294,80 @@ hipError_t group_backward(const ProductCall& c)
     a.ldc = c.lddw;
     a.c_group = c.lddw_group;
     a.c_vec = vec_of(c.dW, c.lddw, c.K) && c.lddw_group % 8 == 0;
-    int shape = G_MID;
-    double best = 0.0;
-    for (int i : {0, 1, 2}) {
-        const double us = tiles_us(kCosts[i], (double)(c.groups * cdiv(c.N, kCosts[i].tm)), c.K, cdiv(S, c.groups),
-                                   c.cus);
-        if (best == 0.0 || us < best) {
-            best = us;
-            shape = kCosts[i].shape;
-        }
-    }
+    const int shape = pick(kDw, c.K, (double)cdiv(cdiv(S, c.groups), 32), c.cus,
+                           [&](int tm) { return (double)(c.groups * cdiv(c.N, tm)); });
     return launch_group_dw(shape, a, 0, c.cus, c.stream);
+}
+
+template <class Args>
+hipError_t launch(const void* kernel, dim3 grid, int block, Args a, hipStream_t s)
+{
+    void* args[] = {&a};
+    return hipLaunchKernel(kernel, grid, dim3((unsigned)block), args, 0, s);
 }
 
 hipError_t adapters_forward(const ProductCall& c)
 {
     const int64_t T = c.T;
+    if (T == 1) {
+        TokenArgs t;
+        t.X = c.X;
+        t.W = c.W;
+        t.ldw = c.ldw;
+        t.A = c.A;
+        t.lda = c.lda;
+        t.a_group = c.lda_group;
+        t.B = c.B;
+        t.ldb = c.ldb;
+        t.b_group = c.ldb_group;
+        t.scale = c.scale;
+        t.offsets = c.offsets;
+        t.groups = (int)c.groups;
+        t.N = (int)c.N;
+        t.K = (int)c.K;
+        t.R = (int)c.R;
+        t.Y = c.Y;
+        // one workgroup of 16 waves a CU, with as many rows a wave as that takes, up to 4
+        constexpr int WAVES = 16;
+        const int64_t rows = std::min<int64_t>(4, cdiv(c.N, (int64_t)c.cus * WAVES));
+        const void* kernel = rows == 1   ? reinterpret_cast<const void*>(&adapter_token_kernel<1, WAVES>)
+                             : rows == 2 ? reinterpret_cast<const void*>(&adapter_token_kernel<2, WAVES>)
+                             : rows == 3 ? reinterpret_cast<const void*>(&adapter_token_kernel<3, WAVES>)
+                                         : reinterpret_cast<const void*>(&adapter_token_kernel<4, WAVES>);
+        return launch(kernel, dim3((unsigned)cdiv(c.N, rows * WAVES)), 64 * WAVES, t, c.stream);
+    }
     const uint32_t x_bytes = (uint32_t)((T - 1) * c.ldx * 2 + c.K * 2);
-    if (c.R > 0 && c.groups > 0) {
-        InnerArgs i;
-        i.X = reinterpret_cast<const uint8_t*>(c.X);
-        i.ldx_b = c.ldx * 2;
-        i.x_bytes = x_bytes;
-        i.offsets = c.offsets;
-        i.order = c.order;
-        i.groups = (int)c.groups;
-        i.S = (int)T;
-        i.A = reinterpret_cast<const uint8_t*>(c.A);
-        i.lda_b = c.lda * 2;
-        i.a_group = c.lda_group * 2;
-        i.scale = c.scale;
-        i.R = (int)c.R;
-        i.K = (int)c.K;
-        i.U = reinterpret_cast<uint16_t*>(c.ws);
-        // 16 rows a workgroup; 32, which read A half as often, where 16 make more
-        // than one round
-        const int64_t cols = c.R > 32 ? 64 : c.R > 16 ? 32 : 16, wide = cdiv(c.R, cols);
-        const bool two = (T / 16 + std::min(c.groups, T)) * wide > c.cus;
-        const int64_t blocks = T / (two ? 32 : 16) + std::min(c.groups, T);
-        void* args[] = {&i};
-        const void* kernel =
-            two ? (cols == 64   ? reinterpret_cast<const void*>(&adapter_inner_kernel<4, 2, 8, 2>)
+    InnerArgs i;
+    i.X = reinterpret_cast<const uint8_t*>(c.X);
+    i.ldx_b = c.ldx * 2;
+    i.x_bytes = x_bytes;
+    i.offsets = c.offsets;
+    i.order = c.order;
+    i.groups = (int)c.groups;
+    i.S = (int)T;
+    i.A = reinterpret_cast<const uint8_t*>(c.A);
+    i.lda_b = c.lda * 2;
+    i.a_group = c.lda_group * 2;
+    i.scale = c.scale;
+    i.R = (int)c.R;
+    i.K = (int)c.K;
+    i.U = reinterpret_cast<uint16_t*>(c.ws);
+    // a row a workgroup for a decode batch; else 16, or 32, which read A half as
+    // often, where 16 make more than one round
+    const int64_t cols = T <= 64 ? 16 : c.R > 32 ? 64 : c.R > 16 ? 32 : 16, wide = cdiv(c.R, cols);
+    const bool two = T > 64 && (T / 16 + std::min(c.groups, T)) * wide > c.cus;
+    const int64_t blocks = T <= 64 ? T : T / (two ? 32 : 16) + std::min(c.groups, T);
+    const void* inner =
+        T <= 64 ? reinterpret_cast<const void*>(&adapter_inner_kernel<1, 1, 16, 4, true>)
+        : two   ? (cols == 64   ? reinterpret_cast<const void*>(&adapter_inner_kernel<4, 2, 8, 2>)
                    : cols == 32 ? reinterpret_cast<const void*>(&adapter_inner_kernel<2, 2, 8, 4>)
                                 : reinterpret_cast<const void*>(&adapter_inner_kernel<1, 2, 8, 4>))
                 : (cols == 64   ? reinterpret_cast<const void*>(&adapter_inner_kernel<4, 1, 16, 2>)
                    : cols == 32 ? reinterpret_cast<const void*>(&adapter_inner_kernel<2, 1, 16, 2>)
                                 : reinterpret_cast<const void*>(&adapter_inner_kernel<1, 1, 16, 4>));
-        const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)blocks, (unsigned)wide),
-                                             dim3(two ? 512 : 1024), args, 0, c.stream);
-        if (e != hipSuccess)
-            return e;
-    }
+    const hipError_t e = launch(inner, dim3((unsigned)blocks, (unsigned)wide), two ? 512 : 1024, i, c.stream);
+    if (e != hipSuccess)
+        return e;
     GroupArgs a = base_args(c);
     a.A = reinterpret_cast<const uint8_t*>(c.X);
     a.lda_b = c.ldx * 2;
@@ -351,12 +385,11 @@ hipError_t adapters_forward(const ProductCall& c)
     a.ldlb_b = c.ldb * 2;
     a.lb_group = c.ldb_group * 2;
     a.R = (int)c.R;
-    // one group of T rows: the number is known
-    const bool narrow = cdiv(c.N, 128) <= 2 * c.cus;
-    const int shape = T <= 16 && cdiv(c.N, 32) <= 8 * c.cus ? G_ONE
-                      : T <= 32 ? (narrow ? G_LOW_SLIM : G_LOW)
-                      : T <= 64 ? (narrow ? G_FEW_SLIM : G_FEW)
-                                : pick({0, 1, 3, 4}, T, 1, c.N, c.K, c.cus);
+    // every row counts, groups or not; the ranks as k-tiles of about as many adapters
+    // as a tile of 64 rows has
+    const int64_t near = std::min<int64_t>(std::min(c.groups, T), cdiv(std::min(c.groups, T) * 64, T) + 1);
+    const double kts = (double)cdiv(c.K, 32) + (double)(near * cdiv(c.R, 16));
+    const int shape = pick(kPlain, c.N, kts, c.cus, [&](int tm) { return (double)cdiv(T, tm); });
     return launch_group_adapt(shape, a, 0, c.cus, c.stream);
 }
 

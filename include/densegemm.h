@@ -614,7 +614,7 @@ gemm_status linear_distillation_grad(const uint16_t* X, int64_t ldx, const uint1
  * each group the slots keep their order.  An id outside [0, groups) takes no
  * part: its slot has place -1 and stands in order behind the n others.
  *   workspace  16-byte aligned, group_sort_workspace_bytes(T, k, groups) bytes (0 up
- *              to 8192 slots: may be NULL); contents unspecified before and after.
+ *              to 4096 slots: may be NULL); contents unspecified before and after.
  *   T == 0: offsets are zeros.
  *
  * group_gather -- Xs[place[t][j]] = X[t]: the rows of X [T, ldx] by sorted

@@ -19,7 +19,7 @@ def _say(*a):
 # workgroup's, where chunks begin), one group, all of 512, empty groups
 SORTS = [(1, 1, 1, "random"), (1, 8, 64, "distinct"), (63, 1, 3, "random"), (65, 3, 512, "random"),
          (341, 3, 7, "distinct"), (1025, 1, 512, "random"), (8192, 1, 8, "one"), (4097, 2, 8, "distinct"),
-         (8193, 1, 512, "random"), (3000, 64, 100, "random"), (300001, 4, 130, "random"), (5000, 1, 9, "runs")]
+         (4096, 1, 12, "random"), (4097, 1, 512, "random"), (8193, 1, 512, "random"), (3000, 64, 100, "random"), (300001, 4, 130, "random"), (140001, 2, 512, "distinct"), (5000, 1, 9, "runs")]
 
 
 @pytest.mark.parametrize("T,k,groups,kind", SORTS)
@@ -239,7 +239,8 @@ def test_linear_grad(T, k, groups, N, K, kind):
 
 
 # T, groups, N, K, R, kind
-ADAPTERS = [(1, 1, 8, 8, 8, "one"), (1, 4, 520, 264, 16, "one"), (3, 2, 33, 24, 8, "random"),
+ADAPTERS = [(1, 1, 8, 8, 8, "one"), (1, 4, 520, 264, 16, "one"), (1, 512, 4099, 2056, 72, "random"),
+            (1, 3, 20011, 5000, 256, "one"), (1, 2, 9000, 40, 24, "random"), (2, 3, 1000, 4104, 16, "random"), (3, 2, 33, 24, 8, "random"),
             (16, 16, 136, 72, 40, "random"), (48, 64, 1032, 264, 16, "random"), (64, 512, 200, 136, 24, "random"),
             (130, 3, 257, 520, 32, "random"), (597, 16, 1000, 136, 32, "runs"), (700, 9, 2056, 264, 64, "random"),
             (2050, 30, 4104, 136, 128, "random"), (2050, 5, 4096, 72, 256, "runs"), (300, 2, 20008, 96, 8, "random"),
@@ -279,3 +280,57 @@ def test_adapters(T, groups, N, K, R, kind, scaled):
     assert bool((out[:, N] == MARK).all())
     Y = dg.linear_adapters(*dev, scale=None if scale is None else scale.cuda())
     assert torch.equal(Y, out[:, :N].contiguous())
+
+
+@pytest.mark.parametrize("T,groups,N,K,R", [(2, 2, 40, 64, 8), (48, 5, 300, 264, 16), (200, 4, 520, 136, 24),
+                                            (600, 3, 2056, 72, 64)])
+def test_adapters_keep_apart(T, groups, N, K, R):
+    """An adapter with infinities and NaN, a row with them, and the memory of rows
+    without an adapter reach no other row."""
+    ids = make_ids(T, 1, groups, T, none=0.2)
+    ids[0], ids[1] = 1, 0
+    off, order, place = sorted_slots(ids, groups)
+    X, W = bf16(T, K, seed=1), bf16(N, K, seed=2, scale=K ** -0.5)
+    A, B = bf16(groups, R, K, seed=3, scale=K ** -0.5), bf16(groups, N, R, seed=4, scale=0.3)
+    ws = torch.full((dg.linear_adapters_workspace_bytes(T, R, groups),), 0xFF, dtype=torch.uint8).cuda()
+    offd, orderd = off.cuda(), order.cuda()
+    good = dg.linear_adapters(X.cuda(), W.cuda(), A.cuda(), B.cuda(), offd, orderd, workspace=ws).cpu()
+    assert bool(torch.isfinite(good).all())
+    B2, A2, X2 = B.clone(), A.clone(), X.clone()
+    B2[1, ::3] = float("inf")
+    B2[1, 1] = float("nan")
+    A2[1, 2] = float("nan")
+    rest = (ids[:, 0] != 1) | (torch.arange(T) == T)
+    got = dg.linear_adapters(X.cuda(), W.cuda(), A2.cuda(), B2.cuda(), offd, orderd, workspace=ws).cpu()
+    assert torch.equal(got[rest], good[rest]) and not bool(torch.isfinite(got[0]).any())
+    X2[0] = float("nan")
+    got = dg.linear_adapters(X2.cuda(), W.cuda(), A.cuda(), B.cuda(), offd, orderd, workspace=ws).cpu()
+    assert torch.equal(got[1:], good[1:]) and bool(torch.isnan(got[0]).all())
+
+
+@pytest.mark.parametrize("T,k,groups,N,K", [(40, 2, 4, 136, 72), (700, 2, 3, 520, 136)])
+def test_linear_keeps_apart(T, k, groups, N, K):
+    """NaN in one group's weight, in one token's row and behind the last row reach
+    nothing else."""
+    off, order, place, X, W = _problem(T, k, groups, N, K, "random")
+    n, S = int(off[-1]), T * k
+    args = (off.cuda(), order.cuda())
+    good = dg.group_linear(X.cuda(), W.cuda(), *args, slots=k)[:n].cpu()
+    W2, X2 = W.clone(), X.clone()
+    W2[1] = float("nan")
+    got = dg.group_linear(X.cuda(), W2.cuda(), *args, slots=k)[:n].cpu()
+    a, b = int(off[1]), int(off[2])
+    assert torch.equal(got[:a], good[:a]) and torch.equal(got[b:], good[b:]) and bool(torch.isnan(got[a:b]).all())
+    X2[5] = float("inf")
+    got = dg.group_linear(X2.cuda(), W.cuda(), *args, slots=k)[:n].cpu()
+    other = (order[:n] // k) != 5
+    assert torch.equal(got[other], good[other])
+    # a group's NaN gradient rows stay in its own dX and dW
+    dY = bf16(S, N, seed=4)
+    dX, dW = dg.group_linear_grad(dY.cuda(), X.cuda(), W.cuda(), *args, slots=k)
+    dY[a:b] = float("nan")
+    dX2, dW2 = dg.group_linear_grad(dY.cuda(), X.cuda(), W.cuda(), *args, slots=k)
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[a:b] = False
+    assert torch.equal(dX2[:n].cpu()[keep], dX[:n].cpu()[keep])
+    assert torch.equal(dW2[0], dW[0]) and torch.equal(dW2[2:], dW[2:]) and bool(torch.isnan(dW2[1]).all())
