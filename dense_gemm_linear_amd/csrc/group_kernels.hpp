@@ -54,8 +54,6 @@ struct GroupArgs {
     const uint8_t* LB;     // ADAPT: [groups][N][ldlb]
     int64_t ldlb_b, lb_group;
     int R;
-    int units, pack;       // set by the launch, which knows the tile: 16-rank units an
-                           // adapter, and whether adapters share k-tiles of them
 };
 
 constexpr int kTableLds = ((int)kMaxGroups + 4) * 4 + 64;
@@ -366,9 +364,9 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
     const int a_step = KT * (int)p.lda_b, b_step = KT * (int)p.ldb_b;         // TRA, TRB
     const int a_rows = A_ROWS * (int)p.lda_b, b_rows = B_ROWS * (int)p.ldb_b;
     uint32_t a_bytes = 0;                                                     // GATHER
-    // ADAPT: the entries of the table that the tile's rows touch, and the k-tiles of
-    // their ranks
-    int xkt = 0, entry0 = 0, entry_end = 0;
+    // ADAPT: the first of the table's entries that the tile's rows touch, and all their
+    // units of 16 ranks
+    int units = 0, entry0 = 0;
     auto set_item = [&](int it) __attribute__((always_inline)) {
         const KernelArgs q = kernel_args();
         int t = ROLE == GROUP_DW ? it : xcd_remap(it, items), tm, tn;
@@ -432,8 +430,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             }
             entry0 = __builtin_amdgcn_readfirstlane(entry0);
             over = __builtin_amdgcn_readfirstlane(over);
-            entry_end = entry0 + over;
-            xkt = (over * q->units + STEPS - 1) / STEPS;
+            units = over * ((q->R + 15) / 16);
         }
         if constexpr (TRB) {
             b_base += (int64_t)n0 * 2;
@@ -503,62 +500,6 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                 a_base += a_step;
             if constexpr (TRB)
                 b_base += b_step;
-        }
-    };
-
-    // ADAPT, behind the k-tiles of X and W: k-tiles of ranks.  One step of the matrix
-    // cores (32 values of K) holds 16 ranks of one adapter: the rows' inner values,
-    // upper halves and then lower ones, against the same columns of B twice.  Unit u
-    // counts those steps, q->units of them an adapter.
-    auto unit_of = [&](KernelArgs q, int u, int& lo, int& hi, int& id, int& rank) __attribute__((always_inline)) {
-        const int i = u / q->units, at = entry0 + i;
-        const bool in = at < entry_end;
-        const int e0 = __builtin_amdgcn_readfirstlane(in ? table.first(at) : 0);
-        const int e1 = __builtin_amdgcn_readfirstlane(in ? table.first(at + 1) : 0);
-        id = __builtin_amdgcn_readfirstlane(in ? table.id(at) : 0);
-        lo = e0 - m0;
-        hi = e1 - m0;
-        rank = in ? (u - i * q->units) * 16 : q->R;          // (no such adapter: no rank)
-    };
-    auto load_ranks = [&](int kt, int stage) __attribute__((always_inline)) {
-        // (the lane as a value of its own, so that nothing that hangs on it lives
-        // through the loop before)
-        int ol = lane;
-        asm volatile("" : "+v"(ol));
-        const KernelArgs q = kernel_args();
-        const int r0 = KTL::ROWS_PER_LOAD * wave + ol / CHUNKS;
-        const int c = (int)((uint32_t)(ol % CHUNKS) ^ KTL::key((uint32_t)r0));
-        int lo, hi, id, rank;
-        unit_of(q, kt * STEPS, lo, hi, id, rank);
-        const uint8_t* from = q->LB + (int64_t)n0 * q->ldlb_b;
-        const int cols = min(TN, q->N - n0);
-        uint32_t records = (uint32_t)((cols - 1) * (int)q->ldlb_b + q->R * 2), at = 0;
-        if (q->pack) {                           // any adapter by a 32-bit offset
-            records = 0x7FFFFFFFu;
-            at = (uint32_t)id * (uint32_t)q->lb_group;
-        } else {                                 // a k-tile is of one adapter
-            from += id * q->lb_group;
-        }
-        if constexpr (STEPS == 2) {
-            int id1, rank1;
-            unit_of(q, kt * STEPS + 1, lo, hi, id1, rank1);
-            rank = c < 4 ? rank : rank1;
-            at = c < 4 || !q->pack ? at : (uint32_t)id1 * (uint32_t)q->lb_group;
-        }
-        const int half = c / 2 % 2;
-        rank += c % 2 * 8;
-        const rsrc_t ru = make_rsrc(uniform(q->U + (int64_t)m0 * q->R * 4), (uint32_t)(rows * q->R * 4));
-        const rsrc_t rl = make_rsrc(uniform(from), records);
-        uint8_t* base = lds + stage * STAGE;
-#pragma unroll
-        for (int n = 0; n < A_DMA; ++n)
-            dma16(ru, base + (wave + WAVES * n) * 1024,
-                  rank < q->R ? (uint32_t)(((r0 + n * A_ROWS) * 2 + half) * q->R + rank) * 2u : kOOB, 0);
-#pragma unroll
-        for (int n = 0; n < B_DMA; ++n) {
-            const int r = r0 + n * B_ROWS;
-            dma16(rl, base + A_BUF + (wave + WAVES * n) * 1024,
-                  rank < q->R && r < cols ? at + (uint32_t)r * (uint32_t)q->ldlb_b + (uint32_t)rank * 2u : kOOB, 0);
         }
     };
 
@@ -743,43 +684,68 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         else
             k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, nomask, load, nothing, nothing);
         if constexpr (ADAPT) {
-            // As many k-tiles as there are stages at a time: all their loads, then
-            // their products.  (As a second pipelined loop its registers were spilled
-            // into the first.)  A unit's products are formed apart and added to the rows
-            // of its adapter: zeros in the other rows' inner values would not keep an
-            // infinity or NaN of one request's adapter out of the others' rows.
-            for (int k0 = 0; k0 < xkt; k0 += ST) {
+            // Behind the k-tiles of X and W: the ranks of the adapters that the tile's rows
+            // have, in units of 16.  One step of the matrix cores holds a unit: the rows'
+            // inner values, upper halves and then lower ones, against the same columns of B
+            // twice, both straight from memory (a few KiB a tile).  A unit's products are
+            // formed apart and added to the rows of its adapter only: zeros in the other
+            // rows' inner values would not keep an infinity or NaN of one request's adapter
+            // out of the others' rows.
+            if (!idle && units > 0) {
+                const KernelArgs q = kernel_args();
+                // (lanes as values of their own, so that nothing that hangs on them lives
+                // through the loop before)
+                int ol = lane;
+                asm volatile("" : "+v"(ol));
+                const int oc = ol & 15, og = ol >> 4;
+                constexpr int UB = MR + NR > 8 ? 1 : MR + NR > 5 ? 3 : 4;      // units in flight
+                const int each = (q->R + 15) / 16;
+                const int cols = min(S::WCOLS, q->N - n0 - (int)col0);
+                const rsrc_t ru = make_rsrc(uniform(q->U + (int64_t)m0 * q->R * 4), (uint32_t)(rows * q->R * 4));
+                for (int u0 = 0; u0 < units; u0 += UB) {
+                    // lane i: unit u0 + i
+                    const int u = min(u0 + min(ol, UB - 1), units - 1);
+                    const int at = u / each;
+                    const int v_lo = table.first(entry0 + at) - m0, v_hi = table.first(entry0 + at + 1) - m0;
+                    const int v_id = table.id(entry0 + at), v_rank = (u - at * each) * 16;
+                    i32x4 uf[UB][MR], wf[UB][NR];
 #pragma unroll
-                for (int t = 0; t < ST; ++t)
-                    if (k0 + t < xkt)
-                        load_ranks(k0 + t, t);
-                DG_STAGE_BARRIER(0);
-                if (!idle) {
-                    const KernelArgs q = kernel_args();
-                    static_for<ST * STEPS>([&](auto ts) __attribute__((always_inline)) {
-                        constexpr int t = decltype(ts)::value / STEPS, s = decltype(ts)::value % STEPS;
-                        int lo, hi, id, rank;
-                        unit_of(q, (k0 + t) * STEPS + s, lo, hi, id, rank);
-                        if (rank >= q->R)
-                            return;
-                        read(t, s, 0, 0, 1);
+                    for (int i = 0; i < UB; ++i) {
+                        const int rank = __builtin_amdgcn_readlane(v_rank, i) + (og & 1) * 8;
+                        const uint8_t* from = q->LB + __builtin_amdgcn_readlane(v_id, i) * q->lb_group +
+                                              (int64_t)(n0 + (int)col0) * q->ldlb_b;
+                        const rsrc_t rl = make_rsrc(uniform(from), cols > 0 ? (uint32_t)((cols - 1) * (int)q->ldlb_b + q->R * 2) : 0u);
+#pragma unroll
+                        for (int j = 0; j < NR; ++j)
+                            wf[i][j] = load16(rl, rank < q->R ? (uint32_t)(j * R + oc) * (uint32_t)q->ldlb_b + (uint32_t)rank * 2u
+                                                              : kOOB);
+#pragma unroll
+                        for (int mi = 0; mi < MR; ++mi)
+                            uf[i][mi] = load16(ru, rank < q->R ? (uint32_t)((((int)row0 + mi * R + oc) * 2 + (og >> 1)) * q->R + rank) * 2u
+                                                               : kOOB);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < UB; ++i) {
+                        if (u0 + i >= units)
+                            break;
+                        const int lo = __builtin_amdgcn_readlane(v_lo, i), hi = __builtin_amdgcn_readlane(v_hi, i);
 #pragma unroll
                         for (int mi = 0; mi < MR; ++mi) {
                             const int r = (int)row0 + mi * R;
                             if (r >= hi || r + R <= lo)
                                 continue;
-                            const bool own = r + lc >= lo && r + lc < hi;
+                            const bool own = r + oc >= lo && r + oc < hi;
 #pragma unroll
                             for (int j = 0; j < NR; ++j) {
-                                const acc_t v = mfma_bf16(bf[0][j], af[0][mi], zero_acc<AT>());
+                                const acc_t v = mfma_bf16(wf[i][j], uf[i][mi], zero_acc<AT>());
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     acc[mi][j][e] += own ? v[e] : 0.f;
                             }
                         }
-                    });
+                    }
                 }
-                DG_STAGE_BARRIER(0);
             }
         }
         // the next item's loads go out before this one's outputs
@@ -793,265 +759,6 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             output(o_group, o_m0, o_n0, o_rows);
         if (!more)
             break;
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Adapters' inner values: u[p] = scale_g A_g x for every sorted row p of a
-// group, as two bf16 halves (the rounded value and the rounded rest: 16 bits of
-// it together, so that what rounding takes from u is far below the rounding of
-// Y).  One workgroup takes 16 MB rows of one group and 16 NR ranks; its waves
-// split K in chunks of 64 values (a whole line of every row), take both operands
-// straight from memory in the fragments' layout, UN chunks in flight, and add
-// their sums in LDS in a fixed order.
-// The group whose rows sorted position x is among: the number of groups that end
-// at or before it (`groups`: none).
-__device__ __forceinline__ int row_group(const int* offsets, int groups, int x, int lane)
-{
-    int n = 0;
-    for (int g = 0; g < groups; g += 64)
-        n += __popcll(__ballot(g + lane < groups && offsets[min(g + lane, groups - 1) + 1] <= x));
-    return __builtin_amdgcn_readfirstlane(n);
-}
-
-struct InnerArgs {
-    const uint8_t* X;
-    int64_t ldx_b;
-    uint32_t x_bytes;
-    const int* offsets;
-    const int* order;
-    int groups, S;
-    const uint8_t* A;      // [groups][R][lda]
-    int64_t lda_b, a_group;
-    const float* scale;
-    int R, K;
-    uint16_t* U;           // [S][2][R]
-};
-
-// BY_ROW (few rows): a workgroup for each row, which finds its group by counting
-// the offsets in front instead of by the table: 48 rows of 16 adapters, K 4096,
-// XXX us against 9.
-template <int NR, int MB, int WAVES, int UN, bool BY_ROW = false>
-__global__ __launch_bounds__(64 * WAVES) void adapter_inner_kernel(InnerArgs p)
-{
-    __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * MB * NR * 1024 + (BY_ROW ? 0 : kTableLds)];
-    f32x4* part = reinterpret_cast<f32x4*>(lds);                     // [WAVES][MB * NR][64]
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lc = lane & 15, lg = lane >> 4;
-    const int block = (int)blockIdx.x;
-    int group, m0, rows;
-    if constexpr (BY_ROW) {
-        static_assert(MB == 1);
-        m0 = block;
-        rows = 1;
-        group = row_group(p.offsets, p.groups, m0, lane);
-        if (group >= p.groups)
-            return;
-    } else {
-        GroupTable table;
-        table.at(lds + WAVES * MB * NR * 1024);
-        build_table<64 * WAVES, false>(table, p.offsets, p.groups, p.S, 16 * MB, 0);
-        if (block >= table.first(p.groups))
-            return;
-        group = __builtin_amdgcn_readfirstlane(find_entry(table, block, lane));
-        const int2 gr = group_rows(p.offsets, group, p.S);
-        m0 = __builtin_amdgcn_readfirstlane(gr.x + (block - table.first(group)) * 16 * MB);
-        rows = min(16 * MB, __builtin_amdgcn_readfirstlane(gr.y) - m0);
-    }
-    const int r0 = (int)blockIdx.y * 16 * NR;
-
-    uint32_t x_off[MB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-        x_off[m] = (uint32_t)p.order[m0 + min(16 * m + lc, rows - 1)];
-    const rsrc_t rx = make_rsrc(p.X, p.x_bytes);
-    const rsrc_t ra = make_rsrc(uniform(p.A + group * p.a_group + r0 * p.lda_b),
-                                (uint32_t)((int64_t)(min(16 * NR, p.R - r0) - 1) * p.lda_b + p.K * 2));
-    f32x4 acc[MB][NR];
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int j = 0; j < NR; ++j)
-            acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int chunks = (p.K + 63) / 64;
-    bool first = true;
-    for (int c0 = wave; c0 < chunks || first; c0 += WAVES * UN) {
-        i32x4 x[UN][2][MB], a[UN][2][NR];
-        // A's loads first: those of X wait for the rows' numbers
-#pragma unroll
-        for (int u = 0; u < UN; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = (c0 + u * WAVES) * 64 + h * 32 + lg * 8;
-#pragma unroll
-                for (int j = 0; j < NR; ++j)
-                    a[u][h][j] = load16(ra, k < p.K ? (uint32_t)(16 * j + lc) * (uint32_t)p.lda_b + (uint32_t)k * 2u
-                                                    : kOOB);
-            }
-        if (first) {
-            first = false;
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-                x_off[m] = 16 * m + lc < rows && x_off[m] < (uint32_t)p.S ? x_off[m] * (uint32_t)p.ldx_b : kOOB;
-        }
-#pragma unroll
-        for (int u = 0; u < UN; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = (c0 + u * WAVES) * 64 + h * 32 + lg * 8;
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-                    x[u][h][m] = load16(rx, k < p.K ? x_off[m] + (uint32_t)k * 2u : kOOB);
-            }
-        // (all of them in flight before the first product)
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < UN; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int j = 0; j < NR; ++j)
-                        acc[m][j] = mfma_bf16(x[u][h][m], a[u][h][j], acc[m][j]);
-    }
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int j = 0; j < NR; ++j)
-            part[(wave * MB * NR + m * NR + j) * 64 + lane] = acc[m][j];
-    __syncthreads();
-    const float scale = p.scale ? p.scale[group] : 1.f;
-    for (int b = wave; b < MB * NR; b += WAVES) {
-        f32x4 sum = part[b * 64 + lane];
-#pragma unroll
-        for (int w = 1; w < WAVES; ++w)
-            sum += part[(w * MB * NR + b) * 64 + lane];
-        const int rank = r0 + 16 * (b % NR) + lc;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = 16 * (b / NR) + 4 * lg + e;
-            if (r < rows && rank < p.R) {
-                const float v = sum[e] * scale;
-                const uint16_t hi = bf16_rne(v);
-                const float rest = v - bf16_to_f32(hi);      // infinite v: none
-                uint16_t* to = p.U + (int64_t)(m0 + r) * 2 * p.R + rank;
-                to[0] = hi;
-                to[p.R] = fabsf(rest) < INFINITY ? bf16_rne(rest) : 0;
-            }
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// One token: y = W x + scale_g B_g (A_g x), all in one launch.  Bound by reading W
-// (11008 x 4096: 90 MB, 13.6 us at the rate of a streaming read), so that the matrix
-// cores have nothing to offer: a wave takes ROWS rows of W, 512 values of K at a
-// time over its lanes, in fp32.  Every workgroup forms the inner values itself, a
-// row of A a wave next to its rows of W (128 KiB for 16 ranks, from the L2, against
-// 256 KiB of W): the launch that does it apart took 7 us of 26.
-struct TokenArgs {
-    const uint16_t* X;
-    const uint16_t* W;
-    int64_t ldw;
-    const uint16_t* A;
-    int64_t lda, a_group;
-    const uint16_t* B;
-    int64_t ldb, b_group;
-    const float* scale;
-    const int* offsets;
-    int groups, N, K, R;
-    uint16_t* Y;
-};
-
-__device__ __forceinline__ float dot8(i32x4 a, i32x4 b, float sum)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sum = fmaf(__uint_as_float((uint32_t)a[i] << 16), __uint_as_float((uint32_t)b[i] << 16), sum);
-        sum = fmaf(__uint_as_float((uint32_t)a[i] & 0xFFFF0000u), __uint_as_float((uint32_t)b[i] & 0xFFFF0000u),
-                   sum);
-    }
-    return sum;
-}
-__device__ __forceinline__ float lanes_sum(float x)
-{
-#pragma unroll
-    for (int d = 32; d; d >>= 1)
-        x += __shfl_xor(x, d);
-    return x;
-}
-
-template <int ROWS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void adapter_token_kernel(TokenArgs p)
-{
-    __shared__ float inner[kMaxRank];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int n0 = ((int)blockIdx.x * WAVES + wave) * ROWS;
-    const int K = p.K;
-    constexpr int UN = 4;
-    const rsrc_t rx = make_rsrc(p.X, (uint32_t)K * 2u);
-    const rsrc_t rw = make_rsrc(uniform(reinterpret_cast<const uint8_t*>(p.W + (int64_t)min(n0, p.N - 1) * p.ldw)),
-                                n0 < p.N ? (uint32_t)((min(ROWS, p.N - n0) - 1) * (int)p.ldw + K) * 2u : 0u);
-    const int group = row_group(p.offsets, p.groups, 0, lane);
-    const bool has = group < p.groups;
-    // rank `wave`, if there is one; a row past the last reads zeros
-    auto rank_row = [&](int r) __attribute__((always_inline)) {
-        const bool in = has && r < p.R;
-        return make_rsrc(uniform(reinterpret_cast<const uint8_t*>(p.A + (in ? group * p.a_group + r * p.lda : 0))),
-                         in ? (uint32_t)K * 2u : 0u);
-    };
-    const rsrc_t ra = rank_row(wave);
-    float acc[ROWS] = {}, rank = 0.f;
-    for (int k0 = lane * 8; k0 < K + lane * 8; k0 += 512 * UN) {
-        i32x4 x[UN], w[UN][ROWS], a[UN];
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int k = k0 + 512 * u;
-            // (past a row's end the next row begins)
-            const uint32_t off = k < K ? (uint32_t)k * 2u : kOOB;
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-                w[u][r] = load16_nt(rw, k < K ? off + (uint32_t)r * (uint32_t)p.ldw * 2u : kOOB);
-            x[u] = load16(rx, off);
-            a[u] = load16(ra, off);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            rank = dot8(a[u], x[u], rank);
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-                acc[r] = dot8(w[u][r], x[u], acc[r]);
-        }
-    }
-    const float scale = has && p.scale ? p.scale[group] : 1.f;
-    rank = lanes_sum(rank);
-    if (lane == 0)
-        inner[wave] = rank * scale;
-    for (int r = wave + WAVES; r < p.R; r += WAVES) {
-        const rsrc_t rr = rank_row(r);
-        float s = 0.f;
-        for (int k = lane * 8; k < K; k += 512)
-            s = dot8(load16(rr, (uint32_t)k * 2u), load16(rx, (uint32_t)k * 2u), s);
-        s = lanes_sum(s);
-        if (lane == 0)
-            inner[r] = s * scale;
-    }
-    __syncthreads();
-    if (has)
-        for (int r = lane; r < p.R; r += 64)
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i)
-                if (n0 + i < p.N)
-                    acc[i] = fmaf(inner[r], bf16_to_f32(p.B[group * p.b_group + (n0 + i) * p.ldb + r]), acc[i]);
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const float y = lanes_sum(acc[i]);
-        if (lane == 0 && n0 + i < p.N)
-            p.Y[n0 + i] = bf16_rne(y);
     }
 }
 

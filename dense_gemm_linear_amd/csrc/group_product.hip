@@ -1,7 +1,11 @@
 // Launches of the grouped products (group_kernels.hpp).  Compiled once per role
 // (DG_GROUP_ROLE), so that the instances build in parallel; role 0's unit holds
 // the entry points.
+#if DG_GROUP_ROLE == 0
+#include "adapter_kernels.hpp"
+#else
 #include "group_kernels.hpp"
+#endif
 #include "internal.hpp"
 
 #include <string.h>
@@ -39,12 +43,6 @@ hipError_t go(const GroupArgs& a, int64_t extra, int cus, hipStream_t s)
 {
     GroupArgs copy = a;
     copy.tiles_n = (int)cdiv(a.N, S::TN);
-    if (ROLE == GROUP_ADAPT) {
-        // adapters that share a k-tile are told apart by 32-bit offsets into B; else an
-        // adapter's units fill whole k-tiles
-        copy.pack = a.groups * a.lb_group < (INT64_C(1) << 31);
-        copy.units = (int)(copy.pack ? cdiv(a.R, 16) : cdiv(a.R, S::KT / 2) * (S::KT / 32));
-    }
     const int64_t tiles_m = ROLE == GROUP_DW ? a.groups * cdiv(a.M, S::TM)
                                              : ROLE == GROUP_ADAPT ? cdiv(a.S, S::TM) : a.S / S::TM + extra;
     const int64_t items = tiles_m * copy.tiles_n;
@@ -306,6 +304,42 @@ hipError_t launch(const void* kernel, dim3 grid, int block, Args a, hipStream_t 
     return hipLaunchKernel(kernel, grid, dim3((unsigned)block), args, 0, s);
 }
 
+// The inner values.  Where a workgroup for each row and 16 ranks makes one round,
+// that; else the smallest tile whose workgroups do (a workgroup takes 2.5 us and 1.9
+// for each 16 rows of X or A, K 4096: 4095 rows of 64 ranks 19 us as 32 x 64, 34 as
+// 16 x 16; 597 of 32 ranks 7.6 as 16 x 16, 13.7 as 64 x 32).
+hipError_t launch_inner(const InnerArgs& i, int cus, hipStream_t s)
+{
+    const int64_t T = i.S, units = cdiv(i.R, 16);
+    if (T * units <= cus)
+        return launch(reinterpret_cast<const void*>(&adapter_inner_row_kernel), dim3((unsigned)T, (unsigned)units),
+                      1024, i, s);
+    struct {
+        const void* kernel;
+        int nr, mb;
+    } const tiles[] = {{reinterpret_cast<const void*>(&adapter_inner_kernel<1, 1>), 1, 1},
+                       {reinterpret_cast<const void*>(&adapter_inner_kernel<1, 2>), 1, 2},
+                       {reinterpret_cast<const void*>(&adapter_inner_kernel<2, 2>), 2, 2},
+                       {reinterpret_cast<const void*>(&adapter_inner_kernel<1, 4>), 1, 4},
+                       {reinterpret_cast<const void*>(&adapter_inner_kernel<4, 2>), 4, 2},
+                       {reinterpret_cast<const void*>(&adapter_inner_kernel<2, 4>), 2, 4},
+                       {reinterpret_cast<const void*>(&adapter_inner_kernel<4, 4>), 4, 4}};
+    // groups in use are not known here; each has a partly filled tile
+    const int64_t some = std::min<int64_t>(std::min<int64_t>(i.groups, 16), T / 16 + 1);
+    int best = 0;
+    for (int t = 0; t < 7; ++t) {
+        if (tiles[t].nr > 1 && tiles[t].nr / 2 >= units)
+            continue;
+        best = t;
+        if ((T / (16 * tiles[t].mb) + some) * cdiv(units, tiles[t].nr) <= cus)
+            break;
+    }
+    return launch(tiles[best].kernel,
+                  dim3((unsigned)(T / (16 * tiles[best].mb) + std::min<int64_t>(i.groups, T)),
+                       (unsigned)cdiv(units, tiles[best].nr)),
+                  512, i, s);
+}
+
 hipError_t adapters_forward(const ProductCall& c)
 {
     const int64_t T = c.T;
@@ -352,20 +386,7 @@ hipError_t adapters_forward(const ProductCall& c)
     i.R = (int)c.R;
     i.K = (int)c.K;
     i.U = reinterpret_cast<uint16_t*>(c.ws);
-    // a row a workgroup for a decode batch; else 16, or 32, which read A half as
-    // often, where 16 make more than one round
-    const int64_t cols = T <= 64 ? 16 : c.R > 32 ? 64 : c.R > 16 ? 32 : 16, wide = cdiv(c.R, cols);
-    const bool two = T > 64 && (T / 16 + std::min(c.groups, T)) * wide > c.cus;
-    const int64_t blocks = T <= 64 ? T : T / (two ? 32 : 16) + std::min(c.groups, T);
-    const void* inner =
-        T <= 64 ? reinterpret_cast<const void*>(&adapter_inner_kernel<1, 1, 16, 4, true>)
-        : two   ? (cols == 64   ? reinterpret_cast<const void*>(&adapter_inner_kernel<4, 2, 8, 2>)
-                   : cols == 32 ? reinterpret_cast<const void*>(&adapter_inner_kernel<2, 2, 8, 4>)
-                                : reinterpret_cast<const void*>(&adapter_inner_kernel<1, 2, 8, 4>))
-                : (cols == 64   ? reinterpret_cast<const void*>(&adapter_inner_kernel<4, 1, 16, 2>)
-                   : cols == 32 ? reinterpret_cast<const void*>(&adapter_inner_kernel<2, 1, 16, 2>)
-                                : reinterpret_cast<const void*>(&adapter_inner_kernel<1, 1, 16, 4>));
-    const hipError_t e = launch(inner, dim3((unsigned)blocks, (unsigned)wide), two ? 512 : 1024, i, c.stream);
+    const hipError_t e = launch_inner(i, c.cus, c.stream);
     if (e != hipSuccess)
         return e;
     GroupArgs a = base_args(c);
