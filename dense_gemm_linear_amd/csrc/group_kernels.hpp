@@ -54,6 +54,8 @@ struct GroupArgs {
     const uint8_t* LB;     // ADAPT: [groups][N][ldlb]
     int64_t ldlb_b, lb_group;
     int R;
+    int units, pack;       // set by the launch, which knows the tile: units of 16 ranks an
+                           // adapter, and whether adapters share k-tiles of them
 };
 
 constexpr int kTableLds = ((int)kMaxGroups + 4) * 4 + 64;
@@ -430,7 +432,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             }
             entry0 = __builtin_amdgcn_readfirstlane(entry0);
             over = __builtin_amdgcn_readfirstlane(over);
-            units = over * ((q->R + 15) / 16);
+            units = over * q->units;
         }
         if constexpr (TRB) {
             b_base += (int64_t)n0 * 2;
@@ -687,65 +689,104 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             // Behind the k-tiles of X and W: the ranks of the adapters that the tile's rows
             // have, in units of 16.  One step of the matrix cores holds a unit: the rows'
             // inner values, upper halves and then lower ones, against the same columns of B
-            // twice, both straight from memory (a few KiB a tile).  A unit's products are
-            // formed apart and added to the rows of its adapter only: zeros in the other
-            // rows' inner values would not keep an infinity or NaN of one request's adapter
-            // out of the others' rows.
-            if (!idle && units > 0) {
-                const KernelArgs q = kernel_args();
+            // twice.  As many k-tiles as there are stages at a time, all their loads and
+            // then their products (as a second pipelined loop they had registers of the
+            // first spilled; straight from memory in the fragments' layout, neighbouring
+            // lanes in different rows, 4095 rows of 64 ranks took 24 us longer).  A unit's
+            // products are formed apart and added to the rows of its adapter only: zeros in
+            // the other rows' inner values would not keep an infinity or NaN of one request's
+            // adapter out of the others' rows.
+            const KernelArgs q = kernel_args();
+            for (int u0 = 0; u0 < units; u0 += ST * STEPS) {
                 // (lanes as values of their own, so that nothing that hangs on them lives
                 // through the loop before)
                 int ol = lane;
                 asm volatile("" : "+v"(ol));
-                const int oc = ol & 15, og = ol >> 4;
-                constexpr int UB = MR + NR > 8 ? 1 : MR + NR > 5 ? 3 : 4;      // units in flight
-                const int each = (q->R + 15) / 16;
-                const int cols = min(S::WCOLS, q->N - n0 - (int)col0);
+                // lane i: unit u0 + i; behind the last one: no row, no rank
+                const int each = q->units, u = u0 + min(ol, ST * STEPS - 1);
+                const int at = min(u, units - 1) / each;
+                const int v_lo = table.first(entry0 + at) - m0;
+                const int v_hi = u < units ? table.first(entry0 + at + 1) - m0 : v_lo;
+                const int v_id = table.id(entry0 + at);
+                const int v_rank = u < units ? (u - at * each) * 16 : q->R;
+                const int cols = min(TN, q->N - n0);
                 const rsrc_t ru = make_rsrc(uniform(q->U + (int64_t)m0 * q->R * 4), (uint32_t)(rows * q->R * 4));
-                for (int u0 = 0; u0 < units; u0 += UB) {
-                    // lane i: unit u0 + i
-                    const int u = min(u0 + min(ol, UB - 1), units - 1);
-                    const int at = u / each;
-                    const int v_lo = table.first(entry0 + at) - m0, v_hi = table.first(entry0 + at + 1) - m0;
-                    const int v_id = table.id(entry0 + at), v_rank = (u - at * each) * 16;
-                    i32x4 uf[UB][MR], wf[UB][NR];
-#pragma unroll
-                    for (int i = 0; i < UB; ++i) {
-                        const int rank = __builtin_amdgcn_readlane(v_rank, i) + (og & 1) * 8;
-                        const uint8_t* from = q->LB + __builtin_amdgcn_readlane(v_id, i) * q->lb_group +
-                                              (int64_t)(n0 + (int)col0) * q->ldlb_b;
-                        const rsrc_t rl = make_rsrc(uniform(from), cols > 0 ? (uint32_t)((cols - 1) * (int)q->ldlb_b + q->R * 2) : 0u);
-#pragma unroll
-                        for (int j = 0; j < NR; ++j)
-                            wf[i][j] = load16(rl, rank < q->R ? (uint32_t)(j * R + oc) * (uint32_t)q->ldlb_b + (uint32_t)rank * 2u
-                                                              : kOOB);
-#pragma unroll
-                        for (int mi = 0; mi < MR; ++mi)
-                            uf[i][mi] = load16(ru, rank < q->R ? (uint32_t)((((int)row0 + mi * R + oc) * 2 + (og >> 1)) * q->R + rank) * 2u
-                                                               : kOOB);
+                const int r0 = KTL::ROWS_PER_LOAD * wave + ol / CHUNKS;
+                const int c = (int)((uint32_t)(ol % CHUNKS) ^ KTL::key((uint32_t)r0));
+#pragma unroll 1
+                for (int t = 0; t < ST && u0 + t * STEPS < units; ++t) {
+                    const int id = __builtin_amdgcn_readlane(v_id, t * STEPS);
+                    int rank = __builtin_amdgcn_readlane(v_rank, t * STEPS);
+                    const uint8_t* from = q->LB + (int64_t)n0 * q->ldlb_b;
+                    uint32_t at = 0, records = (uint32_t)((cols - 1) * (int)q->ldlb_b + q->R * 2);
+                    if (q->pack) {                      // any adapter by a 32-bit offset
+                        records = 0x7FFFFFFFu;
+                        at = (uint32_t)id * (uint32_t)q->lb_group;
+                    } else {                            // a k-tile is of one adapter
+                        from += id * q->lb_group;
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (STEPS == 2) {
+                        const int id1 = __builtin_amdgcn_readlane(v_id, t * STEPS + 1);
+                        const int rank1 = __builtin_amdgcn_readlane(v_rank, t * STEPS + 1);
+                        rank = c < 4 ? rank : rank1;
+                        at = c < 4 || !q->pack ? at : (uint32_t)id1 * (uint32_t)q->lb_group;
+                    }
+                    rank += c % 2 * 8;
+                    const rsrc_t rl = make_rsrc(uniform(from), records);
+                    uint8_t* base = lds + t * STAGE;
 #pragma unroll
-                    for (int i = 0; i < UB; ++i) {
-                        if (u0 + i >= units)
-                            break;
-                        const int lo = __builtin_amdgcn_readlane(v_lo, i), hi = __builtin_amdgcn_readlane(v_hi, i);
+                    for (int n = 0; n < A_DMA; ++n)
+                        dma16(ru, base + (wave + WAVES * n) * 1024,
+                              rank < q->R ? (uint32_t)(((r0 + n * A_ROWS) * 2 + c / 2 % 2) * q->R + rank) * 2u : kOOB,
+                              0);
 #pragma unroll
-                        for (int mi = 0; mi < MR; ++mi) {
-                            const int r = (int)row0 + mi * R;
-                            if (r >= hi || r + R <= lo)
-                                continue;
-                            const bool own = r + oc >= lo && r + oc < hi;
-#pragma unroll
-                            for (int j = 0; j < NR; ++j) {
-                                const acc_t v = mfma_bf16(wf[i][j], uf[i][mi], zero_acc<AT>());
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    acc[mi][j][e] += own ? v[e] : 0.f;
-                            }
-                        }
+                    for (int n = 0; n < B_DMA; ++n) {
+                        const int r = r0 + n * B_ROWS;
+                        dma16(rl, base + A_BUF + (wave + WAVES * n) * 1024,
+                              rank < q->R && r < cols ? at + (uint32_t)r * (uint32_t)q->ldlb_b + (uint32_t)rank * 2u
+                                                      : kOOB,
+                              0);
                     }
                 }
+                DG_STAGE_BARRIER(0);
+#pragma unroll 1
+                for (int i = 0; i < ST * STEPS && !idle; ++i) {
+                    const int lo = __builtin_amdgcn_readlane(v_lo, i), hi = __builtin_amdgcn_readlane(v_hi, i);
+                    if (hi <= lo)
+                        continue;
+                    const int s = i % STEPS;
+                    const uint8_t* base = lds + i / STEPS * STAGE;
+                    const uint32_t chunk = ((uint32_t)(4 * s + (ol >> 4)) ^ KTL::key((uint32_t)(ol % 16))) << 4;
+                    const uint8_t* wp = base + A_BUF + (col0 + (uint32_t)(ol % 16)) * KTB + chunk;
+                    const uint8_t* up = base + (row0 + (uint32_t)(ol % 16)) * KTB + chunk;
+                    i32x4 wf[NR];
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+                        wf[j] = *reinterpret_cast<const i32x4*>(wp + j * R * KTB);
+#pragma unroll
+                    for (int mi = 0; mi < MR; ++mi) {
+                        const int r = (int)row0 + mi * R;
+                        if (r >= hi || r + R <= lo)
+                            continue;
+                        const i32x4 uf = *reinterpret_cast<const i32x4*>(up + mi * R * KTB);
+                        if (r >= lo && r + R <= hi) {        // all 16 rows are its own
+#pragma unroll
+                            for (int j = 0; j < NR; ++j)
+                                acc[mi][j] = mfma_bf16(wf[j], uf, acc[mi][j]);
+                            continue;
+                        }
+                        const bool own = r + ol % 16 >= lo && r + ol % 16 < hi;
+                        acc_t v[NR];
+#pragma unroll
+                        for (int j = 0; j < NR; ++j)
+                            v[j] = mfma_bf16(wf[j], uf, zero_acc<AT>());
+                        if (own)
+#pragma unroll
+                            for (int j = 0; j < NR; ++j)
+                                acc[mi][j] += v[j];
+                    }
+                }
+                DG_STAGE_BARRIER(0);
             }
         }
         // the next item's loads go out before this one's outputs

@@ -43,6 +43,12 @@ hipError_t go(const GroupArgs& a, int64_t extra, int cus, hipStream_t s)
 {
     GroupArgs copy = a;
     copy.tiles_n = (int)cdiv(a.N, S::TN);
+    if (ROLE == GROUP_ADAPT) {
+        // adapters that share a k-tile are told apart by 32-bit offsets into B; else an
+        // adapter's units fill whole k-tiles
+        copy.pack = a.groups * a.lb_group < (INT64_C(1) << 31);
+        copy.units = (int)(copy.pack ? cdiv(a.R, 16) : cdiv(a.R, S::KT / 2) * (S::KT / 32));
+    }
     const int64_t tiles_m = ROLE == GROUP_DW ? a.groups * cdiv(a.M, S::TM)
                                              : ROLE == GROUP_ADAPT ? cdiv(a.S, S::TM) : a.S / S::TM + extra;
     const int64_t items = tiles_m * copy.tiles_n;
