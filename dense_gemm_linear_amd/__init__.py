@@ -882,6 +882,15 @@ def linear_adapters_workspace_bytes(T: int, R: int, groups: int) -> int:
     return int(lib.linear_adapters_workspace_bytes(T, R, groups))
 
 
+# Element types and allocation as plain globals: a call of these takes 3 us in the
+# driver, and as much again went to looking things up.
+import torch as _pt  # noqa: E402  (loaded by _load_lib already)
+
+_BF16, _F32, _I32, _I64 = _pt.bfloat16, _pt.float32, _pt.int32, _pt.int64
+_new = _pt.empty_strided
+_raw_stream, _current_device = _pt._C._cuda_getCurrentRawStream, _pt._C._cuda_getDevice
+
+
 def _refuse(fn: str, name: str, what: str):
     raise ValueError(f"{fn}: {name} must be {what}")
 
@@ -893,42 +902,44 @@ def _extent(shape) -> str:
 def _matrix(fn: str, name: str, t, dtype, rows=None, cols=None):
     """A 2-D view (rows, cols None: any) with contiguous rows: (rows, columns, pitch).
     A single row's stride says nothing; its pitch is the columns in whole 8."""
-    if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
+    if getattr(t, "dtype", None) is not dtype:
         _refuse(fn, name, f"a {dtype} tensor")
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if len(shape) == 2:
         n, w = shape
-        if (rows is None or n == rows) and (cols is None or w == cols) and (w < 2 or stride[1] == 1):
+        p, q = t.stride()
+        if (rows is None or n == rows) and (cols is None or w == cols) and (q == 1 or w < 2):
             if n < 2:
                 return n, w, (w + 7) // 8 * 8
-            if stride[0] >= w:
-                return n, w, stride[0]
+            if p >= w:
+                return n, w, p
     _refuse(fn, name, f"a {_extent((rows, cols))} tensor with contiguous rows")
 
 
 def _stack(fn: str, name: str, t, dtype, groups=None, rows=None, cols=None):
     """A 3-D view with contiguous rows: (groups, rows, columns, pitch, group stride)."""
-    if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
+    if getattr(t, "dtype", None) is not dtype:
         _refuse(fn, name, f"a {dtype} tensor")
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if len(shape) == 3:
         g, n, w = shape
+        s, p, q = t.stride()
         if (groups is None or g == groups) and (rows is None or n == rows) and \
-                (cols is None or w == cols) and (w < 2 or stride[2] == 1) and (n < 2 or stride[1] >= w):
-            pitch = stride[1] if n > 1 else (w + 7) // 8 * 8
-            return g, n, w, pitch, (stride[0] if g > 1 else n * pitch)
+                (cols is None or w == cols) and (q == 1 or w < 2) and (n < 2 or p >= w):
+            pitch = p if n > 1 else (w + 7) // 8 * 8
+            return g, n, w, pitch, (s if g > 1 else n * pitch)
     _refuse(fn, name, f"a {_extent((groups, rows, cols))} tensor with contiguous rows")
 
 
 def _vector(fn: str, name: str, t, dtype, n: int):
-    if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
+    if getattr(t, "dtype", None) is not dtype:
         _refuse(fn, name, f"a {dtype} tensor")
     if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         _refuse(fn, name, f"a contiguous vector of {n} values")
 
 
 def _place(fn: str, place, T=None):
-    T, k, _ = _matrix(fn, "place", place, _torch().int32, T)
+    T, k, _ = _matrix(fn, "place", place, _I32, T)
     if not place.is_contiguous():
         _refuse(fn, "place", "contiguous")
     return T, k
@@ -952,7 +963,7 @@ def _group_workspace(fn: str, device, need: int, workspace):
         if need == 0:
             return None, None, 0
         # freed on return: the caching allocator reuses it on this stream only
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+        workspace = _pt.empty(need, dtype=_pt.uint8, device=device)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         _refuse(fn, "workspace", f"a contiguous device tensor on {device}")
@@ -970,14 +981,11 @@ def _group_call(fn: str, dev: int, *args):
     """The C call on the current stream of the operands' device, whichever device is
     current.  (The stream's handle without the Stream object, and no device guard
     where none is needed: together 3 of 13 us a call.)"""
-    torch = _torch()
-    call = getattr(lib, fn)
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
-        st = call(*args, stream)
+    if _current_device() == dev:
+        st = getattr(lib, fn)(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(dev):
-            st = call(*args, stream)
+        with _pt.cuda.device(dev):
+            st = getattr(lib, fn)(*args, _raw_stream(dev))
     if st != GEMM_OK:
         raise GemmError(fn, st)
 
@@ -989,18 +997,17 @@ def group_sort(ids, groups: int, *, workspace=None):
     order[p] is the slot t * slots + j at position p, place[t, j] the position of a
     slot.  An id outside [0, groups) takes no part: its place is -1, and it
     stands in order behind the others."""
-    torch = _torch()
     fn = "group_sort"
-    if isinstance(ids, torch.Tensor) and ids.dim() == 1:
+    if isinstance(ids, _pt.Tensor) and ids.dim() == 1:
         ids = ids[:, None]
-    T, k, ld = _matrix(fn, "ids", ids, torch.int64)
+    T, k, ld = _matrix(fn, "ids", ids, _I64)
     dev = _one_device(fn, "ids", ids)
     if groups < 1:
         raise ValueError(f"{fn}: groups must be at least 1")
     device = ids.device
-    offsets = torch.empty(groups + 1, dtype=torch.int32, device=device)
-    order = torch.empty(T * k, dtype=torch.int32, device=device)
-    place = torch.empty((T, k), dtype=torch.int32, device=device)
+    offsets = _new((groups + 1,), (1,), dtype=_I32, device=device)
+    order = _new((T * k,), (1,), dtype=_I32, device=device)
+    place = _new((T, k), (k, 1), dtype=_I32, device=device)
     need = lib.group_sort_workspace_bytes(T, k, groups)
     ws, at, nbytes = _group_workspace(fn, device, need, workspace) if need else (None, None, 0)
     _group_call(fn, dev, ids.data_ptr(), ld, T, k, groups, offsets.data_ptr(), order.data_ptr(),
@@ -1012,14 +1019,13 @@ def group_gather(X, place, out=None):
     """Xs [T * slots, D] with Xs[place[t, j]] = X[t]: the rows of X (elements of 1, 2
     or 4 bytes) in sorted order.  Rows behind the last slot that takes part are
     not written.  The gradient of X is group_combine(dXs, place)."""
-    torch = _torch()
     fn = "group_gather"
-    if not isinstance(X, torch.Tensor) or X.element_size() not in (1, 2, 4):
+    if not isinstance(X, _pt.Tensor) or X.element_size() not in (1, 2, 4):
         _refuse(fn, "X", "a tensor of 1-, 2- or 4-byte elements")
     T, D, ldx = _matrix(fn, "X", X, X.dtype)
     T, k = _place(fn, place, T)
     if out is None:
-        out = torch.empty((T * k, D), dtype=X.dtype, device=X.device)
+        out = _new((T * k, D), (D, 1), dtype=X.dtype, device=X.device)
     _, _, ldo = _matrix(fn, "out", out, X.dtype, T * k, D)
     dev = _one_device(fn, "X place out", X, place, out)
     _group_call(fn, dev, X.data_ptr(), ldx, place.data_ptr(), T, k, D, X.element_size(), out.data_ptr(), ldo)
@@ -1030,14 +1036,13 @@ def group_combine(Y, place, weights=None, out=None):
     """out [T, D] with out[t] = sum_j weights[t, j] * Y[place[t, j]] (Y bf16 [T * slots,
     D], weights float32 [T, slots] or None for 1), in fp32, rounded once; slots that
     take no part are left out."""
-    torch = _torch()
     fn = "group_combine"
     T, k = _place(fn, place)
-    _, D, ldy = _matrix(fn, "Y", Y, torch.bfloat16, T * k)
-    ldw = 0 if weights is None else _matrix(fn, "weights", weights, torch.float32, T, k)[2]
+    _, D, ldy = _matrix(fn, "Y", Y, _BF16, T * k)
+    ldw = 0 if weights is None else _matrix(fn, "weights", weights, _F32, T, k)[2]
     if out is None:
-        out = torch.empty((T, D), dtype=torch.bfloat16, device=Y.device)
-    _, _, ldo = _matrix(fn, "out", out, torch.bfloat16, T, D)
+        out = _new((T, D), (D, 1), dtype=_BF16, device=Y.device)
+    _, _, ldo = _matrix(fn, "out", out, _BF16, T, D)
     dev = _one_device(fn, "Y place weights out", Y, place, weights, out)
     _group_call(fn, dev, Y.data_ptr(), ldy, place.data_ptr(), _ptr(weights), ldw, T, k, D, out.data_ptr(), ldo)
     return out
@@ -1049,26 +1054,25 @@ def group_combine_grad(dout, Y, place, weights=None, *, need_dY: bool = True, ne
     dweights float32 [T, slots]), None for one that is not needed.  Rows of dY
     behind the last slot that takes part are not written; dY may be Y itself.  Y is
     used for dweights only (None if not needed)."""
-    torch = _torch()
     fn = "group_combine_grad"
     T, k = _place(fn, place)
-    _, D, ldd = _matrix(fn, "dout", dout, torch.bfloat16, T)
+    _, D, ldd = _matrix(fn, "dout", dout, _BF16, T)
     ldy = 0
     if need_dweights or Y is not None:
-        ldy = _matrix(fn, "Y", Y, torch.bfloat16, T * k, D)[2]
-    ldw = 0 if weights is None else _matrix(fn, "weights", weights, torch.float32, T, k)[2]
+        ldy = _matrix(fn, "Y", Y, _BF16, T * k, D)[2]
+    ldw = 0 if weights is None else _matrix(fn, "weights", weights, _F32, T, k)[2]
     if not need_dY and not need_dweights:
         raise ValueError(f"{fn}: neither dY nor dweights is asked for")
     lddy, dweights = 0, None
     if need_dY:
         if dY is None:
-            dY = torch.empty((T * k, D), dtype=torch.bfloat16, device=dout.device)
-        lddy = _matrix(fn, "dY", dY, torch.bfloat16, T * k, D)[2]
+            dY = _new((T * k, D), (D, 1), dtype=_BF16, device=dout.device)
+        lddy = _matrix(fn, "dY", dY, _BF16, T * k, D)[2]
     elif dY is not None:
         raise ValueError(f"{fn}: dY given, but need_dY is false")
     dev = _one_device(fn, "dout Y place weights dY", dout, Y, place, weights, dY)
     if need_dweights:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+        dweights = _new((T, k), (k, 1), dtype=_F32, device=dout.device)
     _group_call(fn, dev, dout.data_ptr(), ldd, _ptr(Y), ldy, place.data_ptr(), _ptr(weights), ldw, T, k, D,
                 _ptr(dY), lddy, _ptr(dweights))
     return dY, dweights
@@ -1081,7 +1085,7 @@ def _group_order(fn: str, order, T: int, slots: int):
     else:
         if slots < 1:
             raise ValueError(f"{fn}: slots must be at least 1")
-        _vector(fn, "order", order, _torch().int32, T * slots)
+        _vector(fn, "order", order, _I32, T * slots)
 
 
 def group_linear(X, W, offsets, order=None, *, slots: int = 1, activation=None, mul=None, out=None):
@@ -1090,18 +1094,17 @@ def group_linear(X, W, offsets, order=None, *, slots: int = 1, activation=None, 
     slots] (X bf16 [T, K], S = T * slots; no sorted copy is made), or X[p] without an
     order (X sorted, S = T).  activation: one of ACTIVATIONS; mul bf16 [S, N], which
     may be `out` itself.  Rows from offsets[-1] on are not written."""
-    torch = _torch()
     fn = "group_linear"
-    T, K, ldx = _matrix(fn, "X", X, torch.bfloat16)
-    G, N, _, ldw, strw = _stack(fn, "W", W, torch.bfloat16, None, None, K)
-    _vector(fn, "offsets", offsets, torch.int32, G + 1)
+    T, K, ldx = _matrix(fn, "X", X, _BF16)
+    G, N, _, ldw, strw = _stack(fn, "W", W, _BF16, None, None, K)
+    _vector(fn, "offsets", offsets, _I32, G + 1)
     _group_order(fn, order, T, slots)
     S = T * slots
     act = ACTIVATIONS[activation] if not isinstance(activation, int) else activation
-    ldm = 0 if mul is None else _matrix(fn, "mul", mul, torch.bfloat16, S, N)[2]
+    ldm = 0 if mul is None else _matrix(fn, "mul", mul, _BF16, S, N)[2]
     if out is None:
-        out = torch.empty((S, N), dtype=torch.bfloat16, device=X.device)
-    ldo = _matrix(fn, "out", out, torch.bfloat16, S, N)[2]
+        out = _new((S, N), (N, 1), dtype=_BF16, device=X.device)
+    ldo = _matrix(fn, "out", out, _BF16, S, N)[2]
     dev = _one_device(fn, "X W offsets order mul out", X, W, offsets, order, mul, out)
     _group_call(fn, dev, X.data_ptr(), ldx, W.data_ptr(), ldw, strw, offsets.data_ptr(), _ptr(order), T, slots, G,
                 N, K, act, _ptr(mul), ldm, out.data_ptr(), ldo)
@@ -1115,14 +1118,13 @@ def group_linear_grad(dY, X, W, offsets, order=None, *, slots: int = 1, need_dX:
     needed.  group_combine(dX, place) joins the rows of a token.  Rows of dX from
     offsets[-1] on are not written; dW is zero for a group without rows.  workspace:
     a uint8 tensor of group_linear_grad_workspace_bytes bytes (with an order, for dW)."""
-    torch = _torch()
     fn = "group_linear_grad"
-    T, K, ldx = _matrix(fn, "X", X, torch.bfloat16)
-    G, N, _, ldw, strw = _stack(fn, "W", W, torch.bfloat16, None, None, K)
-    _vector(fn, "offsets", offsets, torch.int32, G + 1)
+    T, K, ldx = _matrix(fn, "X", X, _BF16)
+    G, N, _, ldw, strw = _stack(fn, "W", W, _BF16, None, None, K)
+    _vector(fn, "offsets", offsets, _I32, G + 1)
     _group_order(fn, order, T, slots)
     S = T * slots
-    lddy = _matrix(fn, "dY", dY, torch.bfloat16, S, N)[2]
+    lddy = _matrix(fn, "dY", dY, _BF16, S, N)[2]
     if not need_dX and not need_dW:
         raise ValueError(f"{fn}: neither dX nor dW is asked for")
     for name, need, given in (("dX", need_dX, dX), ("dW", need_dW, dW)):
@@ -1131,12 +1133,12 @@ def group_linear_grad(dY, X, W, offsets, order=None, *, slots: int = 1, need_dX:
     lddx, ld_dw = 0, (0, 0)
     if need_dX:
         if dX is None:
-            dX = torch.empty((S, K), dtype=torch.bfloat16, device=X.device)
-        lddx = _matrix(fn, "dX", dX, torch.bfloat16, S, K)[2]
+            dX = _new((S, K), (K, 1), dtype=_BF16, device=X.device)
+        lddx = _matrix(fn, "dX", dX, _BF16, S, K)[2]
     if need_dW:
         if dW is None:
-            dW = torch.empty((G, N, K), dtype=torch.bfloat16, device=X.device)
-        ld_dw = _stack(fn, "dW", dW, torch.bfloat16, G, N, K)[3:]
+            dW = _new((G, N, K), (N * K, K, 1), dtype=_BF16, device=X.device)
+        ld_dw = _stack(fn, "dW", dW, _BF16, G, N, K)[3:]
     dev = _one_device(fn, "X W offsets order dY dX dW", X, W, offsets, order, dY, dX, dW)
     need = lib.group_linear_grad_workspace_bytes(T, slots, K) if need_dW and order is not None else 0
     ws, at, nbytes = _group_workspace(fn, X.device, need, workspace) if need else (None, None, 0)
@@ -1152,19 +1154,18 @@ def linear_adapters(X, W, A, B, offsets, order, *, scale=None, out=None, workspa
     offsets and order as group_sort(adapter of each row, groups) gives them; rows of
     no adapter get the projection alone.  workspace: a uint8 tensor of
     linear_adapters_workspace_bytes bytes."""
-    torch = _torch()
     fn = "linear_adapters"
-    T, K, ldx = _matrix(fn, "X", X, torch.bfloat16)
-    N, _, ldw = _matrix(fn, "W", W, torch.bfloat16, None, K)
-    G, R, _, lda, stra = _stack(fn, "A", A, torch.bfloat16, None, None, K)
-    _, _, _, ldb, strb = _stack(fn, "B", B, torch.bfloat16, G, N, R)
-    _vector(fn, "offsets", offsets, torch.int32, G + 1)
-    _vector(fn, "order", order, torch.int32, T)
+    T, K, ldx = _matrix(fn, "X", X, _BF16)
+    N, _, ldw = _matrix(fn, "W", W, _BF16, None, K)
+    G, R, _, lda, stra = _stack(fn, "A", A, _BF16, None, None, K)
+    _, _, _, ldb, strb = _stack(fn, "B", B, _BF16, G, N, R)
+    _vector(fn, "offsets", offsets, _I32, G + 1)
+    _vector(fn, "order", order, _I32, T)
     if scale is not None:
-        _vector(fn, "scale", scale, torch.float32, G)
+        _vector(fn, "scale", scale, _F32, G)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=X.device)
-    ldo = _matrix(fn, "out", out, torch.bfloat16, T, N)[2]
+        out = _new((T, N), (N, 1), dtype=_BF16, device=X.device)
+    ldo = _matrix(fn, "out", out, _BF16, T, N)[2]
     dev = _one_device(fn, "X W A B offsets order scale out", X, W, A, B, offsets, order, scale, out)
     ws, at, nbytes = _group_workspace(fn, X.device, lib.linear_adapters_workspace_bytes(T, R, G), workspace)
     _group_call(fn, dev, X.data_ptr(), ldx, W.data_ptr(), ldw, A.data_ptr(), lda, stra, B.data_ptr(), ldb, strb,
