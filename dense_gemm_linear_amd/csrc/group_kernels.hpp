@@ -247,6 +247,51 @@ __device__ __forceinline__ KernelArgs kernel_args()
     return a;
 }
 
+// k_loop for items whose k-tiles follow one another without a break: k-tiles 0 ..
+// ST - 2 are in flight at the start, and load(kt ..) for kt from `end` (a multiple of
+// ST) on loads the next item's, which are left in flight at the end; nothing is
+// drained.  Waits count what was issued behind a k-tile's loads (vector memory
+// operations of a wave complete in the order of their issue): the k-tiles after it,
+// and with `stored` at least STORES stores of the item before, issued between the
+// last of its loads and this loop.
+template <int ST, int LOADS, int G, int STORES, class Load, class Read, class Mma>
+__device__ __forceinline__ void k_stream(int end, bool stored, Load& load, Read& read, Mma& mma)
+{
+    constexpr int NS = frag_sets(ST, 1);
+    static_assert((ST - 2) * LOADS + STORES <= 63, "pipeline depth vs vmcnt");
+    if (stored)
+        DG_STAGE_BARRIER((ST - 2) * LOADS + STORES);
+    else
+        DG_STAGE_BARRIER((ST - 2) * LOADS);
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        read(0, 0, 0, g, G);
+    auto phase = [&](int t, auto sc, auto extra) __attribute__((always_inline)) {
+        constexpr int si = decltype(sc)::value;
+        DG_STAGE_BARRIER((ST - 3) * LOADS + decltype(extra)::value);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            read((si + 1) % ST, 0, (si + 1) % NS, g, G);
+            mma(si, 0, si % NS, g, G);
+            load(t + ST - 1, (si + ST - 1) % ST, g, G, std::false_type{});
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    int kt = 0;
+    if (stored) {
+        // the k-tiles loaded before the stores
+        static_for<ST>([&](auto i) __attribute__((always_inline)) {
+            constexpr int I = decltype(i)::value;
+            phase(I, i, std::integral_constant<int, I < ST - 2 ? STORES : 0>{});
+        });
+        kt = ST;
+    }
+    for (; kt < end; kt += ST)
+        static_for<ST>([&](auto i) __attribute__((always_inline)) {
+            phase(kt + decltype(i)::value, i, std::integral_constant<int, 0>{});
+        });
+}
+
 template <class S, int ROLE>
 __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArgs p)
 {
@@ -259,6 +304,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
     constexpr int A_BUF = S::A_BUF, STAGE = S::STAGE, WAVES = S::WAVES, ST = S::ST;
     constexpr int STEPS = KTB / 64, CHUNKS = KTB / 16;
     constexpr bool TRA = ROLE == GROUP_DW, TRB = ROLE == GROUP_DX || ROLE == GROUP_DW;
+    constexpr bool STREAM = ROLE == GROUP_DW;
     constexpr bool ADAPT = ROLE == GROUP_ADAPT, GATHER = ROLE == GROUP_FWD || ROLE == GROUP_GATED || ADAPT;
     static_assert(!TRA || TM >= 128, "a transposed operand's unit key needs 8 units a row");
     static_assert(!TRB || TN >= 128, "a transposed operand's unit key needs 8 units a row");
@@ -366,6 +412,13 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
     const int a_step = KT * (int)p.lda_b, b_step = KT * (int)p.ldb_b;         // TRA, TRB
     const int a_rows = A_ROWS * (int)p.lda_b, b_rows = B_ROWS * (int)p.ldb_b;
     uint32_t a_bytes = 0;                                                     // GATHER
+    // STREAM: what the loads turn to behind the present item's k-tiles
+    struct Operands {
+        const uint8_t *a, *b;
+        int a_span, b_span, nkt;
+    };
+    Operands next = {nullptr, nullptr, 0, 0, 0};
+    int stream_end = -1, k_off = 0;
     // ADAPT: the first of the table's entries that the tile's rows touch, and all their
     // units of 16 ranks
     int units = 0, entry0 = 0;
@@ -465,6 +518,16 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         constexpr bool NOMASK = decltype(nomask_c)::value;
         const bool mask = kt >= last_full;
         uint8_t* base = lds + stage * STAGE;
+        if constexpr (STREAM) {
+            if (part == 0 && kt == stream_end) {           // the next item's k-tiles
+                a_base = next.a;
+                b_base = next.b;
+                a_span = next.a_span;
+                b_span = next.b_span;
+                nkt = next.nkt;
+                k_off = stream_end;
+            }
+        }
         auto one = [&](rsrc_t r, uint8_t* dst, uint32_t goff, uint32_t col, auto tr, int nt)
                        __attribute__((always_inline)) {
             uint32_t off = goff, soff = 0;
@@ -485,14 +548,14 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         for (int i = 0; i < A_DMA; ++i)
             if (i % nparts == part)
                 one(GATHER ? make_rsrc(a_base, a_bytes)
-                    : TRA  ? tr_rsrc(a_base, a_span, kt)
+                    : TRA  ? tr_rsrc(a_base, a_span, kt - k_off)
                            : plain_rsrc(a_base, a_span, i * a_rows),
                     base + (wave + WAVES * i) * 1024, a_goff[i % A_OFFS], a_col,
                     std::integral_constant<bool, TRA>{}, 0);
 #pragma unroll
         for (int i = 0; i < B_DMA; ++i)
             if ((A_DMA + i) % nparts == part)
-                one(TRB ? tr_rsrc(b_base, b_span, kt) : plain_rsrc(b_base, b_span, i * b_rows),
+                one(TRB ? tr_rsrc(b_base, b_span, kt - k_off) : plain_rsrc(b_base, b_span, i * b_rows),
                     base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i % B_OFFS], b_col,
                     std::integral_constant<bool, TRB>{}, TM <= 64 && !TRA ? p.b_nt : 0);
         // a transposed operand's base goes on with the k-tiles (part by part, then
@@ -670,6 +733,45 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         for (int t = 0; t < ST - 1; ++t)
             load(t, t, 0, 1, std::false_type{});
     };
+    if constexpr (STREAM) {
+        // The k-tiles of all items in one stream: while the last ones of an item are
+        // multiplied the first ones of the next are on their way, and its own loop
+        // begins without a wait (8192 rows in 32 equal groups of 1024 x 2048, 8 k-tiles a
+        // tile: 256 x 128 tiles 84 -> 76 us, 128 x 128 79 -> 74).
+        static_assert(STEPS == 1 && ST >= 3);
+        constexpr int STORES = MR * (16 * (S::WCOLS / 8) / 64);       // of a wave's 16-byte stores
+        bool stored = false;
+        set_item(item);
+        preload();
+        for (;;) {
+            const int o_group = group, o_m0 = m0, o_n0 = n0, o_rows = rows;
+            const Operands here = {a_base, b_base, a_span, b_span, nkt};
+            const bool more = next_item();
+            stream_end = max(1, (nkt + ST - 1) / ST) * ST;
+            if (more)
+                set_item(item);
+            next = Operands{a_base, b_base, a_span, b_span, more ? nkt : 0};
+            a_base = here.a;
+            b_base = here.b;
+            a_span = here.a_span;
+            b_span = here.b_span;
+            nkt = here.nkt;
+            k_off = 0;
+#pragma unroll
+            for (int mi = 0; mi < MR; ++mi)
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+                    acc[mi][j] = zero_acc<AT>();
+            k_stream<ST, S::LOADS, step_groups(MR * NR), STORES>(stream_end, stored, load, read, mma);
+            output(o_group, o_m0, o_n0, o_rows);
+            if (!more)
+                break;
+            stored = p.c_vec != 0;
+        }
+        // (loads of no item are still on their way into LDS)
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+        return;
+    }
     set_item(item);
     preload();
     for (;;) {
