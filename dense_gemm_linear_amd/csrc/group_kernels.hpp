@@ -788,6 +788,91 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         else
             k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, nomask, load, nothing, nothing);
         if constexpr (ADAPT) {
+            if constexpr (TM <= 64)
+            if (units > 0 && p.R <= 32) {
+                // A few rows and ranks: a thread takes a column of B at a time, the lanes of
+                // a wave neighbouring ones, whose ranks lie together in memory, for each row
+                // with its own adapter.  Sums in fp32 through LDS into the accumulators'
+                // layout.  (48 rows of 16 adapters of 16 ranks: 4 us; by matrix steps, below,
+                // of which every adapter takes one in all 64 rows, 9.)
+                const KernelArgs q = kernel_args();
+                float* delta = reinterpret_cast<float*>(lds);                  // [TM][TN + 4]
+                float* u_lds = delta + TM * (TN + 4);                          // [TM][32]
+                int* row_id = reinterpret_cast<int*>(u_lds + TM * 32);         // [TM]
+                static_assert((TM * (TN + 4) + TM * 33) * 4 <= S::OUT_AT, "fits the stages");
+                for (int r = tid; r < TM; r += S::THREADS)
+                    row_id[r] = -1;
+                for (int i = tid; i < rows * 4; i += S::THREADS) {
+                    const int r = i / 4, k = i % 4 * 8;
+                    if (k < q->R) {
+                        const uint16_t* u = reinterpret_cast<const uint16_t*>(q->U) + (int64_t)(m0 + r) * 2 * q->R + k;
+                        const i32x4 hi = *reinterpret_cast<const i32x4*>(u);
+                        const i32x4 lo = *reinterpret_cast<const i32x4*>(u + q->R);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            u_lds[r * 32 + k + 2 * e] =
+                                __uint_as_float((uint32_t)hi[e] << 16) + __uint_as_float((uint32_t)lo[e] << 16);
+                            u_lds[r * 32 + k + 2 * e + 1] = __uint_as_float((uint32_t)hi[e] & 0xFFFF0000u) +
+                                                            __uint_as_float((uint32_t)lo[e] & 0xFFFF0000u);
+                        }
+                    }
+                }
+                __syncthreads();
+                const int over = units / q->units;
+                for (int e = tid; e < over; e += S::THREADS) {
+                    const int id = table.id(entry0 + e);
+                    const int hi = min(table.first(entry0 + e + 1) - m0, rows);
+                    for (int r = max(table.first(entry0 + e) - m0, 0); r < hi; ++r)
+                        row_id[r] = id;
+                }
+                __syncthreads();
+                constexpr int EACH = TM * TN / S::THREADS, B = EACH < 8 ? EACH : 8;
+                static_assert(EACH % B == 0, "columns a thread");
+                for (int i0 = 0; i0 < EACH; i0 += B) {
+                    float sum[B] = {};
+                    for (int k = 0; k < q->R; k += 16) {
+                        i32x4 w[B][2];
+#pragma unroll
+                        for (int i = 0; i < B; ++i) {
+                            const int at = (i0 + i) * S::THREADS + tid, r = at / TN, c = at % TN;
+                            const int id = row_id[r];
+                            const bool in = id >= 0 && n0 + c < q->N;
+                            const uint8_t* from = q->LB + (in ? id * q->lb_group + (n0 + c) * q->ldlb_b + k * 2 : 0);
+                            w[i][0] = *reinterpret_cast<const i32x4*>(from);
+                            w[i][1] = *reinterpret_cast<const i32x4*>(from + (in && k + 8 < q->R ? 16 : 0));
+                        }
+#pragma unroll
+                        for (int i = 0; i < B; ++i) {
+                            const int r = ((i0 + i) * S::THREADS + tid) / TN;
+                            const float* u = u_lds + r * 32 + k;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (k + 8 * h < q->R)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        sum[i] = fmaf(u[8 * h + 2 * e], __uint_as_float((uint32_t)w[i][h][e] << 16), sum[i]);
+                                        sum[i] = fmaf(u[8 * h + 2 * e + 1],
+                                                      __uint_as_float((uint32_t)w[i][h][e] & 0xFFFF0000u), sum[i]);
+                                    }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < B; ++i) {
+                        const int at = (i0 + i) * S::THREADS + tid, r = at / TN;
+                        delta[r * (TN + 4) + at % TN] = row_id[r] >= 0 ? sum[i] : 0.f;
+                    }
+                }
+                __syncthreads();
+                // (rows that have none take zeros, and a row's NaN stays its own)
+#pragma unroll
+                for (int mi = 0; mi < MR; ++mi)
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+                        acc[mi][j] += *reinterpret_cast<const f32x4*>(
+                            delta + ((int)row0 + mi * R + lc) * (TN + 4) + (int)col0 + j * R + 4 * lg);
+                __syncthreads();
+                units = 0;
+            }
             // Behind the k-tiles of X and W: the ranks of the adapters that the tile's rows
             // have, in units of 16.  One step of the matrix cores holds a unit: the rows'
             // inner values, upper halves and then lower ones, against the same columns of B
