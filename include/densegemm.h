@@ -603,6 +603,7 @@ gemm_status linear_distillation_grad(const uint16_t* X, int64_t ldx, const uint1
  * are not ascending, and an order or place outside [0, S), give unspecified rows
  * but reach no memory outside the buffers described.
  *
+ * Calls that share a workspace must not overlap in time.
  * Buffers of sorted rows hold S rows.  Rows from n on (there are some if slots
  * take no part) are not written and not read.  Outputs must not overlap inputs
  * unless it is said.  Sums have a fixed order: results are bitwise repeatable.
