@@ -11,7 +11,8 @@ namespace dg {
 
 constexpr int64_t kMaxGroups = 512;
 constexpr int64_t kMaxGroupSlots = 64;               // choices a token
-constexpr int64_t kMaxSorted = INT64_C(1) << 24;     // slots in all
+// slots in all, less than: their rows at 256 threads each make a grid below 2^32 threads
+constexpr int64_t kMaxSorted = INT64_C(1) << 24;
 constexpr int64_t kMaxRank = 256;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }

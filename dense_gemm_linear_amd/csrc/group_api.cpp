@@ -13,6 +13,11 @@ constexpr int64_t kMaxAdapterRows = INT64_C(1) << 20; // their table packs a row
 constexpr int64_t kMaxWidth = INT64_C(1) << 16;
 constexpr int64_t kMaxColumns = INT64_C(1) << 20;
 
+// A single row's pitch, or a single group's distance, says nothing and may be anything:
+// what the kernels see is that of a row as long as it must be.
+int64_t pitch_of(int64_t rows, int64_t ld, int64_t width) { return rows > 1 ? ld : (width + 7) / 8 * 8; }
+int64_t stride_of(int64_t groups, int64_t stride) { return groups > 1 ? stride : 0; }
+
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // T tokens with k choices among `groups` groups
@@ -20,7 +25,7 @@ gemm_status check_slots(int64_t T, int64_t k, int64_t groups)
 {
     if (T < 0 || k < 1 || groups < 1)
         return GEMM_ERR_INVALID_VALUE;
-    if (T > kMaxSorted || k > kMaxGroupSlots || T * k > kMaxSorted || groups > kMaxGroups)
+    if (T >= kMaxSorted || k > kMaxGroupSlots || T * k >= kMaxSorted || groups > kMaxGroups)
         return GEMM_ERR_UNSUPPORTED;
     return GEMM_OK;
 }
@@ -220,12 +225,12 @@ gemm_status group_linear(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
     gemm_status st = dg::first_of({dg::check_slots(T, k, groups), dg::check_sizes(N, K)});
     if (st != GEMM_OK)
         return st;
-    if (activation < GEMM_ACT_NONE || activation > GEMM_ACT_GELU_TANH || (!order && k != 1))
+    if (activation < GEMM_ACT_NONE || activation > GEMM_ACT_GELU_TANH)
         return GEMM_ERR_INVALID_VALUE;
     if (T == 0)
         return GEMM_OK;
     const int64_t S = T * k;
-    if (!offsets || !dg::aligned(offsets, 4) || !dg::aligned(order, 4))
+    if ((!order && k != 1) || !offsets || !dg::aligned(offsets, 4) || !dg::aligned(order, 4))
         return GEMM_ERR_INVALID_VALUE;
     st = dg::first_of({dg::check_operand(X, ldx, T, K), dg::check_operand(W, ldw, N, K),
                        dg::check_stack(w_stride, groups, N, ldw, K, 8), dg::check_output(Y, ldy, S, N),
@@ -239,10 +244,10 @@ gemm_status group_linear(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
     if (st != GEMM_OK)
         return st;
     c.X = X;
-    c.ldx = ldx;
+    c.ldx = dg::pitch_of(T, ldx, K);
     c.W = W;
-    c.ldw = ldw;
-    c.ldw_group = w_stride;
+    c.ldw = dg::pitch_of(N, ldw, K);
+    c.ldw_group = dg::stride_of(groups, w_stride);
     c.offsets = offsets;
     c.order = order;
     c.T = T;
@@ -252,9 +257,9 @@ gemm_status group_linear(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
     c.K = K;
     c.act = activation;
     c.mul = mul;
-    c.ld_mul = ld_mul;
+    c.ld_mul = dg::pitch_of(S, ld_mul, N);
     c.Y = Y;
-    c.ldy = ldy;
+    c.ldy = dg::pitch_of(S, ldy, N);
     c.stream = reinterpret_cast<hipStream_t>(stream);
     return dg::done(dg::group_forward(c));
 }
@@ -276,7 +281,7 @@ gemm_status group_linear_grad(const uint16_t* dY, int64_t lddy, const uint16_t* 
                                    N % 8 != 0 || N > dg::kMaxWidth ? GEMM_ERR_UNSUPPORTED : GEMM_OK});
     if (st != GEMM_OK)
         return st;
-    if ((!order && k != 1) || (!dX && !dW))
+    if (!dX && !dW)
         return GEMM_ERR_INVALID_VALUE;
     const int64_t S = T * k;
     if (dW) {
@@ -285,7 +290,7 @@ gemm_status group_linear_grad(const uint16_t* dY, int64_t lddy, const uint16_t* 
             return st;
     }
     if (T > 0) {
-        if (!offsets || !dg::aligned(offsets, 4) || !dg::aligned(order, 4))
+        if ((!order && k != 1) || !offsets || !dg::aligned(offsets, 4) || !dg::aligned(order, 4))
             return GEMM_ERR_INVALID_VALUE;
         st = dg::first_of({dg::check_operand(dY, lddy, S, N),
                            dX ? dg::check_operand(W, ldw, N, K) : GEMM_OK,
@@ -318,12 +323,12 @@ gemm_status group_linear_grad(const uint16_t* dY, int64_t lddy, const uint16_t* 
         return GEMM_OK;
     }
     c.dY = dY;
-    c.lddy = lddy;
+    c.lddy = dg::pitch_of(S, lddy, N);
     c.X = X;
-    c.ldx = ldx;
+    c.ldx = dg::pitch_of(T, ldx, K);
     c.W = W;
-    c.ldw = ldw;
-    c.ldw_group = w_stride;
+    c.ldw = dg::pitch_of(N, ldw, K);
+    c.ldw_group = dg::stride_of(groups, w_stride);
     c.offsets = offsets;
     c.order = order;
     c.T = T;
@@ -332,10 +337,10 @@ gemm_status group_linear_grad(const uint16_t* dY, int64_t lddy, const uint16_t* 
     c.N = N;
     c.K = K;
     c.dX = dX;
-    c.lddx = lddx;
+    c.lddx = dg::pitch_of(S, lddx, K);
     c.dW = dW;
     c.lddw = lddw;
-    c.lddw_group = dw_stride;
+    c.lddw_group = dg::stride_of(groups, dw_stride);
     c.ws = static_cast<uint8_t*>(workspace);
     return dg::done(dg::group_backward(c));
 }
@@ -377,15 +382,15 @@ gemm_status linear_adapters(const uint16_t* X, int64_t ldx, const uint16_t* W, i
     if (st != GEMM_OK)
         return st;
     c.X = X;
-    c.ldx = ldx;
+    c.ldx = dg::pitch_of(T, ldx, K);
     c.W = W;
-    c.ldw = ldw;
+    c.ldw = dg::pitch_of(N, ldw, K);
     c.A = A;
-    c.lda = lda;
-    c.lda_group = a_stride;
+    c.lda = dg::pitch_of(R, lda, K);
+    c.lda_group = dg::stride_of(groups, a_stride);
     c.B = B;
-    c.ldb = ldb;
-    c.ldb_group = b_stride;
+    c.ldb = dg::pitch_of(N, ldb, R);
+    c.ldb_group = dg::stride_of(groups, b_stride);
     c.scale = scale;
     c.offsets = offsets;
     c.order = order;
@@ -396,7 +401,7 @@ gemm_status linear_adapters(const uint16_t* X, int64_t ldx, const uint16_t* W, i
     c.K = K;
     c.R = R;
     c.Y = Y;
-    c.ldy = ldy;
+    c.ldy = dg::pitch_of(T, ldy, N);
     c.ws = static_cast<uint8_t*>(workspace);
     c.stream = reinterpret_cast<hipStream_t>(stream);
     return dg::done(dg::adapters_forward(c));

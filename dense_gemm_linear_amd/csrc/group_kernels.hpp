@@ -74,7 +74,7 @@ struct GroupShape {
     static constexpr int KT = KTB / 2;
     static constexpr int WCOLS = TN / WN;
     static constexpr int SROW = WCOLS * 2 + 16;
-    static constexpr int REST_KT = TM * TN >= 256 * 256 ? 14 : 8;    // DW, see there
+    static constexpr int REST_KT = 8;    // DW, see there
     // after the stages: the waves' output blocks, the groups' table
     static constexpr int OUT_AT = ST * STAGE, OUT_LDS = WAVES * R * SROW;
     static constexpr int TABLE_AT = OUT_AT + OUT_LDS;
@@ -321,9 +321,11 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
     build_table<S::THREADS, ADAPT>(table, p.offsets, p.groups, p.S, ROLE == GROUP_DW ? KT : TM,
                                    ROLE == GROUP_DW ? S::REST_KT : 0);
     const int w_tiles = ROLE == GROUP_DW ? (p.M + TM - 1) / TM * p.tiles_n : 0;   // DW: tiles of a group
+    // (offsets that are not ascending may claim more rows than there are: nothing is done)
     const int items = __builtin_amdgcn_readfirstlane(
         ROLE == GROUP_DW ? p.groups * w_tiles
-                         : (ADAPT ? (p.S + TM - 1) / TM : table.first(p.groups)) * p.tiles_n);
+        : ADAPT          ? (p.S + TM - 1) / TM * p.tiles_n
+        : table.first(p.groups) <= p.S / TM + p.groups ? table.first(p.groups) * p.tiles_n : 0);
     // DW: a tile takes as long as its group has rows.  Each XCD has a run of tiles
     // of the same cost, counted in k-tiles (with REST_KT for a tile's start and its
     // output), which its workgroups take in turn.  (Items b, b + G, ... as for the
@@ -407,17 +409,18 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
     const int kb_end = ROLE == GROUP_DW ? 0 : p.K * 2;
     const int last_full = ROLE == GROUP_DW ? 0 : kb_end / KTB;
     const uint8_t *a_base = nullptr, *b_base = nullptr;
-    // plain: bytes of the tile's rows; transposed: bytes of the last k-tile
-    int a_span = 0, b_span = 0;
+    // plain: bytes of the tile's rows; transposed: bytes of the last k-tile, and of those
+    // before it
+    int a_span = 0, b_span = 0, a_full = 0, b_full = 0;
     const int a_step = KT * (int)p.lda_b, b_step = KT * (int)p.ldb_b;         // TRA, TRB
     const int a_rows = A_ROWS * (int)p.lda_b, b_rows = B_ROWS * (int)p.ldb_b;
     uint32_t a_bytes = 0;                                                     // GATHER
     // STREAM: what the loads turn to behind the present item's k-tiles
     struct Operands {
         const uint8_t *a, *b;
-        int a_span, b_span, nkt;
+        int a_span, b_span, a_full, b_full, nkt;
     };
-    Operands next = {nullptr, nullptr, 0, 0, 0};
+    Operands next = {nullptr, nullptr, 0, 0, 0, 0, 0};
     int stream_end = -1, k_off = 0;
     // ADAPT: the first of the table's entries that the tile's rows touch, and all their
     // units of 16 ranks
@@ -438,6 +441,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             nkt = (n + KT - 1) / KT;
             a_base = q->A + lo * q->lda_b + (int64_t)m0 * 2;
             a_span = (n - 1) % KT * (int)q->lda_b + (q->M - m0) * 2;
+            a_full = a_step - (int)q->lda_b + (q->M - m0) * 2;
             b_base = q->B + lo * q->ldb_b;
             b_span = (n - 1) % KT * (int)q->ldb_b;
             last_row = 0;
@@ -492,6 +496,7 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             if constexpr (ROLE == GROUP_DX)
                 b_span = (q->K - 1) % KT * (int)q->ldb_b;
             b_span += (q->N - n0) * 2;
+            b_full = b_step - (int)q->ldb_b + (q->N - n0) * 2;
         } else {
             b_base += (int64_t)n0 * q->ldb_b;
             b_span = (min(TN, q->N - n0) - 1) * (int)q->ldb_b + q->K * 2;
@@ -503,16 +508,18 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         a_bytes = (uint32_t)__builtin_amdgcn_readfirstlane((int)a_bytes);
         a_span = __builtin_amdgcn_readfirstlane(a_span);
         b_span = __builtin_amdgcn_readfirstlane(b_span);
+        a_full = __builtin_amdgcn_readfirstlane(a_full);
+        b_full = __builtin_amdgcn_readfirstlane(b_full);
         if constexpr (ROLE == GROUP_DW)
             nkt = __builtin_amdgcn_readfirstlane(nkt);
     };
-    // Rows i rows_b bytes behind the tile's first; or the rows of k-tile kt, all
-    // there before the last k-tile and none behind it.
+    // Rows i rows_b bytes behind the tile's first; or the rows of k-tile kt, none behind
+    // the last one.
     auto plain_rsrc = [&](const uint8_t* base, int span, int behind) __attribute__((always_inline)) {
         return make_rsrc(base + behind, (uint32_t)max(span - behind, 0));
     };
-    auto tr_rsrc = [&](const uint8_t* base, int span, int kt) __attribute__((always_inline)) {
-        return make_rsrc(base, kt + 1 < nkt ? 0x7FFFFFFFu : kt + 1 == nkt ? (uint32_t)span : 0u);
+    auto tr_rsrc = [&](const uint8_t* base, int span, int full, int kt) __attribute__((always_inline)) {
+        return make_rsrc(base, (uint32_t)(kt + 1 < nkt ? full : kt < nkt ? span : 0));
     };
     auto load = [&](int kt, int stage, int part, int nparts, auto nomask_c) __attribute__((always_inline)) {
         constexpr bool NOMASK = decltype(nomask_c)::value;
@@ -524,6 +531,8 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                 b_base = next.b;
                 a_span = next.a_span;
                 b_span = next.b_span;
+                a_full = next.a_full;
+                b_full = next.b_full;
                 nkt = next.nkt;
                 k_off = stream_end;
             }
@@ -548,14 +557,14 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         for (int i = 0; i < A_DMA; ++i)
             if (i % nparts == part)
                 one(GATHER ? make_rsrc(a_base, a_bytes)
-                    : TRA  ? tr_rsrc(a_base, a_span, kt - k_off)
+                    : TRA  ? tr_rsrc(a_base, a_span, a_full, kt - k_off)
                            : plain_rsrc(a_base, a_span, i * a_rows),
                     base + (wave + WAVES * i) * 1024, a_goff[i % A_OFFS], a_col,
                     std::integral_constant<bool, TRA>{}, 0);
 #pragma unroll
         for (int i = 0; i < B_DMA; ++i)
             if ((A_DMA + i) % nparts == part)
-                one(TRB ? tr_rsrc(b_base, b_span, kt - k_off) : plain_rsrc(b_base, b_span, i * b_rows),
+                one(TRB ? tr_rsrc(b_base, b_span, b_full, kt - k_off) : plain_rsrc(b_base, b_span, i * b_rows),
                     base + A_BUF + (wave + WAVES * i) * 1024, b_goff[i % B_OFFS], b_col,
                     std::integral_constant<bool, TRB>{}, TM <= 64 && !TRA ? p.b_nt : 0);
         // a transposed operand's base goes on with the k-tiles (part by part, then
@@ -745,16 +754,18 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         preload();
         for (;;) {
             const int o_group = group, o_m0 = m0, o_n0 = n0, o_rows = rows;
-            const Operands here = {a_base, b_base, a_span, b_span, nkt};
+            const Operands here = {a_base, b_base, a_span, b_span, a_full, b_full, nkt};
             const bool more = next_item();
             stream_end = max(1, (nkt + ST - 1) / ST) * ST;
             if (more)
                 set_item(item);
-            next = Operands{a_base, b_base, a_span, b_span, more ? nkt : 0};
+            next = Operands{a_base, b_base, a_span, b_span, a_full, b_full, more ? nkt : 0};
             a_base = here.a;
             b_base = here.b;
             a_span = here.a_span;
             b_span = here.b_span;
+            a_full = here.a_full;
+            b_full = here.b_full;
             nkt = here.nkt;
             k_off = 0;
 #pragma unroll

@@ -593,7 +593,7 @@ gemm_status linear_distillation_grad(const uint16_t* X, int64_t ldx, const uint1
  * S = T k slots sorted by group (expert, adapter).
  *
  * Common arguments:
- *   groups   1 to 512.  k up to 64, T k up to 2^24 (linear_adapters: T up to 2^20).
+ *   groups   1 to 512.  k up to 64, T k below 2^24 (linear_adapters: T up to 2^20).
  *   offsets  device int32 [groups + 1]: group g's rows are the sorted positions
  *            offsets[g] .. offsets[g + 1] - 1, n = offsets[groups] rows in all.
  *   order    device int32 [S]: the slot t k + j at each sorted position.
