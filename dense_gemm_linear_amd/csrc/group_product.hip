@@ -131,18 +131,18 @@ namespace {
 
 // What one round of tiles (every CU holding its fill of workgroups) takes, in
 // microseconds: kt for each 32 values of K, epi for the rest; kt1 where there is at
-// most one workgroup a CU.  Fitted to the times of all shapes at 61 sizes (1 to 8192
+// most one workgroup a CU; and start, once.  Fitted to the times of all shapes at 61 sizes (1 to 8192
 // tokens, 1 to 8 choices, 4 to 128 groups, N 520 to 11008, K 512 to 11008, with
 // adapters and without): the shape chosen then took 1.5 % longer than the best on
 // average, 16 % at most.
 struct Cost {
     int shape, tm, tn, per_cu;
-    double kt, kt1, epi;
+    double kt, kt1, epi, start;
 };
 template <class S>
-constexpr Cost cost_of(int shape, double kt, double kt1, double epi)
+constexpr Cost cost_of(int shape, double kt, double kt1, double epi, double start = 0.0)
 {
-    return {shape, S::TM, S::TN, S::PER_CU, kt, kt1, epi};
+    return {shape, S::TM, S::TN, S::PER_CU, kt, kt1, epi, start};
 }
 constexpr Cost kPlain[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5),          cost_of<GTall>(G_TALL, 0.48, 0.42, 3.8),
                            cost_of<GLine>(G_LINE, 0.56, 0.38, 2.5),        cost_of<GDeep>(G_DEEP, 0.28, 0.27, 2.3),
@@ -152,9 +152,11 @@ constexpr Cost kPlain[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5),          cost_
 constexpr Cost kDx[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5), cost_of<GTall>(G_TALL, 0.48, 0.42, 3.8),
                         cost_of<GMid>(G_MID, 0.64, 0.50, 0.5), cost_of<GFew>(G_FEW, 0.41, 0.19, 4.6),
                         cost_of<GLow>(G_LOW, 0.40, 0.20, 1.3)};
-// dW: the rest of a tile is its output (4096 rows of K a group and tile would be
-// alike; of the two the wider tile takes longer to start and store)
-constexpr Cost kDw[] = {cost_of<GTall>(G_TALL, 0.48, 0.48, 7.3), cost_of<GMid>(G_MID, 0.64, 0.64, 5.6)};
+// dW, 1 to 6300 rows a group, N 520 to 11008: the smaller tile takes less for few rows
+// (14 a group of 4096 x 4096: 65 us against 72) and few tiles (256 a group, 32 of 1024 x
+// 2048: 58 against 60), the larger one else (1024 a group, 8 of 11008 x 4096: 757
+// against 862; 252 a group, 16 of them: 617 against 678)
+constexpr Cost kDw[] = {cost_of<GTall>(G_TALL, 0.47, 0.47, 3.9, 4.0), cost_of<GMid>(G_MID, 0.57, 0.57, 3.4)};
 
 // Estimated time of `tiles` rows of tiles over `cols` columns and `kts` times 32
 // values of K.
@@ -162,7 +164,7 @@ double tiles_us(const Cost& c, double tiles, int64_t cols, double kts, int cus)
 {
     const double items = tiles * (double)cdiv(cols, c.tn), round = (double)cus * c.per_cu;
     const double full = (double)(int64_t)(items / round), left = items - full * round;
-    return full * (kts * c.kt + c.epi) + (left > 0.5 ? kts * (left > cus ? c.kt : c.kt1) + c.epi : 0.0);
+    return c.start + full * (kts * c.kt + c.epi) + (left > 0.5 ? kts * (left > cus ? c.kt : c.kt1) + c.epi : 0.0);
 }
 
 // Tiles of tm rows that `rows` rows in `used` groups are expected to make: a group's
@@ -173,11 +175,16 @@ double row_tiles(int64_t rows, int64_t used, int tm)
     return (double)used * std::max(mean > 1.5 ? 1.1 : 1.0, mean / tm + 0.55);
 }
 
-// The shape of the least estimate, us(cost).  The smallest tiles only where they
-// make no second round: what bounds such a product is reading W, which they do
-// less well (16 x 2 rows of 8 groups of 4096 x 4096: 51 us against 44).
+// The shape of the least estimate.  `reads`: microseconds that the groups' weights
+// take from memory; a row of tiles past a group's first reads them from the caches, at
+// about three times the rate.  Where that is longer than the products it counts in
+// their place, and these for a little, between shapes that read alike (57 rows a group
+// of 64, N 4096, K 11008: 64 x 128 tiles, of which many groups need two, 1347 us, 128 x
+// 128 1145).  The smallest tiles only where they make no second round: what bounds such
+// a product is reading W, which they do less well (16 x 2 rows of 8 groups of 4096 x
+// 4096: 51 us against 44).
 template <int N, class Tiles>
-int pick(const Cost (&of)[N], int64_t cols, double kts, int cus, Tiles&& tiles)
+int pick(const Cost (&of)[N], int64_t cols, double kts, int cus, double reads, int64_t used, Tiles&& tiles)
 {
     int best = -1;
     double least = 0.0;
@@ -186,12 +193,19 @@ int pick(const Cost (&of)[N], int64_t cols, double kts, int cus, Tiles&& tiles)
         if (c.shape == G_ONE && t * (double)cdiv(cols, c.tn) > (double)cus * c.per_cu)
             continue;
         const double us = tiles_us(c, t, cols, kts, cus);
-        if (best < 0 || us < least) {
+        const double all = std::max(us, reads * (1.0 + (t / (double)used - 1.0) / 3.0)) + 0.05 * us;
+        if (best < 0 || all < least) {
             best = c.shape;
-            least = us;
+            least = all;
         }
     }
     return best;
+}
+
+// Microseconds to read `groups` weights of N x K once, at 5 TB/s.
+double weights_us(int64_t groups, int64_t N, int64_t K)
+{
+    return (double)groups * (double)N * (double)K * 2.0 / 5.0e6;
 }
 
 GroupArgs base_args(const ProductCall& c)
@@ -237,7 +251,7 @@ hipError_t group_forward(const ProductCall& c)
     a.ld_mul = c.ld_mul;
     a.mul_vec = ((uintptr_t)c.mul & 7u) == 0 && c.ld_mul % 4 == 0 && c.N % 4 == 0;
     a.b_nt = 1;
-    const int shape = pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus,
+    const int shape = pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus, weights_us(used, c.N, c.K), used,
                            [&](int tm) { return row_tiles(S, used, tm); });
     return c.act || c.mul ? launch_group_gated(shape, a, used, c.cus, c.stream)
                           : launch_group_fwd(shape, a, used, c.cus, c.stream);
@@ -259,7 +273,7 @@ hipError_t group_backward(const ProductCall& c)
         a.ldc = c.lddx;
         a.c_vec = vec_of(c.dX, c.lddx, c.K);
         a.b_nt = 1;
-        const int shape = pick(kDx, c.K, (double)cdiv(c.N, 32), c.cus,
+        const int shape = pick(kDx, c.K, (double)cdiv(c.N, 32), c.cus, weights_us(used, c.N, c.K), used,
                                [&](int tm) { return row_tiles(S, used, tm); });
         const hipError_t e = launch_group_dx(shape, a, used, c.cus, c.stream);
         if (e != hipSuccess)
@@ -304,7 +318,7 @@ hipError_t group_backward(const ProductCall& c)
     // 2 %, with that kernel they lose up to 5.
     if (a.c_vec)
         a.c_vec = 2;
-    const int shape = pick(kDw, c.K, (double)cdiv(cdiv(S, c.groups), 32), c.cus,
+    const int shape = pick(kDw, c.K, (double)cdiv(cdiv(S, c.groups), 32), c.cus, 0.0, 1,
                            [&](int tm) { return (double)(c.groups * cdiv(c.N, tm)); });
     return launch_group_dw(shape, a, 0, c.cus, c.stream);
 }
@@ -422,7 +436,7 @@ hipError_t adapters_forward(const ProductCall& c)
     // as a tile of 64 rows has
     const int64_t near = std::min<int64_t>(std::min(c.groups, T), cdiv(std::min(c.groups, T) * 64, T) + 1);
     const double kts = (double)cdiv(c.K, 32) + (double)(near * cdiv(c.R, 16));
-    const int shape = pick(kPlain, c.N, kts, c.cus, [&](int tm) { return (double)cdiv(T, tm); });
+    const int shape = pick(kPlain, c.N, kts, c.cus, 0.0, 1, [&](int tm) { return (double)cdiv(T, tm); });
     return launch_group_adapt(shape, a, 0, c.cus, c.stream);
 }
 
