@@ -178,11 +178,18 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
             return p.totals[g];
         }
         if (p.counts) {
-#pragma unroll 16
-            for (int c = 0; c < (int)gridDim.x; ++c) {
-                const int n = p.counts[(int64_t)c * (G + 1) + g];
-                before += c < (int)blockIdx.x ? n : 0;
-                total += n;
+            // (16 loads in flight, whatever the number of chunks)
+            const int chunks = (int)gridDim.x;
+            for (int c0 = 0; c0 < chunks; c0 += 16) {
+                int n[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    n[i] = p.counts[(int64_t)min(c0 + i, chunks - 1) * (G + 1) + g];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    before += c0 + i < (int)blockIdx.x ? n[i] : 0;
+                    total += c0 + i < chunks ? n[i] : 0;
+                }
             }
         } else {
 #pragma unroll
@@ -202,9 +209,10 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
             at += n[v];
         }
     };
-    // thread g: group g (and thread 0 `none`, behind all)
+    // thread g: group g, and behind all others `none` (group G)
     int before = 0;
-    const int total = tid < G ? totals(tid, before) : 0;
+    const int rows = tid <= G ? totals(tid, before) : 0;
+    const int total = tid < G ? rows : 0;
     const int upto = wave_scan(total, lane);
     if (lane == 63)
         sums[wave] = upto;
@@ -214,18 +222,11 @@ __global__ __launch_bounds__(1024) void group_place_kernel(SortArgs p)
         base += v < wave ? sums[v] : 0;
         all += sums[v];
     }
-    if (tid < G) {
-        const int first = base + upto - total;
+    if (tid <= G) {
+        const int first = tid < G ? base + upto - total : all;
         starts(tid, first + before);
         if (blockIdx.x == 0)
             p.offsets[tid] = first;
-    }
-    if (tid == 0) {
-        int none_before;
-        totals(G, none_before);
-        starts(G, all + none_before);
-        if (blockIdx.x == 0)
-            p.offsets[G] = all;
     }
     __syncthreads();
 #pragma unroll
