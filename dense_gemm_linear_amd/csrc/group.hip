@@ -17,7 +17,7 @@ namespace {
 //   1. a slot's number among its wave's slots of the same group: those of the
 //      steps before (a count per wave and group in LDS) and those of the lower
 //      lanes, which log2(groups) ballots tell (LDS atomics on the counts took
-//      longer the fewer groups there were: 12 us for 8190 slots of 8 groups, 8 now);
+//      longer the fewer groups there were: 12 us for 8190 slots of 8 groups, 7 now);
 //   2. thread g adds up group g's counts: rows of all lower groups, then of the
 //      chunks and waves before;
 //   3. each slot's position is the sum of both.
@@ -27,10 +27,12 @@ namespace {
 constexpr int kSortWaves = 16;
 constexpr int kSortBatch = 8;          // slots a lane at most
 constexpr int kSortMost = kSortWaves * 64 * kSortBatch;
-// Slots that one workgroup takes: 2048 in 4.6 us, 4096 in 6.2, 8192 in 9 to 14; two
-// launches over chunks of 1024 take 7 to 8.
+// Slots that one workgroup takes: 2048 in 4.3 us, 4096 in 5.8, 8192 in 9 to 14; two
+// launches over chunks of 1024 take 6.8 to 7.4.
 constexpr int kSortOne = 4096;
-constexpr int kSortScan = 32;          // chunks from which on their counts are summed apart
+// Chunks from which on their counts are summed apart (from 32 on: 65536 slots of 128
+// groups 12.0 us, 9.7 so; 131072 15.8 and 11.6; 524288 25.5 and 21.7).
+constexpr int kSortScan = 97;
 
 struct SortArgs {
     const int64_t* ids;
