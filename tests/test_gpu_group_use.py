@@ -465,3 +465,40 @@ def test_rows_past_4_gib():
     big.zero_()
     dg.group_gather(out, place, out=big)
     assert torch.equal(big[-200::2], out[-100:]) and torch.equal(big[-199::2], out[-100:])
+
+
+# ---- the limits
+
+@pytest.mark.parametrize("T,k,G", [(2 ** 24 - 1, 1, 512), (2 ** 18 - 1, 64, 3), (803000, 1, 130), (98 * 1024, 1, 7),
+                                   (96 * 1024, 1, 512), (1025, 4, 512)])
+def test_sort_of_many(T, k, G):
+    """Up to the most slots there may be, against a stable sort of 64-bit integers."""
+    _say("sort", T, k, G)
+    ids = torch.randint(-1, G + 1, (T, k), generator=torch.Generator().manual_seed(T)).cuda()
+    off, order, place = dg.group_sort(ids, G)
+    key = torch.where((ids >= 0) & (ids < G), ids, G).reshape(-1)
+    _, want = torch.sort(key, stable=True)
+    assert torch.equal(order.long(), want)
+    ends = torch.cumsum(torch.bincount(key.cpu(), minlength=G + 1), 0)[:G]
+    assert int(off[0]) == 0 and torch.equal(off[1:].cpu().long(), ends)
+    n = int(off[-1])
+    at = torch.full((T * k,), -1, dtype=torch.int32, device="cuda")
+    at[want[:n]] = torch.arange(n, dtype=torch.int32, device="cuda")
+    assert torch.equal(place.reshape(-1), at)
+
+
+def test_rows_of_most_tokens():
+    """A workgroup a row and the most rows: 17 GB of them."""
+    T, D = 2 ** 24 - 1, 520
+    X = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    last = bf16(5, D, seed=1).cuda()
+    X[-5:] = last
+    place = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")[:, None]
+    Xs = dg.group_gather(X, place)
+    assert torch.equal(Xs[:5], last.flip(0)) and not bool(Xs[5:].any())
+    out = dg.group_combine(Xs, place)
+    assert torch.equal(out[-5:], last) and not bool(out[:-5].any())
+    dY, dw = dg.group_combine_grad(out, Xs, place)
+    assert torch.equal(dY[:5], last.flip(0)) and not bool(dw[:-5].any())
+    want = (last.double() ** 2).sum(1).cpu()
+    close(dw[-5:, 0], want, (D + 2) * U32 * want, "dw")
