@@ -131,10 +131,10 @@ namespace {
 
 // What one round of tiles (every CU holding its fill of workgroups) takes, in
 // microseconds: kt for each 32 values of K, epi for the rest; kt1 where there is at
-// most one workgroup a CU; and start, once.  Fitted to the times of all shapes at 231
+// most one workgroup a CU; and start, once.  Fitted to the times of all shapes at 242
 // sizes, most drawn at random (1 to 8192 tokens, 1 to 8 choices, 4 to 128 groups, N 256
 // to 11008, K 256 to 11008; 2 to 4095 rows with adapters): the shape chosen takes 2 %
-// longer than the best on average with groups, 0.5 % with adapters, and 30 % at most
+// longer than the best on average with groups, 1 % with adapters, and 30 % at most
 // (groups of equal size just under a whole tile's rows, which the host cannot see).
 struct Cost {
     int shape, tm, tn, per_cu;
@@ -148,12 +148,12 @@ constexpr Cost cost_of(int shape, double kt, double kt1, double epi, double star
 constexpr Cost kPlain[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5),          cost_of<GTall>(G_TALL, 0.48, 0.42, 3.8),
                            cost_of<GLine>(G_LINE, 0.54, 0.37, 2.5),        cost_of<GDeep>(G_DEEP, 0.27, 0.27, 2.3),
                            cost_of<GSlim>(G_SLIM, 0.20, 0.11, 2.0),        cost_of<GFew>(G_FEW, 0.41, 0.22, 4.6),
-                           cost_of<GFewSlim>(G_FEW_SLIM, 0.21, 0.11, 4.3), cost_of<GLowSlim>(G_LOW_SLIM, 0.17, 0.12, 2.7),
+                           cost_of<GFewSlim>(G_FEW_SLIM, 0.21, 0.14, 4.3), cost_of<GLowSlim>(G_LOW_SLIM, 0.17, 0.12, 2.7),
                            cost_of<GOne>(G_ONE, 0.11, 0.08, 1.9)};
 constexpr Cost kAdapt[] = {cost_of<GBig>(G_BIG, 0.74, 0.48, 6.6),          cost_of<GTall>(G_TALL, 0.48, 0.42, 4.3),
                            cost_of<GLine>(G_LINE, 0.43, 0.38, 2.5),        cost_of<GDeep>(G_DEEP, 0.28, 0.27, 2.3),
                            cost_of<GSlim>(G_SLIM, 0.20, 0.19, 2.0),        cost_of<GFew>(G_FEW, 0.41, 0.19, 5.9),
-                           cost_of<GFewSlim>(G_FEW_SLIM, 0.21, 0.13, 4.0), cost_of<GLowSlim>(G_LOW_SLIM, 0.17, 0.12, 2.7),
+                           cost_of<GFewSlim>(G_FEW_SLIM, 0.21, 0.13, 4.0), cost_of<GLowSlim>(G_LOW_SLIM, 0.17, 0.11, 2.9),
                            cost_of<GOne>(G_ONE, 0.12, 0.08, 1.9)};
 constexpr Cost kDx[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5), cost_of<GTall>(G_TALL, 0.48, 0.42, 3.8),
                         cost_of<GMid>(G_MID, 0.56, 0.41, 0.5), cost_of<GFew>(G_FEW, 0.57, 0.15, 4.6),
@@ -183,7 +183,7 @@ double row_tiles(int64_t rows, int64_t used, int tm)
 
 // The shape of the least estimate.  `reads`: microseconds that the groups' weights
 // take from memory; a row of tiles past a group's first reads them from the caches, at
-// two and a half times the rate.  Where that is longer than the products it counts in
+// four times the rate.  Where that is longer than the products it counts in
 // their place, and these for a little, between shapes that read alike (57 rows a group
 // of 64, N 4096, K 11008: 64 x 128 tiles, of which many groups need two, 1347 us, 128 x
 // 128 1145).  The smallest tiles only where they make no second round: what bounds such
@@ -199,7 +199,7 @@ int pick(const Cost (&of)[N], int64_t cols, double kts, int cus, double reads, i
         if (c.shape == G_ONE && t * (double)cdiv(cols, c.tn) > (double)cus * c.per_cu)
             continue;
         const double us = tiles_us(c, t, cols, kts, cus);
-        const double all = std::max(us, reads * (1.0 + (t / (double)used - 1.0) * 0.4)) + 0.05 * us;
+        const double all = std::max(us, reads * (1.0 + (t / (double)used - 1.0) * 0.25)) + 0.05 * us;
         if (best < 0 || all < least) {
             best = c.shape;
             least = all;
