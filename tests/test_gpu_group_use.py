@@ -5,6 +5,7 @@ import torch
 
 import dense_gemm_linear_amd as dg
 from group_reference import UBF, U32, bf16, close, make_ids, product, sorted_slots
+from test_gpu_group import _adapter_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -502,3 +503,79 @@ def test_rows_of_most_tokens():
     assert torch.equal(dY[:5], last.flip(0)) and not bool(dw[:-5].any())
     want = (last.double() ** 2).sum(1).cpu()
     close(dw[-5:, 0], want, (D + 2) * U32 * want, "dw")
+
+
+def test_no_row_takes_part():
+    T, k, G, N, K = 70, 2, 3, 72, 40
+    ids = torch.full((T, k), -1).cuda()
+    off, order, place = dg.group_sort(ids, G)
+    X, W, dY = bf16(T, K, seed=1).cuda(), bf16(G, N, K, seed=2).cuda(), bf16(T * k, N, seed=3).cuda()
+    Y = torch.full((T * k, N), MARK).bfloat16().cuda()
+    dg.group_linear(X, W, off, order, slots=k, out=Y)
+    dg.group_linear(X, W, off, order, slots=k, activation="relu", mul=dY, out=Y)
+    dX = torch.full((T * k, K), MARK).bfloat16().cuda()
+    _, dW = dg.group_linear_grad(dY, X, W, off, order, slots=k, dX=dX)
+    assert bool((Y == MARK).all()) and bool((dX == MARK).all()) and not bool(dW.any())
+    assert not bool(dg.group_combine(Y, place).any())
+    dy, dw = dg.group_combine_grad(dY[:T].contiguous(), Y, place, dY=Y.clone())
+    assert bool((dy == MARK).all()) and not bool(dw.any())
+    Xs = torch.full((T * k, K), MARK).bfloat16().cuda()
+    dg.group_gather(X, place, out=Xs)
+    assert bool((Xs == MARK).all())
+    for rows in (1, 20, 70):
+        off, order, _ = dg.group_sort(ids[:rows, :1].contiguous(), G)
+        A, B = bf16(G, 16, K, seed=4).cuda(), bf16(G, N, 16, seed=5).cuda()
+        got = dg.linear_adapters(X[:rows], W[0], A, B, off, order)
+        close(got, *product(X[:rows].cpu(), W[0].cpu()), "Y")
+
+
+@pytest.mark.parametrize("T,k,G,N,K", [(3, 2, 2, 2 ** 20, 8), (2, 1, 2, 8, 2 ** 16), (130, 1, 2, 2 ** 16, 8),
+                                       (150, 2, 2, 8, 2 ** 16)])
+def test_widest(T, k, G, N, K):
+    _say("widest", T, k, G, N, K)
+    ids = make_ids(T, k, G, T)
+    off, order, place = sorted_slots(ids, G)
+    n = int(off[-1])
+    X, W = bf16(T, K, seed=1), bf16(G, N, K, seed=2, scale=K ** -0.5)
+    dev = X.cuda(), W.cuda(), off.cuda(), order.cuda()
+    Y = dg.group_linear(*dev, slots=k)
+    rows = order[:n].long() // k
+    group = torch.bucketize(torch.arange(n), off[1:].long(), right=True)
+    for g in range(G):
+        at = torch.nonzero(group == g)[:, 0]
+        close(Y[at.cuda()], *product(X[rows[at]], W[g]), f"Y of group {g}")
+    if N > 2 ** 16:
+        return
+    dY = bf16(T * k, N, seed=3)
+    dX, dW = dg.group_linear_grad(dY.cuda(), *dev, slots=k)
+    for g in range(G):
+        at = torch.nonzero(group == g)[:, 0]
+        close(dX[at.cuda()], *product(dY[at], W[g].t()), f"dX of group {g}")
+        close(dW[g], *product(dY[at].t(), X[rows[at]].t()), f"dW of group {g}")
+
+
+def test_widest_rows():
+    T, k, G, D = 3, 2, 2, 2 ** 20
+    ids = make_ids(T, k, G, 1)
+    off, order, place = sorted_slots(ids, G)
+    n = int(off[-1])
+    X = bf16(T, 2 * D, seed=1).cuda().view(torch.float32)
+    Xs = dg.group_gather(X, place.cuda())
+    assert torch.equal(Xs[:n].view(torch.int32), X.view(torch.int32)[(order[:n].long() // k).cuda()])
+    Y, w = bf16(T * k, D, seed=2), torch.rand(T, k)
+    out = dg.group_combine(Y.cuda(), place.cuda(), w.cuda())
+    terms = torch.where((place >= 0)[:, :, None], Y[place.clamp(min=0).long()].double(), 0.0) * w.double()[:, :, None]
+    close(out, terms.sum(1), UBF * terms.sum(1).abs() + k * U32 * terms.abs().sum(1), "out")
+
+
+def test_adapters_of_most_rows():
+    T, G, N, K, R = 2 ** 20, 512, 72, 64, 8
+    ids = make_ids(T, 1, G, 5)
+    X, W = bf16(T, K, seed=1), bf16(N, K, seed=2, scale=K ** -0.5)
+    A, B = bf16(G, R, K, seed=3, scale=K ** -0.5), bf16(G, N, R, seed=4, scale=0.3)
+    scale = torch.rand(G, generator=torch.Generator().manual_seed(5))
+    off, order, _ = dg.group_sort(ids.cuda(), G)
+    Y = dg.linear_adapters(X.cuda(), W.cuda(), A.cuda(), B.cuda(), off, order, scale=scale.cuda())
+    some = torch.cat([torch.arange(300), torch.arange(T // 2, T // 2 + 300), torch.arange(T - 300, T)])
+    o, p, _ = sorted_slots(ids[some], G)
+    close(Y[some.cuda()], *_adapter_reference(X[some], W, A, B, scale, o, p), "Y")
