@@ -1,5 +1,6 @@
 // Kernels of linear_adapters beside the grouped product: the inner values of rows
-// that many requests' adapters have, and the whole of it for one token.
+// that many requests' adapters have, the whole of it for one token, and for few
+// rows in slices of K.
 #pragma once
 
 #include "group_kernels.hpp"
@@ -192,7 +193,7 @@ __device__ __forceinline__ float lanes_sum(float x)
     return x;
 }
 
-// The same for a decode batch: a workgroup a row and 16 ranks, a wave a rank, 512
+// The same for few rows: a workgroup a row and 16 ranks, a wave a rank, 512
 // values of K at a time over its lanes.  The row's group is found by counting the
 // offsets in front.  48 rows of 16 adapters of 16 ranks, K 4096: 4.3 us, 6.2 with the
 // kernel above.
@@ -317,6 +318,263 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_token_kernel(TokenArgs p)
         const float y = lanes_sum(acc[i]);
         if (lane == 0 && n0 + i < p.N)
             p.Y[n0 + i] = bf16_rne(y);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: W x over slices of K, so that all CUs read W, with the inner values
+// formed by further workgroups of the same launch; a second launch adds the slices
+// and the adapters' terms.  A CU's loads bring 45 to 60 KB a microsecond into LDS
+// whatever the tile, and without slices a decode batch has too few tiles (48 rows of
+// 11008 x 4096, 16 adapters of 16 ranks: 35.2 -> 28.4 us; 40 of 4096 x 4096 24.7 -> 16.7).
+struct SplitArgs {
+    const uint8_t* X;
+    int64_t ldx_b;
+    const uint8_t* W;
+    int64_t ldw_b;
+    int T, N, K;
+    int tiles_m, slices, kts;      // kts: k-tiles a slice
+    int main;                      // workgroups of the product; behind them the inner values'
+    int nt;                        // W is read once
+    float* planes;                 // [slices][T][pitch]
+    int pitch;
+    // inner values
+    const int* offsets;
+    const int* order;
+    int groups, R;
+    const uint8_t* A;
+    int64_t lda_b, a_group;
+    const float* scale;
+    float* U;                      // [T][R], by sorted position
+};
+
+// A workgroup a row and 16 ranks, a wave four of them, 512 values of K at a time over
+// its lanes.
+__device__ __forceinline__ void split_inner(const SplitArgs& p, int b, int wave, int lane)
+{
+    const int per_row = (p.R + 15) / 16;
+    const int at = b / per_row, r0 = b % per_row * 16 + wave * 4;
+    const uint32_t row = (uint32_t)__builtin_amdgcn_readfirstlane(p.order[at]);
+    const int group = row_group(p.offsets, p.groups, at, lane);
+    if (group >= p.groups || r0 >= p.R || row >= (uint32_t)p.T)
+        return;
+    const rsrc_t rx = make_rsrc(uniform(p.X + row * p.ldx_b), (uint32_t)p.K * 2u);
+    // (R is a multiple of 8: all four are there)
+    const uint8_t* a = p.A + group * p.a_group + r0 * p.lda_b;
+    rsrc_t ra[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        ra[r] = make_rsrc(uniform(a + r * p.lda_b), (uint32_t)p.K * 2u);
+    constexpr int UN = 2;
+    float sum[4] = {};
+    for (int k0 = lane * 16; k0 < p.K * 2 + lane * 16; k0 += 1024 * UN) {
+        i32x4 x[UN], w[UN][4];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const uint32_t off = (uint32_t)(k0 + 1024 * u);          // (past K: zeros)
+            x[u] = load16(rx, off);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                w[u][r] = load16(ra[r], off);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                sum[r] = dot8(w[u][r], x[u], sum[r]);
+    }
+    const float scale = p.scale ? p.scale[group] : 1.f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float v = lanes_sum(sum[r]);
+        if (lane == 0)
+            p.U[(int64_t)at * p.R + r0 + r] = v * scale;
+    }
+}
+
+template <class S>
+__global__ __launch_bounds__(S::THREADS, S::OCC) void adapter_split_kernel(SplitArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::OUT_AT];
+    using AT = Atom<DT_BF16, 16>;
+    using KTL = KTile<S::KTB>;
+    using acc_t = AT::acc_t;
+    constexpr int TM = S::TM, TN = S::TN, WN = S::WN, R = 16, KTB = S::KTB, WAVES = S::WAVES, ST = S::ST;
+    constexpr int MR = S::MR, NR = S::NR, A_DMA = S::A_DMA, B_DMA = S::B_DMA, A_BUF = S::A_BUF, STAGE = S::STAGE;
+    constexpr int STEPS = KTB / 64;
+    static_assert(WAVES == 4, "split_inner's ranks");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    if ((int)blockIdx.x >= p.main) {
+        split_inner(p, (int)blockIdx.x - p.main, wave, lane);
+        return;
+    }
+    const int wm = wave / WN, wn = wave % WN;
+    const int lc = lane & 15, lg = lane >> 4;
+    const int t = xcd_remap((int)blockIdx.x, p.main);
+    const int tm = t % p.tiles_m, slice = t / p.tiles_m % p.slices, tn = t / p.tiles_m / p.slices;
+    const int m0 = tm * TM, n0 = tn * TN, k0 = slice * p.kts * KTB;
+    const int rows = min(TM, p.T - m0), cols = min(TN, p.N - n0);
+    const int kb_end = min(p.K * 2 - k0, p.kts * KTB), nkt = (kb_end + KTB - 1) / KTB, last_full = kb_end / KTB;
+    const uint8_t* a_base = uniform(p.X + (int64_t)m0 * p.ldx_b + k0);
+    const uint8_t* b_base = uniform(p.W + (int64_t)n0 * p.ldw_b + k0);
+    const int a_span = (rows - 1) * (int)p.ldx_b + kb_end, b_span = (cols - 1) * (int)p.ldw_b + kb_end;
+    constexpr int ROWS = WAVES * 1024 / KTB;           // between two chunks of a wave
+    static_assert(ROWS % 16 == 0, "swizzles repeat");
+    const int a_rows = ROWS * (int)p.ldx_b, b_rows = ROWS * (int)p.ldw_b;
+    const ADma da = a_dma_lane<KTB>(wave, lane, p.ldx_b), db = a_dma_lane<KTB>(wave, lane, p.ldw_b);
+    auto load = [&](int kt, int stage, int part, int nparts, auto nomask_c) __attribute__((always_inline)) {
+        constexpr bool NOMASK = decltype(nomask_c)::value;
+        uint8_t* to = lds + stage * STAGE + wave * 1024;
+        auto offset = [&](const ADma& d) __attribute__((always_inline)) {
+            if constexpr (NOMASK)
+                return d.goff;
+            return (int)((uint32_t)kt * KTB + d.col) < kb_end ? d.goff + (uint32_t)kt * KTB : kOOB;
+        };
+        const uint32_t soff = NOMASK ? (uint32_t)kt * KTB : 0u;
+#pragma unroll
+        for (int i = 0; i < A_DMA; ++i)
+            if (i % nparts == part)
+                dma16(make_rsrc(a_base + i * a_rows, (uint32_t)max(a_span - i * a_rows, 0)), to + WAVES * i * 1024,
+                      offset(da), soff);
+#pragma unroll
+        for (int i = 0; i < B_DMA; ++i)
+            if ((A_DMA + i) % nparts == part) {
+                const rsrc_t r = make_rsrc(b_base + i * b_rows, (uint32_t)max(b_span - i * b_rows, 0));
+                if (p.nt)
+                    dma16_nt(r, to + A_BUF + WAVES * i * 1024, offset(db), soff);
+                else
+                    dma16(r, to + A_BUF + WAVES * i * 1024, offset(db), soff);
+            }
+    };
+    const uint32_t swz = KTL::key((uint32_t)lc);
+    const uint32_t row0 = (uint32_t)(wm * (TM / S::WM)), col0 = (uint32_t)(wn * S::WCOLS);
+    LdsBases<S::OUT_AT> a_at[STEPS], b_at[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const uint32_t chunk = ((uint32_t)AT::a_chunk(s, lane, 0) ^ swz) << 4;
+        a_at[s].init((row0 + (uint32_t)lc) * KTB + chunk);
+        b_at[s].init((col0 + (uint32_t)lc) * KTB + chunk);
+    }
+    i32x4 af[frag_sets(ST, STEPS)][MR], bf[frag_sets(ST, STEPS)][NR];
+    acc_t acc[MR][NR];
+#pragma unroll
+    for (int mi = 0; mi < MR; ++mi)
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+            acc[mi][j] = zero_acc<AT>();
+    auto read = [&](int stage, int s, int set, int g, int G) __attribute__((always_inline)) {
+        constexpr int NF = MR + NR;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            if (f * G / NF != g)
+                continue;
+            if (f < NR)
+                bf[set][f] = *reinterpret_cast<const i32x4*>(
+                    lds + b_at[s].at((uint32_t)(stage * STAGE + A_BUF + f * R * KTB)));
+            else
+                af[set][f - NR] = *reinterpret_cast<const i32x4*>(
+                    lds + a_at[s].at((uint32_t)(stage * STAGE + (f - NR) * R * KTB)));
+        }
+    };
+    auto mma = [&](int, int, int set, int g, int G) __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < MR * NR; ++a)
+            if (a * G / (MR * NR) == g)
+                acc[a / NR][a % NR] = mfma_bf16(bf[set][a % NR], af[set][a / NR], acc[a / NR][a % NR]);
+    };
+    k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR)>(nkt, min(nkt, last_full), load, read, mma);
+    // a lane holds four consecutive columns of a row; the pitch is a multiple of 4
+    float* to = p.planes + ((int64_t)slice * p.T + m0) * p.pitch;
+#pragma unroll
+    for (int mi = 0; mi < MR; ++mi)
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const int r = (int)row0 + mi * R + lc, c = n0 + (int)col0 + j * R + 4 * lg;
+            if (r < rows && c < p.pitch)
+                *reinterpret_cast<f32x4*>(to + (int64_t)r * p.pitch + c) = acc[mi][j];
+        }
+}
+
+struct JoinArgs {
+    const float* planes;
+    int slices, T, N, pitch;
+    const int* offsets;
+    const int* order;
+    int groups, R;
+    const float* U;
+    const uint16_t* B;
+    int64_t ldb, b_group;
+    uint16_t* Y;
+    int64_t ldy;
+};
+
+// y = the sum of the slices, in their order, and u B^T.  A workgroup 256 columns of four
+// rows, a thread a column, with its NP pieces of 8 ranks of B in registers for as long as
+// the rows are of one adapter.
+constexpr int kJoinRows = 4;
+template <int NP>
+__global__ __launch_bounds__(256) void adapter_join_kernel(JoinArgs p)
+{
+    __shared__ __attribute__((aligned(16))) float u[kJoinRows][8 * NP];
+    const int at = (int)blockIdx.x * kJoinRows, lane = threadIdx.x & 63;
+    int token[kJoinRows], group[kJoinRows];
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+        token[i] = at + i < p.T ? __builtin_amdgcn_readfirstlane(p.order[at + i]) : -1;
+        group[i] = at + i < p.T ? row_group(p.offsets, p.groups, at + i, lane) : p.groups;
+    }
+    static_assert(kJoinRows * 8 * NP <= 256, "a thread a rank");
+    const int ui = (int)threadIdx.x / (8 * NP), ur = (int)threadIdx.x % (8 * NP);
+    if (ui < kJoinRows && at + ui < p.T && ur < p.R)
+        u[ui][ur] = p.U[(int64_t)(at + ui) * p.R + ur];
+    __syncthreads();
+    const int c = (int)blockIdx.y * 256 + (int)threadIdx.x;
+    if (c >= p.N)
+        return;
+    const int64_t step = (int64_t)p.T * p.pitch;
+    float sum[kJoinRows] = {};
+    for (int s0 = 0; s0 < p.slices; s0 += 4) {
+        float v[kJoinRows][4];
+#pragma unroll
+        for (int i = 0; i < kJoinRows; ++i) {
+            const float* from = p.planes + (int64_t)((uint32_t)token[i] < (uint32_t)p.T ? token[i] : 0) * p.pitch + c;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                v[i][s] = from[min(s0 + s, p.slices - 1) * step];
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinRows; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                sum[i] += s0 + s < p.slices ? v[i][s] : 0.f;
+    }
+    i32x4 w[NP] = {};
+    int held = -1;
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+        if ((uint32_t)token[i] >= (uint32_t)p.T)
+            continue;
+        if (group[i] < p.groups) {
+            if (group[i] != held) {
+                held = group[i];
+                const uint16_t* b = p.B + held * p.b_group + c * p.ldb;
+#pragma unroll
+                for (int q = 0; q < NP; ++q)
+                    if (8 * q < p.R)
+                        w[q] = *reinterpret_cast<const i32x4*>(b + 8 * q);
+            }
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+                if (8 * q < p.R)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum[i] = fmaf(u[i][8 * q + 2 * e], __uint_as_float((uint32_t)w[q][e] << 16), sum[i]);
+                        sum[i] = fmaf(u[i][8 * q + 2 * e + 1], __uint_as_float((uint32_t)w[q][e] & 0xFFFF0000u), sum[i]);
+                    }
+        }
+        p.Y[token[i] * p.ldy + c] = bf16_rne(sum[i]);
     }
 }
 

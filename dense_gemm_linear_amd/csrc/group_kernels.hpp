@@ -804,8 +804,8 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                 // A few rows and ranks: a thread takes a column of B at a time, the lanes of
                 // a wave neighbouring ones, whose ranks lie together in memory, for each row
                 // with its own adapter.  Sums in fp32 through LDS into the accumulators'
-                // layout.  (48 rows of 16 adapters of 16 ranks: 4 us; by matrix steps, below,
-                // of which every adapter takes one in all 64 rows, 9.)
+                // layout.  (48 rows of 16 adapters of 16 ranks in 64 x 64 tiles: 4 us; by matrix
+                // steps, below, of which every adapter takes one in all 64 rows, 9.)
                 const KernelArgs q = kernel_args();
                 float* delta = reinterpret_cast<float*>(lds);                  // [TM][TN + 4]
                 float* u_lds = delta + TM * (TN + 4);                          // [TM][32]

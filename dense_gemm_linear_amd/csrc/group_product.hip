@@ -189,21 +189,22 @@ double row_tiles(int64_t rows, int64_t used, int tm)
 // 128 1145).  The smallest tiles only where they make no second round: what bounds such
 // a product is reading W, which they do less well (16 x 2 rows of 8 groups of 4096 x
 // 4096: 51 us against 44).
+struct Picked {
+    int shape;
+    double us;
+};
 template <int N, class Tiles>
-int pick(const Cost (&of)[N], int64_t cols, double kts, int cus, double reads, int64_t used, Tiles&& tiles)
+Picked pick(const Cost (&of)[N], int64_t cols, double kts, int cus, double reads, int64_t used, Tiles&& tiles)
 {
-    int best = -1;
-    double least = 0.0;
+    Picked best = {-1, 0.0};
     for (const Cost& c : of) {
         const double t = tiles(c.tm);
         if (c.shape == G_ONE && t * (double)cdiv(cols, c.tn) > (double)cus * c.per_cu)
             continue;
         const double us = tiles_us(c, t, cols, kts, cus);
         const double all = std::max(us, reads * (1.0 + (t / (double)used - 1.0) * 0.25)) + 0.05 * us;
-        if (best < 0 || all < least) {
-            best = c.shape;
-            least = all;
-        }
+        if (best.shape < 0 || all < best.us)
+            best = {c.shape, all};
     }
     return best;
 }
@@ -233,9 +234,17 @@ int vec_of(const uint16_t* C, int64_t ldc, int64_t N)
 
 }  // namespace
 
+// Adapters in slices of K: rows and ranks at most, and what the workspace holds for
+// the slices' sums.
+constexpr int64_t kSplitRows = 512, kSplitRank = 64, kSplitBytes = INT64_C(32) << 20;
+static int64_t inner_bytes(int64_t T, int64_t R) { return cdiv(T * R * 4, 256) * 256; }
+
 int64_t group_grad_workspace(int64_t T, int64_t k, int64_t K) { return T * k * K * 2; }
 
-int64_t adapters_workspace(int64_t T, int64_t R) { return T * R * 4; }
+int64_t adapters_workspace(int64_t T, int64_t R)
+{
+    return inner_bytes(T, R) + (T > 1 && T <= kSplitRows && R <= kSplitRank ? kSplitBytes : 0);
+}
 
 hipError_t group_forward(const ProductCall& c)
 {
@@ -258,7 +267,7 @@ hipError_t group_forward(const ProductCall& c)
     a.mul_vec = ((uintptr_t)c.mul & 7u) == 0 && c.ld_mul % 4 == 0 && c.N % 4 == 0;
     a.b_nt = 1;
     const int shape = pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus, weights_us(used, c.N, c.K), used,
-                           [&](int tm) { return row_tiles(S, used, tm); });
+                           [&](int tm) { return row_tiles(S, used, tm); }).shape;
     return c.act || c.mul ? launch_group_gated(shape, a, used, c.cus, c.stream)
                           : launch_group_fwd(shape, a, used, c.cus, c.stream);
 }
@@ -280,7 +289,7 @@ hipError_t group_backward(const ProductCall& c)
         a.c_vec = vec_of(c.dX, c.lddx, c.K);
         a.b_nt = 1;
         const int shape = pick(kDx, c.K, (double)cdiv(c.N, 32), c.cus, weights_us(used, c.N, c.K), used,
-                               [&](int tm) { return row_tiles(S, used, tm); });
+                               [&](int tm) { return row_tiles(S, used, tm); }).shape;
         const hipError_t e = launch_group_dx(shape, a, used, c.cus, c.stream);
         if (e != hipSuccess)
             return e;
@@ -325,7 +334,7 @@ hipError_t group_backward(const ProductCall& c)
     if (a.c_vec)
         a.c_vec = 2;
     const int shape = pick(kDw, c.K, (double)cdiv(cdiv(S, c.groups), 32), c.cus, 0.0, 1,
-                           [&](int tm) { return (double)(c.groups * cdiv(c.N, tm)); });
+                           [&](int tm) { return (double)(c.groups * cdiv(c.N, tm)); }).shape;
     return launch_group_dw(shape, a, 0, c.cus, c.stream);
 }
 
@@ -372,6 +381,99 @@ hipError_t launch_inner(const InnerArgs& i, int cus, hipStream_t s)
                   512, i, s);
 }
 
+// tiles of the slices
+using SLow = GroupShape<32, 128, 1, 4, 3, 128, 2>;
+using SFew = GroupShape<64, 128, 1, 4, 3, 128, 2>;
+using SMid = GroupShape<128, 128, 2, 2, 4, 128, 2>;
+
+// Few rows: tile rows and slices of the least estimate, in microseconds: a CU's
+// k-tiles of 64 values one after the other, W, the slices' sums, what the inner values
+// read and what the join reads of B.  Fitted to 356 times (2 to 512 rows, N 512 to
+// 11008, K 1024 to 11008, 8 to 64 ranks); the choice takes 4 % longer than the best of
+// these on average, 18 % at most.
+struct AdapterPlan {
+    int tm;
+    int64_t slices;
+    double us;
+};
+AdapterPlan adapter_plan(int64_t T, int64_t N, int64_t K, int64_t R, int cus)
+{
+    constexpr struct {
+        int tm;
+        double kt;                 // for each byte of a k-tile
+    } shapes[] = {{SLow::TM, 7.5e-6}, {SFew::TM, 7.0e-6}, {SMid::TM, 8.5e-6}};
+    AdapterPlan best = {0, 0, 0.0};
+    const int64_t kts = cdiv(K, 64), sums = T * cdiv(N, 4) * 16;
+    const double rest = 5.7 + 0.154e-6 * (double)(N * K * 2) + 0.088e-6 * (double)(T * cdiv(R, 16) * 20 * K * 2) +
+                        0.33e-6 * (double)(cdiv(T, kJoinRows) * N * R * 2);
+    for (const auto& sh : shapes) {
+        const int64_t tiles = cdiv(T, sh.tm) * cdiv(N, SLow::TN);
+        const double kt = sh.kt * (double)((std::min<int64_t>(T, sh.tm) + SLow::TN) * 128);
+        for (int64_t most = 1; most <= 8 && most * sums <= kSplitBytes; ++most) {
+            const int64_t each = cdiv(kts, most), slices = cdiv(kts, each);
+            const double us = rest + kt * (double)(cdiv(tiles * slices, cus) * each) + 0.257e-6 * (double)(slices * sums);
+            if (!best.tm || us < best.us)
+                best = {sh.tm, slices, us};
+        }
+    }
+    return best;
+}
+
+template <class S>
+hipError_t go_split(const ProductCall& c, int64_t slices)
+{
+    const int64_t T = c.T, kts = cdiv(c.K * 2, S::KTB);
+    SplitArgs a;
+    a.X = reinterpret_cast<const uint8_t*>(c.X);
+    a.ldx_b = c.ldx * 2;
+    a.W = reinterpret_cast<const uint8_t*>(c.W);
+    a.ldw_b = c.ldw * 2;
+    a.T = (int)T;
+    a.N = (int)c.N;
+    a.K = (int)c.K;
+    a.tiles_m = (int)cdiv(T, S::TM);
+    a.kts = (int)cdiv(kts, slices);
+    a.slices = (int)cdiv(kts, a.kts);
+    a.main = (int)(a.tiles_m * a.slices * cdiv(c.N, S::TN));
+    a.nt = a.tiles_m == 1;
+    a.planes = reinterpret_cast<float*>(c.ws + inner_bytes(T, c.R));
+    a.pitch = (int)cdiv(c.N, 4) * 4;
+    a.offsets = c.offsets;
+    a.order = c.order;
+    a.groups = (int)c.groups;
+    a.R = (int)c.R;
+    a.A = reinterpret_cast<const uint8_t*>(c.A);
+    a.lda_b = c.lda * 2;
+    a.a_group = c.lda_group * 2;
+    a.scale = c.scale;
+    a.U = reinterpret_cast<float*>(c.ws);
+    const hipError_t e = launch(reinterpret_cast<const void*>(&adapter_split_kernel<S>),
+                                dim3((unsigned)(a.main + T * cdiv(c.R, 16))), S::THREADS, a, c.stream);
+    if (e != hipSuccess)
+        return e;
+    JoinArgs j;
+    j.planes = a.planes;
+    j.slices = a.slices;
+    j.T = a.T;
+    j.N = a.N;
+    j.pitch = a.pitch;
+    j.offsets = c.offsets;
+    j.order = c.order;
+    j.groups = a.groups;
+    j.R = a.R;
+    j.U = a.U;
+    j.B = c.B;
+    j.ldb = c.ldb;
+    j.b_group = c.ldb_group;
+    j.Y = c.Y;
+    j.ldy = c.ldy;
+    static_assert(kSplitRank <= 8 * 8, "the join's instances");
+    const void* join = c.R <= 16   ? reinterpret_cast<const void*>(&adapter_join_kernel<2>)
+                       : c.R <= 32 ? reinterpret_cast<const void*>(&adapter_join_kernel<4>)
+                                   : reinterpret_cast<const void*>(&adapter_join_kernel<8>);
+    return launch(join, dim3((unsigned)cdiv(T, kJoinRows), (unsigned)cdiv(c.N, 256)), 256, j, c.stream);
+}
+
 hipError_t adapters_forward(const ProductCall& c)
 {
     const int64_t T = c.T;
@@ -401,6 +503,22 @@ hipError_t adapters_forward(const ProductCall& c)
                              : rows == 3 ? reinterpret_cast<const void*>(&adapter_token_kernel<3, WAVES>)
                                          : reinterpret_cast<const void*>(&adapter_token_kernel<4, WAVES>);
         return launch(kernel, dim3((unsigned)cdiv(c.N, rows * WAVES)), 64 * WAVES, t, c.stream);
+    }
+    // every row counts, groups or not; the ranks as k-tiles of about as many adapters
+    // as a tile of 64 rows has
+    const int64_t near = std::min<int64_t>(std::min(c.groups, T), cdiv(std::min(c.groups, T) * 64, T) + 1);
+    const double kts = (double)cdiv(c.K, 32) + (double)(near * cdiv(c.R, 16));
+    const Picked whole = pick(kAdapt, c.N, kts, c.cus, 0.0, 1, [&](int tm) { return (double)cdiv(T, tm); });
+    // In slices of K where that takes less: the whole product has the inner values in a
+    // launch before it, and its ranks.  16 ranks: 48 rows of 11008 x 4096 26.6 us against
+    // 35.5, 40 of 4096 x 4096 14.7 against 24.7, 300 of them 26.8 against 32.1; 400 of
+    // 11008 x 4096 82 against 77.
+    if (T <= kSplitRows && c.R <= kSplitRank) {
+        const AdapterPlan s = adapter_plan(T, c.N, c.K, c.R, c.cus);
+        if (s.tm && s.us < 7.3 + 1.05 * whole.us)
+            return s.tm == SLow::TM   ? go_split<SLow>(c, s.slices)
+                   : s.tm == SFew::TM ? go_split<SFew>(c, s.slices)
+                                      : go_split<SMid>(c, s.slices);
     }
     const uint32_t x_bytes = (uint32_t)((T - 1) * c.ldx * 2 + c.K * 2);
     InnerArgs i;
@@ -438,12 +556,7 @@ hipError_t adapters_forward(const ProductCall& c)
     a.ldlb_b = c.ldb * 2;
     a.lb_group = c.ldb_group * 2;
     a.R = (int)c.R;
-    // every row counts, groups or not; the ranks as k-tiles of about as many adapters
-    // as a tile of 64 rows has
-    const int64_t near = std::min<int64_t>(std::min(c.groups, T), cdiv(std::min(c.groups, T) * 64, T) + 1);
-    const double kts = (double)cdiv(c.K, 32) + (double)(near * cdiv(c.R, 16));
-    const int shape = pick(kAdapt, c.N, kts, c.cus, 0.0, 1, [&](int tm) { return (double)cdiv(T, tm); });
-    return launch_group_adapt(shape, a, 0, c.cus, c.stream);
+    return launch_group_adapt(whole.shape, a, 0, c.cus, c.stream);
 }
 
 #endif

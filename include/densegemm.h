@@ -677,7 +677,7 @@ gemm_status group_combine_grad(const uint16_t* dout, int64_t ld_dout, const uint
  *     Y[t] = X[t] W^T + scale[g] (X[t] A_g^T) B_g^T
  * for the slots t = order[p] of group g, and Y[t] = X[t] W^T for the others: order is
  * a permutation of the T tokens, as group_sort writes it for k = 1.  The inner values
- * X A^T are kept in two bf16 halves (16 bits); sums in fp32, rounded once.
+ * X A^T are kept in fp32 or in two bf16 halves (16 bits); sums in fp32, rounded once.
  *   W   device bf16 [N, ldw], A [groups][R][lda], B [groups][N][ldb], as W above; R a
  *       multiple of 8 up to 256 (adapters of lower rank end in zeros).
  *   scale  device fp32 [groups], NULL: 1.

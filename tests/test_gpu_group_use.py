@@ -5,7 +5,7 @@ import torch
 
 import dense_gemm_linear_amd as dg
 from group_reference import UBF, U32, bf16, close, make_ids, product, sorted_slots
-from test_gpu_group import _adapter_reference
+from test_gpu_group import _adapter_reference, test_adapters as check_adapters
 
 pytestmark = pytest.mark.gpu
 
@@ -579,3 +579,15 @@ def test_adapters_of_most_rows():
     some = torch.cat([torch.arange(300), torch.arange(T // 2, T // 2 + 300), torch.arange(T - 300, T)])
     o, p, _ = sorted_slots(ids[some], G)
     close(Y[some.cuda()], *_adapter_reference(X[some], W, A, B, scale, o, p), "Y")
+
+
+# T, groups, N, K, R: few rows in slices of K and just too many for them, ranks around 16,
+# 32 and 64, widths that are no multiple of 4
+@pytest.mark.parametrize("T,groups,N,K,R", [(2, 2, 130, 8200, 8), (5, 3, 1001, 4104, 16), (33, 5, 600, 4104, 24),
+                                            (65, 70, 129, 8200, 40), (130, 9, 1000, 2056, 64), (300, 4, 2050, 1000, 16),
+                                            (512, 3, 264, 1032, 64), (513, 3, 264, 1032, 64), (100, 4, 3, 2056, 32),
+                                            (200, 512, 257, 1032, 72), (520, 3, 1000, 72, 16), (600, 20, 264, 136, 32),
+                                            (900, 512, 72, 40, 24)])
+def test_adapters_in_slices(T, groups, N, K, R):
+    check_adapters(T, groups, N, K, R, "random", True)
+    check_adapters(T, groups, N, K, R, "runs", False)
