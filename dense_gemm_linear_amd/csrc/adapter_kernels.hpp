@@ -511,13 +511,13 @@ struct JoinArgs {
 };
 
 // y = the sum of the slices, in their order, and u B^T.  A workgroup 256 columns of four
-// rows, a thread a column, with its NP pieces of 8 ranks of B in registers for as long as
-// the rows are of one adapter.
+// rows, a thread a column, with NP pieces of 8 ranks of B at a time, in registers for as
+// long as the rows are of one adapter.
 constexpr int kJoinRows = 4;
 template <int NP>
 __global__ __launch_bounds__(256) void adapter_join_kernel(JoinArgs p)
 {
-    __shared__ __attribute__((aligned(16))) float u[kJoinRows][8 * NP];
+    __shared__ __attribute__((aligned(16))) float u[kJoinRows][kMaxRank];
     const int at = (int)blockIdx.x * kJoinRows, lane = threadIdx.x & 63;
     int token[kJoinRows], group[kJoinRows];
 #pragma unroll
@@ -525,10 +525,8 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(JoinArgs p)
         token[i] = at + i < p.T ? __builtin_amdgcn_readfirstlane(p.order[at + i]) : -1;
         group[i] = at + i < p.T ? row_group(p.offsets, p.groups, at + i, lane) : p.groups;
     }
-    static_assert(kJoinRows * 8 * NP <= 256, "a thread a rank");
-    const int ui = (int)threadIdx.x / (8 * NP), ur = (int)threadIdx.x % (8 * NP);
-    if (ui < kJoinRows && at + ui < p.T && ur < p.R)
-        u[ui][ur] = p.U[(int64_t)(at + ui) * p.R + ur];
+    for (int i = (int)threadIdx.x; i < min(kJoinRows, p.T - at) * p.R; i += 256)
+        u[i / p.R][i % p.R] = p.U[(int64_t)at * p.R + i];
     __syncthreads();
     const int c = (int)blockIdx.y * 256 + (int)threadIdx.x;
     if (c >= p.N)
@@ -550,32 +548,36 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(JoinArgs p)
             for (int s = 0; s < 4; ++s)
                 sum[i] += s0 + s < p.slices ? v[i][s] : 0.f;
     }
-    i32x4 w[NP] = {};
-    int held = -1;
+    for (int r0 = 0; r0 < p.R; r0 += 8 * NP) {
+        i32x4 w[NP] = {};
+        int held = -1;
 #pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) {
-        if ((uint32_t)token[i] >= (uint32_t)p.T)
-            continue;
-        if (group[i] < p.groups) {
+        for (int i = 0; i < kJoinRows; ++i) {
+            if (group[i] >= p.groups)
+                continue;
             if (group[i] != held) {
                 held = group[i];
-                const uint16_t* b = p.B + held * p.b_group + c * p.ldb;
+                const uint16_t* b = p.B + held * p.b_group + c * p.ldb + r0;
 #pragma unroll
                 for (int q = 0; q < NP; ++q)
-                    if (8 * q < p.R)
+                    if (r0 + 8 * q < p.R)
                         w[q] = *reinterpret_cast<const i32x4*>(b + 8 * q);
             }
 #pragma unroll
             for (int q = 0; q < NP; ++q)
-                if (8 * q < p.R)
+                if (r0 + 8 * q < p.R)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sum[i] = fmaf(u[i][8 * q + 2 * e], __uint_as_float((uint32_t)w[q][e] << 16), sum[i]);
-                        sum[i] = fmaf(u[i][8 * q + 2 * e + 1], __uint_as_float((uint32_t)w[q][e] & 0xFFFF0000u), sum[i]);
+                        const float* v = &u[i][r0 + 8 * q + 2 * e];
+                        sum[i] = fmaf(v[0], __uint_as_float((uint32_t)w[q][e] << 16), sum[i]);
+                        sum[i] = fmaf(v[1], __uint_as_float((uint32_t)w[q][e] & 0xFFFF0000u), sum[i]);
                     }
         }
-        p.Y[token[i] * p.ldy + c] = bf16_rne(sum[i]);
     }
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i)
+        if ((uint32_t)token[i] < (uint32_t)p.T)
+            p.Y[token[i] * p.ldy + c] = bf16_rne(sum[i]);
 }
 
 }  // namespace dg

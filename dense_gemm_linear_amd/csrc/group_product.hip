@@ -131,24 +131,31 @@ namespace {
 
 // What one round of tiles (every CU holding its fill of workgroups) takes, in
 // microseconds: kt for each 32 values of K, epi for the rest; kt1 where there is at
-// most one workgroup a CU; and start, once.  Fitted to the times of all shapes at 242
+// most one workgroup a CU; start, once; across: how much longer than the others' the
+// k-tiles get where rows of W do not start at whole 64 bytes, so that a piece of a row
+// lies in two lines (32 groups, 25940 rows, N 1776, K 4032 and 4040: 256 x 256 tiles 390
+// and 576 us, 128 x 128 of two stages 432 and 540).  Fitted to the times of all shapes at 242
 // sizes, most drawn at random (1 to 8192 tokens, 1 to 8 choices, 4 to 128 groups, N 256
 // to 11008, K 256 to 11008; 2 to 4095 rows with adapters): the shape chosen takes 2 %
 // longer than the best on average with groups, 1 % with adapters, and 30 % at most
 // (groups of equal size just under a whole tile's rows, which the host cannot see).
 struct Cost {
     int shape, tm, tn, per_cu;
-    double kt, kt1, epi, start;
+    double kt, kt1, epi, start, across;
 };
 template <class S>
-constexpr Cost cost_of(int shape, double kt, double kt1, double epi, double start = 0.0)
+constexpr Cost cost_of(int shape, double kt, double kt1, double epi, double start = 0.0, double across = 1.0)
 {
-    return {shape, S::TM, S::TN, S::PER_CU, kt, kt1, epi, start};
+    return {shape, S::TM, S::TN, S::PER_CU, kt, kt1, epi, start, across};
 }
-constexpr Cost kPlain[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5),          cost_of<GTall>(G_TALL, 0.48, 0.42, 3.8),
-                           cost_of<GLine>(G_LINE, 0.54, 0.37, 2.5),        cost_of<GDeep>(G_DEEP, 0.27, 0.27, 2.3),
-                           cost_of<GSlim>(G_SLIM, 0.20, 0.11, 2.0),        cost_of<GFew>(G_FEW, 0.41, 0.22, 4.6),
-                           cost_of<GFewSlim>(G_FEW_SLIM, 0.21, 0.14, 4.3), cost_of<GLowSlim>(G_LOW_SLIM, 0.17, 0.12, 2.7),
+constexpr Cost kPlain[] = {cost_of<GBig>(G_BIG, 0.74, 0.62, 7.5, 0.0, 1.3),
+                           cost_of<GTall>(G_TALL, 0.48, 0.42, 3.8, 0.0, 1.3),
+                           cost_of<GLine>(G_LINE, 0.54, 0.37, 2.5),
+                           cost_of<GDeep>(G_DEEP, 0.27, 0.27, 2.3, 0.0, 1.1),
+                           cost_of<GSlim>(G_SLIM, 0.20, 0.11, 2.0, 0.0, 1.1),
+                           cost_of<GFew>(G_FEW, 0.41, 0.22, 4.6),
+                           cost_of<GFewSlim>(G_FEW_SLIM, 0.21, 0.14, 4.3),
+                           cost_of<GLowSlim>(G_LOW_SLIM, 0.17, 0.12, 2.7),
                            cost_of<GOne>(G_ONE, 0.11, 0.08, 1.9)};
 constexpr Cost kAdapt[] = {cost_of<GBig>(G_BIG, 0.74, 0.48, 6.6),          cost_of<GTall>(G_TALL, 0.48, 0.42, 4.3),
                            cost_of<GLine>(G_LINE, 0.43, 0.38, 2.5),        cost_of<GDeep>(G_DEEP, 0.28, 0.27, 2.3),
@@ -166,8 +173,10 @@ constexpr Cost kDw[] = {cost_of<GTall>(G_TALL, 0.47, 0.47, 3.9, 4.0), cost_of<GM
 
 // Estimated time of `tiles` rows of tiles over `cols` columns and `kts` times 32
 // values of K.
-double tiles_us(const Cost& c, double tiles, int64_t cols, double kts, int cus)
+double tiles_us(const Cost& c, double tiles, int64_t cols, double kts, int cus, bool across)
 {
+    if (across)
+        kts *= c.across;
     const double items = tiles * (double)cdiv(cols, c.tn), round = (double)cus * c.per_cu;
     const double full = (double)(int64_t)(items / round), left = items - full * round;
     return c.start + full * (kts * c.kt + c.epi) + (left > 0.5 ? kts * (left > cus ? c.kt : c.kt1) + c.epi : 0.0);
@@ -194,14 +203,15 @@ struct Picked {
     double us;
 };
 template <int N, class Tiles>
-Picked pick(const Cost (&of)[N], int64_t cols, double kts, int cus, double reads, int64_t used, Tiles&& tiles)
+Picked pick(const Cost (&of)[N], int64_t cols, double kts, int cus, double reads, int64_t used, bool across,
+            Tiles&& tiles)
 {
     Picked best = {-1, 0.0};
     for (const Cost& c : of) {
         const double t = tiles(c.tm);
         if (c.shape == G_ONE && t * (double)cdiv(cols, c.tn) > (double)cus * c.per_cu)
             continue;
-        const double us = tiles_us(c, t, cols, kts, cus);
+        const double us = tiles_us(c, t, cols, kts, cus, across);
         const double all = std::max(us, reads * (1.0 + (t / (double)used - 1.0) * 0.25)) + 0.05 * us;
         if (best.shape < 0 || all < best.us)
             best = {c.shape, all};
@@ -234,17 +244,18 @@ int vec_of(const uint16_t* C, int64_t ldc, int64_t N)
 
 }  // namespace
 
-// Adapters in slices of K: rows and ranks at most, and what the workspace holds for
-// the slices' sums.
-constexpr int64_t kSplitRows = 512, kSplitRank = 64, kSplitBytes = INT64_C(32) << 20;
+// Adapters in slices of K: rows at most, and what the workspace holds for the
+// slices' sums: 8 slices of 16384 columns, 32 MiB at most.
+constexpr int64_t kSplitRows = 2048;
+static int64_t split_bytes(int64_t T)
+{
+    return T > 1 && T <= kSplitRows ? std::min<int64_t>(T << 19, INT64_C(32) << 20) : 0;
+}
 static int64_t inner_bytes(int64_t T, int64_t R) { return cdiv(T * R * 4, 256) * 256; }
 
 int64_t group_grad_workspace(int64_t T, int64_t k, int64_t K) { return T * k * K * 2; }
 
-int64_t adapters_workspace(int64_t T, int64_t R)
-{
-    return inner_bytes(T, R) + (T > 1 && T <= kSplitRows && R <= kSplitRank ? kSplitBytes : 0);
-}
+int64_t adapters_workspace(int64_t T, int64_t R) { return inner_bytes(T, R) + split_bytes(T); }
 
 hipError_t group_forward(const ProductCall& c)
 {
@@ -266,7 +277,8 @@ hipError_t group_forward(const ProductCall& c)
     a.ld_mul = c.ld_mul;
     a.mul_vec = ((uintptr_t)c.mul & 7u) == 0 && c.ld_mul % 4 == 0 && c.N % 4 == 0;
     a.b_nt = 1;
-    const int shape = pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus, weights_us(used, c.N, c.K), used,
+    const bool across = ((uintptr_t)c.W | (uint64_t)c.ldw * 2 | (uint64_t)c.ldw_group * 2) % 64 != 0;
+    const int shape = pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus, weights_us(used, c.N, c.K), used, across,
                            [&](int tm) { return row_tiles(S, used, tm); }).shape;
     return c.act || c.mul ? launch_group_gated(shape, a, used, c.cus, c.stream)
                           : launch_group_fwd(shape, a, used, c.cus, c.stream);
@@ -288,7 +300,7 @@ hipError_t group_backward(const ProductCall& c)
         a.ldc = c.lddx;
         a.c_vec = vec_of(c.dX, c.lddx, c.K);
         a.b_nt = 1;
-        const int shape = pick(kDx, c.K, (double)cdiv(c.N, 32), c.cus, weights_us(used, c.N, c.K), used,
+        const int shape = pick(kDx, c.K, (double)cdiv(c.N, 32), c.cus, weights_us(used, c.N, c.K), used, false,
                                [&](int tm) { return row_tiles(S, used, tm); }).shape;
         const hipError_t e = launch_group_dx(shape, a, used, c.cus, c.stream);
         if (e != hipSuccess)
@@ -333,7 +345,7 @@ hipError_t group_backward(const ProductCall& c)
     // 2 %, with that kernel they lose up to 5.
     if (a.c_vec)
         a.c_vec = 2;
-    const int shape = pick(kDw, c.K, (double)cdiv(cdiv(S, c.groups), 32), c.cus, 0.0, 1,
+    const int shape = pick(kDw, c.K, (double)cdiv(cdiv(S, c.groups), 32), c.cus, 0.0, 1, false,
                            [&](int tm) { return (double)(c.groups * cdiv(c.N, tm)); }).shape;
     return launch_group_dw(shape, a, 0, c.cus, c.stream);
 }
@@ -409,7 +421,7 @@ AdapterPlan adapter_plan(int64_t T, int64_t N, int64_t K, int64_t R, int cus)
     for (const auto& sh : shapes) {
         const int64_t tiles = cdiv(T, sh.tm) * cdiv(N, SLow::TN);
         const double kt = sh.kt * (double)((std::min<int64_t>(T, sh.tm) + SLow::TN) * 128);
-        for (int64_t most = 1; most <= 8 && most * sums <= kSplitBytes; ++most) {
+        for (int64_t most = 1; most <= 8 && most * sums <= split_bytes(T); ++most) {
             const int64_t each = cdiv(kts, most), slices = cdiv(kts, each);
             const double us = rest + kt * (double)(cdiv(tiles * slices, cus) * each) + 0.257e-6 * (double)(slices * sums);
             if (!best.tm || us < best.us)
@@ -467,7 +479,6 @@ hipError_t go_split(const ProductCall& c, int64_t slices)
     j.b_group = c.ldb_group;
     j.Y = c.Y;
     j.ldy = c.ldy;
-    static_assert(kSplitRank <= 8 * 8, "the join's instances");
     const void* join = c.R <= 16   ? reinterpret_cast<const void*>(&adapter_join_kernel<2>)
                        : c.R <= 32 ? reinterpret_cast<const void*>(&adapter_join_kernel<4>)
                                    : reinterpret_cast<const void*>(&adapter_join_kernel<8>);
@@ -508,12 +519,13 @@ hipError_t adapters_forward(const ProductCall& c)
     // as a tile of 64 rows has
     const int64_t near = std::min<int64_t>(std::min(c.groups, T), cdiv(std::min(c.groups, T) * 64, T) + 1);
     const double kts = (double)cdiv(c.K, 32) + (double)(near * cdiv(c.R, 16));
-    const Picked whole = pick(kAdapt, c.N, kts, c.cus, 0.0, 1, [&](int tm) { return (double)cdiv(T, tm); });
+    const Picked whole = pick(kAdapt, c.N, kts, c.cus, 0.0, 1, false,
+                              [&](int tm) { return (double)cdiv(T, tm); });
     // In slices of K where that takes less: the whole product has the inner values in a
     // launch before it, and its ranks.  16 ranks: 48 rows of 11008 x 4096 26.6 us against
     // 35.5, 40 of 4096 x 4096 14.7 against 24.7, 300 of them 26.8 against 32.1; 400 of
     // 11008 x 4096 82 against 77.
-    if (T <= kSplitRows && c.R <= kSplitRank) {
+    if (T <= kSplitRows) {
         const AdapterPlan s = adapter_plan(T, c.N, c.K, c.R, c.cus);
         if (s.tm && s.us < 7.3 + 1.05 * whole.us)
             return s.tm == SLow::TM   ? go_split<SLow>(c, s.slices)
