@@ -249,7 +249,7 @@ int vec_of(const uint16_t* C, int64_t ldc, int64_t N)
 constexpr int64_t kSplitRows = 2048;
 static int64_t split_bytes(int64_t T)
 {
-    return T > 1 && T <= kSplitRows ? std::min<int64_t>(T << 19, INT64_C(32) << 20) : 0;
+    return T <= kSplitRows ? std::min<int64_t>(T << 19, INT64_C(32) << 20) : 0;
 }
 static int64_t inner_bytes(int64_t T, int64_t R) { return cdiv(T * R * 4, 256) * 256; }
 
@@ -411,9 +411,9 @@ struct AdapterPlan {
 AdapterPlan adapter_plan(int64_t T, int64_t N, int64_t K, int64_t R, int cus)
 {
     constexpr struct {
-        int tm;
+        int tm, start;             // start: in k-tiles
         double kt;                 // for each byte of a k-tile
-    } shapes[] = {{SLow::TM, 7.5e-6}, {SFew::TM, 7.0e-6}, {SMid::TM, 8.5e-6}};
+    } shapes[] = {{SLow::TM, 3, 7.0e-6}, {SFew::TM, 0, 7.0e-6}, {SMid::TM, 0, 8.5e-6}};
     AdapterPlan best = {0, 0, 0.0};
     const int64_t kts = cdiv(K, 64), sums = T * cdiv(N, 4) * 16;
     const double rest = 5.7 + 0.154e-6 * (double)(N * K * 2) + 0.088e-6 * (double)(T * cdiv(R, 16) * 20 * K * 2) +
@@ -423,7 +423,7 @@ AdapterPlan adapter_plan(int64_t T, int64_t N, int64_t K, int64_t R, int cus)
         const double kt = sh.kt * (double)((std::min<int64_t>(T, sh.tm) + SLow::TN) * 128);
         for (int64_t most = 1; most <= 8 && most * sums <= split_bytes(T); ++most) {
             const int64_t each = cdiv(kts, most), slices = cdiv(kts, each);
-            const double us = rest + kt * (double)(cdiv(tiles * slices, cus) * each) + 0.257e-6 * (double)(slices * sums);
+            const double us = rest + kt * (double)(cdiv(tiles * slices, cus) * (each + sh.start)) + 0.257e-6 * (double)(slices * sums);
             if (!best.tm || us < best.us)
                 best = {sh.tm, slices, us};
         }
@@ -488,7 +488,10 @@ hipError_t go_split(const ProductCall& c, int64_t slices)
 hipError_t adapters_forward(const ProductCall& c)
 {
     const int64_t T = c.T;
-    if (T == 1) {
+    // One token in one launch, where that forms the inner values in every workgroup in
+    // little time (4096 x 4096, rank 32: 12 us, in slices 14; rank 64 16 and 14, rank 256 57
+    // and 17; 2048 x 2048, rank 64: 11 and 14).
+    if (T == 1 && c.R * c.K <= 1 << 17) {
         TokenArgs t;
         t.X = c.X;
         t.W = c.W;
@@ -527,7 +530,7 @@ hipError_t adapters_forward(const ProductCall& c)
     // 11008 x 4096 82 against 77.
     if (T <= kSplitRows) {
         const AdapterPlan s = adapter_plan(T, c.N, c.K, c.R, c.cus);
-        if (s.tm && s.us < 7.3 + 1.05 * whole.us)
+        if (s.tm && (T == 1 || s.us < 7.3 + 1.05 * whole.us))
             return s.tm == SLow::TM   ? go_split<SLow>(c, s.slices)
                    : s.tm == SFew::TM ? go_split<SFew>(c, s.slices)
                                       : go_split<SMid>(c, s.slices);

@@ -586,7 +586,8 @@ def test_adapters_of_most_rows():
 @pytest.mark.parametrize("T,groups,N,K,R", [(2, 2, 130, 8200, 8), (5, 3, 1001, 4104, 16), (33, 5, 600, 4104, 24),
                                             (65, 70, 129, 8200, 40), (130, 9, 1000, 2056, 64), (300, 4, 2050, 1000, 16),
                                             (512, 3, 264, 1032, 64), (513, 3, 264, 1032, 64), (100, 4, 3, 2056, 32),
-                                            (2048, 5, 100, 1032, 16), (2049, 5, 100, 1032, 16), (40, 5, 333, 1032, 256),
+                                            (1, 3, 333, 8200, 16), (1, 3, 1001, 1032, 256), (1, 2, 140003, 520, 256),
+                                            (3, 2, 140003, 72, 16), (2048, 5, 100, 1032, 16), (2049, 5, 100, 1032, 16), (40, 5, 333, 1032, 256),
                                             (30, 5, 333, 4104, 136),
                                             (200, 512, 257, 1032, 72), (520, 3, 1000, 72, 16), (600, 20, 264, 136, 32),
                                             (900, 512, 72, 40, 24)])
