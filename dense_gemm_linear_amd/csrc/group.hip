@@ -565,6 +565,14 @@ hipError_t group_sort(const SortCall& c)
     return launch(group_place_kernel, pl.chunks, 1024, c.stream, a);
 }
 
+// Stored past the caches: see kCacheBytes.  Not where rows start inside 64 bytes, whose
+// ends would go to memory as parts of lines (8192 x 8 rows of 2056: gather 78 us, 66 through
+// the caches, gradient 134 and 116; past 1 GB, 7992 a row, 285 and 293, 509 and 537).
+static bool past_caches(const void* rows, int64_t pitch_b, int64_t bytes)
+{
+    return bytes >= kCacheBytes && ((uintptr_t)rows | (uint64_t)pitch_b) % 64 == 0;
+}
+
 hipError_t group_gather(const GatherCall& c)
 {
     GatherArgs a;
@@ -580,7 +588,7 @@ hipError_t group_gather(const GatherCall& c)
     a.ldxs_b = c.ldxs_b;
     if (a.pieces <= 64)
         return launch(group_gather_kernel<64, false>, cdiv(c.T, 4), 256, c.stream, a);
-    if (c.T * c.k * c.row_b < kCacheBytes)
+    if (!past_caches(c.Xs, c.ldxs_b, c.T * c.k * c.row_b))
         return launch(group_gather_kernel<256, false>, c.T, 256, c.stream, a);
     return launch(group_gather_kernel<256, true>, c.T, 256, c.stream, a);
 }
@@ -638,7 +646,7 @@ hipError_t group_combine(const CombineCall& c)
 
 hipError_t group_combine_grad(const CombineCall& c)
 {
-    if (c.T * c.k * c.D * 2 < kCacheBytes)
+    if (!past_caches(c.dY, c.lddy * 2, c.T * c.k * c.D * 2))
         return launch(group_combine_grad_kernel<false>, cdiv(c.T * c.k, 4), 256, c.stream, combine_args(c),
                       divide_by(c.k));
     return launch(group_combine_grad_kernel<true>, cdiv(c.T * c.k, 4), 256, c.stream, combine_args(c),

@@ -342,8 +342,10 @@ hipError_t group_backward(const ProductCall& c)
     // Stored past the caches: an optimizer reads dW when it is long out of them, and the
     // rows of X and dY stay (32 groups of 1024 x 2048: 256 rows a group 84 -> 57 us, 16
     // rows 42 -> 36).  Y and dX, which the next kernel reads, are not: alone they gain 0 to
-    // 2 %, with that kernel they lose up to 5.
-    if (a.c_vec)
+    // 2 %, with that kernel they lose up to 5.  Not where rows start inside 64 bytes: the
+    // ends of a tile's rows would go to memory as parts of lines (15 rows in 62 groups of
+    // 984 x 5528: 357 us, 189 through the caches; of 984 x 5504 159 and 164).
+    if (a.c_vec && ((uintptr_t)c.dW | (uint64_t)c.lddw * 2 | (uint64_t)c.lddw_group * 2) % 64 == 0)
         a.c_vec = 2;
     const int shape = pick(kDw, c.K, (double)cdiv(cdiv(S, c.groups), 32), c.cus, 0.0, 1, false,
                            [&](int tm) { return (double)(c.groups * cdiv(c.N, tm)); }).shape;
