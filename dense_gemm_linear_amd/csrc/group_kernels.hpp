@@ -180,9 +180,9 @@ __device__ __forceinline__ int find_entry(const GroupTable& t, int x, int lane)
 // A wave's block of accumulators as bf16 into rows of C, through its own LDS
 // region, 16 rows at a time: a lane holds four consecutive columns of one row
 // (one 8-byte LDS write) and stores 16-byte pieces of rows, or single elements
-// where C's rows do not allow that.  finish(r, col, v) turns the four sums of row
-// r of the tile, columns col .. col + 3, into outputs; row_of(r) is C's row, or
-// negative: not stored.
+// where C's rows do not allow that.  finish(mi, j, r, col, v) turns the four sums of
+// block (mi, j), row r of the tile, columns col .. col + 3, into outputs; row_of(r) is
+// C's row, or negative: not stored.
 template <int MR, int NR, int SROW, class Finish, class RowOf>
 __device__ __forceinline__ void store_group_block(uint16_t* C, int64_t ldc, int N, int c_vec,
                                                   const f32x4 (&acc)[MR][NR], uint8_t* stage, int row0,
@@ -196,7 +196,7 @@ __device__ __forceinline__ void store_group_block(uint16_t* C, int64_t ldc, int 
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
             f32x4 v = acc[mi][j];
-            finish(r0 + lc, col_w + j * 16 + 4 * lg, v);
+            finish(mi, j, r0 + lc, col_w + j * 16 + 4 * lg, v);
             uint2 o;
             const float v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
             o.x = (uint32_t)bf16_rne(v0) | (uint32_t)bf16_rne(v1) << 16;
@@ -225,6 +225,11 @@ __device__ __forceinline__ void store_group_block(uint16_t* C, int64_t ldc, int 
         }
         wave_lds_order();
     });
+}
+
+__device__ __forceinline__ uint2 load8(rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
 }
 
 __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p)
@@ -657,6 +662,25 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             acc[mi][j] = mfma_bf16(bf[set][j], af[set][mi], acc[mi][j]);
         }
     };
+    // GATED: the multipliers of blocks of 16 rows, AHEAD of them on their way, the first
+    // ones before the next item's loads (39200 rows of 2048 x 512 with SiLU: 144 us, 189
+    // where they were read as they were used, one block after the other).
+    constexpr bool MUL = ROLE == GROUP_GATED;
+    constexpr int AHEAD = MR < 2 ? MR : 2;
+    uint2 mulv[MUL ? AHEAD + 1 : 1][MUL ? NR : 1];
+    auto load_mul = [&](int mi, int m0, int n0, int rows) __attribute__((always_inline)) {
+        const KernelArgs q = kernel_args();
+        int ol = lane;
+        asm volatile("" : "+v"(ol));
+        const rsrc_t r = make_rsrc(uniform(reinterpret_cast<const uint8_t*>(q->mul + (int64_t)m0 * q->ld_mul)),
+                                   (uint32_t)((rows - 1) * (int)q->ld_mul + q->N) * 2u);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const int col = n0 + (int)col0 + j * R + 4 * (ol >> 4);
+            const int at = ((int)row0 + mi * R + (ol & 15)) * (int)q->ld_mul + col;
+            mulv[mi % (AHEAD + 1)][j] = load8(r, col < q->N ? (uint32_t)at * 2u : kOOB);
+        }
+    };
     auto output = [&](int group, int m0, int n0, int rows) __attribute__((always_inline)) {
         const KernelArgs q = kernel_args();
         // the lane again, as a value of its own, so that what the outputs derive
@@ -667,49 +691,57 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
         uint8_t* stage = lds + S::OUT_AT + wave * (R * S::SROW);
         if constexpr (ADAPT) {
             store_group_block<MR, NR, S::SROW>(
-                q->C, q->ldc, q->N, q->c_vec, acc, stage, (int)row0, col_w, ol, [](int, int, f32x4&) {},
+                q->C, q->ldc, q->N, q->c_vec, acc, stage, (int)row0, col_w, ol,
+                [](int, int, int, int, f32x4&) {},
                 [&](int r) __attribute__((always_inline)) {
                     const int to = r < rows ? q->order[m0 + r] : -1;
                     return to < q->S ? to : -1;
                 });
         } else if constexpr (ROLE == GROUP_GATED) {
-            auto gated = [&](auto cls) __attribute__((always_inline)) {
+            auto gated = [&](auto cls, auto vec) __attribute__((always_inline)) {
+                constexpr bool VEC = decltype(vec)::value;
                 store_group_block<MR, NR, S::SROW>(
                     q->C + (int64_t)m0 * q->ldc, q->ldc, q->N, q->c_vec, acc, stage, (int)row0, col_w, ol,
-                    [&](int r, int col, f32x4& v) __attribute__((always_inline)) {
+                    [&](int mi, int j, int r, int col, f32x4& v) __attribute__((always_inline)) {
+                        if (VEC && j == 0 && mi + AHEAD < MR)
+                            load_mul(mi + AHEAD, m0, n0, rows);
                         float f[4] = {1.f, 1.f, 1.f, 1.f};
-                        if (q->mul && r < rows && col < q->N) {
+                        if constexpr (VEC) {
+                            const uint2 u = mulv[mi % (AHEAD + 1)][j];
+                            f[0] = __uint_as_float(u.x << 16);
+                            f[1] = __uint_as_float(u.x & 0xFFFF0000u);
+                            f[2] = __uint_as_float(u.y << 16);
+                            f[3] = __uint_as_float(u.y & 0xFFFF0000u);
+                        } else if (q->mul && r < rows && col < q->N) {
                             const uint16_t* from = q->mul + (int64_t)(m0 + r) * q->ld_mul + col;
-                            if (q->mul_vec) {
-                                const uint2 u = *reinterpret_cast<const uint2*>(from);
-                                f[0] = __uint_as_float(u.x << 16);
-                                f[1] = __uint_as_float(u.x & 0xFFFF0000u);
-                                f[2] = __uint_as_float(u.y << 16);
-                                f[3] = __uint_as_float(u.y & 0xFFFF0000u);
-                            } else {
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    f[e] = bf16_to_f32(from[min(e, q->N - 1 - col)]);
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                f[e] = bf16_to_f32(from[min(e, q->N - 1 - col)]);
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float a = activate_c<decltype(cls)::value>(q->act, v[e]);
-                            v[e] = q->mul ? a * f[e] : a;
+                            v[e] = VEC || q->mul ? a * f[e] : a;
                         }
                     },
                     [&](int r) __attribute__((always_inline)) { return r < rows ? r : -1; });
             };
-            switch (act_class(q->act)) {
-            case 1:
-                gated(std::integral_constant<int, 1>{});
-                break;
-            case 2:
-                gated(std::integral_constant<int, 2>{});
-                break;
-            default:
-                gated(std::integral_constant<int, 0>{});
-            }
+            auto activated = [&](auto vec) __attribute__((always_inline)) {
+                switch (act_class(q->act)) {
+                case 1:
+                    gated(std::integral_constant<int, 1>{}, vec);
+                    break;
+                case 2:
+                    gated(std::integral_constant<int, 2>{}, vec);
+                    break;
+                default:
+                    gated(std::integral_constant<int, 0>{}, vec);
+                }
+            };
+            if (q->mul_vec)
+                activated(std::true_type{});
+            else
+                activated(std::false_type{});
         } else {
             store_bf16_block<MR, NR, 1, S::SROW>(q->C + group * q->c_group, q->ldc, q->N, q->c_vec, acc, stage,
                                                  m0, rows, (int)row0, col_w, ol);
@@ -986,6 +1018,20 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                 }
                 DG_STAGE_BARRIER(0);
             }
+        }
+        if constexpr (MUL) {
+            if (!idle && kernel_args()->mul_vec) {
+#pragma unroll
+                for (int mi = 0; mi < AHEAD; ++mi)
+                    load_mul(mi, m0, n0, rows);
+            } else {                           // (or they would be kept from the item before)
+#pragma unroll
+                for (int mi = 0; mi < AHEAD; ++mi)
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+                        mulv[mi][j] = make_uint2(0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         // the next item's loads go out before this one's outputs
         const int o_group = group, o_m0 = m0, o_n0 = n0, o_rows = rows;

@@ -275,7 +275,7 @@ hipError_t group_forward(const ProductCall& c)
     a.act = c.act;
     a.mul = c.mul;
     a.ld_mul = c.ld_mul;
-    a.mul_vec = ((uintptr_t)c.mul & 7u) == 0 && c.ld_mul % 4 == 0 && c.N % 4 == 0;
+    a.mul_vec = c.mul && ((uintptr_t)c.mul & 7u) == 0 && c.ld_mul % 4 == 0 && c.N % 4 == 0;
     a.b_nt = 1;
     const bool across = ((uintptr_t)c.W | (uint64_t)c.ldw * 2 | (uint64_t)c.ldw_group * 2) % 64 != 0;
     const int shape = pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus, weights_us(used, c.N, c.K), used, across,
