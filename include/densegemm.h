@@ -681,7 +681,8 @@ gemm_status group_combine_grad(const uint16_t* dout, int64_t ld_dout, const uint
  *   W   device bf16 [N, ldw], A [groups][R][lda], B [groups][N][ldb], as W above; R a
  *       multiple of 8 up to 256 (adapters of lower rank end in zeros).
  *   scale  device fp32 [groups], NULL: 1.
- *   workspace  256-byte aligned, linear_adapters_workspace_bytes(T, R, groups) bytes.
+ *   workspace  256-byte aligned, linear_adapters_workspace_bytes(T, R, groups) bytes (up to
+ *              2048 rows with room for sums over slices of K, 32 MiB at most).
  *
  * Errors of these: as above, and INVALID_VALUE for a misaligned operand or pitch;
  * UNSUPPORTED for K (grad: or N) not a multiple of 8, K > 2^16, N > 2^20 (grad: 2^16), R
