@@ -16,7 +16,7 @@
 // any order cost what sorted ones cost, and no sorted copy of X is made.
 //
 // How many rows a group has is known on the device only.  Every workgroup
-// turns the offsets into the groups' first tiles (a scan over at most 1024
+// turns the offsets into the groups' first tiles (a scan over at most 512
 // groups in LDS, under 2 us) and walks a persistent range of tiles; no host
 // synchronisation, no table from another launch.
 #pragma once
