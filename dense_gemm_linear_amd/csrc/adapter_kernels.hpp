@@ -18,10 +18,11 @@ namespace dg {
 // at 15 bytes a clock and CU).  The waves turn them in LDS of their own, without
 // barriers, and add their sums at the end in a fixed order.
 // The group whose rows sorted position x is among: the number of groups that end
-// at or before it (`groups`: none).
+// at or before it (`groups`: none, as for a row in front of the first group's, which a
+// range of a larger table's offsets has).
 __device__ __forceinline__ int row_group(const int* offsets, int groups, int x, int lane)
 {
-    int n = 0;
+    int n = x < offsets[0] ? groups : 0;
     for (int g = 0; g < groups; g += 64)
         n += __popcll(__ballot(g + lane < groups && offsets[min(g + lane, groups - 1) + 1] <= x));
     return __builtin_amdgcn_readfirstlane(n);

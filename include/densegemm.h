@@ -599,7 +599,9 @@ gemm_status linear_distillation_grad(const uint16_t* X, int64_t ldx, const uint1
  *   order    device int32 [S]: the slot t k + j at each sorted position.
  *   place    device int32 [T][k]: the sorted position of each slot, -1 for a slot
  *            that takes no part.
- * group_sort writes the three; they may also come from elsewhere.  Offsets that
+ * group_sort writes the three; they may also come from elsewhere.  offsets[0] is 0 there;
+ * where it is not (offsets + g of a larger table, with group g's weights first), the rows
+ * in front belong to no group, as those from n on.  Offsets that
  * are not ascending, and an order or place outside [0, S), give unspecified rows
  * but reach no memory outside the buffers described.
  *
