@@ -8,6 +8,7 @@
 #endif
 #include "internal.hpp"
 
+#include <stdio.h>
 #include <string.h>
 
 #include <algorithm>
@@ -252,6 +253,8 @@ int vec_of(const uint16_t* C, int64_t ldc, int64_t N)
 // Adapters in slices of K: rows at most, and what the workspace holds for the
 // slices' sums: 8 slices of 16384 columns, 32 MiB at most.
 constexpr int64_t kSplitRows = 2048;
+// waves of a workgroup of one token's kernel
+constexpr int kTokenWaves = 16;
 static int64_t split_bytes(int64_t T)
 {
     return T <= kSplitRows ? std::min<int64_t>(T << 19, INT64_C(32) << 20) : 0;
@@ -261,6 +264,26 @@ static int64_t inner_bytes(int64_t T, int64_t R) { return cdiv(T * R * 4, 256) *
 int64_t group_grad_workspace(int64_t T, int64_t k, int64_t K) { return T * k * K * 2; }
 
 int64_t adapters_workspace(int64_t T, int64_t R) { return inner_bytes(T, R) + split_bytes(T); }
+
+// The shapes of a call's products.
+static int forward_shape(const ProductCall& c)
+{
+    const int64_t used = std::min(c.groups, c.T * c.k);
+    const bool across = ((uintptr_t)c.W | (uint64_t)c.ldw * 2 | (uint64_t)c.ldw_group * 2) % 64 != 0;
+    return pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus, weights_us(used, c.N, c.K), used, across,
+                [&](int tm) { return row_tiles(c.T, c.k, c.groups, used, tm); }).shape;
+}
+static int dx_shape(const ProductCall& c)
+{
+    const int64_t used = std::min(c.groups, c.T * c.k);
+    return pick(kDx, c.K, (double)cdiv(c.N, 32), c.cus, weights_us(used, c.N, c.K), used, false,
+                [&](int tm) { return row_tiles(c.T, c.k, c.groups, used, tm); }).shape;
+}
+static int dw_shape(const ProductCall& c)
+{
+    return pick(kDw, c.K, (double)cdiv(cdiv(c.T * c.k, c.groups), 32), c.cus, 0.0, 1, false,
+                [&](int tm) { return (double)(c.groups * cdiv(c.N, tm)); }).shape;
+}
 
 hipError_t group_forward(const ProductCall& c)
 {
@@ -282,9 +305,7 @@ hipError_t group_forward(const ProductCall& c)
     a.ld_mul = c.ld_mul;
     a.mul_vec = c.mul && ((uintptr_t)c.mul & 7u) == 0 && c.ld_mul % 4 == 0 && c.N % 4 == 0;
     a.b_nt = 1;
-    const bool across = ((uintptr_t)c.W | (uint64_t)c.ldw * 2 | (uint64_t)c.ldw_group * 2) % 64 != 0;
-    const int shape = pick(kPlain, c.N, (double)cdiv(c.K, 32), c.cus, weights_us(used, c.N, c.K), used, across,
-                           [&](int tm) { return row_tiles(c.T, c.k, c.groups, used, tm); }).shape;
+    const int shape = forward_shape(c);
     return c.act || c.mul ? launch_group_gated(shape, a, used, c.cus, c.stream)
                           : launch_group_fwd(shape, a, used, c.cus, c.stream);
 }
@@ -305,9 +326,7 @@ hipError_t group_backward(const ProductCall& c)
         a.ldc = c.lddx;
         a.c_vec = vec_of(c.dX, c.lddx, c.K);
         a.b_nt = 1;
-        const int shape = pick(kDx, c.K, (double)cdiv(c.N, 32), c.cus, weights_us(used, c.N, c.K), used, false,
-                               [&](int tm) { return row_tiles(c.T, c.k, c.groups, used, tm); }).shape;
-        const hipError_t e = launch_group_dx(shape, a, used, c.cus, c.stream);
+        const hipError_t e = launch_group_dx(dx_shape(c), a, used, c.cus, c.stream);
         if (e != hipSuccess)
             return e;
     }
@@ -352,9 +371,7 @@ hipError_t group_backward(const ProductCall& c)
     // 984 x 5528: 357 us, 189 through the caches; of 984 x 5504 159 and 164).
     if (a.c_vec && ((uintptr_t)c.dW | (uint64_t)c.lddw * 2 | (uint64_t)c.lddw_group * 2) % 64 == 0)
         a.c_vec = 2;
-    const int shape = pick(kDw, c.K, (double)cdiv(cdiv(S, c.groups), 32), c.cus, 0.0, 1, false,
-                           [&](int tm) { return (double)(c.groups * cdiv(c.N, tm)); }).shape;
-    return launch_group_dw(shape, a, 0, c.cus, c.stream);
+    return launch_group_dw(dw_shape(c), a, 0, c.cus, c.stream);
 }
 
 template <class Args>
@@ -368,35 +385,47 @@ hipError_t launch(const void* kernel, dim3 grid, int block, Args a, hipStream_t 
 // that; else the smallest tile whose workgroups do (a workgroup takes 2.5 us and 1.9
 // for each 16 rows of X or A, K 4096: 4095 rows of 64 ranks 19 us as 32 x 64, 34 as
 // 16 x 16; 597 of 32 ranks 7.6 as 16 x 16, 13.7 as 64 x 32).
+constexpr struct {
+    int nr, mb;
+} kInner[] = {{1, 1}, {1, 2}, {2, 2}, {1, 4}, {4, 2}, {2, 4}, {4, 4}};
+constexpr int kInnerTiles = (int)(sizeof kInner / sizeof kInner[0]);
+
+// The tile, or -1: a workgroup a row.
+int inner_tile(int64_t T, int64_t groups, int64_t R, int cus)
+{
+    const int64_t units = cdiv(R, 16);
+    if (T * units <= cus)
+        return -1;
+    // groups in use are not known here; each has a partly filled tile
+    const int64_t some = std::min<int64_t>(std::min<int64_t>(groups, 16), T / 16 + 1);
+    int best = 0;
+    for (int t = 0; t < kInnerTiles; ++t) {
+        if (kInner[t].nr > 1 && kInner[t].nr / 2 >= units)
+            continue;
+        best = t;
+        if ((T / (16 * kInner[t].mb) + some) * cdiv(units, kInner[t].nr) <= cus)
+            break;
+    }
+    return best;
+}
+
 hipError_t launch_inner(const InnerArgs& i, int cus, hipStream_t s)
 {
     const int64_t T = i.S, units = cdiv(i.R, 16);
-    if (T * units <= cus)
+    const int t = inner_tile(T, i.groups, i.R, cus);
+    if (t < 0)
         return launch(reinterpret_cast<const void*>(&adapter_inner_row_kernel), dim3((unsigned)T, (unsigned)units),
                       1024, i, s);
-    struct {
-        const void* kernel;
-        int nr, mb;
-    } const tiles[] = {{reinterpret_cast<const void*>(&adapter_inner_kernel<1, 1>), 1, 1},
-                       {reinterpret_cast<const void*>(&adapter_inner_kernel<1, 2>), 1, 2},
-                       {reinterpret_cast<const void*>(&adapter_inner_kernel<2, 2>), 2, 2},
-                       {reinterpret_cast<const void*>(&adapter_inner_kernel<1, 4>), 1, 4},
-                       {reinterpret_cast<const void*>(&adapter_inner_kernel<4, 2>), 4, 2},
-                       {reinterpret_cast<const void*>(&adapter_inner_kernel<2, 4>), 2, 4},
-                       {reinterpret_cast<const void*>(&adapter_inner_kernel<4, 4>), 4, 4}};
-    // groups in use are not known here; each has a partly filled tile
-    const int64_t some = std::min<int64_t>(std::min<int64_t>(i.groups, 16), T / 16 + 1);
-    int best = 0;
-    for (int t = 0; t < 7; ++t) {
-        if (tiles[t].nr > 1 && tiles[t].nr / 2 >= units)
-            continue;
-        best = t;
-        if ((T / (16 * tiles[t].mb) + some) * cdiv(units, tiles[t].nr) <= cus)
-            break;
-    }
-    return launch(tiles[best].kernel,
-                  dim3((unsigned)(T / (16 * tiles[best].mb) + std::min<int64_t>(i.groups, T)),
-                       (unsigned)cdiv(units, tiles[best].nr)),
+    const void* const kernels[kInnerTiles] = {reinterpret_cast<const void*>(&adapter_inner_kernel<1, 1>),
+                                              reinterpret_cast<const void*>(&adapter_inner_kernel<1, 2>),
+                                              reinterpret_cast<const void*>(&adapter_inner_kernel<2, 2>),
+                                              reinterpret_cast<const void*>(&adapter_inner_kernel<1, 4>),
+                                              reinterpret_cast<const void*>(&adapter_inner_kernel<4, 2>),
+                                              reinterpret_cast<const void*>(&adapter_inner_kernel<2, 4>),
+                                              reinterpret_cast<const void*>(&adapter_inner_kernel<4, 4>)};
+    return launch(kernels[t],
+                  dim3((unsigned)(T / (16 * kInner[t].mb) + std::min<int64_t>(i.groups, T)),
+                       (unsigned)cdiv(units, kInner[t].nr)),
                   512, i, s);
 }
 
@@ -492,13 +521,48 @@ hipError_t go_split(const ProductCall& c, int64_t slices)
     return launch(join, dim3((unsigned)cdiv(T, kJoinRows), (unsigned)cdiv(c.N, 256)), 256, j, c.stream);
 }
 
+// How a call of linear_adapters is done.
+struct AdapterChoice {
+    int64_t token_rows;            // > 0: one token in one launch, rows of W a wave
+    AdapterPlan split;             // tm > 0: slices of K
+    int shape;                     // else the whole product's
+};
+AdapterChoice adapter_choice(const ProductCall& c)
+{
+    const int64_t T = c.T;
+    AdapterChoice a = {0, {0, 0, 0.0}, -1};
+    // One token in one launch, where that forms the inner values in every workgroup in
+    // little time (4096 x 4096, rank 32: 12 us, in slices 14; rank 64 16 and 14, rank 256 57
+    // and 17; 2048 x 2048, rank 64: 11 and 14): one workgroup of 16 waves a CU, with as
+    // many rows a wave as that takes, up to 4.
+    if (T == 1 && c.R * c.K <= 1 << 17) {
+        a.token_rows = std::min<int64_t>(4, cdiv(c.N, (int64_t)c.cus * kTokenWaves));
+        return a;
+    }
+    // every row counts, groups or not; the ranks as k-tiles of about as many adapters
+    // as a tile of 64 rows has
+    const int64_t near = std::min<int64_t>(std::min(c.groups, T), cdiv(std::min(c.groups, T) * 64, T) + 1);
+    const double kts = (double)cdiv(c.K, 32) + (double)(near * cdiv(c.R, 16));
+    const Picked whole = pick(kAdapt, c.N, kts, c.cus, 0.0, 1, false,
+                              [&](int tm) { return (double)cdiv(T, tm); });
+    a.shape = whole.shape;
+    // In slices of K where that takes less: the whole product has the inner values in a
+    // launch before it, and its ranks.  16 ranks: 48 rows of 11008 x 4096 26.6 us against
+    // 35.5, 40 of 4096 x 4096 14.7 against 24.7, 300 of them 26.8 against 32.1; 400 of
+    // 11008 x 4096 82 against 77.
+    if (T <= kSplitRows) {
+        const AdapterPlan s = adapter_plan(T, c.N, c.K, c.R, c.cus);
+        if (s.tm && (T == 1 || s.us < 7.3 + 1.05 * whole.us))
+            a.split = s;
+    }
+    return a;
+}
+
 hipError_t adapters_forward(const ProductCall& c)
 {
     const int64_t T = c.T;
-    // One token in one launch, where that forms the inner values in every workgroup in
-    // little time (4096 x 4096, rank 32: 12 us, in slices 14; rank 64 16 and 14, rank 256 57
-    // and 17; 2048 x 2048, rank 64: 11 and 14).
-    if (T == 1 && c.R * c.K <= 1 << 17) {
+    const AdapterChoice choice = adapter_choice(c);
+    if (choice.token_rows > 0) {
         TokenArgs t;
         t.X = c.X;
         t.W = c.W;
@@ -516,32 +580,17 @@ hipError_t adapters_forward(const ProductCall& c)
         t.K = (int)c.K;
         t.R = (int)c.R;
         t.Y = c.Y;
-        // one workgroup of 16 waves a CU, with as many rows a wave as that takes, up to 4
-        constexpr int WAVES = 16;
-        const int64_t rows = std::min<int64_t>(4, cdiv(c.N, (int64_t)c.cus * WAVES));
-        const void* kernel = rows == 1   ? reinterpret_cast<const void*>(&adapter_token_kernel<1, WAVES>)
-                             : rows == 2 ? reinterpret_cast<const void*>(&adapter_token_kernel<2, WAVES>)
-                             : rows == 3 ? reinterpret_cast<const void*>(&adapter_token_kernel<3, WAVES>)
-                                         : reinterpret_cast<const void*>(&adapter_token_kernel<4, WAVES>);
-        return launch(kernel, dim3((unsigned)cdiv(c.N, rows * WAVES)), 64 * WAVES, t, c.stream);
+        const int64_t rows = choice.token_rows;
+        const void* kernel = rows == 1   ? reinterpret_cast<const void*>(&adapter_token_kernel<1, kTokenWaves>)
+                             : rows == 2 ? reinterpret_cast<const void*>(&adapter_token_kernel<2, kTokenWaves>)
+                             : rows == 3 ? reinterpret_cast<const void*>(&adapter_token_kernel<3, kTokenWaves>)
+                                         : reinterpret_cast<const void*>(&adapter_token_kernel<4, kTokenWaves>);
+        return launch(kernel, dim3((unsigned)cdiv(c.N, rows * kTokenWaves)), 64 * kTokenWaves, t, c.stream);
     }
-    // every row counts, groups or not; the ranks as k-tiles of about as many adapters
-    // as a tile of 64 rows has
-    const int64_t near = std::min<int64_t>(std::min(c.groups, T), cdiv(std::min(c.groups, T) * 64, T) + 1);
-    const double kts = (double)cdiv(c.K, 32) + (double)(near * cdiv(c.R, 16));
-    const Picked whole = pick(kAdapt, c.N, kts, c.cus, 0.0, 1, false,
-                              [&](int tm) { return (double)cdiv(T, tm); });
-    // In slices of K where that takes less: the whole product has the inner values in a
-    // launch before it, and its ranks.  16 ranks: 48 rows of 11008 x 4096 26.6 us against
-    // 35.5, 40 of 4096 x 4096 14.7 against 24.7, 300 of them 26.8 against 32.1; 400 of
-    // 11008 x 4096 82 against 77.
-    if (T <= kSplitRows) {
-        const AdapterPlan s = adapter_plan(T, c.N, c.K, c.R, c.cus);
-        if (s.tm && (T == 1 || s.us < 7.3 + 1.05 * whole.us))
-            return s.tm == SLow::TM   ? go_split<SLow>(c, s.slices)
-                   : s.tm == SFew::TM ? go_split<SFew>(c, s.slices)
-                                      : go_split<SMid>(c, s.slices);
-    }
+    if (choice.split.tm)
+        return choice.split.tm == SLow::TM   ? go_split<SLow>(c, choice.split.slices)
+               : choice.split.tm == SFew::TM ? go_split<SFew>(c, choice.split.slices)
+                                             : go_split<SMid>(c, choice.split.slices);
     const uint32_t x_bytes = (uint32_t)((T - 1) * c.ldx * 2 + c.K * 2);
     InnerArgs i;
     i.X = reinterpret_cast<const uint8_t*>(c.X);
@@ -578,7 +627,37 @@ hipError_t adapters_forward(const ProductCall& c)
     a.ldlb_b = c.ldb * 2;
     a.lb_group = c.ldb_group * 2;
     a.R = (int)c.R;
-    return launch_group_adapt(whole.shape, a, 0, c.cus, c.stream);
+    return launch_group_adapt(choice.shape, a, 0, c.cus, c.stream);
+}
+
+// What a call takes, as a text: for the tests, which are to reach every instance.
+extern "C" int dg_group_choice(int op, int64_t T, int64_t k, int64_t groups, int64_t N, int64_t K, int64_t R, int cus,
+                               char* text, size_t bytes)
+{
+    static const char* const names[] = {"256x256", "256x128", "128x128 transposed", "128x128", "128x128 deep", "128x64",
+                                        "64x128", "64x64", "32x128", "32x64", "16x32"};
+    ProductCall c;
+    memset(&c, 0, sizeof c);
+    c.T = T;
+    c.k = k;
+    c.groups = groups;
+    c.N = N;
+    c.K = K;
+    c.R = R;
+    c.cus = cus;
+    c.ldw = K;
+    c.ldw_group = N * K;
+    if (op < GROUP_ADAPT)
+        return snprintf(text, bytes, "%s",
+                        names[op == GROUP_FWD ? forward_shape(c) : op == GROUP_DX ? dx_shape(c) : dw_shape(c)]);
+    const AdapterChoice a = adapter_choice(c);
+    if (a.token_rows > 0)
+        return snprintf(text, bytes, "token %d", (int)a.token_rows);
+    if (a.split.tm)
+        return snprintf(text, bytes, "slices %d", a.split.tm);
+    const int t = inner_tile(T, groups, R, cus);
+    return t < 0 ? snprintf(text, bytes, "whole %s, inner row", names[a.shape])
+                 : snprintf(text, bytes, "whole %s, inner %dx%d", names[a.shape], 16 * kInner[t].mb, 16 * kInner[t].nr);
 }
 
 #endif
