@@ -42,10 +42,13 @@ struct InnerArgs {
     uint16_t* U;           // [S][2][R]
 };
 
-// u in its two halves
+// u in its two halves.  A finite value that would round to infinity has the largest
+// finite one as its upper half, which leaves a finite rest.
 __device__ __forceinline__ void store_inner(uint16_t* to, int R, float v)
 {
-    const uint16_t hi = bf16_rne(v);
+    uint16_t hi = bf16_rne(v);
+    if ((hi & 0x7FFFu) == 0x7F80u && fabsf(v) < INFINITY)
+        --hi;
     const float rest = v - bf16_to_f32(hi);      // infinite v: none
     to[0] = hi;
     to[R] = fabsf(rest) < INFINITY ? bf16_rne(rest) : 0;
