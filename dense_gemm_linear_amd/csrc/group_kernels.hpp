@@ -58,6 +58,8 @@ struct GroupArgs {
                            // adapter, and whether adapters share k-tiles of them
 };
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kTableLds = ((int)kMaxGroups + 4) * 4 + 64;
 
 // Tile shape: TM x TN outputs, WM x WN waves, ST stages of KTB bytes of K, OCC
@@ -978,6 +980,40 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
                               0);
                     }
                 }
+                // An infinity of B counts against the upper halves only: against a lower one,
+                // zero or of the other sign, it would turn the row's infinity into NaN.  Every
+                // lane looks at the pieces that it loaded, before the others may (stages that
+                // hold no units have something of before, which nobody reads).
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+                asm volatile("" ::: "memory");
+                auto piece = [&](int t, int n) __attribute__((always_inline)) {
+                    return reinterpret_cast<i32x4*>(lds + t * STAGE + A_BUF + (wave + WAVES * n) * 1024 + ol * 16);
+                };
+                u16x2 largest = {0, 0};
+#pragma unroll
+                for (int t = 0; t < ST; ++t)
+#pragma unroll
+                    for (int n = 0; n < B_DMA; ++n) {
+                        const i32x4 w = *piece(t, n);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            largest = __builtin_elementwise_max(largest,
+                                                                __builtin_bit_cast(u16x2, w[e] & 0x7FFF7FFF));
+                    }
+                if (c / 2 % 2 && max(largest[0], largest[1]) >= 0x7F80)
+#pragma unroll 1
+                    for (int t = 0; t < ST; ++t)
+#pragma unroll 1
+                        for (int n = 0; n < B_DMA; ++n) {
+                            i32x4 w = *piece(t, n);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t v = (uint32_t)w[e];
+                                w[e] = (int)(((v & 0x7F80u) == 0x7F80u ? 0u : v & 0xFFFFu) |
+                                             ((v & 0x7F800000u) == 0x7F800000u ? 0u : v & 0xFFFF0000u));
+                            }
+                            *piece(t, n) = w;
+                        }
                 DG_STAGE_BARRIER(0);
 #pragma unroll 1
                 for (int i = 0; i < ST * STEPS && !idle; ++i) {

@@ -1,5 +1,5 @@
-"""Inner values near fp32's largest give the same on every path: what the definition
-gives."""
+"""Infinities in an adapter, and inner values near fp32's largest, give the same on
+every path: what the definition gives."""
 import pytest
 import torch
 
@@ -16,6 +16,23 @@ def _check(got, X, W, A, B, off, order):
     want, err = (t.cpu() for t in _adapter_reference(X, W, A, B, None, off, order))
     assert not bool(torch.isnan(want).any())
     close(got, want, err, "Y")
+
+
+@pytest.mark.parametrize("form,T,groups,N,K,R", ADAPTER_SIZES)
+def test_infinite_entries(form, T, groups, N, K, R):
+    """One infinity in some columns of B: its rows get it with the sign of their inner
+    value, whatever bits that has; other columns stay finite."""
+    _say("infinite", form, T, groups, N, K, R)
+    ids, off, order, X, W, A, B, _ = _adapters(T, groups, N, K, R)
+    its = int(ids[T - 1])
+    # a row whose inner values are exact in bf16, next to those that are not
+    X[T - 1] = 0
+    X[T - 1, 0] = 1
+    B[its, ::3, R // 2] = float("inf")
+    B[its, 1::6, 0] = float("-inf")
+    got = dg.linear_adapters(X, W, A, B, off, order)
+    assert bool(torch.isinf(got[T - 1, ::3]).all())
+    _check(got, X, W, A, B, off, order)
 
 
 @pytest.mark.parametrize("form,T,groups,N,K,R", ADAPTER_SIZES)
