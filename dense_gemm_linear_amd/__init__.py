@@ -888,7 +888,15 @@ import torch as _pt  # noqa: E402  (loaded by _load_lib already)
 
 _BF16, _F32, _I32, _I64 = _pt.bfloat16, _pt.float32, _pt.int32, _pt.int64
 _new = _pt.empty_strided
-_raw_stream, _current_device = _pt._C._cuda_getCurrentRawStream, _pt._C._cuda_getDevice
+
+
+def _public_stream(dev: int) -> int:
+    return _pt.cuda.current_stream(dev).cuda_stream
+
+
+# (where this build of torch has the shorter ways)
+_raw_stream = getattr(_pt._C, "_cuda_getCurrentRawStream", _public_stream)
+_current_device = getattr(_pt._C, "_cuda_getDevice", _pt.cuda.current_device)
 
 
 def _refuse(fn: str, name: str, what: str):

@@ -1,0 +1,39 @@
+"""The grouped rows' binding: the import, streams, and arguments that name themselves
+when they are refused."""
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import dense_gemm_linear_amd as dg
+from conftest import ROOT
+
+CODE = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import dense_gemm_linear_amd as dg
+print(dg.select_tile(512, 512, 512, num_cus=256).name)
+try:
+    dg.group_sort(torch.zeros(4, 2, dtype=torch.int64), 4)
+except ValueError as e:
+    print(e)
+"""
+
+
+def test_import_without_private_names():
+    """The host's functions and the refusals need nothing that only some builds of
+    torch have."""
+    r = subprocess.run([sys.executable, "-c", CODE], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert dg.select_tile(512, 512, 512, num_cus=256).name in r.stdout and "group_sort: ids must be a device tensor" in r.stdout
+
+
+@pytest.mark.gpu
+def test_both_ways_to_the_stream():
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            assert dg._public_stream(0) == dg._raw_stream(0) == stream.cuda_stream
+            assert dg._current_device() == torch.cuda.current_device()
