@@ -1108,7 +1108,10 @@ def group_linear(X, W, offsets, order=None, *, slots: int = 1, activation=None, 
     _vector(fn, "offsets", offsets, _I32, G + 1)
     _group_order(fn, order, T, slots)
     S = T * slots
-    act = ACTIVATIONS[activation] if not isinstance(activation, int) else activation
+    act = activation if isinstance(activation, int) else \
+        ACTIVATIONS.get(activation) if activation is None or isinstance(activation, str) else None
+    if act is None:
+        _refuse(fn, "activation", "one of " + ", ".join(str(a) for a in ACTIVATIONS))
     ldm = 0 if mul is None else _matrix(fn, "mul", mul, _BF16, S, N)[2]
     if out is None:
         out = _new((S, N), (N, 1), dtype=_BF16, device=X.device)

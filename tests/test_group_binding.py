@@ -37,3 +37,10 @@ def test_both_ways_to_the_stream():
         with torch.cuda.stream(stream):
             assert dg._public_stream(0) == dg._raw_stream(0) == stream.cuda_stream
             assert dg._current_device() == torch.cuda.current_device()
+
+
+@pytest.mark.parametrize("activation", ["swish", "", ["silu"], 1.0])
+def test_activation_names_itself(activation):
+    X, W = torch.zeros(8, 64, dtype=torch.bfloat16), torch.zeros(4, 32, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="group_linear: activation"):
+        dg.group_linear(X, W, torch.zeros(5, dtype=torch.int32), activation=activation)
