@@ -1099,8 +1099,8 @@ def _group_order(fn: str, order, T: int, slots: int):
 def group_linear(X, W, offsets, order=None, *, slots: int = 1, activation=None, mul=None, out=None):
     """Y [S, N] with Y[p] = act(x W[g]^T) * mul[p] for the rows p of group g, offsets[g] <=
     p < offsets[g + 1]; W bf16 [groups, N, K] as it lies in memory.  x is X[order[p] //
-    slots] (X bf16 [T, K], S = T * slots; no sorted copy is made), or X[p] without an
-    order (X sorted, S = T).  activation: one of ACTIVATIONS; mul bf16 [S, N], which
+    slots] (X bf16 [T, K] of less than 2 GiB, S = T * slots; no sorted copy is made), or
+    X[p] without an order (X sorted, S = T).  activation: one of ACTIVATIONS; mul bf16 [S, N], which
     may be `out` itself.  Rows from offsets[-1] on are not written."""
     fn = "group_linear"
     T, K, ldx = _matrix(fn, "X", X, _BF16)
@@ -1163,8 +1163,8 @@ def linear_adapters(X, W, A, B, offsets, order, *, scale=None, out=None, workspa
     shared projection (W bf16 [N, K]) and the low-rank adapters of many requests
     (A bf16 [groups, R, K], B bf16 [groups, N, R], scale float32 [groups] or None for 1).
     offsets and order as group_sort(adapter of each row, groups) gives them; rows of
-    no adapter get the projection alone.  workspace: a uint8 tensor of
-    linear_adapters_workspace_bytes bytes."""
+    no adapter get the projection alone.  X of 2 GiB or more goes in pieces of rows, each
+    sorted by itself.  workspace: a uint8 tensor of linear_adapters_workspace_bytes bytes."""
     fn = "linear_adapters"
     T, K, ldx = _matrix(fn, "X", X, _BF16)
     N, _, ldw = _matrix(fn, "W", W, _BF16, None, K)

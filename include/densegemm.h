@@ -607,7 +607,7 @@ gemm_status linear_distillation_grad(const uint16_t* X, int64_t ldx, const uint1
  *
  * Calls that share a workspace must not overlap in time.
  * Buffers of sorted rows hold S rows.  Rows from n on (there are some if slots
- * take no part) are not written and not read.  Outputs must not overlap inputs
+ * take no part) are not written, and nothing depends on them.  Outputs must not overlap inputs
  * unless it is said.  Sums have a fixed order: results are bitwise repeatable.
  * Work is enqueued on `stream` without allocation, synchronisation or memset
  * nodes, and may be captured in a graph; how many rows a group has is read on the
@@ -688,8 +688,10 @@ gemm_status group_combine_grad(const uint16_t* dout, int64_t ld_dout, const uint
  *
  * Errors of these: as above, and INVALID_VALUE for a misaligned operand or pitch;
  * UNSUPPORTED for K (grad: or N) not a multiple of 8, K > 2^16, N > 2^20 (grad: 2^16), R
- * not a multiple of 8 or > 256, a pitch above 2^21 elements, and with an order for rows
- * of X that span 2 GiB or more (group_gather sorts those).
+ * not a multiple of 8 or > 256, a pitch above 2^21 elements, and rows of X that span 2 GiB
+ * or more: in group_linear with an order (group_gather sorts those; without an order, and
+ * in group_linear_grad, there is no such limit), and in linear_adapters (a larger batch
+ * goes in pieces of rows, each with offsets and an order of its own).
  */
 gemm_status group_linear(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
                          int64_t w_stride, const int32_t* offsets, const int32_t* order, int64_t T,

@@ -66,3 +66,34 @@ def test_products_of_a_range(T, k, groups, N, K):
     a, b = int(off[g0]), int(off[g1])
     for t in (Y, dX):
         assert bool((t[:a] == MARK).all()) and bool((t[b:] == MARK).all())
+
+
+def test_gradients_of_far_rows():
+    """group_linear_grad with an order takes rows of X past 2 GiB; linear_adapters takes
+    them in pieces."""
+    T, G, N, K, tail = (1 << 20) - 8, 3, 24, 1032, 300
+    ids = torch.full((T, 1), -1)
+    ids[-tail:] = make_ids(tail, 1, G, 1)
+    off, order, _ = dg.group_sort(ids.cuda(), G)
+    n = int(off[-1])
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    rows, W, dYn = bf16(tail, K, seed=1), bf16(G, N, K, seed=2), bf16(n, N, seed=3)
+    X[-tail:] = rows.cuda()
+    dY = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+    dY[:n] = dYn.cuda()
+    dX, dW = dg.group_linear_grad(dY, X, W.cuda(), off, order)
+    at = order[:n].cpu().long() - (T - tail)
+    for g in range(G):
+        a, b = int(off[g]), int(off[g + 1])
+        close(dX[a:b], *product(dYn[a:b], W[g].t()), f"dX of group {g}")
+        close(dW[g], *product(dYn[a:b].t(), rows[at[a:b]].t()), f"dW of group {g}")
+    del dX, dY
+    A, B, Wd = bf16(G, 8, K, seed=4, scale=K ** -0.5), bf16(G, N, 8, seed=5), bf16(N, K, seed=6, scale=K ** -0.5)
+    dev = Wd.cuda(), A.cuda(), B.cuda()
+    with pytest.raises(dg.GemmError):
+        dg.linear_adapters(X, *dev, off, order)
+    half = X[T // 2:]
+    off, order, _ = dg.group_sort(ids[T // 2:].cuda(), G)
+    Y = dg.linear_adapters(half, *dev, off, order)[-tail:]
+    o, p, _ = sorted_slots(ids[-tail:], G)
+    close(Y, *_adapter_reference(rows, Wd, A, B, None, o, p), "Y")

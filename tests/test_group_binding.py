@@ -44,3 +44,15 @@ def test_activation_names_itself(activation):
     X, W = torch.zeros(8, 64, dtype=torch.bfloat16), torch.zeros(4, 32, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="group_linear: activation"):
         dg.group_linear(X, W, torch.zeros(5, dtype=torch.int32), activation=activation)
+
+
+def test_rows_of_2_gib():
+    """Rows of X that span 2 GiB: refused where the loads pick them up by 32-bit offsets."""
+    P, K = 0x10000, 1024
+    fits = ((1 << 31) - K * 2 - 1) // (K * 2) + 1
+    for T, status in ((fits, dg.GEMM_ERR_INVALID_VALUE), (fits + 1, dg.GEMM_ERR_UNSUPPORTED)):
+        # (a null pointer elsewhere refuses what the size does not)
+        Y = None if status == dg.GEMM_ERR_INVALID_VALUE else P
+        assert dg.lib.group_linear(P, K, P, K, 8 * K, P, P, T, 1, 4, 8, K, 0, None, 0, Y, 8, None) == status
+        assert dg.lib.linear_adapters(P, K, P, K, P, K, 8 * K, P, 8, 64, None, P, P, T, 8, K, 8, 4, Y, 8, P, 1 << 40,
+                                      None) == status
