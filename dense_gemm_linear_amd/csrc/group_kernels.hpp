@@ -834,12 +834,16 @@ __global__ __launch_bounds__(S::THREADS, S::OCC) void group_gemm_kernel(GroupArg
             k_loop<ST, STEPS, S::LOADS, step_groups(MR * NR), true>(nkt, nomask, load, nothing, nothing);
         if constexpr (ADAPT) {
             if constexpr (TM <= 64)
-            if (units > 0 && p.R <= 32) {
-                // A few rows and ranks: a thread takes a column of B at a time, the lanes of
-                // a wave neighbouring ones, whose ranks lie together in memory, for each row
-                // with its own adapter.  Sums in fp32 through LDS into the accumulators'
-                // layout.  (48 rows of 16 adapters of 16 ranks in 64 x 64 tiles: 4 us; by matrix
-                // steps, below, of which every adapter takes one in all 64 rows, 9.)
+            if (p.R <= 32 && units > p.units * (TM / 8)) {
+                // A few rows and ranks, and an adapter for every eighth row or more: a thread
+                // takes a column of B at a time, the lanes of a wave neighbouring ones, whose
+                // ranks lie together in memory, for each row with its own adapter.  Sums in fp32
+                // through LDS into the accumulators' layout.  They take the same time however
+                // many adapters the rows have, where the matrix steps, below, take one of all
+                // rows for each (28672 x 2048, 32 rows of 16 ranks in 32 x 64 tiles: 33.0 to 33.7
+                // us; 31.0 for one adapter, 32.8 for 4, 34.5 for 8, 41.7 for 32; 16 rows in 16 x 32
+                // tiles 31.6 to 32.4, and 31.6 for one, 32.0 for 2, 33.0 for 4, 36.2 for 16; 3000
+                // rows of 264 x 1024, 64 adapters, two in a 64 x 64 tile: 21.6 and 17.4).
                 const KernelArgs q = kernel_args();
                 float* delta = reinterpret_cast<float*>(lds);                  // [TM][TN + 4]
                 float* u_lds = delta + TM * (TN + 4);                          // [TM][32]

@@ -37,11 +37,15 @@ ADAPTER_SIZES = [("token 1", 1, 4, 1001, 264, 32), ("token 2", 1, 4, 4313, 264, 
                  ("slices 32", 130, 6, 5765, 936, 24), ("slices 64", 33, 5, 600, 4104, 24),
                  ("slices 128", 529, 9, 4241, 584, 8), ("slices 128", 67, 49, 8764, 584, 32),
                  ("slices 128", 66, 42, 8310, 648, 112),
-                 # ranks summed row by row: up to 64 rows a tile and 32 ranks
+                 # up to 64 rows a tile and 32 ranks: of many adapters summed row by row, of few
+                 # as steps of the matrix cores
+                 ("whole 16x32, inner 32x16", 2438, 512, 9, 272, 24), ("whole 32x64, inner row", 32, 32, 28673, 2056, 16),
+                 ("whole 64x64, inner 32x16", 2188, 512, 237, 872, 24),
+                 ("whole 64x128, inner row", 38, 96, 160811, 288, 24),
                  ("whole 16x32, inner 32x16", 2438, 58, 9, 272, 24), ("whole 32x64, inner row", 2, 6, 141613, 368, 24),
                  ("whole 64x64, inner 32x16", 2189, 35, 237, 872, 24),
                  ("whole 64x128, inner row", 37, 37, 160811, 288, 24),
-                 # and as steps of the matrix cores
+                 # more ranks
                  ("whole 16x32, inner 32x16", 294, 4, 9, 552, 208), ("whole 32x64, inner 32x32", 620, 39, 193, 536, 224),
                  ("whole 64x64, inner 64x64", 3420, 17, 133, 296, 248),
                  ("whole 64x128, inner 32x16", 171, 23, 8808, 296, 256), ("whole 128x64, inner 32x32", 3376, 8, 129, 272, 40),
