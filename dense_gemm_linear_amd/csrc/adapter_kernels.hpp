@@ -199,8 +199,8 @@ __device__ __forceinline__ float lanes_sum(float x)
 
 // The same for few rows: a workgroup a row and 16 ranks, a wave a rank, 512
 // values of K at a time over its lanes.  The row's group is found by counting the
-// offsets in front.  48 rows of 16 adapters of 16 ranks, K 4096: 4.3 us, 6.2 with the
-// kernel above.
+// offsets in front.  A whole call of 8 rows of 16 ranks, 14336 x 4096: 31.0 us, 32.9 with the
+// kernel above; 64 rows of 28672 x 4096 67.9 and 70.1, 200 of 14336 x 4096 61.1 and 64.0.
 __global__ __launch_bounds__(1024) void adapter_inner_row_kernel(InnerArgs p)
 {
     const int lane = threadIdx.x & 63;
